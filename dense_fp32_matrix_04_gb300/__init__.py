@@ -12,6 +12,9 @@ library is missing or fails to load, ``load()`` raises.
   status.
 * ``matmul(A, B, out=None)`` -- convenience wrapper for 2-D float32 CUDA tensors
   with unit column stride (row-major, possibly with a padded row stride).
+* ``block_norm``, ``quantize_i8``, ``matmul_i8``, ``linear_i8``, ``logprobs`` and
+  the two backward passes -- the operators of a language model around its
+  products, on CUDA tensors (``layers``; include/sgemm_layers.h).
 """
 
 from __future__ import annotations
@@ -19,6 +22,8 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+
+from . import layers
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm.so")
@@ -87,6 +92,8 @@ _SIGNATURES = {
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "sgemm_f32_host_workspace_size": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
     "sgemm_device_status": (ctypes.c_int, [ctypes.c_void_p]),
+    # the operators around the products (include/sgemm_layers.h)
+    **layers.SIGNATURES,
     # test-only interface (include/sgemm_testing.h)
     "sgemm_test_switches": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong]),
     "sgemm_test_tiny_path": (ctypes.c_int, [ctypes.c_int]),
@@ -400,3 +407,7 @@ def matmul(A, B, out=None, stream=None):
         raise ValueError("out has the wrong shape")
     sgemm_f32(M, N, K, A, lda, B, ldb, out, ldc, stream)
     return out
+
+
+from .layers import (block_norm, block_norm_backward, linear_i8, logprobs, logprobs_backward, matmul_i8,  # noqa: E402
+                     quantize_i8)

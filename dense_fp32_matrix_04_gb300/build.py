@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,7 +20,7 @@ LIB = os.path.join(PKG, "libsgemm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["sgemm_api.cu"]
+SOURCES = ["sgemm_api.cu", "layers_api.cu", "i8_api.cu"]
 
 
 def _nvcc() -> str:
@@ -31,7 +32,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
-    files += [os.path.join(ROOT, "include", h) for h in ("sgemm.h", "sgemm_testing.h")]
+    files += [os.path.join(ROOT, "include", h) for h in ("sgemm.h", "sgemm_layers.h", "sgemm_testing.h")]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -47,19 +48,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v",
-           "-shared", "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),
-           "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    tag = f".tmp{os.getpid()}"
+    common = [_nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xptxas", "-v", "-Xcompiler", "-fPIC,-O2",
+              "-I", os.path.join(ROOT, "include")]
+    # one object per source, compiled side by side, then one link
+    objects = [os.path.join(BUILD_DIR, s + tag + ".o") for s in SOURCES]
+    jobs = [[*common, "-c", "-o", o, os.path.join(CSRC, s)] for o, s in zip(objects, SOURCES)]
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        done = list(pool.map(lambda cmd: subprocess.run(cmd, capture_output=True, text=True), jobs))
+    if not any(r.returncode for r in done):
+        jobs.append([*common, "-shared", "-o", LIB + tag, *objects])
+        done.append(subprocess.run(jobs[-1], capture_output=True, text=True))
+    report = "".join(r.stdout + r.stderr for r in done)
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"nvcc failed ({res.returncode}); see {BUILD_DIR}/ptxas.log")
+        f.write("".join(" ".join(cmd) + "\n" for cmd in jobs) + report)
+    for o in objects:
+        if os.path.exists(o):
+            os.remove(o)
+    if any(r.returncode for r in done):
+        sys.stderr.write(report)
+        raise RuntimeError(f"nvcc failed; see {BUILD_DIR}/ptxas.log")
     if verbose:
-        sys.stdout.write(res.stdout + res.stderr)
-    os.replace(tmp, LIB)
+        sys.stdout.write(report)
+    os.replace(LIB + tag, LIB)
     return LIB
 
 

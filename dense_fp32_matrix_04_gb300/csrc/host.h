@@ -1,0 +1,76 @@
+// Host-side facts and checks that the library's translation units share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+#include <utility>
+
+#include "../../include/sgemm_layers.h"
+
+namespace sgemm_host {
+
+constexpr int kMaxDevices = 64;
+
+// The current device, its SM count and the address of its error word
+// (SGEMM_OK or SGEMM_ERR_DEVICE); queried once per device (sgemm_api.cu).
+struct Device {
+    int dev = 0;
+    int sms = 0;
+    int *err_word = nullptr;
+};
+__attribute__((visibility("hidden"))) int device(Device &out);
+
+// Nanoseconds a kernel may wait for its own copies before it gives up.
+__attribute__((visibility("hidden"))) unsigned long long wait_limit_ns();
+
+inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// A buffer's byte range; empty when it has no elements.
+struct Range {
+    uintptr_t lo = 0, hi = 0;
+    Range() = default;
+    Range(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t size)
+        : lo(reinterpret_cast<uintptr_t>(p)),
+          hi(p && rows > 0 && cols > 0 ? lo + (uintptr_t)(((rows - 1) * ld + cols) * size) : lo) {}
+    bool overlaps(const Range &o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Launches a kernel, in clusters of `cluster` blocks along x where that is
+// more than one; SGEMM_OK, or SGEMM_ERR_LAUNCH with the error cleared.
+template <class... Params, class... Args>
+int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,
+           Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess) return SGEMM_OK;
+    (void)cudaGetLastError();
+    return SGEMM_ERR_LAUNCH;
+}
+
+// Calls f(std::integral_constant<int, dtype>) for one of the three element types.
+template <class F>
+int by_dtype(int dtype, F &&f) {
+    switch (dtype) {
+        case SGEMM_F32: return f(std::integral_constant<int, SGEMM_F32>{});
+        case SGEMM_BF16: return f(std::integral_constant<int, SGEMM_BF16>{});
+        case SGEMM_F16: return f(std::integral_constant<int, SGEMM_F16>{});
+        default: return SGEMM_ERR_INVALID_ARG;
+    }
+}
+
+inline int dtype_size(int dtype) { return dtype == SGEMM_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == SGEMM_F32 || dtype == SGEMM_BF16 || dtype == SGEMM_F16; }
+
+}  // namespace sgemm_host

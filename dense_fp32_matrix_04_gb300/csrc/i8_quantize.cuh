@@ -1,0 +1,81 @@
+// Rows quantised to 8-bit integers with one scale each: s = max|x| / 127,
+// q = rint(x (127 / max|x|)).  The row is read once into registers (or, when
+// it is too wide for them, a second time from L2) and written as bytes: the
+// kernel is bound by memory.
+#pragma once
+
+#include <cstdint>
+
+#include "rows.cuh"
+
+namespace sgemm {
+
+// n 8-bit values to p, whole words at a time where `vec` says that they are aligned.
+template <int N>
+__device__ __forceinline__ void store_bytes(int8_t *p, const int8_t (&b)[N], bool vec) {
+    if constexpr (N % 4 == 0) {
+        if (vec) {
+            uint32_t w[N / 4];
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                w[i / 4] = (uint32_t)(uint8_t)b[i] | (uint32_t)(uint8_t)b[i + 1] << 8 |
+                           (uint32_t)(uint8_t)b[i + 2] << 16 | (uint32_t)(uint8_t)b[i + 3] << 24;
+            if constexpr (N == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(p) = w[0];
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = b[i];
+}
+
+template <int DT, int VW, int NV>
+__global__ void __launch_bounds__(1024)
+    quantize_i8_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
+                       int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale, int q_vec) {
+    using P = Piece<DT, VW>;
+    __shared__ float slots[64];
+    RowReducer red{slots, (int)(blockDim.x >> 5)};
+    const int threads = blockDim.x;
+    const int step = gridDim.x * blockDim.y;
+    for (int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; m < M; m += step) {
+        float v[NV * VW];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + (int)threadIdx.x) * VW;
+            P::unpack(c < K ? P::load(x + m * ldx + c) : P::zero(), v + i * VW);
+        }
+#pragma unroll
+        for (int i = 0; i < NV * VW; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+        const I8Scale s(red.max(top));
+        if (threadIdx.x == 0) scale[m] = s.scale;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + (int)threadIdx.x) * VW;
+            if (c >= K) continue;
+            int8_t b[VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) b[e] = s(v[i * VW + e]);
+            store_bytes(q + m * ldq + c, b, q_vec);
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(1024)
+    quantize_i8_wide_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
+                            int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
+    __shared__ float slots[64];
+    RowReducer red{slots, (int)(blockDim.x >> 5)};
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+        uint32_t top = 0;
+        for (int c = threadIdx.x; c < K; c += blockDim.x)
+            top = max(top, __float_as_uint(Elem<DT>::to_float(x[m * ldx + c])) & 0x7fffffffu);
+        const I8Scale s(red.max(top));
+        if (threadIdx.x == 0) scale[m] = s.scale;
+        for (int c = threadIdx.x; c < K; c += blockDim.x) q[m * ldq + c] = s(Elem<DT>::to_float(x[m * ldx + c]));
+    }
+}
+
+}  // namespace sgemm

@@ -1,0 +1,286 @@
+// The C interface of the row-wise operators: argument checks, kernel choice
+// and launch.  The contract is in include/sgemm_layers.h.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "block_norm.cuh"
+#include "host.h"
+#include "logprobs.cuh"
+
+namespace {
+
+using namespace sgemm;
+using sgemm_host::aligned;
+using sgemm_host::by_dtype;
+using sgemm_host::Device;
+using sgemm_host::dtype_ok;
+using sgemm_host::dtype_size;
+using sgemm_host::launch;
+using sgemm_host::Range;
+
+// A matrix of rows as an operator sees it.
+struct Rows {
+    const void *p;
+    int ld;
+    // 16-byte pieces: aligned base and rows
+    bool vec(int size) const { return !p || (aligned(p, 16) && (int64_t)ld * size % 16 == 0); }
+    bool ok(int cols, int size) const { return p && aligned(p, (unsigned)size) && ld >= std::max(cols, 1); }
+    Range range(int64_t rows, int cols, int size) const { return Range(p, rows, cols, ld, size); }
+    bool same(const Rows &o) const { return p == o.p && ld == o.ld; }
+};
+
+// The threads that share a row of D elements, `per` of them each: whole warps.
+int row_threads(int D, int per) { return ((D + per - 1) / per + 31) / 32 * 32; }
+
+constexpr int kMaxRows = 1 << 30, kMaxWidth = 65536;
+
+bool finite(float v) { return std::isfinite(v); }
+
+// ---------------------------------------------------------------- block norm
+
+template <int DT, int VW, int NV>
+int launch_norm(const BlockNormArgs &a, const Device &dev, cudaStream_t stream) {
+    const int threads = row_threads(a.D, VW * NV);
+    // a warp per row: four rows to a block
+    const dim3 block(threads, threads == 32 ? 4 : 1);
+    const int64_t groups = ((int64_t)a.T + block.y - 1) / block.y;
+    const int64_t most = (int64_t)dev.sms * std::max(1, 2048 / (int)(block.x * block.y));
+    const dim3 grid((unsigned)std::min(groups, most));
+    if (VW == 1 || threads <= 512) return launch(block_norm_kernel<DT, VW, NV, 512>, grid, block, 0, stream, 1, a);
+    if constexpr (VW > 1) return launch(block_norm_kernel<DT, VW, NV, 1024>, grid, block, 0, stream, 1, a);
+    return SGEMM_ERR_INVALID_ARG;
+}
+
+template <int DT>
+int norm_by_width(const BlockNormArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
+    constexpr int VEC = Elem<DT>::VEC;
+    // what the registers of a block hold: 8 elements a thread, 1024 threads on 16-byte pieces and
+    // 512 on single elements (whose addresses take more registers)
+    if (a.D > (vec ? 8192 : 4096))
+        return launch(block_norm_wide_kernel<DT>, dim3((unsigned)std::min(a.T, 2 * dev.sms)), dim3(1024), 0, stream, 1,
+                      a);
+    if (vec) return launch_norm<DT, VEC, 8 / VEC>(a, dev, stream);
+    return launch_norm<DT, 1, 8>(a, dev, stream);
+}
+
+// Blocks of the gradient: runs of rows, two blocks per SM.
+int grad_blocks(int T, int sms) { return std::min(T, 2 * sms); }
+
+template <int DT, int VW, int NV>
+int launch_norm_grad(const BlockNormGradArgs &a, int blocks, cudaStream_t stream) {
+    return launch(block_norm_grad_kernel<DT, VW, NV>, dim3(blocks), dim3(row_threads(a.D, VW * NV)), 0, stream, 1, a);
+}
+
+template <int DT>
+int norm_grad_by_width(const BlockNormGradArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
+    constexpr int VEC = Elem<DT>::VEC;
+    const int blocks = grad_blocks(a.T, dev.sms);
+    int st;
+    if (a.D > 4096) st = launch(block_norm_grad_wide_kernel<DT>, dim3(blocks), dim3(1024), 0, stream, 1, a);
+    else if (vec) st = launch_norm_grad<DT, VEC, 8 / VEC>(a, blocks, stream);
+    else st = launch_norm_grad<DT, 1, 8>(a, blocks, stream);
+    if (st != SGEMM_OK) return st;
+    const unsigned what = a.gate_period ? 2 + (blocks - 1) : 2;
+    return launch(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, what), dim3(32, 8), 0, stream, 1, a, blocks);
+}
+
+// Checks that the forward and the backward pass share.
+bool norm_shape_ok(int T, int D, int dtype, int wdtype, const void *w_pre, const void *w_post, const Rows &gate,
+                   int gate_rows, float scale) {
+    if (T < 0 || D < 0 || T > kMaxRows || D > kMaxWidth || !dtype_ok(dtype)) return false;
+    if (wdtype != SGEMM_F32 && wdtype != dtype) return false;
+    if (!finite(scale) || gate_rows < 0) return false;
+    if (T == 0 || D == 0) return true;
+    const unsigned ws = dtype_size(wdtype);
+    if (!w_pre || !aligned(w_pre, ws) || !aligned(w_post, ws)) return false;
+    if ((gate_rows > 0) != (gate.p != nullptr)) return false;
+    return !gate.p || (gate_rows <= T && T % gate_rows == 0 && gate.ok(D, dtype_size(dtype)));
+}
+
+// ---------------------------------------------------------------- log probabilities
+
+template <int DT, bool TOP>
+int launch_logprobs(const LogprobArgs &a, const Device &dev, cudaStream_t stream) {
+    // rows of few calls are shared by clusters of up to 8 blocks, until two blocks per SM are reached
+    unsigned parts = 1;
+    while (parts < 8 && (int64_t)a.T * parts * 2 <= 2 * dev.sms && a.V / (int)(parts * 2) >= 2048) parts *= 2;
+    const unsigned rows = (unsigned)std::min(a.T, 65535);
+    return launch(logprobs_kernel<DT, 256, 4, TOP>, dim3(parts, rows), dim3(256), 0, stream, parts, a);
+}
+
+template <int DT, int VW>
+int launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t stream) {
+    constexpr int THREADS = 256, U = VW > 1 ? 4 : 8;
+    const unsigned cols = (unsigned)std::max(1, (a.V / VW + THREADS * U - 1) / (THREADS * U));
+    const unsigned rows = (unsigned)std::min(a.T, 65535);
+    return launch(logprobs_grad_kernel<DT, VW, THREADS, U>, dim3(cols, rows), dim3(THREADS), 0, stream, 1, a);
+}
+
+bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, const int32_t *mask, int ldm,
+                       int mask_rows) {
+    if (T < 0 || V < 0 || T > kMaxRows || V > kMaxRows || !dtype_ok(dtype)) return false;
+    if (!finite(scale) || !(scale > 0.f) || mask_rows < 0) return false;
+    if (T == 0) return true;
+    if (V > 0 && !z.ok(V, dtype_size(dtype))) return false;
+    if ((mask != nullptr) != (mask_rows > 0)) return false;
+    if (!mask) return true;
+    return aligned(mask, 4) && (mask_rows == 1 || mask_rows == T) && (mask_rows == 1 || ldm >= (V + 31) / 32);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sgemm_block_norm(int T, int D, int dtype, const void *x, int ldx, const void *y, int ldy, const void *w_pre,
+                     const void *w_post, int wdtype, const void *gate, int ldg, int gate_rows, float scale, float eps,
+                     void *r, int ldr, void *n, int ldn, signed char *q, int ldq, float *q_scale, float *rstd,
+                     cudaStream_t stream) {
+    const Rows X{x, ldx}, Y{y, ldy}, G{gate, ldg}, R{r, ldr}, N{n, ldn}, Q{q, ldq};
+    if (!norm_shape_ok(T, D, dtype, wdtype, w_pre, w_post, G, gate_rows, scale)) return SGEMM_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !finite(eps)) return SGEMM_ERR_INVALID_ARG;
+    if (T == 0 || D == 0) return SGEMM_OK;
+    const int size = dtype_size(dtype);
+    if (!X.ok(D, size) || !Y.ok(D, size) || !R.ok(D, size) || (n && !N.ok(D, size)) || (!n && !q))
+        return SGEMM_ERR_INVALID_ARG;
+    if ((q && (!Q.ok(D, 1) || !q_scale)) || !aligned(q_scale, 4) || !aligned(rstd, 4)) return SGEMM_ERR_INVALID_ARG;
+
+    const Range in[5] = {X.range(T, D, size), Y.range(T, D, size), G.range(gate_rows, D, size),
+                         Range(w_pre, 1, D, D, dtype_size(wdtype)), Range(w_post, 1, D, D, dtype_size(wdtype))};
+    const Range out[5] = {R.range(T, D, size), N.range(T, D, size), Q.range(T, D, 1), Range(q_scale, 1, q ? T : 0, T, 4),
+                          Range(rstd, 2, T, T, 4)};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < 5; ++i)
+            if (out[o].overlaps(in[i]) && !(o == 0 && i == 0 && R.same(X))) return SGEMM_ERR_ALIAS;
+        for (int p = 0; p < o; ++p)
+            if (out[o].overlaps(out[p])) return SGEMM_ERR_ALIAS;
+    }
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    BlockNormArgs a{T, D, x, y, gate, ldx, ldy, ldg, w_pre, w_post, wdtype == SGEMM_F32,
+                    gate_rows ? T / gate_rows : 0, scale, eps, r, n, ldr, ldn, q, ldq, q_scale, rstd, 0};
+    const int vec_elems = 16 / size;
+    const bool vec = D % vec_elems == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && R.vec(size) && N.vec(size);
+    a.q_vec = aligned(q, (unsigned)vec_elems) && ldq % vec_elems == 0;
+    return by_dtype(dtype, [&](auto dt) { return norm_by_width<decltype(dt)::value>(a, vec, dev, stream); });
+}
+
+size_t sgemm_block_norm_backward_workspace_size(int T, int D) {
+    Device dev;
+    if (T <= 0 || D <= 0 || sgemm_host::device(dev) != SGEMM_OK) return 0;
+    return (size_t)grad_blocks(T, dev.sms) * 4 * (size_t)D * sizeof(float);
+}
+
+int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, const void *y, int ldy,
+                              const void *w_pre, const void *w_post, int wdtype, const void *gate, int ldg,
+                              int gate_rows, float scale, const float *rstd, const void *dn, int lddn, const void *dr,
+                              int lddr, void *dx, int lddx, void *dy, int lddy, void *dw_pre, void *dw_post,
+                              void *dgate, int lddg, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const Rows X{x, ldx}, Y{y, ldy}, G{gate, ldg}, DN{dn, lddn}, DR{dr, lddr}, DX{dx, lddx}, DY{dy, lddy}, DG{dgate, lddg};
+    if (!norm_shape_ok(T, D, dtype, wdtype, w_pre, w_post, G, gate_rows, scale)) return SGEMM_ERR_INVALID_ARG;
+    const int size = dtype_size(dtype), wsize = dtype_size(wdtype);
+    if (D == 0) return SGEMM_OK;
+    if (!dw_pre || !aligned(dw_pre, (unsigned)wsize) || !aligned(dw_post, (unsigned)wsize)) return SGEMM_ERR_INVALID_ARG;
+    if ((w_post != nullptr) != (dw_post != nullptr) || (gate != nullptr) != (dgate != nullptr))
+        return SGEMM_ERR_INVALID_ARG;
+    if (T == 0) {
+        // sums over no rows
+        if (cudaMemsetAsync(dw_pre, 0, (size_t)D * wsize, stream) != cudaSuccess ||
+            (dw_post && cudaMemsetAsync(dw_post, 0, (size_t)D * wsize, stream) != cudaSuccess)) {
+            (void)cudaGetLastError();
+            return SGEMM_ERR_LAUNCH;
+        }
+        return SGEMM_OK;
+    }
+    if (!X.ok(D, size) || !Y.ok(D, size) || !DN.ok(D, size) || (dr && !DR.ok(D, size)) || !DX.ok(D, size) ||
+        !DY.ok(D, size) || (dgate && !DG.ok(D, size)) || !rstd || !aligned(rstd, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    const size_t need = sgemm_block_norm_backward_workspace_size(T, D);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return SGEMM_ERR_INVALID_ARG;
+
+    const Range in[8] = {DN.range(T, D, size), DR.range(T, D, size), X.range(T, D, size), Y.range(T, D, size),
+                         G.range(gate_rows, D, size), Range(w_pre, 1, D, D, wsize), Range(w_post, 1, D, D, wsize),
+                         Range(rstd, 2, T, T, 4)};
+    const Range out[6] = {DX.range(T, D, size), DY.range(T, D, size), DG.range(gate_rows, D, size),
+                          Range(dw_pre, 1, D, D, wsize), Range(dw_post, 1, D, D, wsize),
+                          Range(workspace, 1, (int64_t)need, (int64_t)need, 1)};
+    const Rows *outs[2] = {&DX, &DY}, *ins[2] = {&DN, &DR};
+    for (int o = 0; o < 6; ++o) {
+        for (int i = 0; i < 8; ++i)
+            if (out[o].overlaps(in[i]) && !(o < 2 && i < 2 && outs[o]->same(*ins[i]))) return SGEMM_ERR_ALIAS;
+        for (int p = 0; p < o; ++p)
+            if (out[o].overlaps(out[p])) return SGEMM_ERR_ALIAS;
+    }
+    const BlockNormGradArgs a{T, D, x, y, gate, dn, dr, ldx, ldy, ldg, lddn, lddr, w_pre, w_post, wdtype == SGEMM_F32,
+                              gate_rows ? T / gate_rows : 0, scale, rstd, dx, dy, dgate, lddx, lddy, lddg, dw_pre,
+                              dw_post, static_cast<float *>(workspace)};
+    const bool vec = D % (16 / size) == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && DN.vec(size) &&
+                     DR.vec(size) && DX.vec(size) && DY.vec(size);
+    return by_dtype(dtype, [&](auto dt) { return norm_grad_by_width<decltype(dt)::value>(a, vec, dev, stream); });
+}
+
+int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float scale, const int32_t *mask, int ldm,
+                   int mask_rows, const int64_t *target, float *logprob, float *entropy, float *lse, int top,
+                   float *top_logprob, int32_t *top_id, cudaStream_t stream) {
+    const Rows Z{logits, ldz};
+    if (!logprobs_shape_ok(T, V, dtype, Z, scale, mask, ldm, mask_rows)) return SGEMM_ERR_INVALID_ARG;
+    if (top < 0 || top > 32) return SGEMM_ERR_INVALID_ARG;
+    if (T == 0) return SGEMM_OK;
+    if ((top > 0 && (!top_logprob || !top_id)) || (logprob && !target)) return SGEMM_ERR_INVALID_ARG;
+    if (!aligned(target, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) ||
+        !aligned(top_logprob, 4) || !aligned(top_id, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    const int words = (V + 31) / 32;
+    const Range in[3] = {Z.range(T, V, dtype_size(dtype)), Range(mask, mask_rows, words, ldm, 4), Range(target, 1, T, T, 8)};
+    const Range out[5] = {Range(logprob, 1, T, T, 4), Range(entropy, 1, T, T, 4), Range(lse, 1, T, T, 4),
+                          Range(top ? top_logprob : nullptr, T, top, top, 4), Range(top ? top_id : nullptr, T, top, top, 4)};
+    for (int o = 0; o < 5; ++o) {
+        for (const Range &i : in)
+            if (out[o].overlaps(i)) return SGEMM_ERR_ALIAS;
+        for (int p = 0; p < o; ++p)
+            if (out[o].overlaps(out[p])) return SGEMM_ERR_ALIAS;
+    }
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    const LogprobArgs a{T, V, logits, ldz, scale, mask, mask_rows > 1 ? ldm : 0, target, logprob, entropy, lse, top,
+                        top_logprob, top_id};
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return top ? launch_logprobs<DT, true>(a, dev, stream) : launch_logprobs<DT, false>(a, dev, stream);
+    });
+}
+
+int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz, float scale, const int32_t *mask,
+                            int ldm, int mask_rows, const int64_t *target, const float *lse, const float *entropy,
+                            const float *g_logprob, const float *g_entropy, void *dz, int lddz, cudaStream_t stream) {
+    const Rows Z{logits, ldz}, DZ{dz, lddz};
+    if (!logprobs_shape_ok(T, V, dtype, Z, scale, mask, ldm, mask_rows)) return SGEMM_ERR_INVALID_ARG;
+    if (T == 0 || V == 0) return SGEMM_OK;
+    const int size = dtype_size(dtype);
+    if (!DZ.ok(V, size) || !target || !lse || !g_logprob || (g_entropy && !entropy)) return SGEMM_ERR_INVALID_ARG;
+    if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logprob, 4) || !aligned(g_entropy, 4))
+        return SGEMM_ERR_INVALID_ARG;
+    const int words = (V + 31) / 32;
+    const Range out = DZ.range(T, V, size);
+    const Range in[6] = {Range(mask, mask_rows, words, ldm, 4), Range(target, 1, T, T, 8), Range(lse, 1, T, T, 4),
+                         Range(entropy, 1, T, T, 4), Range(g_logprob, 1, T, T, 4), Range(g_entropy, 1, T, T, 4)};
+    for (const Range &i : in)
+        if (out.overlaps(i)) return SGEMM_ERR_ALIAS;
+    if (out.overlaps(Z.range(T, V, size)) && !DZ.same(Z)) return SGEMM_ERR_ALIAS;
+    const LogprobGradArgs a{T, V, logits, ldz, scale, mask, mask_rows > 1 ? ldm : 0, target, lse, entropy, g_logprob,
+                            g_entropy, dz, lddz};
+    // 16-byte pieces where z and dz are at the same distance from a 16-byte boundary in every row
+    const bool vec = (reinterpret_cast<uintptr_t>(logits) & 15u) == (reinterpret_cast<uintptr_t>(dz) & 15u) &&
+                     (T == 1 || ((int64_t)ldz - lddz) * size % 16 == 0);
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return vec ? launch_logprobs_grad<DT, Elem<DT>::VEC>(a, stream) : launch_logprobs_grad<DT, 1>(a, stream);
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,160 @@
+// What the row-wise kernels share: element types, vector loads and stores that
+// convert to and from FP32, and reductions over a warp or a block.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "../../include/sgemm_layers.h"
+
+namespace sgemm {
+
+// An element type and the number of its elements in 16 bytes.
+template <int DT>
+struct Elem;
+template <>
+struct Elem<SGEMM_F32> {
+    using type = float;
+    static constexpr int VEC = 4;
+    __device__ static float to_float(float v) { return v; }
+    __device__ static float from_float(float v) { return v; }
+};
+template <>
+struct Elem<SGEMM_BF16> {
+    using type = __nv_bfloat16;
+    static constexpr int VEC = 8;
+    __device__ static float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+    __device__ static __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<SGEMM_F16> {
+    using type = __half;
+    static constexpr int VEC = 8;
+    __device__ static float to_float(__half v) { return __half2float(v); }
+    __device__ static __half from_float(float v) { return __float2half_rn(v); }
+};
+
+// 16 bytes of elements as FP32 values.
+template <int DT>
+__device__ __forceinline__ void unpack16(const uint4 &raw, float *out) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == SGEMM_F32) {
+            out[i] = __uint_as_float(w[i]);
+        } else if constexpr (DT == SGEMM_BF16) {
+            out[2 * i] = __uint_as_float(w[i] << 16);
+            out[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            out[2 * i] = f.x;
+            out[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// The inverse, each value rounded once to nearest even.
+template <int DT>
+__device__ __forceinline__ uint4 pack16(const float *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == SGEMM_F32) {
+            w[i] = __float_as_uint(v[i]);
+        } else if constexpr (DT == SGEMM_BF16) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        } else {
+            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's part of a row: NV pieces of VW elements, piece v at column
+// (v * threads + thread) * VW.  VW is 16 bytes' worth (rows that are 16-byte
+// aligned and whole pieces long) or 1 (any other row).
+template <int DT, int VW>
+struct Piece {
+    using type = typename Elem<DT>::type;
+    using raw = uint4;
+    __device__ static raw load(const type *p) { return *reinterpret_cast<const uint4 *>(p); }
+    __device__ static raw zero() { return make_uint4(0, 0, 0, 0); }
+    __device__ static void unpack(const raw &r, float *out) { unpack16<DT>(r, out); }
+    __device__ static void store(type *p, const float *v) { *reinterpret_cast<uint4 *>(p) = pack16<DT>(v); }
+};
+template <int DT>
+struct Piece<DT, 1> {
+    using type = typename Elem<DT>::type;
+    using raw = type;
+    __device__ static raw load(const type *p) { return *p; }
+    __device__ static raw zero() { return Elem<DT>::from_float(0.f); }
+    __device__ static void unpack(const raw &r, float *out) { out[0] = Elem<DT>::to_float(r); }
+    __device__ static void store(type *p, const float *v) { *p = Elem<DT>::from_float(v[0]); }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// Sums over the threads that share a row: a warp (warps == 1), or the block's
+// warps through shared memory, in an order fixed by the number of warps.
+// Each call alternates between two sets of slots, so one barrier per call
+// separates it from the next.
+struct RowReducer {
+    float *slots;  // 2 x 32 floats of shared memory
+    int warps, turn = 0;
+    __device__ float sum(float v) {
+        v = warp_sum(v);
+        if (warps == 1) return v;
+        float *s = slots + 32 * turn;
+        turn ^= 1;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) s[warp] = v;
+        __syncthreads();
+        return warp_sum(lane < warps ? s[lane] : 0.f);
+    }
+    __device__ uint32_t max(uint32_t v) {
+        v = warp_max(v);
+        if (warps == 1) return v;
+        uint32_t *s = reinterpret_cast<uint32_t *>(slots + 32 * turn);
+        turn ^= 1;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) s[warp] = v;
+        __syncthreads();
+        return warp_max(lane < warps ? s[lane] : 0u);
+    }
+};
+
+// A row's scale and multiplier for 8 bits from the largest magnitude in it
+// (as FP32 bits, so that a NaN counts as the largest): s = max / 127 and
+// 127 / max.  Below 2^-100 the quotient could overflow: such rows are first
+// multiplied by 2^64, exactly, in both factors.
+struct I8Scale {
+    float pre, inv, scale;
+    __device__ explicit I8Scale(uint32_t max_bits) {
+        const float m = __uint_as_float(max_bits);
+        pre = 1.f;
+        inv = 0.f;
+        scale = m / 127.f;
+        if (max_bits == 0) scale = 0.f;
+        if (max_bits > 0 && max_bits < 0x7f800000u) {
+            if (m < 0x1p-100f) pre = 0x1p64f;
+            inv = 127.f / (m * pre);
+        }
+    }
+    __device__ int8_t operator()(float x) const {
+        // |x pre inv| <= 127 (1 + 2^-23); infinities and NaN have inv = 0 and become 0
+        const int q = __float2int_rn(x * pre * inv);
+        return (int8_t)(q > 127 ? 127 : q < -127 ? -127 : q);
+    }
+};
+
+}  // namespace sgemm

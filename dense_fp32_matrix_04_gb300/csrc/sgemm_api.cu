@@ -42,6 +42,7 @@
 #include "ffma_tma_ksplit.cuh"
 #include "ffma_tma_streamk.cuh"
 #include "ffma_tiny.cuh"
+#include "host.h"
 #include "ladder.cuh"
 #include "splitk_reduce.cuh"
 #include "tf32_split.cuh"
@@ -121,6 +122,23 @@ int device_info(DeviceInfo &out) {
     out = info[dev];
     return SGEMM_OK;
 }
+
+}  // namespace
+
+// The same for the library's other translation units (host.h).
+int sgemm_host::device(sgemm_host::Device &out) {
+    DeviceInfo info;
+    const int st = device_info(info);
+    if (st == SGEMM_OK) {
+        out.dev = info.dev;
+        out.sms = info.sms;
+        out.err_word = info.err_word;
+    }
+    return st;
+}
+unsigned long long sgemm_host::wait_limit_ns() { return g_wait_limit_ns.load(); }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
