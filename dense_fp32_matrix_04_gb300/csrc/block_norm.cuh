@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "i8_quantize.cuh"
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace sgemm {
@@ -30,6 +31,7 @@ struct BlockNormArgs {
     float *q_scale;
     float *rstd;
     int q_vec;         // rows of q allow stores of a whole piece
+    int ranks, width;  // blocks that share a row, and the columns of each
 };
 
 struct BlockNormGradArgs {
@@ -44,7 +46,9 @@ struct BlockNormGradArgs {
     void *dx, *dy, *dgate;
     int64_t lddx, lddy, lddg;
     void *dw_pre, *dw_post;
-    float *partial;    // blocks x 4 x D: dw_pre, dw_post, and the gate rows a block holds a part of
+    float *partial;    // runners x 4 x D: dw_pre, dw_post, and the gate rows a runner has a part of
+    int runners;
+    int ranks, width;  // as above
 };
 
 template <int DT>
@@ -60,415 +64,456 @@ __device__ __forceinline__ void store_weight(void *w, int w_f32, int64_t c, floa
     else static_cast<typename E::type *>(w)[c] = E::from_float(v);
 }
 
-// blockDim.x threads share a row; blockDim.y rows run side by side in a block
-// (more than one only where a warp is enough for a row).
-// Up to MAXT = 512 threads the weights stay in registers from row to row; 1024
-// threads have half the registers and read them again (from L1).
-template <int DT, int VW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) block_norm_kernel(const BlockNormArgs a) {
-    using P = Piece<DT, VW>;
-    using type = typename P::type;
-    __shared__ float slots[64];
-    RowReducer red{slots, (int)(blockDim.x >> 5)};
-    const int threads = blockDim.x, D = a.D;
-    const float inv_d = 1.f / (float)D;
-
-    constexpr bool KEEP = MAXT <= 512;
-    float w_pre[NV * VW], w_post[NV * VW];
-    auto load_weights = [&](float *w, const void *from) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int c = (v * threads + (int)threadIdx.x) * VW + e;
-                w[v * VW + e] = c < D ? load_weight<DT>(from, a.w_f32, c) : 0.f;
-            }
-    };
-    if (KEEP) {
-        load_weights(w_pre, a.w_pre);
-        if (a.w_post) load_weights(w_post, a.w_post);
+// ---------------------------------------------------------------- rows through shared memory
+//
+// The threads that share a row copy the next rows' inputs into shared memory
+// (cp.async, whole 16-byte pieces) while they work on this one, so what is in
+// flight does not depend on how many blocks fit an SM.  With ALIGNED rows
+// (16-byte aligned and a whole number of pieces) each thread copies the pieces
+// it will read itself and needs no barrier; any other row is copied as the
+// pieces that enclose it (up to 15 bytes in front and behind are read and
+// never used), a barrier lets the row's threads see each other's copies, and
+// they read single elements.
+template <int DT, bool ALIGNED, int NV>
+struct RowLayout {
+    using type = typename Elem<DT>::type;
+    static constexpr int VEC = Elem<DT>::VEC, N = NV * VEC;  // elements a thread
+    // column of this thread's element i
+    __device__ static int col(int i, int threads, int tx) {
+        return ALIGNED ? ((i / VEC) * threads + tx) * VEC + i % VEC : i * threads + tx;
     }
-
-    const int step = gridDim.x * blockDim.y;
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += step) {
-        const type *x = static_cast<const type *>(a.x) + t * a.ldx;
-        const type *y = static_cast<const type *>(a.y) + t * a.ldy;
-        typename P::raw rx[NV], ry[NV], rg[NV];
-        const type *gate =
-            a.gate_period ? static_cast<const type *>(a.gate) + (t / a.gate_period) * a.ldg : nullptr;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * threads + (int)threadIdx.x) * VW;
-            rx[v] = c < D ? P::load(x + c) : P::zero();
-            ry[v] = c < D ? P::load(y + c) : P::zero();
-            if (gate) rg[v] = c < D ? P::load(gate + c) : P::zero();
-        }
-        float h[NV * VW], r[NV * VW];
-        float ss = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            P::unpack(ry[v], h + v * VW);
-            P::unpack(rx[v], r + v * VW);
-        }
-        float rho = 1.f;
-        if (a.w_post) {
-#pragma unroll
-            for (int i = 0; i < NV * VW; ++i) ss = fmaf(h[i], h[i], ss);
-            rho = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
-            if (!KEEP) load_weights(w_post, a.w_post);
-        }
-        ss = 0.f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float g[VW];
-            if (gate) P::unpack(rg[v], g);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int i = v * VW + e;
-                float hv = a.w_post ? h[i] * rho * w_post[i] : h[i];
-                if (gate) hv *= g[e];
-                r[i] = fmaf(a.scale, hv, r[i]);
-                ss = fmaf(r[i], r[i], ss);
-            }
-        }
-        const float rho2 = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
-        if (a.rstd && threadIdx.x == 0) {
-            a.rstd[t] = rho;
-            a.rstd[a.T + t] = rho2;
-        }
-        if (!KEEP) load_weights(w_pre, a.w_pre);
-        type *out_r = static_cast<type *>(a.r) + t * a.ldr;
-        uint32_t top = 0;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * threads + (int)threadIdx.x) * VW;
-            if (c < D) P::store(out_r + c, r + v * VW);
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int i = v * VW + e;
-                r[i] = r[i] * rho2 * w_pre[i];
-                top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
-            }
-            if (a.n && c < D) P::store(static_cast<type *>(a.n) + t * a.ldn + c, r + v * VW);
-        }
-        if (a.q) {
-            const I8Scale q(red.max(top));
-            if (threadIdx.x == 0) a.q_scale[t] = q.scale;
-            int8_t *out = a.q + t * a.ldq;
+    // starts the copies of a row into `slot`
+    __device__ static void copy(uint4 *slot, const type *row, int D, int threads, int tx) {
+        if constexpr (ALIGNED) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const int c = (v * threads + (int)threadIdx.x) * VW;
-                if (c >= D) continue;
-                int8_t b[VW];
-#pragma unroll
-                for (int e = 0; e < VW; ++e) b[e] = q(r[v * VW + e]);
-                store_bytes(out + c, b, a.q_vec);
+                const int p = v * threads + tx;
+                if (p * VEC < D) cp_async_16(smem_addr(slot + p), row + p * VEC, 16);
             }
+        } else {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15;
+            const int pieces = (int)((reinterpret_cast<uintptr_t>(row + D) + 15 - lo) >> 4);
+            for (int p = tx; p < pieces; p += threads)
+                cp_async_16(smem_addr(slot + p), reinterpret_cast<const void *>(lo + 16 * (uintptr_t)p), 16);
         }
     }
+    // this thread's elements of the row that was copied from `row`; 0 past its end
+    __device__ static void read(const uint4 *slot, const type *row, int D, int threads, int tx, float *out) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int p = v * threads + tx;
+                unpack16<DT>(p * VEC < D ? slot[p] : make_uint4(0, 0, 0, 0), out + v * VEC);
+            }
+        } else {
+            const type *e = reinterpret_cast<const type *>(slot) + (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(type);
+#pragma unroll
+            for (int i = 0; i < N; ++i) out[i] = i * threads + tx < D ? Elem<DT>::to_float(e[i * threads + tx]) : 0.f;
+        }
+    }
+    __device__ static void store(type *row, int D, int threads, int tx, const float *v) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int p = k * threads + tx;
+                if (p * VEC < D) *reinterpret_cast<uint4 *>(row + p * VEC) = pack16<DT>(v + k * VEC);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i * threads + tx < D) row[i * threads + tx] = Elem<DT>::from_float(v[i]);
+        }
+    }
+    // 0 past the row's end; ALIGNED weights start on 16 bytes
+    __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, float *out) {
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * threads + tx) * VEC;
+                if (c >= D) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) out[v * VEC + e] = 0.f;
+                } else if (w_f32) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 4) {
+                        const float4 q = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c0 + c + e));
+                        out[v * VEC + e] = q.x, out[v * VEC + e + 1] = q.y;
+                        out[v * VEC + e + 2] = q.z, out[v * VEC + e + 3] = q.w;
+                    }
+                } else {
+                    unpack16<DT>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const type *>(w) + c0 + c)), out + v * VEC);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                out[i] = i * threads + tx < D ? load_weight<DT>(w, w_f32, c0 + i * threads + tx) : 0.f;
+        }
+    }
+};
+
+// Rows a thread keeps on their way (and the one it works on).
+constexpr int kNormStages = 3;
+
+// Copies of the inputs of one row, by the threads that share it.
+__host__ __device__ constexpr int row_pieces(int D, int size) { return (D * size + 15) / 16 + 1; }
+
+// The barrier of the threads that share a row.
+__device__ __forceinline__ void row_sync(int warps) {
+    if (warps == 1) __syncwarp();
+    else __syncthreads();
 }
 
-// Rows too wide for the registers of a block: one block per row reads it
-// again for each step (three times in all; the later reads come from L2).
-template <int DT>
-__global__ void __launch_bounds__(1024, 1) block_norm_wide_kernel(const BlockNormArgs a) {
-    using E = Elem<DT>;
-    using type = typename E::type;
+// The threads of a row: blockDim.x of a block (and blockDim.y rows side by
+// side in it, more than one only where a warp is enough for a row), in each of
+// the `ranks` blocks of a cluster, which take `width` columns each.
+template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormArgs a) {
+    using L = RowLayout<DT, ALIGNED, NV>;
+    using type = typename L::type;
+    constexpr int N = L::N, S = kNormStages;
+    extern __shared__ uint4 ring[];
     __shared__ float slots[64];
-    RowReducer red{slots, (int)(blockDim.x >> 5)};
-    const int D = a.D;
-    const float inv_d = 1.f / (float)D;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const type *x = static_cast<const type *>(a.x) + t * a.ldx;
-        const type *y = static_cast<const type *>(a.y) + t * a.ldy;
-        const type *gate =
-            a.gate_period ? static_cast<const type *>(a.gate) + (t / a.gate_period) * a.ldg : nullptr;
-        float rho = 1.f, ss = 0.f;
+    RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
+    const int threads = blockDim.x, tx = threadIdx.x;
+    const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
+    const int c0 = rank * a.width, D = min(a.width, a.D - c0);  // this block's columns
+    const float inv_d = 1.f / (float)a.D;
+    const bool token_gate = a.gate_period == 1;
+    const int arrays = token_gate ? 3 : 2, pieces = row_pieces(a.width, sizeof(type));
+    uint4 *mine = ring + threadIdx.y * S * arrays * pieces;
+
+    float w_pre[N], w_post[N];
+    L::weights(a.w_pre, a.w_f32, c0, D, threads, tx, w_pre);
+    if (a.w_post) L::weights(a.w_post, a.w_f32, c0, D, threads, tx, w_post);
+
+    const int64_t first = (int64_t)group_id * blockDim.y + threadIdx.y;
+    const int64_t step = (int64_t)(gridDim.x / (unsigned)a.ranks) * blockDim.y;
+    auto x_row = [&](int64_t t) { return static_cast<const type *>(a.x) + t * a.ldx + c0; };
+    auto y_row = [&](int64_t t) { return static_cast<const type *>(a.y) + t * a.ldy + c0; };
+    auto g_row = [&](int64_t t) { return static_cast<const type *>(a.gate) + (t / a.gate_period) * a.ldg + c0; };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T) {
+            uint4 *slot = mine + stage * arrays * pieces;
+            L::copy(slot, x_row(t), D, threads, tx);
+            L::copy(slot + pieces, y_row(t), D, threads, tx);
+            if (token_gate) L::copy(slot + 2 * pieces, g_row(t), D, threads, tx);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(first + s * step, s);
+
+    int stage = 0;
+    for (int64_t t = first; t < a.T; t += step) {
+        cp_async_wait<S - 2>();
+        if (!ALIGNED) row_sync(red.warps);
+        const uint4 *slot = mine + stage * arrays * pieces;
+        float h[N], r[N];
+        L::read(slot + pieces, y_row(t), D, threads, tx, h);
+        L::read(slot, x_row(t), D, threads, tx, r);
+        float rho = 1.f;
         if (a.w_post) {
-            for (int c = threadIdx.x; c < D; c += blockDim.x) {
-                const float v = E::to_float(y[c]);
-                ss = fmaf(v, v, ss);
-            }
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) ss = fmaf(h[i], h[i], ss);
             rho = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
+#pragma unroll
+            for (int i = 0; i < N; ++i) h[i] *= rho * w_post[i];
         }
-        auto residual = [&](int c) {
-            float h = E::to_float(y[c]);
-            if (a.w_post) h = h * rho * load_weight<DT>(a.w_post, a.w_f32, c);
-            if (gate) h *= E::to_float(gate[c]);
-            return fmaf(a.scale, h, E::to_float(x[c]));
-        };
-        ss = 0.f;
-        for (int c = threadIdx.x; c < D; c += blockDim.x) {
-            const float r = residual(c);
-            ss = fmaf(r, r, ss);
+        if (a.gate_period) {
+            float g[N];
+            if (token_gate) {
+                L::read(slot + 2 * pieces, g_row(t), D, threads, tx, g);
+            } else if constexpr (ALIGNED) {
+                const type *row = g_row(t);  // the same for many rows: from L1
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int c = (v * threads + tx) * L::VEC;
+                    unpack16<DT>(c < D ? __ldg(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0),
+                                 g + v * L::VEC);
+                }
+            } else {
+                const type *row = g_row(t);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    g[i] = i * threads + tx < D ? Elem<DT>::to_float(row[i * threads + tx]) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) h[i] *= g[i];
         }
+        // the slot that the previous row was read from takes the row after the next ones
+        fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            r[i] = fmaf(a.scale, h[i], r[i]);
+            ss = fmaf(r[i], r[i], ss);
+        }
+        L::store(static_cast<type *>(a.r) + t * a.ldr + c0, D, threads, tx, r);
         const float rho2 = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
-        if (a.rstd && threadIdx.x == 0) {
+        if (a.rstd && tx == 0 && rank == 0) {
             a.rstd[t] = rho;
             a.rstd[a.T + t] = rho2;
         }
-        I8Scale q(0u);
-        if (a.q) {
-            uint32_t top = 0;
-            for (int c = threadIdx.x; c < D; c += blockDim.x)
-                top = max(top, __float_as_uint(residual(c) * rho2 * load_weight<DT>(a.w_pre, a.w_f32, c)) & 0x7fffffffu);
-            q = I8Scale(red.max(top));
-            if (threadIdx.x == 0) a.q_scale[t] = q.scale;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            r[i] *= rho2 * w_pre[i];
+            top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
         }
-        // r may be x: each element is read before the same thread writes it
-        for (int c = threadIdx.x; c < D; c += blockDim.x) {
-            const float r = residual(c);
-            const float n = r * rho2 * load_weight<DT>(a.w_pre, a.w_f32, c);
-            static_cast<type *>(a.r)[t * a.ldr + c] = E::from_float(r);
-            if (a.n) static_cast<type *>(a.n)[t * a.ldn + c] = E::from_float(n);
-            if (a.q) a.q[t * a.ldq + c] = q(n);
+        if (a.n) L::store(static_cast<type *>(a.n) + t * a.ldn + c0, D, threads, tx, r);
+        if (a.q) {
+            const I8Scale q(red.max(top));
+            if (tx == 0 && rank == 0) a.q_scale[t] = q.scale;
+            int8_t *out = a.q + t * a.ldq + c0;
+            if constexpr (ALIGNED) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int c = (v * threads + tx) * L::VEC;
+                    if (c >= D) continue;
+                    int8_t b[L::VEC];
+#pragma unroll
+                    for (int e = 0; e < L::VEC; ++e) b[e] = q(r[v * L::VEC + e]);
+                    store_bytes(out + c, b, a.q_vec);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i * threads + tx < D) out[i * threads + tx] = q(r[i]);
+            }
         }
     }
+    if (a.ranks > 1) cluster_sync();
 }
 
 // ---------------------------------------------------------------- gradient
 
-// Block b takes the rows [first_row(b), first_row(b + 1)): consecutive rows,
-// so that a gate row's sum stays in registers until the row changes.
-__device__ __forceinline__ int block_first_row(int b, int T, int blocks) {
-    return (int)((int64_t)b * T / blocks);
-}
+// Runner b (a block, or a warp of one) takes the rows [first_row(b),
+// first_row(b + 1)): consecutive rows, so that a gate row's sum stays in
+// registers until the row changes.
+__device__ __forceinline__ int first_row(int b, int T, int runners) { return (int)((int64_t)b * T / runners); }
 
 // The gradient of a row needs, with u = dn w_pre and v = dh w_post,
 //     dx = dr + rho2 (u - r rho2^2 mean(u r)),   dh = a g dx,
 //     dy = rho (v - y rho^2 mean(v y)),
 // so two sums over the row, one after the other; rho and rho2 come from the
 // forward pass.  Sums over rows (weights and gate) are kept in registers, and
-// written per block to `partial`: a second kernel adds the blocks in order.
-template <int DT, int VW, int NV>
-__global__ void __launch_bounds__(512, 1) block_norm_grad_kernel(const BlockNormGradArgs a) {
-    using P = Piece<DT, VW>;
+// written per runner to `partial`: a second kernel adds the runners in order.
+template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_grad_kernel(const BlockNormGradArgs a) {
+    using L = RowLayout<DT, ALIGNED, NV>;
     using E = Elem<DT>;
-    using type = typename P::type;
-    constexpr int N = NV * VW;
+    using type = typename L::type;
+    constexpr int N = L::N, S = kNormStages;
+    extern __shared__ uint4 ring[];
     __shared__ float slots[64];
-    RowReducer red{slots, (int)(blockDim.x >> 5)};
-    const int threads = blockDim.x, D = a.D;
-    const float inv_d = 1.f / (float)D;
-    const int begin = block_first_row(blockIdx.x, a.T, gridDim.x);
-    const int end = block_first_row(blockIdx.x + 1, a.T, gridDim.x);
+    RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
+    const int threads = blockDim.x, tx = threadIdx.x;
+    const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
+    const int c0 = rank * a.width, D = min(a.width, a.D - c0);  // this block's columns
+    const float inv_d = 1.f / (float)a.D;
+    const int runner = group_id * blockDim.y + threadIdx.y;
+    if (runner >= a.runners) return;  // only where a warp is a runner: no barrier spans warps
+    const int begin = first_row(runner, a.T, a.runners), end = first_row(runner + 1, a.T, a.runners);
+    const bool token_gate = a.gate_period == 1;
+    const int pieces = row_pieces(a.width, sizeof(type));
+    const int g_at = 3 * pieces, dr_at = (token_gate ? 4 : 3) * pieces;
+    const int stride = dr_at + (a.dr ? pieces : 0);
+    uint4 *mine = ring + threadIdx.y * S * stride;
 
+    // registers hold the row and the sums; what else of a row is needed twice is read again (from
+    // L1 or the ring) where a thread has 16 elements, and w_pre always
+    constexpr bool KEEP = N <= 8;
     float w_pre[N], w_post[N], dw_pre[N], dw_post[N], dgate[N];
+    auto load_post = [&] {
+        if (a.w_post) {
+            L::weights(a.w_post, a.w_f32, c0, D, threads, tx, w_post);
+        } else {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            const int c = (v * threads + (int)threadIdx.x) * VW + e;
-            const int i = v * VW + e;
-            w_pre[i] = c < D ? load_weight<DT>(a.w_pre, a.w_f32, c) : 0.f;
-            w_post[i] = c < D && a.w_post ? load_weight<DT>(a.w_post, a.w_f32, c) : 1.f;
-            dw_pre[i] = dw_post[i] = dgate[i] = 0.f;
+            for (int i = 0; i < N; ++i) w_post[i] = 1.f;
         }
-    float *partial = a.partial + (int64_t)blockIdx.x * 4 * D;
+    };
+    if (KEEP) load_post();
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw_pre[i] = dw_post[i] = dgate[i] = 0.f;
+    float *partial = a.partial + (int64_t)runner * 4 * a.D + c0;  // four sums of a.D columns
 
-    for (int64_t t = begin; t < end; ++t) {
-        const type *x = static_cast<const type *>(a.x) + t * a.ldx;
-        const type *y = static_cast<const type *>(a.y) + t * a.ldy;
-        const type *pn = static_cast<const type *>(a.dn) + t * a.lddn;
-        const type *pr = a.dr ? static_cast<const type *>(a.dr) + t * a.lddr : nullptr;
-        const int group = a.gate_period ? (int)(t / a.gate_period) : 0;
-        const type *gate = a.gate_period ? static_cast<const type *>(a.gate) + group * a.ldg : nullptr;
-        const float rho = a.w_post ? a.rstd[t] : 1.f, rho2 = a.rstd[a.T + t];
-        float r[N], h[N], u[N], dr[N], g[N];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * threads + (int)threadIdx.x) * VW;
-            const bool in = c < D;
-            P::unpack(in ? P::load(x + c) : P::zero(), r + v * VW);
-            P::unpack(in ? P::load(y + c) : P::zero(), h + v * VW);
-            P::unpack(in ? P::load(pn + c) : P::zero(), u + v * VW);
-            P::unpack(in && pr ? P::load(pr + c) : P::zero(), dr + v * VW);
-            if (gate) P::unpack(in ? P::load(gate + c) : P::zero(), g + v * VW);
+    auto x_row = [&](int64_t t) { return static_cast<const type *>(a.x) + t * a.ldx + c0; };
+    auto y_row = [&](int64_t t) { return static_cast<const type *>(a.y) + t * a.ldy + c0; };
+    auto n_row = [&](int64_t t) { return static_cast<const type *>(a.dn) + t * a.lddn + c0; };
+    auto r_row = [&](int64_t t) { return static_cast<const type *>(a.dr) + t * a.lddr + c0; };
+    auto g_row = [&](int64_t g) { return static_cast<const type *>(a.gate) + g * a.ldg + c0; };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < end) {
+            uint4 *slot = mine + stage * stride;
+            L::copy(slot, x_row(t), D, threads, tx);
+            L::copy(slot + pieces, y_row(t), D, threads, tx);
+            L::copy(slot + 2 * pieces, n_row(t), D, threads, tx);
+            if (token_gate) L::copy(slot + g_at, g_row(t), D, threads, tx);
+            if (a.dr) L::copy(slot + dr_at, r_row(t), D, threads, tx);
         }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(begin + s, s);
+
+    int stage = 0;
+    for (int64_t t = begin; t < end; ++t) {
+        cp_async_wait<S - 2>();
+        if (!ALIGNED) row_sync(red.warps);
+        const uint4 *slot = mine + stage * stride;
+        fetch(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        const int group = token_gate ? (int)t : a.gate_period ? (int)(t / a.gate_period) : 0;
+        const float rho = a.w_post ? a.rstd[t] : 1.f, rho2 = a.rstd[a.T + t];
+        float r[N], h[N], u[N], g[N];
+        L::read(slot, x_row(t), D, threads, tx, r);
+        L::read(slot + pieces, y_row(t), D, threads, tx, h);
+        L::read(slot + 2 * pieces, n_row(t), D, threads, tx, u);
+        // the factor of dx in the gradient of h
+        auto load_gate = [&] {
+            if (token_gate) {
+                L::read(slot + g_at, g_row(t), D, threads, tx, g);
+            } else if (a.gate_period) {
+                const type *row = g_row(group);  // the same for many rows: from L1
+                if constexpr (ALIGNED) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        const int c = (v * threads + tx) * L::VEC;
+                        unpack16<DT>(c < D ? __ldg(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0),
+                                     g + v * L::VEC);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) g[i] = i * threads + tx < D ? E::to_float(row[i * threads + tx]) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = a.gate_period ? a.scale * g[i] : a.scale;
+        };
+        load_gate();
+        L::weights(a.w_pre, a.w_f32, c0, D, threads, tx, w_pre);
+        if (!KEEP) load_post();
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (!gate) g[i] = 1.f;
             // h becomes y rho; r the residual sum; u = dn w_pre
             h[i] *= rho;
-            r[i] = fmaf(a.scale * g[i], h[i] * w_post[i], r[i]);
+            r[i] = fmaf(g[i], h[i] * w_post[i], r[i]);
             dw_pre[i] = fmaf(u[i], r[i] * rho2, dw_pre[i]);
             u[i] *= w_pre[i];
             sum = fmaf(u[i], r[i], sum);
         }
         sum = red.sum(sum) * inv_d * rho2 * rho2;
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = rho2 * fmaf(-r[i], sum, u[i]);
+        if (a.dr) {
+            L::read(slot + dr_at, r_row(t), D, threads, tx, u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i] += u[i];
+        }
+        L::store(static_cast<type *>(a.dx) + t * a.lddx + c0, D, threads, tx, r);
+        if (!KEEP) {
+            load_post();
+            load_gate();
+        }
         float sum2 = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int i = v * VW + e;
-                const float dx = fmaf(rho2, fmaf(-r[i], sum, u[i]), dr[i]);
-                r[i] = dx;
-                const float dh = a.scale * dx;
-                dgate[i] = fmaf(dh, h[i] * w_post[i], dgate[i]);
-                u[i] = dh * g[i];
-                dw_post[i] = fmaf(u[i], h[i], dw_post[i]);
-                u[i] *= w_post[i];
-                sum2 = fmaf(u[i], h[i], sum2);
-            }
+        for (int i = 0; i < N; ++i) {
+            dgate[i] = fmaf(a.scale * r[i], h[i] * w_post[i], dgate[i]);
+            u[i] = g[i] * r[i];
+            dw_post[i] = fmaf(u[i], h[i], dw_post[i]);
+            u[i] *= w_post[i];
+            sum2 = fmaf(u[i], h[i], sum2);
         }
         // with h = y rho: dy = rho (v - h mean(v h)); without the norm rho is 1 and dy = v
         sum2 = a.w_post ? red.sum(sum2) * inv_d : 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * threads + (int)threadIdx.x) * VW;
-            if (c >= D) continue;
-            P::store(static_cast<type *>(a.dx) + t * a.lddx + c, r + v * VW);
-            float dy[VW];
-#pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int i = v * VW + e;
-                dy[e] = rho * fmaf(-h[i], sum2, u[i]);
-            }
-            P::store(static_cast<type *>(a.dy) + t * a.lddy + c, dy);
-        }
-        if (gate && (t + 1 == end || (t + 1) % a.gate_period == 0)) {
-            // the gate row's sum: whole when all of its rows are this block's, otherwise one
-            // of the block's two partial sums (the first gate row it meets, or the last)
+        for (int i = 0; i < N; ++i) u[i] = rho * fmaf(-h[i], sum2, u[i]);
+        L::store(static_cast<type *>(a.dy) + t * a.lddy + c0, D, threads, tx, u);
+        if (a.gate_period && (token_gate || t + 1 == end || (t + 1) % a.gate_period == 0)) {
+            // the gate row's sum: whole when all of its rows are this runner's, otherwise one
+            // of the runner's two partial sums (the first gate row it meets, or the last)
             const int64_t g0 = (int64_t)group * a.gate_period, g1 = g0 + a.gate_period;
-            const bool whole = g0 >= begin && g1 <= end;
-            const int slot = group == begin / a.gate_period ? 2 : 3;
+            if (g0 >= begin && g1 <= end) {
+                L::store(static_cast<type *>(a.dgate) + group * a.lddg + c0, D, threads, tx, dgate);
+            } else {
+                float *to = partial + (int64_t)(group == begin / a.gate_period ? 2 : 3) * a.D;
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int e = 0; e < VW; ++e) {
-                    const int c = (v * threads + (int)threadIdx.x) * VW + e, i = v * VW + e;
-                    if (c < D) {
-                        if (whole)
-                            static_cast<type *>(a.dgate)[group * a.lddg + c] = E::from_float(dgate[i]);
-                        else
-                            partial[(int64_t)slot * D + c] = dgate[i];
-                    }
-                    dgate[i] = 0.f;
+                for (int i = 0; i < N; ++i) {
+                    const int c = L::col(i, threads, tx);
+                    if (c < D) to[c] = dgate[i];
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) dgate[i] = 0.f;
         }
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            const int c = (v * threads + (int)threadIdx.x) * VW + e, i = v * VW + e;
-            if (c < D) {
-                partial[c] = dw_pre[i];
-                partial[D + c] = dw_post[i];
-            }
-        }
-}
-
-// The same for rows too wide for a block's registers: the row is read again
-// for each step, and the sums over rows live in `partial`.
-template <int DT>
-__global__ void __launch_bounds__(1024, 1) block_norm_grad_wide_kernel(const BlockNormGradArgs a) {
-    using E = Elem<DT>;
-    using type = typename E::type;
-    __shared__ float slots[64];
-    RowReducer red{slots, (int)(blockDim.x >> 5)};
-    const int D = a.D;
-    const float inv_d = 1.f / (float)D;
-    const int begin = block_first_row(blockIdx.x, a.T, gridDim.x);
-    const int end = block_first_row(blockIdx.x + 1, a.T, gridDim.x);
-    float *partial = a.partial + (int64_t)blockIdx.x * 4 * D;
-    for (int c = threadIdx.x; c < D; c += blockDim.x) partial[c] = partial[D + c] = 0.f;
-    for (int64_t t = begin; t < end; ++t) {
-        const int group = a.gate_period ? (int)(t / a.gate_period) : 0;
-        const float rho = a.w_post ? a.rstd[t] : 1.f, rho2 = a.rstd[a.T + t];
-        const int64_t g0 = (int64_t)group * a.gate_period, g1 = g0 + a.gate_period;
-        const bool whole = g0 >= begin && g1 <= end;
-        const bool first = a.gate_period && (t == begin || t % a.gate_period == 0);
-        const bool last = a.gate_period && (t + 1 == end || (t + 1) % a.gate_period == 0);
-        float *gate_sum = partial + (int64_t)(a.gate_period && group == begin / a.gate_period ? 2 : 3) * D;
-        struct Row {
-            float h, g, w_post, r, u, dn;
-        };
-        auto row = [&](int c) {
-            Row e;
-            e.h = E::to_float(static_cast<const type *>(a.y)[t * a.ldy + c]) * rho;
-            e.g = a.gate_period ? E::to_float(static_cast<const type *>(a.gate)[group * a.ldg + c]) : 1.f;
-            e.w_post = a.w_post ? load_weight<DT>(a.w_post, a.w_f32, c) : 1.f;
-            e.r = fmaf(a.scale * e.g, e.h * e.w_post, E::to_float(static_cast<const type *>(a.x)[t * a.ldx + c]));
-            e.dn = E::to_float(static_cast<const type *>(a.dn)[t * a.lddn + c]);
-            e.u = e.dn * load_weight<DT>(a.w_pre, a.w_f32, c);
-            return e;
-        };
-        float sum = 0.f;
-        for (int c = threadIdx.x; c < D; c += blockDim.x) {
-            const Row e = row(c);
-            sum = fmaf(e.u, e.r, sum);
-        }
-        sum = red.sum(sum) * inv_d * rho2 * rho2;
-        auto grad_x = [&](const Row &e, int c) {
-            const float dr = a.dr ? E::to_float(static_cast<const type *>(a.dr)[t * a.lddr + c]) : 0.f;
-            return fmaf(rho2, fmaf(-e.r, sum, e.u), dr);
-        };
-        float sum2 = 0.f;
-        if (a.w_post) {
-            for (int c = threadIdx.x; c < D; c += blockDim.x) {
-                const Row e = row(c);
-                sum2 = fmaf(a.scale * grad_x(e, c) * e.g * e.w_post, e.h, sum2);
-            }
-            sum2 = red.sum(sum2) * inv_d;
-        }
-        // dx and dy may overwrite dn and dr: each element is read before the same thread writes it
-        for (int c = threadIdx.x; c < D; c += blockDim.x) {
-            const Row e = row(c);
-            const float dx = grad_x(e, c), dh = a.scale * dx;
-            partial[c] = fmaf(e.dn, e.r * rho2, partial[c]);
-            partial[D + c] = fmaf(dh * e.g, e.h, partial[D + c]);
-            if (a.gate_period) {
-                const float s = (first ? 0.f : gate_sum[c]) + dh * e.h * e.w_post;
-                gate_sum[c] = s;
-                if (last && whole) static_cast<type *>(a.dgate)[group * a.lddg + c] = E::from_float(s);
-            }
-            static_cast<type *>(a.dx)[t * a.lddx + c] = E::from_float(dx);
-            static_cast<type *>(a.dy)[t * a.lddy + c] =
-                E::from_float(rho * fmaf(-e.h, sum2, dh * e.g * e.w_post));
+    for (int i = 0; i < N; ++i) {
+        const int c = L::col(i, threads, tx);
+        if (c < D) {
+            partial[c] = dw_pre[i];
+            partial[a.D + c] = dw_post[i];
         }
     }
+    if (a.ranks > 1) cluster_sync();
 }
 
-// Adds the blocks' partial sums: blockIdx.y 0 and 1 for the weights, 2 + b for
-// the gate row that block b + 1 starts inside (once, by the first such block).
-// 32 columns by 8 slices of the blocks, added in slice order.
+// The runner that has row t.
+__device__ __forceinline__ int runner_of(int64_t t, int T, int runners) {
+    int b = (int)min((int64_t)runners - 1, t * runners / T);
+    while (first_row(b, T, runners) > t) --b;
+    while (first_row(b + 1, T, runners) <= t) ++b;
+    return b;
+}
+
+// Adds the runners' partial sums: blockIdx.y 0 and 1 for the weights, from 2
+// on for the gate rows that more than one runner has a part of.  32 columns by
+// 32 slices of the runners, added in slice order.
 template <int DT>
-__global__ void __launch_bounds__(256) block_norm_grad_join_kernel(const BlockNormGradArgs a, int blocks) {
-    __shared__ float part[8][33];
-    const int D = a.D, c = blockIdx.x * 32 + threadIdx.x;
-    const int what = blockIdx.y;
-    int b0 = 0, b1 = blocks, group = 0;
-    if (what >= 2) {
-        const int b = what - 1, row = block_first_row(b, a.T, blocks);
-        if (row % a.gate_period == 0) return;  // block b starts a gate row of its own
-        group = row / a.gate_period;
-        const int64_t g0 = (int64_t)group * a.gate_period, g1 = g0 + a.gate_period;
-        if (block_first_row(b - 1, a.T, blocks) > g0) return;  // an earlier block started inside it
-        b0 = b - 1;
-        b1 = b + 1;
-        while (b1 < blocks && block_first_row(b1, a.T, blocks) < g1) ++b1;
-    } else if (what == 1 && !a.w_post) {
+__global__ void __launch_bounds__(1024) block_norm_grad_join_kernel(const BlockNormGradArgs a) {
+    __shared__ float part[32][33];
+    const int D = a.D, c = blockIdx.x * 32 + threadIdx.x, runners = a.runners;
+    // the sum over runners [b0, b1) of the partial sum that slot(b) names; valid in slice 0
+    auto join = [&](int b0, int b1, auto slot) {
+        float s = 0.f;
+        if (c < D)
+            for (int b = b0 + (int)threadIdx.y; b < b1; b += 32) s += a.partial[((int64_t)b * 4 + slot(b)) * D + c];
+        part[threadIdx.y][threadIdx.x] = s;
+        __syncthreads();
+        if (threadIdx.y == 0)
+#pragma unroll
+            for (int i = 1; i < 32; ++i) s += part[i][threadIdx.x];
+        __syncthreads();
+        return s;
+    };
+    const bool writes = threadIdx.y == 0 && c < D;
+    if (blockIdx.y < 2) {
+        if (blockIdx.y == 1 && !a.w_post) return;
+        const float s = join(0, runners, [&](int) { return (int)blockIdx.y; });
+        if (writes) store_weight<DT>(blockIdx.y ? a.dw_post : a.dw_pre, a.w_f32, c, s);
         return;
     }
-    float s = 0.f;
-    if (c < D) {
-        for (int b = b0 + threadIdx.y; b < b1; b += 8) {
-            int slot = what;
-            if (what >= 2) slot = group == block_first_row(b, a.T, blocks) / a.gate_period ? 2 : 3;
-            s += a.partial[((int64_t)b * 4 + slot) * D + c];
+    // gate rows by number where they are few; otherwise by the runners that start inside one
+    const int groups = a.T / a.gate_period, count = min(groups, runners - 1);
+    for (int i = blockIdx.y - 2; i < count; i += gridDim.y - 2) {
+        int group = i;
+        if (groups > runners - 1) {
+            const int row = first_row(i + 1, a.T, runners);
+            group = row / a.gate_period;
+            const int64_t g0 = (int64_t)group * a.gate_period;
+            if (g0 == row || first_row(i, a.T, runners) > g0) continue;  // not the first runner to start inside it
         }
-    }
-    part[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < D) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
-        if (what == 0) store_weight<DT>(a.dw_pre, a.w_f32, c, s);
-        else if (what == 1) store_weight<DT>(a.dw_post, a.w_f32, c, s);
-        else store_weight<DT>(a.dgate, 0, (int64_t)group * a.lddg + c, s);
+        const int64_t g0 = (int64_t)group * a.gate_period;
+        const int b0 = runner_of(g0, a.T, runners), b1 = runner_of(g0 + a.gate_period - 1, a.T, runners) + 1;
+        if (b1 - b0 < 2) continue;  // one runner had all of it
+        const float s = join(b0, b1, [&](int b) {
+            return group == first_row(b, a.T, runners) / a.gate_period ? 2 : 3;
+        });
+        if (writes) store_weight<DT>(a.dgate, 0, (int64_t)group * a.lddg + c, s);
     }
 }
 

@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 #include <utility>
@@ -57,6 +59,28 @@ int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaSt
     if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
+}
+
+// Blocks of a kernel that fit an SM, from the registers it was compiled to use;
+// on a device's first use of it (`regs` is the caller's cache for the kernel)
+// its shared-memory limit is raised.  0 if the device refuses.
+template <class Kernel>
+int blocks_per_sm(std::atomic<int> (&regs)[kMaxDevices], const Device &dev, Kernel kernel, int threads, int smem) {
+    int r = regs[dev.dev].load(std::memory_order_acquire);
+    if (r == 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 227 * 1024 - (int)at.sharedSizeBytes) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        r = at.numRegs;
+        regs[dev.dev].store(r, std::memory_order_release);
+    }
+    const int warps = (threads + 31) / 32;
+    const int by_regs = 65536 / ((r + 7) / 8 * 8 * 32 * warps), by_smem = 227 * 1024 / (smem + 2048);
+    return std::max(1, std::min({by_regs, by_smem, 64 / warps, 32}));
 }
 
 // Calls f(std::integral_constant<int, dtype>) for one of the three element types.

@@ -11,6 +11,9 @@
 #include "host.h"
 #include "logprobs.cuh"
 
+#ifndef LP_N
+#define LP_N 16
+#endif
 namespace {
 
 using namespace sgemm;
@@ -36,56 +39,82 @@ struct Rows {
 // The threads that share a row of D elements, `per` of them each: whole warps.
 int row_threads(int D, int per) { return ((D + per - 1) / per + 31) / 32 * 32; }
 
-constexpr int kMaxRows = 1 << 30, kMaxWidth = 65536;
+constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxWidth = 24576;  // eight blocks of 3072: FP32 rows with every input fit their rings
 
 bool finite(float v) { return std::isfinite(v); }
 
 // ---------------------------------------------------------------- block norm
 
-template <int DT, int VW, int NV>
-int launch_norm(const BlockNormArgs &a, const Device &dev, cudaStream_t stream) {
-    const int threads = row_threads(a.D, VW * NV);
-    // a warp per row: four rows to a block
-    const dim3 block(threads, threads == 32 ? 4 : 1);
-    const int64_t groups = ((int64_t)a.T + block.y - 1) / block.y;
-    const int64_t most = (int64_t)dev.sms * std::max(1, 2048 / (int)(block.x * block.y));
-    const dim3 grid((unsigned)std::min(groups, most));
-    if (VW == 1 || threads <= 512) return launch(block_norm_kernel<DT, VW, NV, 512>, grid, block, 0, stream, 1, a);
-    if constexpr (VW > 1) return launch(block_norm_kernel<DT, VW, NV, 1024>, grid, block, 0, stream, 1, a);
-    return SGEMM_ERR_INVALID_ARG;
+// How a row is shared out: `ranks` blocks of a cluster with `width` columns
+// each, in pieces that no 16 bytes span; `per` elements a thread.  A block
+// takes at most `most` threads, and its ring of copies at most 225 KB.
+// Where a warp is enough for a row, a block has four.
+struct RowPlan {
+    int ranks = 1, width;
+    dim3 block;
+    size_t smem;
+    RowPlan(int D, int size, int arrays, int per, int most) : width(D) {
+        for (;; ranks *= 2) {
+            const int vec = 16 / size;
+            width = ranks == 1 ? D : ((D + ranks - 1) / ranks + vec - 1) / vec * vec;
+            const int threads = row_threads(width, per);
+            block = dim3(threads, threads == 32 && ranks == 1 ? 4 : 1);
+            smem = (size_t)kNormStages * arrays * row_pieces(width, size) * 16 * block.y;
+            if (ranks == 8 || (threads <= most && smem <= 225 * 1024)) break;
+        }
+    }
+    int threads() const { return (int)(block.x * block.y); }
+};
+
+template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
+int launch_norm(BlockNormArgs a, const Device &dev, cudaStream_t stream) {
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = block_norm_kernel<DT, ALIGNED, NV, MAXT, MINB>;
+    constexpr int size = sizeof(typename Elem<DT>::type);
+    const RowPlan plan(a.D, size, a.gate_period == 1 ? 3 : 2, NV * Elem<DT>::VEC, MAXT);
+    a.ranks = plan.ranks;
+    a.width = plan.width;
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem);
+    if (!fit) return SGEMM_ERR_LAUNCH;
+    const int64_t groups = ((int64_t)a.T + plan.block.y - 1) / plan.block.y;
+    const int64_t most = std::max(1, dev.sms * fit / plan.ranks);
+    return launch(kernel, dim3((unsigned)(std::min(groups, most) * plan.ranks)), plan.block, plan.smem, stream,
+                  (unsigned)plan.ranks, a);
 }
 
-template <int DT>
-int norm_by_width(const BlockNormArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
+template <int DT, bool ALIGNED>
+int norm_by_width(const BlockNormArgs &a, const Device &dev, cudaStream_t stream) {
     constexpr int VEC = Elem<DT>::VEC;
-    // what the registers of a block hold: 8 elements a thread, 1024 threads on 16-byte pieces and
-    // 512 on single elements (whose addresses take more registers)
-    if (a.D > (vec ? 8192 : 4096))
-        return launch(block_norm_wide_kernel<DT>, dim3((unsigned)std::min(a.T, 2 * dev.sms)), dim3(1024), 0, stream, 1,
-                      a);
-    if (vec) return launch_norm<DT, VEC, 8 / VEC>(a, dev, stream);
-    return launch_norm<DT, 1, 8>(a, dev, stream);
+    // narrow rows take 8 elements a thread, so that a block has warps to hide its barriers; wide
+    // ones 16, so that a row needs fewer of them
+    if (a.D > 2048) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
+    return launch_norm<DT, ALIGNED, 8 / VEC, 256, 3>(a, dev, stream);
 }
 
-// Blocks of the gradient: runs of rows, two blocks per SM.
-int grad_blocks(int T, int sms) { return std::min(T, 2 * sms); }
-
-template <int DT, int VW, int NV>
-int launch_norm_grad(const BlockNormGradArgs &a, int blocks, cudaStream_t stream) {
-    return launch(block_norm_grad_kernel<DT, VW, NV>, dim3(blocks), dim3(row_threads(a.D, VW * NV)), 0, stream, 1, a);
+// Runners of the gradient's rows: a block (or a cluster) each, or for narrow
+// rows a warp each.  Every one writes its own partial sums, so there are no
+// more than fill the GPU: rows beyond 2048 elements leave room for one block
+// per SM.
+int grad_runners(int T, int D, int sms) {
+    const int per_sm = D > 2048 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : 16;
+    return std::min(T, std::max(1, per_sm * sms / (D > 4096 ? (D + 4095) / 4096 : 1)));
 }
 
-template <int DT>
-int norm_grad_by_width(const BlockNormGradArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
-    constexpr int VEC = Elem<DT>::VEC;
-    const int blocks = grad_blocks(a.T, dev.sms);
-    int st;
-    if (a.D > 4096) st = launch(block_norm_grad_wide_kernel<DT>, dim3(blocks), dim3(1024), 0, stream, 1, a);
-    else if (vec) st = launch_norm_grad<DT, VEC, 8 / VEC>(a, blocks, stream);
-    else st = launch_norm_grad<DT, 1, 8>(a, blocks, stream);
+template <int DT, bool ALIGNED>
+int launch_norm_grad(BlockNormGradArgs a, const Device &dev, cudaStream_t stream) {
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = block_norm_grad_kernel<DT, ALIGNED, 8 / Elem<DT>::VEC, 512, 1>;
+    constexpr int size = sizeof(typename Elem<DT>::type);
+    const RowPlan plan(a.D, size, 3 + (a.gate_period == 1) + (a.dr != nullptr), 8, 512);
+    a.ranks = plan.ranks;
+    a.width = plan.width;
+    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem)) return SGEMM_ERR_LAUNCH;
+    const unsigned groups = (a.runners + plan.block.y - 1) / plan.block.y;
+    const int st = launch(kernel, dim3(groups * plan.ranks), plan.block, plan.smem, stream, (unsigned)plan.ranks, a);
     if (st != SGEMM_OK) return st;
-    const unsigned what = a.gate_period ? 2 + (blocks - 1) : 2;
-    return launch(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, what), dim3(32, 8), 0, stream, 1, a, blocks);
+    const int gates = a.gate_period > 1 ? std::min({a.T / a.gate_period, a.runners - 1, 16}) : 0;
+    return launch(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, 2 + gates), dim3(32, 32), 0, stream, 1, a);
 }
 
 // Checks that the forward and the backward pass share.
@@ -105,11 +134,14 @@ bool norm_shape_ok(int T, int D, int dtype, int wdtype, const void *w_pre, const
 
 template <int DT, bool TOP>
 int launch_logprobs(const LogprobArgs &a, const Device &dev, cudaStream_t stream) {
-    // rows of few calls are shared by clusters of up to 8 blocks, until two blocks per SM are reached
+    // few rows are shared by clusters of up to 8 blocks, until there are two blocks per SM
     unsigned parts = 1;
     while (parts < 8 && (int64_t)a.T * parts * 2 <= 2 * dev.sms && a.V / (int)(parts * 2) >= 2048) parts *= 2;
-    const unsigned rows = (unsigned)std::min(a.T, 65535);
-    return launch(logprobs_kernel<DT, 256, 4, TOP>, dim3(parts, rows), dim3(256), 0, stream, parts, a);
+    const dim3 grid(parts, (unsigned)std::min(a.T, 65535));
+    // logits a thread has in flight beside those it adds up
+    constexpr int U = LP_N / Elem<DT>::VEC;
+    if (a.mask) return launch(logprobs_kernel<DT, U, TOP, true>, grid, dim3(kLogprobThreads), 0, stream, parts, a);
+    return launch(logprobs_kernel<DT, U, TOP, false>, grid, dim3(kLogprobThreads), 0, stream, parts, a);
 }
 
 template <int DT, int VW>
@@ -117,7 +149,9 @@ int launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t stream) {
     constexpr int THREADS = 256, U = VW > 1 ? 4 : 8;
     const unsigned cols = (unsigned)std::max(1, (a.V / VW + THREADS * U - 1) / (THREADS * U));
     const unsigned rows = (unsigned)std::min(a.T, 65535);
-    return launch(logprobs_grad_kernel<DT, VW, THREADS, U>, dim3(cols, rows), dim3(THREADS), 0, stream, 1, a);
+    const dim3 grid(cols, rows);
+    if (a.mask) return launch(logprobs_grad_kernel<DT, VW, THREADS, U, true>, grid, dim3(THREADS), 0, stream, 1, a);
+    return launch(logprobs_grad_kernel<DT, VW, THREADS, U, false>, grid, dim3(THREADS), 0, stream, 1, a);
 }
 
 bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, const int32_t *mask, int ldm,
@@ -163,15 +197,19 @@ int sgemm_block_norm(int T, int D, int dtype, const void *x, int ldx, const void
     BlockNormArgs a{T, D, x, y, gate, ldx, ldy, ldg, w_pre, w_post, wdtype == SGEMM_F32,
                     gate_rows ? T / gate_rows : 0, scale, eps, r, n, ldr, ldn, q, ldq, q_scale, rstd, 0};
     const int vec_elems = 16 / size;
-    const bool vec = D % vec_elems == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && R.vec(size) && N.vec(size);
+    const bool vec = D % vec_elems == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && R.vec(size) && N.vec(size) &&
+                     aligned(w_pre, 16) && aligned(w_post, 16);
     a.q_vec = aligned(q, (unsigned)vec_elems) && ldq % vec_elems == 0;
-    return by_dtype(dtype, [&](auto dt) { return norm_by_width<decltype(dt)::value>(a, vec, dev, stream); });
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return vec ? norm_by_width<DT, true>(a, dev, stream) : norm_by_width<DT, false>(a, dev, stream);
+    });
 }
 
 size_t sgemm_block_norm_backward_workspace_size(int T, int D) {
     Device dev;
     if (T <= 0 || D <= 0 || sgemm_host::device(dev) != SGEMM_OK) return 0;
-    return (size_t)grad_blocks(T, dev.sms) * 4 * (size_t)D * sizeof(float);
+    return (size_t)grad_runners(T, D, dev.sms) * 4 * (size_t)D * sizeof(float);
 }
 
 int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, const void *y, int ldy,
@@ -218,10 +256,14 @@ int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
     }
     const BlockNormGradArgs a{T, D, x, y, gate, dn, dr, ldx, ldy, ldg, lddn, lddr, w_pre, w_post, wdtype == SGEMM_F32,
                               gate_rows ? T / gate_rows : 0, scale, rstd, dx, dy, dgate, lddx, lddy, lddg, dw_pre,
-                              dw_post, static_cast<float *>(workspace)};
+                              dw_post, static_cast<float *>(workspace), grad_runners(T, D, dev.sms)};
     const bool vec = D % (16 / size) == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && DN.vec(size) &&
-                     DR.vec(size) && DX.vec(size) && DY.vec(size);
-    return by_dtype(dtype, [&](auto dt) { return norm_grad_by_width<decltype(dt)::value>(a, vec, dev, stream); });
+                     DR.vec(size) && DX.vec(size) && DY.vec(size) && DG.vec(size) && aligned(w_pre, 16) &&
+                     aligned(w_post, 16);
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return vec ? launch_norm_grad<DT, true>(a, dev, stream) : launch_norm_grad<DT, false>(a, dev, stream);
+    });
 }
 
 int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float scale, const int32_t *mask, int ldm,

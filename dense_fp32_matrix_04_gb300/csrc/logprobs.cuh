@@ -10,9 +10,11 @@
 //
 // Each warp keeps the `top` best columns it has met as a list over its lanes,
 // best first.  A chunk whose largest logits do not reach the list's last entry
-// costs one comparison a lane; otherwise its columns are first held to the
-// top-th largest of the 32 lanes' maxima (at least `top` columns reach that),
-// and those left are inserted one by one.
+// costs one comparison a lane; otherwise the columns of the lanes that do are
+// looked at, 32 at a time, one a lane.  After 1, 2, 4, ... chunks the block also
+// takes the top-th largest of the maxima of 32 groups of its threads, which
+// every column has to reach from then on: a warp alone would let eight times
+// as many through.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -65,7 +67,7 @@ __device__ __forceinline__ bool better(float v, int id, float v2, int id2) {
     return v > v2 || (v == v2 && id < id2);
 }
 
-// The running sums of a thread.
+// The running sums of a thread, or of several joined.
 struct SoftmaxState {
     float m = -INFINITY, s = 0.f, s1 = 0.f;
     // raises the maximum to at least m2; where d is far below 0, 2^d is 0 and the bound on d
@@ -78,10 +80,35 @@ struct SoftmaxState {
             m = m2;
         }
     }
-    __device__ void add(float z, float c) {
-        const float t = (z - m) * c, e = exp2_approx(t);
-        s += e;
-        s1 = fmaf(e, fmaxf(t, -1000.f), s1);  // as in raise()
+    // adds the n logits v, none of them above m (finite or +infinity), two at a time
+    template <int N>
+    __device__ void add(const float *v, float c) {
+        if constexpr (N % 2 == 0) {
+            const uint64_t mm = f32x2_dup(-m), cc = f32x2_dup(c);
+            uint64_t sum = f32x2_pair(s, 0.f), sum1 = f32x2_pair(s1, 0.f);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const uint64_t t = f32x2_mul(f32x2_add(f32x2_pair(v[j], v[j + 1]), mm), cc);
+                const float2 x = f32x2_unpack(t);
+                const uint64_t e = f32x2_pair(exp2_approx(x.x), exp2_approx(x.y));
+                sum = f32x2_add(sum, e);
+                f32x2_fma(sum1, e, t);
+            }
+            const float2 a = f32x2_unpack(sum), b = f32x2_unpack(sum1);
+            const float s_new = a.x + a.y, s1_new = b.x + b.y;
+            if (s1_new == s1_new) {
+                s = s_new;
+                s1 = s1_new;
+                return;
+            }
+        }
+        // a term of 0 times -infinity (a logit of -infinity), or a NaN
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float t = (v[j] - m) * c, e = exp2_approx(t);
+            s += e;
+            s1 = fmaf(e, fmaxf(t, -1000.f), s1);
+        }
     }
     __device__ void join(float m2, float s2, float s12, float c) {
         if (m2 == -INFINITY) {
@@ -93,12 +120,34 @@ struct SoftmaxState {
         s1 = fmaf(f, fmaf(s2, fmaxf(d, -1000.f), s12), s1);
         s = fmaf(s2, f, s);
     }
+    // joins the states of 2 * FROM lanes, in an order that the lanes' numbers fix
+    template <int FROM>
+    __device__ void join_lanes(float c) {
+#pragma unroll
+        for (int o = FROM; o; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
+                        s12 = __shfl_xor_sync(0xffffffffu, s1, o);
+            join(m2, s2, s12, c);
+        }
+    }
 };
 
-// The `top` best columns of a warp, lane i holding the i-th (none: -infinity).
+// Exchanges (v, id) with the lane `stride` away, keeping the better of the two
+// where `keep_better` holds and the other elsewhere.
+__device__ __forceinline__ void exchange(float &v, int &id, int stride, bool keep_better) {
+    const float ov = __shfl_xor_sync(0xffffffffu, v, stride);
+    const int oid = __shfl_xor_sync(0xffffffffu, id, stride);
+    if (better(ov, oid, v, id) == keep_better) {
+        v = ov;
+        id = oid;
+    }
+}
+
+// The best columns of a warp in order, lane i holding the i-th (none: -infinity).
 struct WarpTop {
     float v = -INFINITY;
     int id = INT_MAX;
+    // one more column
     __device__ void insert(float cv, int cid, int lane) {
         const bool ahead = better(v, id, cv, cid);
         const int pos = __popc(__ballot_sync(0xffffffffu, ahead));
@@ -112,6 +161,23 @@ struct WarpTop {
             id = uid;
         }
     }
+    // one column a lane (none: -infinity): a bitonic sort of the new ones, the better halves of
+    // both lists, and a bitonic merge
+    __device__ void merge(float cv, int cid, int lane) {
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int stride = size >> 1; stride; stride >>= 1)
+                exchange(cv, cid, stride, ((lane & stride) == 0) == ((lane & size) == 0));
+        const float rv = __shfl_xor_sync(0xffffffffu, cv, 31);
+        const int rid = __shfl_xor_sync(0xffffffffu, cid, 31);
+        if (better(rv, rid, v, id)) {
+            v = rv;
+            id = rid;
+        }
+#pragma unroll
+        for (int stride = 16; stride; stride >>= 1) exchange(v, id, stride, (lane & stride) == 0);
+    }
 };
 
 // The k-th largest (k = 1 .. 32) of the lanes' values: a bitonic sort over lanes.
@@ -121,36 +187,68 @@ __device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
 #pragma unroll
         for (int stride = size >> 1; stride; stride >>= 1) {
             const float o = __shfl_xor_sync(0xffffffffu, x, stride);
-            const bool down = (lane & size) == 0 || size == 32;   // this run sorts from large to small
-            const bool lower = (lane & stride) == 0;
-            x = down == lower ? fmaxf(x, o) : fminf(x, o);
+            x = ((lane & stride) == 0) == ((lane & size) == 0) ? fmaxf(x, o) : fminf(x, o);
         }
     return __shfl_sync(0xffffffffu, x, k - 1);
 }
 
-constexpr int kTopBuffer = 64;  // columns a warp collects before it inserts them
+// Joins the block's THREADS entries, one a thread, which are lists in order
+// with `top` entries each: `top` best into out, in order.  No entry below the
+// largest of the lists' last entries can be among them (that list alone has
+// `top` better ones), so only those that reach it are compared with each
+// other: an entry's place is the number of better ones.
+template <int THREADS>
+struct TopJoin {
+    Candidate entry[THREADS];
+    float last[THREADS / 32];
+    int count;
+    __device__ void run(float v, int id, int top, Candidate *out) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == top - 1) last[warp] = v;
+        if (threadIdx.x == 0) count = 0;
+        if (threadIdx.x < 32) out[threadIdx.x] = {-INFINITY, INT_MAX};
+        __syncthreads();
+        float floor_v = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) floor_v = fmaxf(floor_v, last[w]);
+        const bool in = lane < top && v > -INFINITY && v >= floor_v;
+        if (in) entry[atomicAdd(&count, 1)] = {v, id};  // their order does not matter
+        __syncthreads();
+        if (in) {
+            int place = 0;
+            for (int i = 0, n = count; i < n; ++i) place += better(entry[i].v, entry[i].id, v, id);
+            if (place < top) out[place] = {v, id};
+        }
+        __syncthreads();
+    }
+};
+
+constexpr int kLogprobThreads = 256;
 
 // A cluster of gridDim.x blocks shares row blockIdx.y (+ gridDim.y, ...): each
 // takes a run of 16-byte pieces; the last also the columns before the first
 // and after the last aligned piece.  Block 0 joins the blocks' results through
-// distributed shared memory.
-template <int DT, int THREADS, int U, bool TOP>
-__global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobArgs a) {
+// distributed shared memory.  A thread loads U pieces ahead of those it adds up.
+template <int DT, int U, bool TOP, bool MASK>
+__global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 : 2) logprobs_kernel(const LogprobArgs a) {
     using E = Elem<DT>;
     using type = typename E::type;
-    constexpr int VEC = E::VEC, WARPS = THREADS / 32;
+    constexpr int VEC = E::VEC, THREADS = kLogprobThreads, WARPS = THREADS / 32;
     __shared__ float warp_state[3][WARPS];
     __shared__ float block_state[3];
-    __shared__ Candidate lists[TOP ? WARPS : 1][32];
     __shared__ Candidate block_list[TOP ? 32 : 1];
-    __shared__ Candidate buffer[TOP ? WARPS : 1][TOP ? kTopBuffer : 1];
+    __shared__ TopJoin<TOP ? THREADS : 32> top_join;
+    // a warp's columns on their way to its list, and the lanes that they come from
+    __shared__ __align__(16) float columns[TOP ? WARPS : 1][TOP ? 32 * U * VEC : 4];
+    __shared__ uint8_t from_lane[TOP ? WARPS : 1][32];
+    __shared__ float group_max[2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = gridDim.x, part = blockIdx.x;
     const float c = a.scale * kLog2e;
 
     for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
         const type *z = static_cast<const type *>(a.z) + t * a.ldz;
-        const int32_t *mask = a.mask ? a.mask + t * a.ldm : nullptr;
+        const int32_t *mask = MASK ? a.mask + t * a.ldm : nullptr;
         const int off = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(type));
         const int head = min(off ? VEC - off : 0, a.V);
         const int pieces = (a.V - head) / VEC;
@@ -160,8 +258,14 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobArgs a) 
 
         SoftmaxState st;
         WarpTop best;
-        // the columns v[0 .. n) of this thread, column j at col(j); -infinity where there is none
-        auto chunk = [&](const float *v, auto n_const, auto col) {
+        // a column joins the warp's list if it is better than the list's last entry, and reaches
+        // floor_v (which `top` of the row's columns are known to reach)
+        float last_v = -INFINITY, floor_v = -INFINITY;
+        int last_id = INT_MAX;
+        // adds the columns v[0 .. n) of this thread, -infinity where there is none; column i of
+        // lane l's has number col(l, i).  round: how many chunks the block has behind it, or -1
+        // where only one warp is here
+        auto chunk = [&](const float *v, auto n_const, int round, auto col) {
             constexpr int n = decltype(n_const)::value;
             float top = v[0];
 #pragma unroll
@@ -172,166 +276,160 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobArgs a) 
                 for (int j = 0; j < n; ++j)
                     if (v[j] != v[j]) st.s = v[j];
             } else {
-#pragma unroll
-                for (int j = 0; j < n; ++j) st.add(v[j], c);
+                st.template add<n>(v, c);
             }
             if constexpr (TOP) {
-                const float last_v = __shfl_sync(0xffffffffu, best.v, a.top - 1);
-                const unsigned reach = __ballot_sync(0xffffffffu, top >= last_v && top > -INFINITY);
+                if ((round & (round + 1)) == 0 && round >= 0) {
+                    // after 1, 2, 4, ... chunks: `top` columns reach the top-th largest of the
+                    // maxima of the block's 32 groups of threads
+                    float g = st.m;
+#pragma unroll
+                    for (int o = 32 / WARPS; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+                    float *group = group_max[__popc(round) & 1];
+                    if (lane < 32 / WARPS) group[warp * (32 / WARPS) + lane] = g;
+                    __syncthreads();
+                    floor_v = fmaxf(floor_v, warp_kth_largest(group[lane], a.top, lane));
+                }
+                const bool reaches = top >= fmaxf(last_v, floor_v) && top > -INFINITY;
+                const unsigned reach = __ballot_sync(0xffffffffu, reaches);
                 if (reach) {
-                    const int last_id = __shfl_sync(0xffffffffu, best.id, a.top - 1);
-                    float floor_v = -INFINITY;
-                    if (__popc(reach) > a.top) floor_v = warp_kth_largest(top, a.top, lane);
-                    uint32_t keep = 0;
+                    // the columns of the lanes that reach it, one a lane, 32 at a time
+                    if (reaches) {
+                        const int rank = __popc(reach & ((1u << lane) - 1));
+                        from_lane[warp][rank] = (uint8_t)lane;
+                        float *to = &columns[warp][rank * n];
+                        if constexpr (n % 4 == 0) {
 #pragma unroll
-                    for (int j = 0; j < n; ++j)
-                        if (v[j] >= floor_v && v[j] > -INFINITY && better(v[j], col(j), last_v, last_id)) keep |= 1u << j;
-                    int at = __popc(keep), total;
+                            for (int j = 0; j < n; j += 4)
+                                *reinterpret_cast<float4 *>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        } else {
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int up = __shfl_up_sync(0xffffffffu, at, o);
-                        if (lane >= o) at += up;
-                    }
-                    total = __shfl_sync(0xffffffffu, at, 31);
-                    at -= __popc(keep);
-                    for (int from = 0; from < total; from += kTopBuffer) {
-                        int k = at;
-#pragma unroll
-                        for (int j = 0; j < n; ++j)
-                            if (keep >> j & 1) {
-                                if (k >= from && k < from + kTopBuffer) buffer[warp][k - from] = {v[j], col(j)};
-                                ++k;
-                            }
-                        __syncwarp();
-                        const int count = min(kTopBuffer, total - from);
-                        for (int i = 0; i < count; ++i) {
-                            const Candidate e = buffer[warp][i];
-                            const float lv = __shfl_sync(0xffffffffu, best.v, a.top - 1);
-                            const int li = __shfl_sync(0xffffffffu, best.id, a.top - 1);
-                            if (better(e.v, e.id, lv, li)) best.insert(e.v, e.id, lane);
+                            for (int j = 0; j < n; ++j) to[j] = v[j];
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
+                    for (int i = 0, count = __popc(reach) * n; i < count; i += 32) {
+                        Candidate e{-INFINITY, INT_MAX};
+                        if (i + lane < count) {
+                            e.v = columns[warp][i + lane];
+                            e.id = col(from_lane[warp][(i + lane) / n], (i + lane) % n);
+                        }
+                        const bool in = e.v >= floor_v && e.v > -INFINITY && better(e.v, e.id, last_v, last_id);
+                        unsigned who = __ballot_sync(0xffffffffu, in);
+                        if (!who) continue;
+                        if (__popc(who) > 6) {
+                            best.merge(in ? e.v : -INFINITY, in ? e.id : INT_MAX, lane);
+                        } else {
+                            for (; who; who &= who - 1) {
+                                const int src = __ffs(who) - 1;
+                                best.insert(__shfl_sync(0xffffffffu, e.v, src), __shfl_sync(0xffffffffu, e.id, src), lane);
+                            }
+                        }
+                        last_v = __shfl_sync(0xffffffffu, best.v, a.top - 1);
+                        last_id = __shfl_sync(0xffffffffu, best.id, a.top - 1);
+                    }
+                    __syncwarp();
                 }
             }
         };
+        auto allowed = [&](int col) { return !MASK || (mask[col >> 5] >> (col & 31) & 1); };
 
-        for (int p = p0; p < p1; p += THREADS * U) {
-            uint4 raw[U];
-            uint32_t bits[U];
+        auto load = [&](int p, uint4(&raw)[U], uint32_t(&bits)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = p + u * THREADS + (int)threadIdx.x;
-                if (at < p1) raw[u] = body[at];
-                bits[u] = at < p1 ? ~0u : 0u;
-                if (mask && at < p1) bits[u] = mask_bits(mask, head + at * VEC, VEC, a.V);
+                if (at < p1) raw[u] = __ldg(body + at);
+                if (MASK && at < p1) bits[u] = mask_bits(mask, head + at * VEC, VEC, a.V);
             }
+        };
+        uint4 raw[U];
+        uint32_t bits[U];
+        load(p0, raw, bits);
+        int round = 0;
+        for (int p = p0; p < p1; p += THREADS * U) {
             float v[U * VEC];
+            const bool whole = p + THREADS * U <= p1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 unpack16<DT>(raw[u], v + u * VEC);
+                if (MASK) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (!(bits[u] >> e & 1)) v[u * VEC + e] = -INFINITY;
+                    for (int e = 0; e < VEC; ++e)
+                        if (!(bits[u] >> e & 1)) v[u * VEC + e] = -INFINITY;
+                }
+                if (!whole && p + u * THREADS + (int)threadIdx.x >= p1) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[u * VEC + e] = -INFINITY;
+                }
             }
-            chunk(v, std::integral_constant<int, U * VEC>{}, [&](int j) {
-                return head + (p + (j / VEC) * THREADS + (int)threadIdx.x) * VEC + j % VEC;
+            if (p + THREADS * U < p1) load(p + THREADS * U, raw, bits);
+            chunk(v, std::integral_constant<int, U * VEC>{}, round++, [&](int src, int i) {
+                return head + (p + (i / VEC) * THREADS + warp * 32 + src) * VEC + i % VEC;
             });
         }
         if (part == parts - 1) {
-            // fewer than 2 * VEC columns outside the pieces: one a thread
+            // fewer than 2 * VEC columns outside the pieces: one a lane of the first warp
             const int outside = head + a.V - tail0;
-            float v = -INFINITY;
-            int col = INT_MAX;
-            if ((int)threadIdx.x < outside) {
-                col = (int)threadIdx.x < head ? (int)threadIdx.x : tail0 + (int)threadIdx.x - head;
-                if (!mask || (mask[col >> 5] >> (col & 31) & 1)) v = E::to_float(z[col]);
+            if (warp == 0 && outside > 0) {
+                auto column = [&](int l, int) { return l < head ? l : tail0 + l - head; };
+                float v = -INFINITY;
+                if (lane < outside && allowed(column(lane, 0))) v = E::to_float(z[column(lane, 0)]);
+                chunk(&v, std::integral_constant<int, 1>{}, -1, column);
             }
-            if (warp == 0 && outside > 0) chunk(&v, std::integral_constant<int, 1>{}, [&](int) { return col; });
         }
 
         // ---- join the lanes, the warps, and the cluster's blocks
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, st.m, o), s2 = __shfl_xor_sync(0xffffffffu, st.s, o),
-                        s12 = __shfl_xor_sync(0xffffffffu, st.s1, o);
-            st.join(m2, s2, s12, c);
-        }
+        st.template join_lanes<16>(c);
         if (lane == 0) {
             warp_state[0][warp] = st.m;
             warp_state[1][warp] = st.s;
             warp_state[2][warp] = st.s1;
         }
-        if constexpr (TOP) {
-            lists[warp][lane] = lane < a.top ? Candidate{best.v, best.id} : Candidate{-INFINITY, INT_MAX};
-            if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
-        }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            SoftmaxState all;
-            for (int w = 0; w < WARPS; ++w) all.join(warp_state[0][w], warp_state[1][w], warp_state[2][w], c);
-            block_state[0] = all.m;
-            block_state[1] = all.s;
-            block_state[2] = all.s1;
-        }
-        if constexpr (TOP) {
-            // an entry's place in the block's list is the number of better entries
-            const Candidate e = lists[warp][lane];
-            if (e.v > -INFINITY) {
-                int place = 0;
-                for (int w = 0; w < WARPS; ++w)
-                    for (int i = 0; i < a.top; ++i) {
-                        const Candidate o = lists[w][i];
-                        if (!better(o.v, o.id, e.v, e.id)) break;  // the lists are in order
-                        ++place;
-                    }
-                if (place < a.top) block_list[place] = e;
+        SoftmaxState all;
+        if (warp == 0) {
+            if (lane < WARPS) {
+                all.m = warp_state[0][lane];
+                all.s = warp_state[1][lane];
+                all.s1 = warp_state[2][lane];
+            }
+            all.template join_lanes<WARPS / 2>(c);
+            if (parts > 1 && lane == 0) {
+                block_state[0] = all.m;
+                block_state[1] = all.s;
+                block_state[2] = all.s1;
             }
         }
-        if (parts > 1) cluster_sync();
-        else __syncthreads();
-        if (part == 0 && warp == 0) {
-            SoftmaxState all;
-            WarpTop joined;
-            for (int b = 0; b < parts; ++b) {
-                const uint32_t s = parts > 1 ? dsmem_map(smem_addr(block_state), (uint32_t)b) : 0;
-                float m2, s2, s12;
-                if (parts > 1) {
-                    m2 = __uint_as_float(dsmem_ld_u32(s));
-                    s2 = __uint_as_float(dsmem_ld_u32(s + 4));
-                    s12 = __uint_as_float(dsmem_ld_u32(s + 8));
-                } else {
-                    m2 = block_state[0];
-                    s2 = block_state[1];
-                    s12 = block_state[2];
+        if constexpr (TOP) top_join.run(best.v, best.id, a.top, block_list);
+        if (parts > 1) {
+            __syncthreads();
+            cluster_sync();
+            if (part == 0) {
+                if (warp == 0) {
+                    all = SoftmaxState{};
+                    if (lane < parts) {
+                        const uint32_t s = dsmem_map(smem_addr(block_state), (uint32_t)lane);
+                        all.m = __uint_as_float(dsmem_ld_u32(s));
+                        all.s = __uint_as_float(dsmem_ld_u32(s + 4));
+                        all.s1 = __uint_as_float(dsmem_ld_u32(s + 8));
+                    }
+                    all.template join_lanes<4>(c);
                 }
-                all.join(m2, s2, s12, c);
                 if constexpr (TOP) {
-                    float cv;
-                    int ci;
-                    if (parts > 1) {
-                        const uint32_t l = dsmem_map(smem_addr(&block_list[lane]), (uint32_t)b);
-                        cv = __uint_as_float(dsmem_ld_u32(l));
-                        ci = (int)dsmem_ld_u32(l + 4);
-                    } else {
-                        cv = block_list[lane].v;
-                        ci = block_list[lane].id;
+                    Candidate e{-INFINITY, INT_MAX};
+                    if (warp < parts) {
+                        const uint32_t l = dsmem_map(smem_addr(&block_list[lane]), (uint32_t)warp);
+                        e.v = __uint_as_float(dsmem_ld_u32(l));
+                        e.id = (int)dsmem_ld_u32(l + 4);
                     }
-                    if (b == 0) {
-                        joined.v = cv;
-                        joined.id = ci;
-                    } else {
-                        for (int i = 0; i < a.top; ++i) {
-                            const float ev = __shfl_sync(0xffffffffu, cv, i);
-                            const int ei = __shfl_sync(0xffffffffu, ci, i);
-                            const float lv = __shfl_sync(0xffffffffu, joined.v, a.top - 1);
-                            const int li = __shfl_sync(0xffffffffu, joined.id, a.top - 1);
-                            if (!(ev > -INFINITY) || !better(ev, ei, lv, li)) break;
-                            joined.insert(ev, ei, lane);
-                        }
-                    }
+                    __syncthreads();  // block 0's own list has been read before it is written
+                    top_join.run(e.v, e.id, a.top, block_list);
                 }
             }
+        }
+        if (part == 0 && warp == 0) {
+            all.m = __shfl_sync(0xffffffffu, all.m, 0);
+            all.s = __shfl_sync(0xffffffffu, all.s, 0);
             const bool none = all.m == -INFINITY && !(all.s != all.s);
             const float log_s = logf(all.s);
             if (lane == 0) {
@@ -343,8 +441,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobArgs a) 
                     if (y >= a.V) {
                         lp = NAN;
                     } else if (y >= 0) {
-                        const bool allowed = !mask || (mask[y >> 5] >> (y & 31) & 1);
-                        const float zy = allowed ? E::to_float(z[y]) : -INFINITY;
+                        const float zy = allowed((int)y) ? E::to_float(z[y]) : -INFINITY;
                         lp = none ? -INFINITY : fmaf(zy - all.m, a.scale, -log_s);
                     }
                     a.logprob[t] = lp;
@@ -352,16 +449,16 @@ __global__ void __launch_bounds__(THREADS) logprobs_kernel(const LogprobArgs a) 
             }
             if constexpr (TOP) {
                 if (lane < a.top) {
+                    const Candidate e = block_list[lane];
                     const bool bad = all.s != all.s;
-                    const bool has = joined.v > -INFINITY && !bad;
-                    a.top_logprob[t * a.top + lane] =
-                        bad ? NAN : has ? fmaf(joined.v - all.m, a.scale, -log_s) : -INFINITY;
-                    a.top_id[t * a.top + lane] = has ? joined.id : -1;
+                    const bool has = e.v > -INFINITY && !bad;
+                    a.top_logprob[t * a.top + lane] = bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_s) : -INFINITY;
+                    a.top_id[t * a.top + lane] = has ? e.id : -1;
                 }
             }
         }
-        if (parts > 1) cluster_sync();
-        else __syncthreads();
+        __syncthreads();
+        if (parts > 1) cluster_sync();  // no block leaves, or starts another row, while block 0 reads its results
     }
 }
 
@@ -395,26 +492,36 @@ struct LogprobGradRow {
         B = -a.scale * gh;
         hit = a.scale * g;
     }
-    __device__ float operator()(float z, bool allowed, int64_t col) const {
-        if (!allowed || lse == -INFINITY) return 0.f;
-        const float logp = fmaf(z, scale, -lse), p = exp2_approx(logp * kLog2e);
-        // p = 0 leaves nothing of B log p (log p may be -infinity there)
-        const float d = p * fmaf(B, fmaxf(logp, -1000.f), A);
-        return col == target && z > -INFINITY ? d + hit : d;
+    // the N columns from `col` on; bits: which of them the mask allows
+    template <int N>
+    __device__ void apply(float *v, uint32_t bits, int col) const {
+        const bool near = target >= col && target < (int64_t)col + N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float logp = fmaf(v[e], scale, -lse), p = exp2_approx(logp * kLog2e);
+            // p = 0 leaves nothing of B log p (log p may be -infinity there)
+            float d = p * fmaf(B, fmaxf(logp, -1000.f), A);
+            if (near && target - col == e && v[e] > -INFINITY) d += hit;
+            v[e] = !(bits >> e & 1) ? 0.f : d;
+        }
+        if (lse == -INFINITY) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = 0.f;
+        }
     }
 };
 
 // blockIdx.y (+ gridDim.y, ...): rows; blockIdx.x: runs of THREADS * U pieces
 // of VW elements.  Every element is read before the same thread writes it, so
 // dz may be the logits.
-template <int DT, int VW, int THREADS, int U>
+template <int DT, int VW, int THREADS, int U, bool MASK>
 __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(const LogprobGradArgs a) {
     using E = Elem<DT>;
     using type = typename E::type;
     for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
         const type *z = static_cast<const type *>(a.z) + t * a.ldz;
         type *dz = static_cast<type *>(a.dz) + t * a.lddz;
-        const int32_t *mask = a.mask ? a.mask + t * a.ldm : nullptr;
+        const int32_t *mask = MASK ? a.mask + t * a.ldm : nullptr;
         const LogprobGradRow row(a, t);
         // 16-byte pieces need both rows at the same distance from a 16-byte boundary
         const int off = VW > 1 ? (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(type)) : 0;
@@ -430,7 +537,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(const LogprobGra
             const int at = base + u * THREADS + (int)threadIdx.x;
             if (at < pieces) raw[u] = P::load(z + head + (int64_t)at * VW);
             bits[u] = ~0u;
-            if (mask && at < pieces) bits[u] = mask_bits(mask, head + at * VW, VW, a.V);
+            if (MASK && at < pieces) bits[u] = mask_bits(mask, head + at * VW, VW, a.V);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -439,14 +546,15 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(const LogprobGra
             float v[VW];
             P::unpack(raw[u], v);
             const int col = head + at * VW;
-#pragma unroll
-            for (int e = 0; e < VW; ++e) v[e] = row(v[e], bits[u] >> e & 1, col + e);
+            row.template apply<VW>(v, bits[u], col);
             P::store(dz + col, v);
         }
         if (VW > 1 && blockIdx.x == gridDim.x - 1 && (int)threadIdx.x < head + a.V - tail0) {
             const int col = (int)threadIdx.x < head ? (int)threadIdx.x : tail0 + (int)threadIdx.x - head;
-            const bool allowed = !mask || (mask[col >> 5] >> (col & 31) & 1);
-            dz[col] = E::from_float(row(E::to_float(z[col]), allowed, col));
+            const bool allowed = !MASK || (mask[col >> 5] >> (col & 31) & 1);
+            float v = E::to_float(z[col]);
+            row.template apply<1>(&v, allowed, col);
+            dz[col] = E::from_float(v);
         }
     }
 }

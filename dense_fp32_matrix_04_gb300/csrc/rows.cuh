@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "../../include/sgemm_layers.h"
+#include "ptx.cuh"
 
 namespace sgemm {
 
@@ -104,32 +105,46 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
-// Sums over the threads that share a row: a warp (warps == 1), or the block's
-// warps through shared memory, in an order fixed by the number of warps.
-// Each call alternates between two sets of slots, so one barrier per call
-// separates it from the next.
+// Sums and maxima over the threads that share a row: a warp (warps == 1), the
+// block's warps through shared memory, or those of a cluster of `ranks` blocks
+// of up to 16 warps through distributed shared memory; in an order that the
+// numbers of warps and ranks fix, so every thread has the same bits.  Calls
+// alternate between two sets of slots, so one barrier a call is enough.
+// (Blocks of a cluster meet once more before they leave.)
 struct RowReducer {
     float *slots;  // 2 x 32 floats of shared memory
-    int warps, turn = 0;
-    __device__ float sum(float v) {
-        v = warp_sum(v);
-        if (warps == 1) return v;
+    int warps, ranks = 1, turn = 0;
+    template <class Join>
+    __device__ uint32_t all(uint32_t v, uint32_t none, Join join) {
         float *s = slots + 32 * turn;
         turn ^= 1;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) s[warp] = v;
-        __syncthreads();
-        return warp_sum(lane < warps ? s[lane] : 0.f);
+        if (lane == 0) s[warp] = __uint_as_float(v);
+        uint32_t got = none;
+        if (ranks == 1) {
+            __syncthreads();
+            if (lane < warps) got = __float_as_uint(s[lane]);
+        } else {
+            __syncwarp();
+            cluster_sync();
+            const int w = lane & 15;
+            if (w < warps)
+                for (int r = lane >> 4; r < ranks; r += 2)
+                    got = join(got, dsmem_ld_u32(dsmem_map(smem_addr(s + w), (uint32_t)r)));
+        }
+        return got;
+    }
+    __device__ float sum(float v) {
+        v = warp_sum(v);
+        if (warps == 1 && ranks == 1) return v;
+        return warp_sum(__uint_as_float(all(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+        })));
     }
     __device__ uint32_t max(uint32_t v) {
         v = warp_max(v);
-        if (warps == 1) return v;
-        uint32_t *s = reinterpret_cast<uint32_t *>(slots + 32 * turn);
-        turn ^= 1;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) s[warp] = v;
-        __syncthreads();
-        return warp_max(lane < warps ? s[lane] : 0u);
+        if (warps == 1 && ranks == 1) return v;
+        return warp_max(all(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }));
     }
 };
 

@@ -53,7 +53,7 @@ typedef enum {
  *   rstd: 2 x T FP32: rsqrt(mean(y^2) + eps) of each row (1 without w_post),
  *       then rsqrt(mean(r^2) + eps); the backward pass reads them.  May be
  *       NULL.
- * T <= 2^30, D <= 65536.
+ * T <= 2^30, D <= 24576.
  */
 int sgemm_block_norm(int T, int D, int dtype,
                      const void *x, int ldx, const void *y, int ldy,
