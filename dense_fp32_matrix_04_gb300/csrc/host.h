@@ -1,6 +1,7 @@
 // Host-side facts and checks that the library's translation units share.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,8 +25,17 @@ struct Device {
 };
 __attribute__((visibility("hidden"))) int device(Device &out);
 
+// Tensor map of a row-major FP16 matrix (16-byte aligned base and rows), read in
+// boxes of box_rows rows by 64 columns into 128-byte swizzled rows; zeros
+// outside the matrix.
+__attribute__((visibility("hidden"))) bool encode_f16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols,
+                                                      int64_t ld, int box_rows);
+
 // Nanoseconds a kernel may wait for its own copies before it gives up.
 __attribute__((visibility("hidden"))) unsigned long long wait_limit_ns();
+
+// The test-only switches (sgemm_testing.h); 0 unless a test turned some on.
+__attribute__((visibility("hidden"))) int test_flags();
 
 inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
@@ -40,8 +50,10 @@ struct Range {
 };
 
 // Launches a kernel, in clusters of `cluster` blocks along x where that is
-// more than one; SGEMM_OK, or SGEMM_ERR_LAUNCH with the error cleared.
-template <class... Params, class... Args>
+// more than one, and with EARLY as soon as every block of the kernel before
+// allows it (griddepcontrol); SGEMM_OK, or SGEMM_ERR_LAUNCH with the error
+// cleared.
+template <bool EARLY = false, class... Params, class... Args>
 int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,
            Args &&...args) {
     cudaLaunchConfig_t cfg = {};
@@ -49,13 +61,20 @@ int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaSt
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (EARLY) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = n;
     if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess) return SGEMM_OK;
     (void)cudaGetLastError();
     return SGEMM_ERR_LAUNCH;
@@ -65,7 +84,7 @@ int launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaSt
 // on a device's first use of it (`regs` is the caller's cache for the kernel)
 // its shared-memory limit is raised.  0 if the device refuses.
 template <class Kernel>
-int blocks_per_sm(std::atomic<int> (&regs)[kMaxDevices], const Device &dev, Kernel kernel, int threads, int smem) {
+inline int blocks_per_sm(std::atomic<int> (&regs)[kMaxDevices], const Device &dev, Kernel kernel, int threads, int smem) {
     int r = regs[dev.dev].load(std::memory_order_acquire);
     if (r == 0) {
         cudaFuncAttributes at;

@@ -29,12 +29,17 @@ __device__ __forceinline__ void store_bytes(int8_t *p, const int8_t (&b)[N], boo
     for (int i = 0; i < N; ++i) p[i] = b[i];
 }
 
-template <int DT, int VW, int NV>
+// The codes of a row as 8-bit integers or, for the tensor cores, as FP16 values.
+__device__ __forceinline__ void put_code(int8_t *p, int8_t c) { *p = c; }
+__device__ __forceinline__ void put_code(__half *p, int8_t c) { *p = __int2half_rn(c); }
+
+template <int DT, int VW, int NV, class Code>
 __global__ void __launch_bounds__(1024)
     quantize_i8_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
-                       int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale, int q_vec) {
+                       Code *__restrict__ q, int64_t ldq, float *__restrict__ scale, int q_vec) {
     using P = Piece<DT, VW>;
     __shared__ float slots[64];
+    griddep_launch_dependents();
     RowReducer red{slots, (int)(blockDim.x >> 5)};
     const int threads = blockDim.x;
     const int step = gridDim.x * blockDim.y;
@@ -57,16 +62,32 @@ __global__ void __launch_bounds__(1024)
             int8_t b[VW];
 #pragma unroll
             for (int e = 0; e < VW; ++e) b[e] = s(v[i * VW + e]);
-            store_bytes(q + m * ldq + c, b, q_vec);
+            if constexpr (sizeof(Code) == 1) {
+                store_bytes(q + m * ldq + c, b, q_vec);
+            } else if constexpr (VW > 1) {
+                float f[VW];
+#pragma unroll
+                for (int e = 0; e < VW; ++e) f[e] = (float)b[e];
+                if constexpr (VW == 8) {
+                    *reinterpret_cast<uint4 *>(q + m * ldq + c) = pack16<SGEMM_F16>(f);
+                } else {
+                    const __half2 lo = __floats2half2_rn(f[0], f[1]), hi = __floats2half2_rn(f[2], f[3]);
+                    *reinterpret_cast<uint2 *>(q + m * ldq + c) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                }
+            } else {
+                put_code(q + m * ldq + c, b[0]);
+            }
         }
     }
 }
 
-template <int DT>
+template <int DT, class Code>
 __global__ void __launch_bounds__(1024)
     quantize_i8_wide_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
-                            int8_t *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
+                            Code *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
     __shared__ float slots[64];
+    griddep_launch_dependents();
     RowReducer red{slots, (int)(blockDim.x >> 5)};
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
         uint32_t top = 0;
@@ -74,7 +95,8 @@ __global__ void __launch_bounds__(1024)
             top = max(top, __float_as_uint(Elem<DT>::to_float(x[m * ldx + c])) & 0x7fffffffu);
         const I8Scale s(red.max(top));
         if (threadIdx.x == 0) scale[m] = s.scale;
-        for (int c = threadIdx.x; c < K; c += blockDim.x) q[m * ldq + c] = s(Elem<DT>::to_float(x[m * ldx + c]));
+        for (int c = threadIdx.x; c < K; c += blockDim.x)
+            put_code(q + m * ldq + c, s(Elem<DT>::to_float(x[m * ldx + c])));
     }
 }
 

@@ -137,6 +137,7 @@ int sgemm_host::device(sgemm_host::Device &out) {
     return st;
 }
 unsigned long long sgemm_host::wait_limit_ns() { return g_wait_limit_ns.load(); }
+int sgemm_host::test_flags() { return g_debug_flags.load(); }
 
 namespace {
 
@@ -154,20 +155,33 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Row-major rows x cols FP32 matrix with leading dimension ld, read in boxes of
+// Row-major rows x cols matrix with leading dimension ld, read in boxes of
 // box_rows x box_cols; out-of-bounds elements read as zero.
-bool encode_2d(CUtensorMap *map, const float *ptr, int rows, int cols, int ld, int box_rows, int box_cols,
-               CUtensorMapSwizzle swizzle) {
+bool encode_rows(CUtensorMap *map, CUtensorMapDataType type, int size, const void *ptr, int64_t rows, int64_t cols,
+                 int64_t ld, int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * sizeof(float)};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t elem[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(ptr), dims, strides, box, elem,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, type, 2, const_cast<void *>(ptr), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+bool encode_2d(CUtensorMap *map, const float *ptr, int rows, int cols, int ld, int box_rows, int box_cols,
+               CUtensorMapSwizzle swizzle) {
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, rows, cols, ld, box_rows, box_cols, swizzle);
+}
+
+}  // namespace
+
+bool sgemm_host::encode_f16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, rows, cols, ld, box_rows, 64,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+namespace {
 
 // The four phase maps of a rows x cols operand (leading dimension ld, rows
 // >= 4, base 4-byte aligned): phase s holds rows s, s + 4, ..., 4 ld floats
