@@ -31,6 +31,10 @@ __attribute__((visibility("hidden"))) int device(Device &out);
 __attribute__((visibility("hidden"))) bool encode_f16(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols,
                                                       int64_t ld, int box_rows);
 
+// The same of 8-bit integers, in boxes of 128 or 64 columns into swizzled rows of as many bytes.
+__attribute__((visibility("hidden"))) bool encode_i8(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols,
+                                                     int64_t ld, int box_rows, int box_cols);
+
 // Nanoseconds a kernel may wait for its own copies before it gives up.
 __attribute__((visibility("hidden"))) unsigned long long wait_limit_ns();
 

@@ -7,9 +7,9 @@
 #include <cstdint>
 
 #include "host.h"
-#include "i8_decode.cuh"
 #include "i8_quantize.cuh"
-#include "i8_tcgen05.cuh"
+#include "i8_rows.cuh"
+#include "i8_stream.cuh"
 
 namespace {
 
@@ -57,136 +57,146 @@ int quantize(int M, int K, int dtype, const void *x, int ldx, Code *q, int64_t l
 // Rows of 8-bit integers that start on 16 bytes.
 bool rows16(const int8_t *p, int64_t ld) { return aligned(p, 16) && ld % 16 == 0; }
 
-// ---------------------------------------------------------------- few rows of A
-
-constexpr int kDecodeRows = 64;
-
-template <class T, bool EARLY, bool AA, bool AB>
-int launch_decode(const I8Args &p, const Device &dev, cudaStream_t stream) {
-    static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = i8_decode_kernel<T, AA, AB>;
-    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, T::THREADS, T::SMEM)) return SGEMM_ERR_LAUNCH;
-    const int tiles = (p.N + T::ROWS - 1) / T::ROWS;
-    // few rows of B: clusters of up to 8 blocks share k, while each keeps 512 of it
-    unsigned ranks = 1;
-    while (ranks < 8 && (int64_t)tiles * ranks < 2 * dev.sms && p.K / (int)(ranks * 2) >= 512) ranks *= 2;
-    return launch<EARLY>(kernel, dim3(tiles * ranks), dim3(T::THREADS), T::SMEM, stream, ranks, p, (int)ranks);
-}
-
-template <bool EARLY, bool AA, bool AB>
-int decode_by_rows(const I8Args &p, const Device &dev, cudaStream_t stream) {
-    if (p.M <= 8) return launch_decode<I8DecodeTile<1, 1, 8>, EARLY, AA, AB>(p, dev, stream);
-    if (p.M <= 16) return launch_decode<I8DecodeTile<1, 2, 4>, EARLY, AA, AB>(p, dev, stream);
-    if (p.M <= 32) return launch_decode<I8DecodeTile<2, 4, 2>, EARLY, AA, AB>(p, dev, stream);
-    return launch_decode<I8DecodeTile<2, 8, 2>, EARLY, AA, AB>(p, dev, stream);
-}
-
-// EARLY: A comes from the kernel launched just before, which B does not.
-template <bool EARLY>
-int decode(const I8Args &p, const Device &dev, cudaStream_t stream) {
-    const bool aa = EARLY || rows16(p.A, p.lda), ab = rows16(p.B, p.ldb);
-    if constexpr (!EARLY) {
-        if (!aa) return ab ? decode_by_rows<false, false, true>(p, dev, stream) : decode_by_rows<false, false, false>(p, dev, stream);
-    }
-    return ab ? decode_by_rows<EARLY, true, true>(p, dev, stream) : decode_by_rows<EARLY, true, false>(p, dev, stream);
-}
-
-// ---------------------------------------------------------------- many rows of A
-
+int64_t ld16(int K) { return ((int64_t)K + 15) / 16 * 16; }
 int64_t ld8(int K) { return ((int64_t)K + 7) / 8 * 8; }
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Tile width and k-splits of a product: the smallest estimate of rounds over
-// the SMs times the length of one, in cycles of the tensor cores.
-struct GemmPlan {
-    int bn = 256, splits = 1;
-    GemmPlan(int M, int N, int K, int sms) {
-        const int steps = (K + 63) / 64;
+// ---------------------------------------------------------------- up to four tokens
+
+// Whether the kernel that reads whole rows takes the product: its tokens' codes
+// have to fit shared memory beside three other blocks'.
+bool takes_rows(int M, int K) {
+    const int tokens = M <= 1 ? 1 : M <= 2 ? 2 : 4;
+    return M <= kRowsTokens && K > 0 && tokens * rows_pitch(K) <= 52 * 1024;
+}
+
+template <int MT, int XT, bool ALIGNED>
+int launch_rows(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = i8_rows_kernel<MT, XT, ALIGNED>;
+    const int smem = MT * rows_pitch(p.K);
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, kRowsThreads, smem);
+    if (!fit) return SGEMM_ERR_LAUNCH;
+    constexpr int warps = kRowsThreads / 32;
+    const int blocks = std::min((p.N + warps - 1) / warps, dev.sms * fit);
+    return launch(kernel, dim3(blocks), dim3(kRowsThreads), smem, stream, 1, p, X, ldx);
+}
+
+template <int XT>
+int rows_product(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    auto by_alignment = [&](auto mt) {
+        constexpr int MT = decltype(mt)::value;
+        return rows16(p.B, p.ldb) ? launch_rows<MT, XT, true>(p, X, ldx, dev, stream)
+                                  : launch_rows<MT, XT, false>(p, X, ldx, dev, stream);
+    };
+    if (p.M <= 1) return by_alignment(std::integral_constant<int, 1>{});
+    if (p.M <= 2) return by_alignment(std::integral_constant<int, 2>{});
+    return by_alignment(std::integral_constant<int, 4>{});
+}
+
+// ---------------------------------------------------------------- more tokens
+
+// EARLY: beside the kernel before, which neither reads nor writes these.
+template <bool EARLY, class Code>
+int lay_out(int rows, int K, const int8_t *q, int64_t ldq, Code *out, int64_t ld, const Device &dev, cudaStream_t stream) {
+    const int64_t pieces = (int64_t)rows * ((K + 15) / 16);
+    const dim3 grid((unsigned)std::min<int64_t>((pieces + 255) / 256, (int64_t)dev.sms * 8));
+    return rows16(q, ldq)
+               ? launch<EARLY>(i8_lay_out_kernel<true, Code>, grid, dim3(256), 0, stream, 1, rows, K, q, ldq, out, ld)
+               : launch<EARLY>(i8_lay_out_kernel<false, Code>, grid, dim3(256), 0, stream, 1, rows, K, q, ldq, out, ld);
+}
+
+int join(const I8Args &p, int splits, const float *partials, int64_t ldp, cudaStream_t stream) {
+    const dim3 grid((p.N + 4 * kJoinThreads - 1) / (4 * kJoinThreads), std::min(p.M, 65535));
+    return launch(i8_join_kernel, grid, dim3(kJoinThreads), 0, stream, 1, p, splits, partials, ldp);
+}
+
+// Tokens a tile, and k-splits: the smallest estimate, in cycles, of rounds over
+// the SMs times the length of one, from steps measured on GB300, and of adding
+// the splits' sums.  With few tokens, few tiles of B: the splits fill the SMs;
+// with some hundreds, narrower tiles of tokens do, at the price of converting
+// B again for each.
+struct StreamPlan {
+    int tok = 256, splits = 1;
+    StreamPlan() = default;
+    StreamPlan(int M, int N, int K, int sms) {
+        static constexpr struct {
+            int tok, bk;
+            double step;
+        } kSteps[] = {{16, 128, 760}, {32, 128, 770}, {64, 128, 850}, {128, 128, 1050}, {256, 64, 680}};
         double best = 1e300;
-        for (int width : {256, 128, 64}) {
-            const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + width - 1) / width);
-            const double step = width == 256 ? 560 : width == 128 ? 320 : 220;
+        for (const auto &c : kSteps) {
+            const int steps = (K + c.bk - 1) / c.bk;
+            const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + 127) / 128);
             for (int s = 1; s <= 16 && s <= (steps + 3) / 4; ++s) {
                 const int64_t rounds = (tiles * s + sms - 1) / sms;
-                double t = (double)rounds * (((steps + s - 1) / s) * step) + 1500 + width * 4;
-                if (s > 1) t += 4000 + (double)s * M * N * 8 / 3000;  // the slabs out and in again, and a launch
-                if (t < best) best = t, bn = width, splits = s;
+                double t = (double)rounds * (((steps + s - 1) / s) * c.step + 12 * c.tok) + 2000;
+                if (s > 1) t += 5000 + (double)s * M * N * 8 / 2500;
+                if (t < best) best = t, tok = c.tok, splits = s;
             }
+            if (M <= c.tok) break;
         }
     }
     int64_t ldp(int N) const { return ((int64_t)N + 3) / 4 * 4; }
     int64_t partial_bytes(int M, int N) const { return splits > 1 ? (int64_t)splits * M * ldp(N) * 4 : 0; }
 };
 
-template <int BN, int CT>
-int launch_gemm(const I8Args &p, const __half *a, const __half *b, const GemmPlan &plan, float *partials, int vec,
-                const Device &dev, cudaStream_t stream) {
-    using T = I8Tile<BN>;
+template <int TOK>
+int launch_stream(const I8Args &p, const __half *x, const StreamPlan &plan, float *partials, const Device &dev,
+                  cudaStream_t stream) {
+    using T = I8StreamTile<TOK>;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = i8_tcgen05_kernel<BN, CT>;
+    const auto kernel = i8_stream_kernel<TOK>;
     if (!sgemm_host::blocks_per_sm(regs, dev, kernel, T::THREADS, T::SMEM_BYTES)) return SGEMM_ERR_LAUNCH;
-    CUtensorMap ta, tb;
-    if (!sgemm_host::encode_f16(&ta, a, p.M, p.K, ld8(p.K), T::BM) ||
-        !sgemm_host::encode_f16(&tb, b, p.N, p.K, ld8(p.K), BN))
+    CUtensorMap tw, tx;
+    if (!sgemm_host::encode_i8(&tw, p.B, p.N, p.K, p.ldb, T::ROWS, T::BK) ||
+        !sgemm_host::encode_f16(&tx, x, p.M, p.K, ld8(p.K), TOK))
         return SGEMM_ERR_LAUNCH;
-    const int64_t units = (int64_t)((p.M + T::BM - 1) / T::BM) * ((p.N + BN - 1) / BN) * plan.splits;
+    const int64_t units = (int64_t)((p.M + TOK - 1) / TOK) * ((p.N + 127) / 128) * plan.splits;
     return launch<true>(kernel, dim3((unsigned)std::min<int64_t>(units, dev.sms)), dim3(T::THREADS), T::SMEM_BYTES,
-                        stream, 1, ta, tb, p, plan.splits, partials, plan.ldp(p.N), vec, dev.err_word,
+                        stream, 1, tw, tx, p, plan.splits, partials, plan.ldp(p.N), dev.err_word,
                         sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
 }
 
-template <int CT>
-int gemm_by_width(const I8Args &p, const __half *a, const __half *b, const GemmPlan &plan, float *partials, int vec,
-                  const Device &dev, cudaStream_t stream) {
-    switch (plan.bn) {
-        case 64: return launch_gemm<64, CT>(p, a, b, plan, partials, vec, dev, stream);
-        case 128: return launch_gemm<128, CT>(p, a, b, plan, partials, vec, dev, stream);
-        default: return launch_gemm<256, CT>(p, a, b, plan, partials, vec, dev, stream);
+// The product of FP16 codes x (M x K, on rows of ld8(K)) with the rows of p.B,
+// which are first laid out in `rows` where TMA could not read them.
+int stream_product(I8Args p, const __half *x, int8_t *rows, float *partials, const StreamPlan &plan, const Device &dev,
+                   cudaStream_t stream) {
+    int st = SGEMM_OK;
+    if (!rows16(p.B, p.ldb)) {
+        st = lay_out<true>(p.N, p.K, p.B, p.ldb, rows, ld16(p.K), dev, stream);
+        if (st != SGEMM_OK) return st;
+        p.B = rows;
+        p.ldb = ld16(p.K);
     }
-}
-
-// EARLY: beside the kernel before, which neither reads nor writes these.
-template <bool EARLY>
-int expand(int rows, int K, const int8_t *q, int64_t ldq, __half *h, const Device &dev, cudaStream_t stream) {
-    const int64_t pieces = (int64_t)rows * ((K + 15) / 16);
-    const dim3 grid((unsigned)std::min<int64_t>((pieces + 255) / 256, (int64_t)dev.sms * 8));
-    return rows16(q, ldq) ? launch<EARLY>(i8_expand_kernel<true>, grid, dim3(256), 0, stream, 1, rows, K, q, ldq, h, ld8(K))
-                          : launch<EARLY>(i8_expand_kernel<false>, grid, dim3(256), 0, stream, 1, rows, K, q, ldq, h, ld8(K));
-}
-
-int join(const I8Args &p, int splits, const float *partials, int64_t ldp, const Device &dev, cudaStream_t stream) {
-    const int64_t blocks = std::min<int64_t>(((int64_t)p.M * p.N + 255) / 256, (int64_t)dev.sms * 8);
-    return launch(i8_join_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, 1, p, splits, partials, ldp);
-}
-
-// The product of FP16 codes a (M x K) with the rows of p.B, which are expanded
-// into b first; both on rows of ld8(K).
-int gemm(const I8Args &p, const __half *a, __half *b, float *partials, const GemmPlan &plan, const Device &dev,
-         cudaStream_t stream) {
-    int st = expand<true>(p.N, p.K, p.B, p.ldb, b, dev, stream);
-    if (st != SGEMM_OK) return st;
-    if (plan.splits > 1) {
-        st = gemm_by_width<SGEMM_F32>(p, a, b, plan, partials, 1, dev, stream);
-        return st == SGEMM_OK ? join(p, plan.splits, partials, plan.ldp(p.N), dev, stream) : st;
+    switch (plan.tok) {
+        case 16: st = launch_stream<16>(p, x, plan, partials, dev, stream); break;
+        case 32: st = launch_stream<32>(p, x, plan, partials, dev, stream); break;
+        case 64: st = launch_stream<64>(p, x, plan, partials, dev, stream); break;
+        case 128: st = launch_stream<128>(p, x, plan, partials, dev, stream); break;
+        default: st = launch_stream<256>(p, x, plan, partials, dev, stream);
     }
-    const int vec = aligned(p.C, 16) && p.ldc * dtype_size(p.ctype) % 16 == 0;
-    return by_dtype(p.ctype, [&](auto ct) {
-        return gemm_by_width<decltype(ct)::value>(p, a, b, plan, nullptr, vec, dev, stream);
-    });
+    if (st != SGEMM_OK || plan.splits == 1) return st;
+    return join(p, plan.splits, partials, plan.ldp(p.N), stream);
 }
 
-// Bytes of the FP16 operands and of the k-splits' partial sums.
-int64_t gemm_workspace(int M, int N, int K, int sms) {
-    return up256(2 * M * ld8(K)) + up256(2 * N * ld8(K)) + GemmPlan(M, N, K, sms).partial_bytes(M, N);
-}
+// The workspace of a product: the tokens' scales, their codes as FP16, the rows
+// of B where they have to be laid out, and the k-splits' partial sums.
+struct Workspace {
+    int64_t codes, rows, partials, bytes;
+    Workspace(int M, int N, int K, bool lay_out_rows, const StreamPlan &plan) {
+        codes = up256(4 * (int64_t)M);
+        rows = codes + up256(2 * M * ld8(K));
+        partials = rows + (lay_out_rows ? up256(N * ld16(K)) : 0);
+        bytes = partials + plan.partial_bytes(M, N);
+    }
+};
 
 int device_sms() {
     Device dev;
     return sgemm_host::device(dev) == SGEMM_OK ? dev.sms : 0;
 }
 
-// Rows of the quantised activations in sgemm_linear_i8's workspace.
-int64_t ld16(int K) { return ((int64_t)K + 15) / 16 * 16; }
 
 bool output_ok(int M, int N, int K, const signed char *B, int ldb, const float *b_scale, const float *bias,
                const void *C, int ldc, int ctype) {
@@ -195,6 +205,23 @@ bool output_ok(int M, int N, int K, const signed char *B, int ldb, const float *
     if (M == 0 || N == 0) return true;
     if ((K > 0 && !B) || !b_scale || !C || !aligned(b_scale, 4) || !aligned(bias, 4)) return false;
     return aligned(C, (unsigned)dtype_size(ctype));
+}
+
+// The output and the workspace against the inputs and each other.  `least` is
+// what the workspace has to hold whatever the device; `need` its size, asked
+// for last because it queries the device.
+template <class Need>
+int check_buffers(const Range *in, int n, const Range &c, void *workspace, size_t bytes, size_t least, Need need) {
+    for (int i = 0; i < n; ++i)
+        if (c.overlaps(in[i])) return SGEMM_ERR_ALIAS;
+    const Range ws(bytes ? workspace : nullptr, 1, (int64_t)bytes, (int64_t)bytes, 1);
+    if (ws.overlaps(c)) return SGEMM_ERR_ALIAS;
+    for (int i = 0; i < n; ++i)
+        if (ws.overlaps(in[i])) return SGEMM_ERR_ALIAS;
+    if (!aligned(workspace, 16)) return SGEMM_ERR_INVALID_ARG;
+    if (least && (!workspace || bytes < least)) return SGEMM_ERR_INVALID_ARG;
+    least = need();
+    return least && (!workspace || bytes < least) ? SGEMM_ERR_INVALID_ARG : SGEMM_OK;
 }
 
 }  // namespace
@@ -211,13 +238,22 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx, signed ch
     if (out.overlaps(in) || scale.overlaps(in) || scale.overlaps(out)) return SGEMM_ERR_ALIAS;
     Device dev;
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
-    return quantize(M, K, dtype, x, ldx, q, ldq, s, dev, stream);
+    return quantize(M, K, dtype, x, ldx, reinterpret_cast<int8_t *>(q), ldq, s, dev, stream);
 }
 
-size_t sgemm_i8_workspace_size(int M, int N, int K) {
-    if (M <= kDecodeRows || N <= 0 || K <= 0) return 0;
+// Bytes of a workspace without k-splits, which depend on the device.
+static size_t least_workspace(int M, int N, int K, const signed char *B, int ldb) {
+    if (M <= 0 || N <= 0 || K < 0 || takes_rows(M, K)) return 0;
+    return (size_t)Workspace(M, N, K, !rows16(reinterpret_cast<const int8_t *>(B), ldb), StreamPlan()).bytes;
+}
+
+// One workspace serves both entry points: with 8-bit tokens the place of their
+// scales stays unused.
+size_t sgemm_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb) {
+    if (M <= 0 || N <= 0 || K < 0) return 0;
     const int sms = device_sms();
-    return sms ? (size_t)gemm_workspace(M, N, K, sms) : 0;
+    if (!sms || takes_rows(M, K)) return 0;
+    return (size_t)Workspace(M, N, K, !rows16(reinterpret_cast<const int8_t *>(B), ldb), StreamPlan(M, N, K, sms)).bytes;
 }
 
 int sgemm_i8(int M, int N, int K, const signed char *A, int lda, const float *a_scale, const signed char *B, int ldb,
@@ -226,31 +262,30 @@ int sgemm_i8(int M, int N, int K, const signed char *A, int lda, const float *a_
     if (!output_ok(M, N, K, B, ldb, b_scale, bias, C, ldc, ctype) || lda < std::max(K, 1)) return SGEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return SGEMM_OK;
     if ((K > 0 && !A) || !a_scale || !aligned(a_scale, 4)) return SGEMM_ERR_INVALID_ARG;
-    const size_t need = sgemm_i8_workspace_size(M, N, K);
-    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return SGEMM_ERR_INVALID_ARG;
     const Range in[5] = {Range(A, M, K, lda, 1), Range(a_scale, 1, M, M, 4), Range(B, N, K, ldb, 1),
                          Range(b_scale, 1, N, N, 4), Range(bias, 1, N, N, 4)};
-    const Range c(C, M, N, ldc, dtype_size(ctype)), ws(need ? workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
-    for (const Range &i : in)
-        if (c.overlaps(i) || ws.overlaps(i)) return SGEMM_ERR_ALIAS;
-    if (ws.overlaps(c)) return SGEMM_ERR_ALIAS;
+    int st = check_buffers(in, 5, Range(C, M, N, ldc, dtype_size(ctype)), workspace, workspace_bytes,
+                           least_workspace(M, N, K, B, ldb), [&] { return sgemm_i8_workspace_size(M, N, K, B, ldb); });
+    if (st != SGEMM_OK) return st;
     Device dev;
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
-    const I8Args p{M, N, K, A, B, lda, ldb, a_scale, b_scale, bias, C, ldc, ctype};
-    if (K == 0) return join(p, 0, nullptr, 0, dev, stream);
-    if (M <= kDecodeRows) return decode<false>(p, dev, stream);
-    __half *a = static_cast<__half *>(workspace), *b = a + up256(2 * M * ld8(K)) / 2;
-    float *partials = reinterpret_cast<float *>(b + up256(2 * N * ld8(K)) / 2);
-    const int st = expand<false>(M, K, A, lda, a, dev, stream);
-    return st == SGEMM_OK ? gemm(p, a, b, partials, GemmPlan(M, N, K, dev.sms), dev, stream) : st;
+    const I8Args p{M, N, K, reinterpret_cast<const int8_t *>(A), reinterpret_cast<const int8_t *>(B), lda, ldb, a_scale,
+                   b_scale, bias, C, ldc, ctype};
+    if (K == 0) return join(p, 0, nullptr, 0, stream);
+    if (takes_rows(M, K)) return rows_product<-1>(p, nullptr, 0, dev, stream);
+    const StreamPlan plan(M, N, K, dev.sms);
+    const Workspace at(M, N, K, !rows16(p.B, ldb), plan);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    __half *codes = reinterpret_cast<__half *>(ws + at.codes);
+    st = lay_out<false>(M, K, p.A, lda, codes, ld8(K), dev, stream);
+    if (st != SGEMM_OK) return st;
+    return stream_product(p, codes, reinterpret_cast<int8_t *>(ws + at.rows), reinterpret_cast<float *>(ws + at.partials),
+                          plan, dev, stream);
 }
 
-size_t sgemm_linear_i8_workspace_size(int M, int N, int K) {
-    if (M <= 0 || N <= 0 || K < 0) return 0;
-    const int64_t scales = up256(4 * (int64_t)M);
-    if (M <= kDecodeRows || K == 0) return (size_t)(scales + M * ld16(K));
-    const int sms = device_sms();
-    return sms ? (size_t)(scales + gemm_workspace(M, N, K, sms)) : 0;
+size_t sgemm_linear_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb) {
+    // K = 0 quantises rows of nothing, for their scales
+    return K == 0 && M > 0 && N > 0 ? (size_t)up256(4 * (int64_t)M) : sgemm_i8_workspace_size(M, N, K, B, ldb);
 }
 
 int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx, const signed char *B, int ldb,
@@ -261,31 +296,26 @@ int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx, cons
     if (M == 0 || N == 0) return SGEMM_OK;
     const int size = dtype_size(xtype);
     if (K > 0 && (!X || !aligned(X, (unsigned)size))) return SGEMM_ERR_INVALID_ARG;
-    const size_t need = sgemm_linear_i8_workspace_size(M, N, K);
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return SGEMM_ERR_INVALID_ARG;
     const Range in[4] = {Range(X, M, K, ldx, size), Range(B, N, K, ldb, 1), Range(b_scale, 1, N, N, 4),
                          Range(bias, 1, N, N, 4)};
-    const Range c(C, M, N, ldc, dtype_size(ctype)), ws(workspace, 1, (int64_t)need, (int64_t)need, 1);
-    for (const Range &i : in)
-        if (c.overlaps(i) || ws.overlaps(i)) return SGEMM_ERR_ALIAS;
-    if (ws.overlaps(c)) return SGEMM_ERR_ALIAS;
+    int st = check_buffers(in, 4, Range(C, M, N, ldc, dtype_size(ctype)), workspace, workspace_bytes,
+                           least_workspace(M, N, K, B, ldb), [&] { return sgemm_linear_i8_workspace_size(M, N, K, B, ldb); });
+    if (st != SGEMM_OK) return st;
     Device dev;
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
-    float *s = static_cast<float *>(workspace);
-    unsigned char *rest = static_cast<unsigned char *>(workspace) + up256(4 * (int64_t)M);
-    I8Args p{M, N, K, nullptr, B, 0, ldb, s, b_scale, bias, C, ldc, ctype};
-    if (M <= kDecodeRows || K == 0) {
-        int8_t *q = reinterpret_cast<int8_t *>(rest);
-        const int st = quantize(M, K, xtype, X, ldx, q, ld16(K), s, dev, stream);
-        if (st != SGEMM_OK) return st;
-        p.A = q;
-        p.lda = ld16(K);
-        return K == 0 ? join(p, 0, nullptr, 0, dev, stream) : decode<true>(p, dev, stream);
-    }
-    __half *a = reinterpret_cast<__half *>(rest), *b = a + up256(2 * M * ld8(K)) / 2;
-    float *partials = reinterpret_cast<float *>(b + up256(2 * N * ld8(K)) / 2);
-    const int st = quantize(M, K, xtype, X, ldx, a, ld8(K), s, dev, stream);
-    return st == SGEMM_OK ? gemm(p, a, b, partials, GemmPlan(M, N, K, dev.sms), dev, stream) : st;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    float *s = reinterpret_cast<float *>(ws);
+    const I8Args p{M, N, K, nullptr, reinterpret_cast<const int8_t *>(B), 0, ldb, s, b_scale, bias, C, ldc, ctype};
+    if (takes_rows(M, K))
+        return by_dtype(xtype, [&](auto xt) { return rows_product<decltype(xt)::value>(p, X, ldx, dev, stream); });
+    const StreamPlan plan(M, N, K, dev.sms);
+    const Workspace at(M, N, K, !rows16(p.B, ldb), plan);
+    __half *codes = reinterpret_cast<__half *>(ws + at.codes);
+    st = quantize(M, K, xtype, X, ldx, codes, ld8(K), s, dev, stream);
+    if (st != SGEMM_OK) return st;
+    if (K == 0) return join(p, 0, nullptr, 0, stream);
+    return stream_product(p, codes, reinterpret_cast<int8_t *>(ws + at.rows), reinterpret_cast<float *>(ws + at.partials),
+                          plan, dev, stream);
 }
 
 }  // extern "C"

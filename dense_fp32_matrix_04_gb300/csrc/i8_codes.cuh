@@ -24,29 +24,33 @@ __device__ __forceinline__ uint2 i8x4_to_f16(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// 16 bytes from byte `shift` (0 .. 15) of the 32 in a and b: by two words, by
+// one word, by bytes.
+__device__ __forceinline__ uint4 shift_codes(const uint4 &a, const uint4 &b, unsigned shift) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+    const unsigned bits = 8 * (shift & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // Bytes k .. k + 15 of a row of K 8-bit integers, of any alignment; bytes from K
 // on are unspecified, and nothing beyond the 16-byte granule of the row's last
-// byte is read.  ALIGNED: the row starts on 16 bytes and k is a multiple of 16.
+// byte is read.  ALIGNED: the row starts on 16 bytes; k is a multiple of 16.
 template <bool ALIGNED>
 __device__ __forceinline__ uint4 load_codes(const int8_t *row, int k, int K) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if constexpr (ALIGNED) {
         return k < K ? __ldg(reinterpret_cast<const uint4 *>(row + k)) : zero;
     } else {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(row) + k, lo = at & ~(uintptr_t)15;
-        const uintptr_t last = reinterpret_cast<uintptr_t>(row) + K - 1;
-        const unsigned shift = (unsigned)(at & 15);
+        const uintptr_t lo = (reinterpret_cast<uintptr_t>(row) + k) & ~(uintptr_t)15;
         const uint4 a = k < K ? __ldg(reinterpret_cast<const uint4 *>(lo)) : zero;
-        const uint4 b = shift && lo + 16 <= last ? __ldg(reinterpret_cast<const uint4 *>(lo + 16)) : zero;
-        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        // the 16 bytes from byte `shift` on: by two words, by one word, by bytes
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
-        const unsigned bits = 8 * (shift & 3);
-        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+        const uint4 b = k < K && lo + 16 < reinterpret_cast<uintptr_t>(row) + K
+                            ? __ldg(reinterpret_cast<const uint4 *>(lo + 16)) : zero;
+        return shift_codes(a, b, (unsigned)(reinterpret_cast<uintptr_t>(row) & 15));
     }
 }
 
@@ -66,12 +70,12 @@ __device__ __forceinline__ void store_c(void *C, int64_t at, int ctype, float v)
     else static_cast<__half *>(C)[at] = __float2half_rn(v);
 }
 
-// Rows of 8-bit integers written out as FP16, 16 at a time; ldh is a multiple
-// of 8 and h is 16-byte aligned.  Elements between K and ldh are not read by
-// what follows.
-template <bool ALIGNED>
+// Rows of 8-bit integers written out on padded, 16-byte aligned rows: as FP16
+// (Code __half, ld a multiple of 8) or as they are (int8_t, ld a multiple of
+// 16).  Elements between K and ld are not read by what follows.
+template <bool ALIGNED, class Code>
 __global__ void __launch_bounds__(256)
-    i8_expand_kernel(int rows, int K, const int8_t *__restrict__ q, int64_t ldq, __half *__restrict__ h, int64_t ldh) {
+    i8_lay_out_kernel(int rows, int K, const int8_t *__restrict__ q, int64_t ldq, Code *__restrict__ out, int64_t ld) {
     griddep_launch_dependents();
     const int pieces = (K + 15) / 16;
     const int64_t total = (int64_t)rows * pieces;
@@ -79,10 +83,14 @@ __global__ void __launch_bounds__(256)
         const int64_t row = i / pieces;
         const int k = (int)(i - row * pieces) * 16;
         const uint4 c = load_codes<ALIGNED>(q + row * ldq, k, K);
-        __half *to = h + row * ldh + k;
-        const uint2 a = i8x4_to_f16(c.x), b = i8x4_to_f16(c.y), d = i8x4_to_f16(c.z), e = i8x4_to_f16(c.w);
-        *reinterpret_cast<uint4 *>(to) = make_uint4(a.x, a.y, b.x, b.y);
-        if (k + 8 < ldh) *reinterpret_cast<uint4 *>(to + 8) = make_uint4(d.x, d.y, e.x, e.y);
+        Code *to = out + row * ld + k;
+        if constexpr (sizeof(Code) == 1) {
+            *reinterpret_cast<uint4 *>(to) = c;
+        } else {
+            const uint2 a = i8x4_to_f16(c.x), b = i8x4_to_f16(c.y), d = i8x4_to_f16(c.z), e = i8x4_to_f16(c.w);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(a.x, a.y, b.x, b.y);
+            if (k + 8 < ld) *reinterpret_cast<uint4 *>(to + 8) = make_uint4(d.x, d.y, e.x, e.y);
+        }
     }
     // this kernel may run beside the one before, which the next one needs as well
     griddep_wait();

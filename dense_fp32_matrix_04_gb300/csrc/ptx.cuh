@@ -172,6 +172,32 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     return false;
 }
 
+// The same for one thread that polls while others of its SM work: it sleeps
+// `sleep_ns` (0: not at all) between probes, because spinning takes issue slots
+// and shared-memory cycles from them, and reads the timer, which costs hundreds
+// of cycles, only every 64 probes.
+__device__ __forceinline__ bool mbar_wait_polite(uint32_t bar, uint32_t parity, uint64_t limit_ns, uint32_t sleep_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t probe = 1; probe < (1u << 30); ++probe) {
+        if (sleep_ns) asm volatile("nanosleep.u32 %0;\n" ::"r"(sleep_ns));
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((probe & 63u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > limit_ns) return false;
+        }
+    }
+    return false;
+}
+
+// The same for a whole warp, of which one lane polls.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns, uint32_t sleep_ns) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_polite(bar, parity, limit_ns, sleep_ns);
+    return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+
 // 2-D tiled TMA load of the box at (x, y) (x innermost) into shared memory,
 // completing `bytes` of transaction count on the mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void *tensor_map, int x, int y, uint32_t bar) {

@@ -181,6 +181,12 @@ bool sgemm_host::encode_f16(CUtensorMap *map, const void *ptr, int64_t rows, int
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool sgemm_host::encode_i8(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                           int box_cols) {
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, rows, cols, ld, box_rows, box_cols,
+                       box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 namespace {
 
 // The four phase maps of a rows x cols operand (leading dimension ld, rows

@@ -23,9 +23,9 @@ SIGNATURES = {
     "sgemm_block_norm_backward_workspace_size": (_S, [_I, _I]),
     "sgemm_quantize_i8": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P]),
     "sgemm_i8": (_I, [_I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, _I, _I, _P, _S, _P]),
-    "sgemm_i8_workspace_size": (_S, [_I, _I, _I]),
+    "sgemm_i8_workspace_size": (_S, [_I, _I, _I, _P, _I]),
     "sgemm_linear_i8": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _P, _S, _P]),
-    "sgemm_linear_i8_workspace_size": (_S, [_I, _I, _I]),
+    "sgemm_linear_i8_workspace_size": (_S, [_I, _I, _I, _P, _I]),
     "sgemm_logprobs": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
     "sgemm_logprobs_backward": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
 }
@@ -239,7 +239,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, works
         code = _dtype(out, "out")
         po, ldo = _matrix(out, "out", out_dtype or out.dtype, M, N, dev)
         lib = _library()
-        need = lib.sgemm_i8_workspace_size(M, N, K)
+        need = lib.sgemm_i8_workspace_size(M, N, K, pw, ldw)
         if workspace is None and need:
             workspace = c.empty((need,), torch.uint8)
         size = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -267,12 +267,12 @@ def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None
         code = _dtype(out, "out")
         po, ldo = _matrix(out, "out", out_dtype or out.dtype, M, N, dev)
         lib = _library()
-        need = lib.sgemm_linear_i8_workspace_size(M, N, K)
-        if workspace is None:
+        need = lib.sgemm_linear_i8_workspace_size(M, N, K, pw, ldw)
+        if workspace is None and need:
             workspace = c.empty((need,), torch.uint8)
-        size = workspace.numel() * workspace.element_size()
-        _check(lib.sgemm_linear_i8(M, N, K, xcode, px, ldx, pw, ldw, pt, pb, po, ldo, code, workspace.data_ptr(), size,
-                                   c.handle), "sgemm_linear_i8")
+        size = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(lib.sgemm_linear_i8(M, N, K, xcode, px, ldx, pw, ldw, pt, pb, po, ldo, code,
+                                   workspace.data_ptr() if size else 0, size, c.handle), "sgemm_linear_i8")
     return out
 
 

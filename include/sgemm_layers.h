@@ -121,7 +121,7 @@ int sgemm_i8(int M, int N, int K,
              const float *bias, void *C, int ldc, int ctype,
              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
-size_t sgemm_i8_workspace_size(int M, int N, int K);
+size_t sgemm_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb);
 
 /*
  * The linear layer with 8-bit weights on activations that are not quantised
@@ -132,7 +132,7 @@ int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx,
                     const float *bias, void *C, int ldc, int ctype,
                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
-size_t sgemm_linear_i8_workspace_size(int M, int N, int K);
+size_t sgemm_linear_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb);
 
 /*
  * For each of T rows of V logits z, the distribution p = softmax(scale * z)

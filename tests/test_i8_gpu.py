@@ -208,4 +208,34 @@ def test_python_refusals(sg):
     with pytest.raises(TypeError):
         sg.linear_i8(a, b, sb)
     with pytest.raises(sg.SgemmError):
-        sg.linear_i8(torch.randn(4, 64, device="cuda"), b, sb, workspace=torch.empty(16, device="cuda"))
+        sg.linear_i8(torch.randn(40, 64, device="cuda"), b, sb, workspace=torch.empty(16, device="cuda"))
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 4096, 512), (40, 130, 8192), (300, 520, 4096)])
+def test_a_wait_that_runs_out_is_reported(sg, M, N, K):
+    import torch
+    a, b, sa, sb, _ = operands(M, N, K, 12)
+    want = sg.matmul_i8(a, sa, b, sb)
+    out = torch.full((M, N), 3.0, device="cuda")
+    sg.sgemm_test_switches(1, 50_000_000)     # no copies: every wait runs out after 50 ms
+    try:
+        sg.matmul_i8(a, sa, b, sb, out=out)
+        assert sg.sgemm_device_status() == sg.SGEMM_ERR_TIMEOUT
+    finally:
+        sg.sgemm_test_switches(0)
+    # nothing was stored, or (with the sums over k divided) NaN
+    assert bool(((out == 3.0) | torch.isnan(out)).all())
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+    assert bool((sg.matmul_i8(a, sa, b, sb) == want).all())
+
+
+@pytest.mark.parametrize("M", [5, 24, 100, 200])
+def test_many_steps_wrap_the_rings(sg, M):
+    # every tile of B on one SM over a long k: each ring of stages is walked many times
+    N, K = 4096, 16384
+    a, b, sa, sb, bias = operands(M, N, K, M)
+    got = sg.matmul_i8(a, sa, b, sb, bias)
+    rows = slice(0, 3)
+    check(got[rows], a[rows], b, sa[rows], sb, bias, "f32")
+    again = sg.matmul_i8(a, sa, b, sb, bias)
+    assert bool((got == again).all())

@@ -95,7 +95,7 @@ def test_i8_refuses(lib, change, want):
 
 
 def test_linear_i8_refuses(lib):
-    def call(M=4, N=8, K=64, xtype=BF16, X=P[0], ldx=64, B=P[2], ldb=64, s=P[3], bias=0, C=P[5], ldc=8, ctype=BF16,
+    def call(M=40, N=8, K=64, xtype=BF16, X=P[0], ldx=64, B=P[2], ldb=64, s=P[3], bias=0, C=P[5], ldc=8, ctype=BF16,
              ws=P[6], size=1 << 30):
         return lib.sgemm_linear_i8(M, N, K, xtype, X, ldx, B, ldb, s, bias, C, ldc, ctype, ws, size, None)
     for change in [dict(M=-1), dict(xtype=3), dict(X=0), dict(ldx=63), dict(X=P[0] + 1), dict(ws=0), dict(size=16),
