@@ -124,6 +124,29 @@ struct RowLayout {
                 if (i * threads + tx < D) row[i * threads + tx] = Elem<DT>::from_float(v[i]);
         }
     }
+    // the same, two elements to a register pair
+    __device__ static void read(const uint4 *slot, const type *row, int D, int threads, int tx, F2 *out) {
+        float v[N];
+        read(slot, row, D, threads, tx, v);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) out[i] = F2(v[2 * i], v[2 * i + 1]);
+    }
+    __device__ static void store(type *row, int D, int threads, int tx, const F2 *v) {
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 b = v[i].both();
+            f[2 * i] = b.x;
+            f[2 * i + 1] = b.y;
+        }
+        store(row, D, threads, tx, f);
+    }
+    __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, F2 *out) {
+        float v[N];
+        weights(w, w_f32, c0, D, threads, tx, v);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) out[i] = F2(v[2 * i], v[2 * i + 1]);
+    }
     // 0 past the row's end; ALIGNED weights start on 16 bytes
     __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, float *out) {
         if constexpr (ALIGNED) {
@@ -153,7 +176,8 @@ struct RowLayout {
 };
 
 // Rows a thread keeps on their way (and the one it works on).
-constexpr int kNormStages = 3;
+constexpr int kNormStages = 4;
+constexpr int kNormGradStages = 3;
 
 // Copies of the inputs of one row, by the threads that share it.
 __host__ __device__ constexpr int row_pieces(int D, int size) { return (D * size + 15) / 16 + 1; }
@@ -173,7 +197,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormA
     using type = typename L::type;
     constexpr int N = L::N, S = kNormStages;
     extern __shared__ uint4 ring[];
-    __shared__ float slots[64];
+    __shared__ float slots[RowReducer::SLOTS];
     RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
     const int threads = blockDim.x, tx = threadIdx.x;
     const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
@@ -191,7 +215,7 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormA
     const int64_t step = (int64_t)(gridDim.x / (unsigned)a.ranks) * blockDim.y;
     auto x_row = [&](int64_t t) { return static_cast<const type *>(a.x) + t * a.ldx + c0; };
     auto y_row = [&](int64_t t) { return static_cast<const type *>(a.y) + t * a.ldy + c0; };
-    auto g_row = [&](int64_t t) { return static_cast<const type *>(a.gate) + (t / a.gate_period) * a.ldg + c0; };
+    auto g_row = [&](int64_t t) { return static_cast<const type *>(a.gate) + (int64_t)((unsigned)t / (unsigned)a.gate_period) * a.ldg + c0; };
     auto fetch = [&](int64_t t, int stage) {
         if (t < a.T) {
             uint4 *slot = mine + stage * arrays * pieces;
@@ -290,25 +314,36 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormA
 
 // ---------------------------------------------------------------- gradient
 
-// Runner b (a block, or a warp of one) takes the rows [first_row(b),
-// first_row(b + 1)): consecutive rows, so that a gate row's sum stays in
-// registers until the row changes.
-__device__ __forceinline__ int first_row(int b, int T, int runners) { return (int)((int64_t)b * T / runners); }
+// Runner b (a block, or a warp of one) takes consecutive rows, so that a gate
+// row's sum stays in registers until the row changes: T / runners of them, and
+// the first T % runners runners one more.  No division of 64 bits is on the way
+// of a row (each cost about 100 instructions).
+struct RowRuns {
+    int each, more;
+    __device__ RowRuns(int T, int runners) : each(T / runners), more(T % runners) {}
+    __device__ int first(int b) const { return b * each + min(b, more); }
+    __device__ int runner_of(int t) const {
+        const int wide = more * (each + 1);
+        return t < wide ? t / (each + 1) : more + (t - wide) / each;
+    }
+};
 
 // The gradient of a row needs, with u = dn w_pre and v = dh w_post,
 //     dx = dr + rho2 (u - r rho2^2 mean(u r)),   dh = a g dx,
 //     dy = rho (v - y rho^2 mean(v y)),
-// so two sums over the row, one after the other; rho and rho2 come from the
-// forward pass.  Sums over rows (weights and gate) are kept in registers, and
+// with rho and rho2 from the forward pass.  The second mean need not wait for
+// the first: with P = a g w_post rho y,
+//     sum(v rho y) = sum(P (dr + rho2 u)) - rho2^3 mean(u r) sum(P r),
+// so three sums are taken at once, and a row costs one barrier.  Sums over rows (weights and gate) are kept in registers, and
 // written per runner to `partial`: a second kernel adds the runners in order.
 template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) block_norm_grad_kernel(const BlockNormGradArgs a) {
     using L = RowLayout<DT, ALIGNED, NV>;
     using E = Elem<DT>;
     using type = typename L::type;
-    constexpr int N = L::N, S = kNormStages;
+    constexpr int H = L::N / 2, S = kNormGradStages;  // pairs of elements a thread
     extern __shared__ uint4 ring[];
-    __shared__ float slots[64];
+    __shared__ float slots[RowReducer::SLOTS];
     RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
     const int threads = blockDim.x, tx = threadIdx.x;
     const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
@@ -316,29 +351,35 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_grad_kernel(const Block
     const float inv_d = 1.f / (float)a.D;
     const int runner = group_id * blockDim.y + threadIdx.y;
     if (runner >= a.runners) return;  // only where a warp is a runner: no barrier spans warps
-    const int begin = first_row(runner, a.T, a.runners), end = first_row(runner + 1, a.T, a.runners);
+    const RowRuns runs(a.T, a.runners);
+    const int begin = runs.first(runner), end = runs.first(runner + 1);
     const bool token_gate = a.gate_period == 1;
     const int pieces = row_pieces(a.width, sizeof(type));
     const int g_at = 3 * pieces, dr_at = (token_gate ? 4 : 3) * pieces;
     const int stride = dr_at + (a.dr ? pieces : 0);
     uint4 *mine = ring + threadIdx.y * S * stride;
 
-    // registers hold the row and the sums; what else of a row is needed twice is read again (from
-    // L1 or the ring) where a thread has 16 elements, and w_pre always
-    constexpr bool KEEP = N <= 8;
-    float w_pre[N], w_post[N], dw_pre[N], dw_post[N], dgate[N];
-    auto load_post = [&] {
-        if (a.w_post) {
-            L::weights(a.w_post, a.w_f32, c0, D, threads, tx, w_post);
-        } else {
+    // registers hold the row, the sums and w_post; w_pre is read again for each row (from L1)
+    F2 w_pre[H], w_post[H], dw_pre[H], dw_post[H], dgate[H];
+    if (a.w_post) {
+        L::weights(a.w_post, a.w_f32, c0, D, threads, tx, w_post);
+    } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) w_post[i] = 1.f;
+        for (int i = 0; i < H; ++i) w_post[i] = F2(1.f);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) dw_pre[i] = dw_post[i] = dgate[i] = F2(0.f);
+    float *partial = a.partial + (int64_t)runner * 4 * a.D + c0;  // four sums of a.D columns
+
+    auto put = [&](float *to, const F2 *v) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const float2 f = v[i].both();
+            const int c = L::col(2 * i, threads, tx), c1 = L::col(2 * i + 1, threads, tx);
+            if (c < D) to[c] = f.x;
+            if (c1 < D) to[c1] = f.y;
         }
     };
-    if (KEEP) load_post();
-#pragma unroll
-    for (int i = 0; i < N; ++i) dw_pre[i] = dw_post[i] = dgate[i] = 0.f;
-    float *partial = a.partial + (int64_t)runner * 4 * a.D + c0;  // four sums of a.D columns
 
     auto x_row = [&](int64_t t) { return static_cast<const type *>(a.x) + t * a.ldx + c0; };
     auto y_row = [&](int64_t t) { return static_cast<const type *>(a.y) + t * a.ldy + c0; };
@@ -359,6 +400,9 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_grad_kernel(const Block
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) fetch(begin + s, s);
 
+    // the gate row of row t, the rows of it behind the runner's first, and the rows left of it
+    const int first_group = a.gate_period ? begin / a.gate_period : 0;
+    int group = first_group, left = a.gate_period ? a.gate_period - (begin - first_group * a.gate_period) : 0;
     int stage = 0;
     for (int64_t t = begin; t < end; ++t) {
         cp_async_wait<S - 2>();
@@ -366,108 +410,89 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_grad_kernel(const Block
         const uint4 *slot = mine + stage * stride;
         fetch(t + S - 1, stage == 0 ? S - 1 : stage - 1);
         stage = stage == S - 1 ? 0 : stage + 1;
-        const int group = token_gate ? (int)t : a.gate_period ? (int)(t / a.gate_period) : 0;
         const float rho = a.w_post ? a.rstd[t] : 1.f, rho2 = a.rstd[a.T + t];
-        float r[N], h[N], u[N], g[N];
+        F2 r[H], h[H], u[H], g[H];
         L::read(slot, x_row(t), D, threads, tx, r);
         L::read(slot + pieces, y_row(t), D, threads, tx, h);
         L::read(slot + 2 * pieces, n_row(t), D, threads, tx, u);
         // the factor of dx in the gradient of h
-        auto load_gate = [&] {
+        {
             if (token_gate) {
                 L::read(slot + g_at, g_row(t), D, threads, tx, g);
             } else if (a.gate_period) {
                 const type *row = g_row(group);  // the same for many rows: from L1
+                float v[L::N];
                 if constexpr (ALIGNED) {
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        const int c = (v * threads + tx) * L::VEC;
+                    for (int k = 0; k < NV; ++k) {
+                        const int c = (k * threads + tx) * L::VEC;
                         unpack16<DT>(c < D ? __ldg(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0),
-                                     g + v * L::VEC);
+                                     v + k * L::VEC);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) g[i] = i * threads + tx < D ? E::to_float(row[i * threads + tx]) : 0.f;
+                    for (int i = 0; i < L::N; ++i) v[i] = i * threads + tx < D ? E::to_float(row[i * threads + tx]) : 0.f;
                 }
+#pragma unroll
+                for (int i = 0; i < H; ++i) g[i] = F2(v[2 * i], v[2 * i + 1]);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = a.gate_period ? a.scale * g[i] : a.scale;
-        };
-        load_gate();
-        L::weights(a.w_pre, a.w_f32, c0, D, threads, tx, w_pre);
-        if (!KEEP) load_post();
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            // h becomes y rho; r the residual sum; u = dn w_pre
-            h[i] *= rho;
-            r[i] = fmaf(g[i], h[i] * w_post[i], r[i]);
-            dw_pre[i] = fmaf(u[i], r[i] * rho2, dw_pre[i]);
-            u[i] *= w_pre[i];
-            sum = fmaf(u[i], r[i], sum);
+            for (int i = 0; i < H; ++i) g[i] = a.gate_period ? g[i] * F2(a.scale) : F2(a.scale);
         }
-        sum = red.sum(sum) * inv_d * rho2 * rho2;
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = rho2 * fmaf(-r[i], sum, u[i]);
+        L::weights(a.w_pre, a.w_f32, c0, D, threads, tx, w_pre);
+        F2 part[3] = {F2(0.f), F2(0.f), F2(0.f)}, dr[H];
         if (a.dr) {
-            L::read(slot + dr_at, r_row(t), D, threads, tx, u);
+            L::read(slot + dr_at, r_row(t), D, threads, tx, dr);
+        } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) r[i] += u[i];
+            for (int i = 0; i < H; ++i) dr[i] = F2(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            // h becomes y rho; r the residual sum; u = dn w_pre
+            h[i] = h[i] * F2(rho);
+            const F2 P = g[i] * (h[i] * w_post[i]);
+            r[i] = r[i] + P;
+            dw_pre[i] = fma(u[i], r[i] * F2(rho2), dw_pre[i]);
+            u[i] = u[i] * w_pre[i];
+            part[0] = fma(u[i], r[i], part[0]);
+            part[1] = fma(P, fma(u[i], F2(rho2), dr[i]), part[1]);
+            part[2] = fma(P, r[i], part[2]);
+        }
+        float sums[3] = {part[0].sum(), part[1].sum(), part[2].sum()};
+        red.sum(sums);
+        const float c = sums[0] * inv_d * rho2 * rho2;
+        // with h = y rho: dy = rho (v - h mean(v h)); without the norm rho is 1 and dy = v
+        const float c2 = a.w_post ? fmaf(-rho2 * c, sums[2], sums[1]) * inv_d : 0.f;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            r[i] = fma(fma(r[i], F2(-c), u[i]), F2(rho2), dr[i]);
+            dgate[i] = fma(r[i], h[i] * w_post[i], dgate[i]);  // times a.scale when it is written
+            u[i] = g[i] * r[i];
+            dw_post[i] = fma(u[i], h[i], dw_post[i]);
+            u[i] = fma(h[i], F2(-c2), u[i] * w_post[i]) * F2(rho);
         }
         L::store(static_cast<type *>(a.dx) + t * a.lddx + c0, D, threads, tx, r);
-        if (!KEEP) {
-            load_post();
-            load_gate();
-        }
-        float sum2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            dgate[i] = fmaf(a.scale * r[i], h[i] * w_post[i], dgate[i]);
-            u[i] = g[i] * r[i];
-            dw_post[i] = fmaf(u[i], h[i], dw_post[i]);
-            u[i] *= w_post[i];
-            sum2 = fmaf(u[i], h[i], sum2);
-        }
-        // with h = y rho: dy = rho (v - h mean(v h)); without the norm rho is 1 and dy = v
-        sum2 = a.w_post ? red.sum(sum2) * inv_d : 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = rho * fmaf(-h[i], sum2, u[i]);
         L::store(static_cast<type *>(a.dy) + t * a.lddy + c0, D, threads, tx, u);
-        if (a.gate_period && (token_gate || t + 1 == end || (t + 1) % a.gate_period == 0)) {
+        if (a.gate_period && (--left == 0 || t + 1 == end)) {
             // the gate row's sum: whole when all of its rows are this runner's, otherwise one
             // of the runner's two partial sums (the first gate row it meets, or the last)
-            const int64_t g0 = (int64_t)group * a.gate_period, g1 = g0 + a.gate_period;
-            if (g0 >= begin && g1 <= end) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) dgate[i] = dgate[i] * F2(a.scale);
+            if (left == 0 && (group > first_group || begin == group * a.gate_period)) {
                 L::store(static_cast<type *>(a.dgate) + group * a.lddg + c0, D, threads, tx, dgate);
             } else {
-                float *to = partial + (int64_t)(group == begin / a.gate_period ? 2 : 3) * a.D;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int c = L::col(i, threads, tx);
-                    if (c < D) to[c] = dgate[i];
-                }
+                put(partial + (int64_t)(group == first_group ? 2 : 3) * a.D, dgate);
             }
+            ++group;
+            left = a.gate_period;
 #pragma unroll
-            for (int i = 0; i < N; ++i) dgate[i] = 0.f;
+            for (int i = 0; i < H; ++i) dgate[i] = F2(0.f);
         }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int c = L::col(i, threads, tx);
-        if (c < D) {
-            partial[c] = dw_pre[i];
-            partial[a.D + c] = dw_post[i];
-        }
-    }
+    put(partial, dw_pre);
+    put(partial + a.D, dw_post);
     if (a.ranks > 1) cluster_sync();
-}
-
-// The runner that has row t.
-__device__ __forceinline__ int runner_of(int64_t t, int T, int runners) {
-    int b = (int)min((int64_t)runners - 1, t * runners / T);
-    while (first_row(b, T, runners) > t) --b;
-    while (first_row(b + 1, T, runners) <= t) ++b;
-    return b;
 }
 
 // Adds the runners' partial sums: blockIdx.y 0 and 1 for the weights, from 2
@@ -490,6 +515,7 @@ __global__ void __launch_bounds__(1024) block_norm_grad_join_kernel(const BlockN
         __syncthreads();
         return s;
     };
+    griddep_wait();
     const bool writes = threadIdx.y == 0 && c < D;
     if (blockIdx.y < 2) {
         if (blockIdx.y == 1 && !a.w_post) return;
@@ -498,21 +524,21 @@ __global__ void __launch_bounds__(1024) block_norm_grad_join_kernel(const BlockN
         return;
     }
     // gate rows by number where they are few; otherwise by the runners that start inside one
+    const RowRuns runs(a.T, runners);
     const int groups = a.T / a.gate_period, count = min(groups, runners - 1);
     for (int i = blockIdx.y - 2; i < count; i += gridDim.y - 2) {
         int group = i;
         if (groups > runners - 1) {
-            const int row = first_row(i + 1, a.T, runners);
+            const int row = runs.first(i + 1);
             group = row / a.gate_period;
-            const int64_t g0 = (int64_t)group * a.gate_period;
-            if (g0 == row || first_row(i, a.T, runners) > g0) continue;  // not the first runner to start inside it
+            const int g0 = group * a.gate_period;
+            if (g0 == row || runs.first(i) > g0) continue;  // not the first runner to start inside it
         }
-        const int64_t g0 = (int64_t)group * a.gate_period;
-        const int b0 = runner_of(g0, a.T, runners), b1 = runner_of(g0 + a.gate_period - 1, a.T, runners) + 1;
+        const int g0 = group * a.gate_period;
+        const int b0 = runs.runner_of(g0), b1 = runs.runner_of(g0 + a.gate_period - 1) + 1;
         if (b1 - b0 < 2) continue;  // one runner had all of it
-        const float s = join(b0, b1, [&](int b) {
-            return group == first_row(b, a.T, runners) / a.gate_period ? 2 : 3;
-        });
+        // a runner that starts in an earlier gate row has this one's part in its second place
+        const float s = join(b0, b1, [&](int b) { return runs.first(b) >= g0 ? 2 : 3; });
         if (writes) store_weight<DT>(a.dgate, 0, (int64_t)group * a.lddg + c, s);
     }
 }

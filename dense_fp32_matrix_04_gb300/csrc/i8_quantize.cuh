@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(1024)
     quantize_i8_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
                        Code *__restrict__ q, int64_t ldq, float *__restrict__ scale, int q_vec) {
     using P = Piece<DT, VW>;
-    __shared__ float slots[64];
+    __shared__ float slots[RowReducer::SLOTS];
     griddep_launch_dependents();
     RowReducer red{slots, (int)(blockDim.x >> 5)};
     const int threads = blockDim.x;
@@ -86,7 +86,7 @@ template <int DT, class Code>
 __global__ void __launch_bounds__(1024)
     quantize_i8_wide_kernel(int M, int K, const typename Elem<DT>::type *__restrict__ x, int64_t ldx,
                             Code *__restrict__ q, int64_t ldq, float *__restrict__ scale) {
-    __shared__ float slots[64];
+    __shared__ float slots[RowReducer::SLOTS];
     griddep_launch_dependents();
     RowReducer red{slots, (int)(blockDim.x >> 5)};
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {

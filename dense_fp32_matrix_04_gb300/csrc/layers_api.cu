@@ -11,9 +11,6 @@
 #include "host.h"
 #include "logprobs.cuh"
 
-#ifndef LP_N
-#define LP_N 16
-#endif
 namespace {
 
 using namespace sgemm;
@@ -48,19 +45,19 @@ bool finite(float v) { return std::isfinite(v); }
 
 // How a row is shared out: `ranks` blocks of a cluster with `width` columns
 // each, in pieces that no 16 bytes span; `per` elements a thread.  A block
-// takes at most `most` threads, and its ring of copies at most 225 KB.
+// takes at most `most` threads, and its ring of `slots` rows at most 225 KB.
 // Where a warp is enough for a row, a block has four.
 struct RowPlan {
     int ranks = 1, width;
     dim3 block;
     size_t smem;
-    RowPlan(int D, int size, int arrays, int per, int most) : width(D) {
+    RowPlan(int D, int size, int slots, int per, int most) : width(D) {
         for (;; ranks *= 2) {
             const int vec = 16 / size;
             width = ranks == 1 ? D : ((D + ranks - 1) / ranks + vec - 1) / vec * vec;
             const int threads = row_threads(width, per);
             block = dim3(threads, threads == 32 && ranks == 1 ? 4 : 1);
-            smem = (size_t)kNormStages * arrays * row_pieces(width, size) * 16 * block.y;
+            smem = (size_t)slots * row_pieces(width, size) * 16 * block.y;
             if (ranks == 8 || (threads <= most && smem <= 225 * 1024)) break;
         }
     }
@@ -72,7 +69,7 @@ int launch_norm(BlockNormArgs a, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
     const auto kernel = block_norm_kernel<DT, ALIGNED, NV, MAXT, MINB>;
     constexpr int size = sizeof(typename Elem<DT>::type);
-    const RowPlan plan(a.D, size, a.gate_period == 1 ? 3 : 2, NV * Elem<DT>::VEC, MAXT);
+    const RowPlan plan(a.D, size, kNormStages * (a.gate_period == 1 ? 3 : 2), NV * Elem<DT>::VEC, MAXT);
     a.ranks = plan.ranks;
     a.width = plan.width;
     const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem);
@@ -88,33 +85,34 @@ int norm_by_width(const BlockNormArgs &a, const Device &dev, cudaStream_t stream
     constexpr int VEC = Elem<DT>::VEC;
     // narrow rows take 8 elements a thread, so that a block has warps to hide its barriers; wide
     // ones 16, so that a row needs fewer of them
-    if (a.D > 2048) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
+    if (a.D > 5120) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
+    if (a.D > 2048) return launch_norm<DT, ALIGNED, 16 / VEC, 320, ALIGNED ? 2 : 1>(a, dev, stream);
     return launch_norm<DT, ALIGNED, 8 / VEC, 256, 3>(a, dev, stream);
 }
 
-// Runners of the gradient's rows: a block (or a cluster) each, or for narrow
-// rows a warp each.  Every one writes its own partial sums, so there are no
-// more than fill the GPU: rows beyond 2048 elements leave room for one block
-// per SM.
-int grad_runners(int T, int D, int sms) {
-    const int per_sm = D > 2048 ? 1 : D > 1024 ? 2 : D > 256 ? 4 : 16;
-    return std::min(T, std::max(1, per_sm * sms / (D > 4096 ? (D + 4095) / 4096 : 1)));
-}
+// Runners of the gradient's rows: a block (or a cluster of blocks) each, or for
+// narrow rows a warp each.  Every one writes its own partial sums, so there are
+// no more than the SMs hold at once, 512 threads of 128 registers each; this is
+// the most there can be for any type and alignment.
+int most_grad_runners(int T, int D, int sms) { return std::min(T, std::max(1, 512 * sms / row_threads(D, 8))); }
 
 template <int DT, bool ALIGNED>
 int launch_norm_grad(BlockNormGradArgs a, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = block_norm_grad_kernel<DT, ALIGNED, 8 / Elem<DT>::VEC, 512, 1>;
+    constexpr int most = ALIGNED ? 512 : 480;  // single elements take more registers
+    const auto kernel = block_norm_grad_kernel<DT, ALIGNED, 8 / Elem<DT>::VEC, most, 1>;
     constexpr int size = sizeof(typename Elem<DT>::type);
-    const RowPlan plan(a.D, size, 3 + (a.gate_period == 1) + (a.dr != nullptr), 8, 512);
+    const RowPlan plan(a.D, size, kNormGradStages * (3 + (a.gate_period == 1) + (a.dr != nullptr)), 8, most);
     a.ranks = plan.ranks;
     a.width = plan.width;
     if (!sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem)) return SGEMM_ERR_LAUNCH;
+    const int fit = std::max(1, std::min(512 / plan.threads(), 226 * 1024 / (int)(plan.smem + 2048)));
+    a.runners = std::min(a.T, std::max(1, dev.sms * fit / plan.ranks) * (int)plan.block.y);
     const unsigned groups = (a.runners + plan.block.y - 1) / plan.block.y;
     const int st = launch(kernel, dim3(groups * plan.ranks), plan.block, plan.smem, stream, (unsigned)plan.ranks, a);
     if (st != SGEMM_OK) return st;
     const int gates = a.gate_period > 1 ? std::min({a.T / a.gate_period, a.runners - 1, 16}) : 0;
-    return launch(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, 2 + gates), dim3(32, 32), 0, stream, 1, a);
+    return launch<true>(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, 2 + gates), dim3(32, 32), 0, stream, 1, a);
 }
 
 // Checks that the forward and the backward pass share.
@@ -132,16 +130,32 @@ bool norm_shape_ok(int T, int D, int dtype, int wdtype, const void *w_pre, const
 
 // ---------------------------------------------------------------- log probabilities
 
-template <int DT, bool TOP>
-int launch_logprobs(const LogprobArgs &a, const Device &dev, cudaStream_t stream) {
-    // few rows are shared by clusters of up to 8 blocks, until there are two blocks per SM
+#ifndef SHORT_ROW
+#define SHORT_ROW 16384
+#endif
+constexpr int kShortRow = SHORT_ROW;
+
+template <int DT, int THREADS, bool TOP, bool MASK>
+int launch_logprobs(const LogprobArgs &a, unsigned parts, const Device &dev, cudaStream_t stream) {
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = logprobs_kernel<DT, THREADS, TOP, MASK>;
+    constexpr int smem = kLogprobRing<DT, THREADS, MASK>;
+    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, THREADS, smem)) return SGEMM_ERR_LAUNCH;
+    const dim3 grid(parts, (unsigned)std::min(a.T, 1024 / THREADS * dev.sms));
+    return launch(kernel, grid, dim3(THREADS), smem, stream, parts, a);
+}
+
+template <int DT, bool MASK>
+int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t stream) {
+    // few rows are shared by clusters of up to 8 blocks, until there are two blocks per SM; many
+    // are walked by the blocks the SMs hold
     unsigned parts = 1;
     while (parts < 8 && (int64_t)a.T * parts * 2 <= 2 * dev.sms && a.V / (int)(parts * 2) >= 2048) parts *= 2;
-    const dim3 grid(parts, (unsigned)std::min(a.T, 65535));
-    // logits a thread has in flight beside those it adds up
-    constexpr int U = LP_N / Elem<DT>::VEC;
-    if (a.mask) return launch(logprobs_kernel<DT, U, TOP, true>, grid, dim3(kLogprobThreads), 0, stream, parts, a);
-    return launch(logprobs_kernel<DT, U, TOP, false>, grid, dim3(kLogprobThreads), 0, stream, parts, a);
+    if (parts == 1 && a.V < kShortRow)
+        return a.top ? launch_logprobs<DT, 64, true, MASK>(a, 1, dev, stream)
+                     : launch_logprobs<DT, 64, false, MASK>(a, 1, dev, stream);
+    return a.top ? launch_logprobs<DT, 256, true, MASK>(a, parts, dev, stream)
+                 : launch_logprobs<DT, 256, false, MASK>(a, parts, dev, stream);
 }
 
 template <int DT, int VW>
@@ -209,7 +223,7 @@ int sgemm_block_norm(int T, int D, int dtype, const void *x, int ldx, const void
 size_t sgemm_block_norm_backward_workspace_size(int T, int D) {
     Device dev;
     if (T <= 0 || D <= 0 || sgemm_host::device(dev) != SGEMM_OK) return 0;
-    return (size_t)grad_runners(T, D, dev.sms) * 4 * (size_t)D * sizeof(float);
+    return (size_t)most_grad_runners(T, D, dev.sms) * 4 * (size_t)D * sizeof(float);
 }
 
 int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, const void *y, int ldy,
@@ -256,7 +270,7 @@ int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
     }
     const BlockNormGradArgs a{T, D, x, y, gate, dn, dr, ldx, ldy, ldg, lddn, lddr, w_pre, w_post, wdtype == SGEMM_F32,
                               gate_rows ? T / gate_rows : 0, scale, rstd, dx, dy, dgate, lddx, lddy, lddg, dw_pre,
-                              dw_post, static_cast<float *>(workspace), grad_runners(T, D, dev.sms)};
+                              dw_post, static_cast<float *>(workspace), 0};
     const bool vec = D % (16 / size) == 0 && X.vec(size) && Y.vec(size) && G.vec(size) && DN.vec(size) &&
                      DR.vec(size) && DX.vec(size) && DY.vec(size) && DG.vec(size) && aligned(w_pre, 16) &&
                      aligned(w_post, 16);
@@ -293,7 +307,7 @@ int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float s
                         top_logprob, top_id};
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        return top ? launch_logprobs<DT, true>(a, dev, stream) : launch_logprobs<DT, false>(a, dev, stream);
+        return mask ? logprobs_by_length<DT, true>(a, dev, stream) : logprobs_by_length<DT, false>(a, dev, stream);
     });
 }
 

@@ -1,20 +1,21 @@
 // Log probabilities of given columns, entropy, log-sum-exp and the most likely
 // columns of rows of logits, in one pass over them; and the gradient.
 //
-// With m the largest logit seen, t_j = (z_j - m) scale log2(e), the pass keeps
+// With m the largest logit seen, c = scale log2(e), M = m c rounded to FP32 and
+// t_j = z_j c - M (one fused operation), the pass keeps
 //     s = sum 2^t_j   and   s1 = sum 2^t_j t_j,
-// which a larger m turns into f s and f (s1 + s d), d = (m - m') scale log2(e),
-// f = 2^d.  At the end lse = scale m + ln s, entropy = ln s - ln 2 s1 / s, and
-// log p_y = scale (z_y - m) - ln s.  The difference z_j - m is taken before the
-// scale, so that logits of the type's lowest value stay finite.
+// which a larger M' turns into f s and f (s1 + s d), d = M - M', f = 2^d: the
+// rounding of M is the same for every term, so it costs no accuracy.  At the end
+// lse = ln 2 M + ln s, taken as scale m + ln s + ln 2 (M - m c) with an exact
+// difference; entropy = ln s - ln 2 s1 / s; log p_y = scale (z_y - m) - ln s -
+// ln 2 (M - m c).  Logits beyond 1e37, whose products with c could overflow
+// (masks of the type's lowest value), take t_j = (z_j - m) c instead.
 //
-// Each warp keeps the `top` best columns it has met as a list over its lanes,
-// best first.  A chunk whose largest logits do not reach the list's last entry
-// costs one comparison a lane; otherwise the columns of the lanes that do are
-// looked at, 32 at a time, one a lane.  After 1, 2, 4, ... chunks the block also
-// takes the top-th largest of the maxima of 32 groups of its threads, which
-// every column has to reach from then on: a warp alone would let eight times
-// as many through.
+// The alternatives cost the pass nothing: each thread knows the largest logit it
+// has met, and at the row's end at least `top` columns reach the top-th largest
+// of the maxima of 32 groups of threads.  Only the threads that have such a
+// column, a handful, have theirs looked at again, and the few columns that
+// reach it are inserted into a list over a warp's lanes.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -58,6 +59,23 @@ __device__ __forceinline__ uint32_t mask_bits(const int32_t *row, int c, int n, 
     return __funnelshift_r(lo, hi, s);
 }
 
+// The largest of the 16 bytes' elements (a NaN only where all are).
+template <int DT>
+__device__ __forceinline__ float max16(const uint4 &raw) {
+    if constexpr (DT == SGEMM_F32) {
+        return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)),
+                     fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+    } else if constexpr (DT == SGEMM_BF16) {
+        auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(raw.x), h(raw.y)), __hmax2(h(raw.z), h(raw.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    } else {
+        auto h = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
+        const __half2 m = __hmax2(__hmax2(h(raw.x), h(raw.y)), __hmax2(h(raw.z), h(raw.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+}
+
 // A column and its logit; "better" orders by the logit, then by the lowest column.
 struct Candidate {
     float v;
@@ -69,66 +87,68 @@ __device__ __forceinline__ bool better(float v, int id, float v2, int id2) {
 
 // The running sums of a thread, or of several joined.
 struct SoftmaxState {
-    float m = -INFINITY, s = 0.f, s1 = 0.f;
-    // raises the maximum to at least m2; where d is far below 0, 2^d is 0 and the bound on d
-    // keeps the product from being 0 times infinity
+    float m = -INFINITY, M = -INFINITY, s = 0.f, s1 = 0.f;
+    static constexpr float kLarge = 1e37f;
+    // (a product of its own: fused into a difference it would not be the M that the terms saw)
+    __device__ static float reference(float m, float c) { return fabsf(m) < kLarge ? __fmul_rn(m, c) : m; }
+    // log2 of the factor from one maximum to another; far below 0, 2^d is 0 and the bound on d
+    // keeps products with it from being 0 times infinity
+    __device__ static float step(float m, float M, float m2, float M2, float c) {
+        return fabsf(m) < kLarge && fabsf(m2) < kLarge ? M - M2 : (m - m2) * c;
+    }
+    // raises the maximum to at least m2
     __device__ void raise(float m2, float c) {
         if (m2 > m) {
-            const float d = (m - m2) * c, f = exp2_approx(d);
+            const float M2 = reference(m2, c), d = step(m, M, m2, M2, c), f = exp2_approx(d);
             s1 = m == -INFINITY ? s1 : f * fmaf(s, fmaxf(d, -1000.f), s1);
             s *= f;
             m = m2;
+            M = M2;
         }
     }
-    // adds the n logits v, none of them above m (finite or +infinity), two at a time
+    // adds the N logits v, none of them above m, two at a time (N is 1 or even)
     template <int N>
     __device__ void add(const float *v, float c) {
-        if constexpr (N % 2 == 0) {
-            const uint64_t mm = f32x2_dup(-m), cc = f32x2_dup(c);
-            uint64_t sum = f32x2_pair(s, 0.f), sum1 = f32x2_pair(s1, 0.f);
+        if (N > 1 && fabsf(m) < kLarge) {
+            F2 sum(s, 0.f), sum1(s1, 0.f);
+            const F2 cc(c), MM(-M);
 #pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const uint64_t t = f32x2_mul(f32x2_add(f32x2_pair(v[j], v[j + 1]), mm), cc);
-                const float2 x = f32x2_unpack(t);
-                const uint64_t e = f32x2_pair(exp2_approx(x.x), exp2_approx(x.y));
-                sum = f32x2_add(sum, e);
-                f32x2_fma(sum1, e, t);
+            for (int j = 0; j + 1 < N; j += 2) {
+                const F2 t = fma(F2(v[j], v[j + 1]), cc, MM);
+                const float2 x = t.both();
+                const F2 e(exp2_approx(x.x), exp2_approx(x.y));
+                sum = sum + e;
+                sum1 = fma(e, t, sum1);
             }
-            const float2 a = f32x2_unpack(sum), b = f32x2_unpack(sum1);
-            const float s_new = a.x + a.y, s1_new = b.x + b.y;
+            const float s1_new = sum1.sum();
             if (s1_new == s1_new) {
-                s = s_new;
+                s = sum.sum();
                 s1 = s1_new;
                 return;
             }
         }
-        // a term of 0 times -infinity (a logit of -infinity), or a NaN
+        // a term of 0 times -infinity (a logit of -infinity), a NaN, or large logits
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float t = (v[j] - m) * c, e = exp2_approx(t);
+            const float t = fabsf(m) < kLarge ? fmaf(v[j], c, -M) : (v[j] - m) * c, e = exp2_approx(t);
             s += e;
             s1 = fmaf(e, fmaxf(t, -1000.f), s1);
         }
     }
-    __device__ void join(float m2, float s2, float s12, float c) {
-        if (m2 == -INFINITY) {
-            s += s2;  // 0, or NaN
-            return;
-        }
-        raise(m2, c);
-        const float d = (m2 - m) * c, f = exp2_approx(d);
-        s1 = fmaf(f, fmaf(s2, fmaxf(d, -1000.f), s12), s1);
-        s = fmaf(s2, f, s);
-    }
-    // joins the states of 2 * FROM lanes, in an order that the lanes' numbers fix
-    template <int FROM>
+    // joins the states of the warp's lanes: the largest maximum first, then plain sums relative to it
     __device__ void join_lanes(float c) {
+        float m2 = m;
 #pragma unroll
-        for (int o = FROM; o; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o),
-                        s12 = __shfl_xor_sync(0xffffffffu, s1, o);
-            join(m2, s2, s12, c);
+        for (int o = 16; o; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+        if (m > -INFINITY) {  // otherwise s is 0, or NaN
+            const float d = step(m, M, m2, reference(m2, c), c), f = exp2_approx(d);
+            s1 = f * fmaf(s, fmaxf(d, -1000.f), s1);
+            s *= f;
         }
+        m = m2;
+        M = reference(m2, c);
+        s = warp_sum(s);
+        s1 = warp_sum(s1);
     }
 };
 
@@ -192,84 +212,128 @@ __device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
     return __shfl_sync(0xffffffffu, x, k - 1);
 }
 
-// Joins the block's THREADS entries, one a thread, which are lists in order
-// with `top` entries each: `top` best into out, in order.  No entry below the
-// largest of the lists' last entries can be among them (that list alone has
-// `top` better ones), so only those that reach it are compared with each
-// other: an entry's place is the number of better ones.
-template <int THREADS>
-struct TopJoin {
-    Candidate entry[THREADS];
-    float last[THREADS / 32];
+// Columns that may be among a row's best, in any order, up to CAP of them.
+template <int CAP>
+struct Candidates {
+    Candidate entry[CAP];
     int count;
-    __device__ void run(float v, int id, int top, Candidate *out) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == top - 1) last[warp] = v;
-        if (threadIdx.x == 0) count = 0;
-        if (threadIdx.x < 32) out[threadIdx.x] = {-INFINITY, INT_MAX};
-        __syncthreads();
-        float floor_v = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) floor_v = fmaxf(floor_v, last[w]);
-        const bool in = lane < top && v > -INFINITY && v >= floor_v;
-        if (in) entry[atomicAdd(&count, 1)] = {v, id};  // their order does not matter
-        __syncthreads();
-        if (in) {
+    __device__ void push(float v, int id) {
+        const int at = atomicAdd(&count, 1);  // their order does not matter
+        if (at < CAP) entry[at] = {v, id};
+    }
+    // after a barrier: the `top` best into out, in order; an entry's place is the number of better ones
+    __device__ void best(int top, Candidate *out) const {
+        const int n = count;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            const Candidate e = entry[i];
             int place = 0;
-            for (int i = 0, n = count; i < n; ++i) place += better(entry[i].v, entry[i].id, v, id);
-            if (place < top) out[place] = {v, id};
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) place += better(entry[j].v, entry[j].id, e.v, e.id);
+            if (place < top) out[place] = e;
         }
-        __syncthreads();
     }
 };
 
-constexpr int kLogprobThreads = 256;
+constexpr int kTopBuffer = 512;  // columns; at least the 256 that a cluster's lists, or a block's warps', hold
 
 // A cluster of gridDim.x blocks shares row blockIdx.y (+ gridDim.y, ...): each
 // takes a run of 16-byte pieces; the last also the columns before the first
 // and after the last aligned piece.  Block 0 joins the blocks' results through
-// distributed shared memory.  A thread loads U pieces ahead of those it adds up.
-template <int DT, int U, bool TOP, bool MASK>
-__global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 : 2) logprobs_kernel(const LogprobArgs a) {
+// distributed shared memory.  Each thread copies its own pieces (U to a chunk,
+// 16 elements) into its own places of a ring in shared memory, kLogprobDepth
+// chunks ahead and on into the block's next row, so that memory is busy while a
+// row's results are joined.
+constexpr int kLogprobDepth = 4;
+template <int DT>
+constexpr int kLogprobPieces = 16 / Elem<DT>::VEC;
+// bytes of the ring: a piece, and with a mask the two words that hold its bits
+template <int DT, int THREADS, bool MASK>
+constexpr int kLogprobRing = kLogprobDepth * kLogprobPieces<DT> * THREADS * (MASK ? 24 : 16);
+
+// THREADS: 256, or 64 for rows so short that what a row costs a warp beside its
+// columns counts.  Registers for 1024 threads an SM (768 where it takes more).
+template <int DT, int THREADS, bool TOP, bool MASK>
+__global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !TOP ? 768 : 1024) / THREADS)
+    logprobs_kernel(const LogprobArgs a) {
     using E = Elem<DT>;
     using type = typename E::type;
-    constexpr int VEC = E::VEC, THREADS = kLogprobThreads, WARPS = THREADS / 32;
+    constexpr int VEC = E::VEC, WARPS = THREADS / 32, U = kLogprobPieces<DT>,
+                  DEPTH = kLogprobDepth;
+    extern __shared__ uint4 ring[];
     __shared__ float warp_state[3][WARPS];
     __shared__ float block_state[3];
     __shared__ Candidate block_list[TOP ? 32 : 1];
-    __shared__ TopJoin<TOP ? THREADS : 32> top_join;
-    // a warp's columns on their way to its list, and the lanes that they come from
-    __shared__ __align__(16) float columns[TOP ? WARPS : 1][TOP ? 32 * U * VEC : 4];
-    __shared__ uint8_t from_lane[TOP ? WARPS : 1][32];
-    __shared__ float group_max[2][32];
+    __shared__ Candidates<TOP ? kTopBuffer : 1> found;
+    __shared__ uint8_t again[TOP ? THREADS : 1];
+    __shared__ int again_count;
+    __shared__ float group_max[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = gridDim.x, part = blockIdx.x;
+    const int parts = gridDim.x, part = blockIdx.x, log_parts = __ffs(parts) - 1;  // parts: a power of two
     const float c = a.scale * kLog2e;
 
+    // a row as this block reads it: `head` columns before the first aligned piece, pieces [p0, p1)
+    struct Row {
+        const type *z;
+        const int32_t *mask;
+        int head, pieces, p0, p1;
+    };
+    auto row_of = [&](int64_t t) {
+        Row r;
+        r.z = static_cast<const type *>(a.z) + t * a.ldz;
+        r.mask = MASK ? a.mask + t * a.ldm : nullptr;
+        const int off = (int)((reinterpret_cast<uintptr_t>(r.z) & 15u) / sizeof(type));
+        r.head = min(off ? VEC - off : 0, a.V);
+        r.pieces = (a.V - r.head) / VEC;
+        r.p0 = (int)((int64_t)r.pieces * part >> log_parts);
+        r.p1 = (int)((int64_t)r.pieces * (part + 1) >> log_parts);
+        return r;
+    };
+    // the chunk that is copied next: of row `ahead_t`, from piece `ahead_p` on
+    int64_t ahead_t = blockIdx.y;
+    Row ahead;
+    int ahead_p = 0;
+    auto next_row = [&](int64_t t) {
+        for (ahead_t = t; ahead_t < a.T; ahead_t += gridDim.y) {
+            ahead = row_of(ahead_t);
+            ahead_p = ahead.p0;
+            if (ahead.p0 < ahead.p1) break;
+        }
+    };
+    auto copy = [&](int slot) {
+        if (ahead_t < a.T) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = ahead_p + u * THREADS + (int)threadIdx.x, place = (slot * U + u) * THREADS + threadIdx.x;
+                if (at < ahead.p1) {
+                    cp_async_16(smem_addr(ring + place), ahead.z + ahead.head + (int64_t)at * VEC, 16);
+                    if (MASK) {
+                        const uint32_t to = smem_addr(reinterpret_cast<uint2 *>(ring + DEPTH * U * THREADS) + place);
+                        const int w = (ahead.head + at * VEC) >> 5, last = (a.V - 1) >> 5;
+                        cp_async_4(to, ahead.mask + w, 4);
+                        cp_async_4(to + 4, ahead.mask + min(w + 1, last), 4);
+                    }
+                }
+            }
+            ahead_p += THREADS * U;
+            if (ahead_p >= ahead.p1) next_row(ahead_t + gridDim.y);
+        }
+        cp_async_commit();
+    };
+    next_row(blockIdx.y);
+#pragma unroll
+    for (int s = 0; s < DEPTH; ++s) copy(s);
+    int slot = 0;
+
     for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
-        const type *z = static_cast<const type *>(a.z) + t * a.ldz;
-        const int32_t *mask = MASK ? a.mask + t * a.ldm : nullptr;
-        const int off = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(type));
-        const int head = min(off ? VEC - off : 0, a.V);
-        const int pieces = (a.V - head) / VEC;
-        const int tail0 = head + pieces * VEC;
-        const int p0 = (int)((int64_t)pieces * part / parts), p1 = (int)((int64_t)pieces * (part + 1) / parts);
-        const uint4 *body = reinterpret_cast<const uint4 *>(z + head);
+        const Row row = row_of(t);
+        const type *z = row.z;
+        const int32_t *mask = row.mask;
+        const int head = row.head, tail0 = head + row.pieces * VEC;
 
         SoftmaxState st;
-        WarpTop best;
-        // a column joins the warp's list if it is better than the list's last entry, and reaches
-        // floor_v (which `top` of the row's columns are known to reach)
-        float last_v = -INFINITY, floor_v = -INFINITY;
-        int last_id = INT_MAX;
-        // adds the columns v[0 .. n) of this thread, -infinity where there is none; column i of
-        // lane l's has number col(l, i).  round: how many chunks the block has behind it, or -1
-        // where only one warp is here
-        auto chunk = [&](const float *v, auto n_const, int round, auto col) {
+        // adds the n columns v of this thread, -infinity where there is none; top: their largest
+        auto add = [&](const float *v, float top, auto n_const) {
             constexpr int n = decltype(n_const)::value;
-            float top = v[0];
-#pragma unroll
-            for (int j = 1; j < n; ++j) top = fmaxf(top, v[j]);
             st.raise(top, c);
             if (st.m == -INFINITY) {
 #pragma unroll
@@ -278,108 +342,116 @@ __global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 :
             } else {
                 st.template add<n>(v, c);
             }
-            if constexpr (TOP) {
-                if ((round & (round + 1)) == 0 && round >= 0) {
-                    // after 1, 2, 4, ... chunks: `top` columns reach the top-th largest of the
-                    // maxima of the block's 32 groups of threads
-                    float g = st.m;
-#pragma unroll
-                    for (int o = 32 / WARPS; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-                    float *group = group_max[__popc(round) & 1];
-                    if (lane < 32 / WARPS) group[warp * (32 / WARPS) + lane] = g;
-                    __syncthreads();
-                    floor_v = fmaxf(floor_v, warp_kth_largest(group[lane], a.top, lane));
-                }
-                const bool reaches = top >= fmaxf(last_v, floor_v) && top > -INFINITY;
-                const unsigned reach = __ballot_sync(0xffffffffu, reaches);
-                if (reach) {
-                    // the columns of the lanes that reach it, one a lane, 32 at a time
-                    if (reaches) {
-                        const int rank = __popc(reach & ((1u << lane) - 1));
-                        from_lane[warp][rank] = (uint8_t)lane;
-                        float *to = &columns[warp][rank * n];
-                        if constexpr (n % 4 == 0) {
-#pragma unroll
-                            for (int j = 0; j < n; j += 4)
-                                *reinterpret_cast<float4 *>(to + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < n; ++j) to[j] = v[j];
-                        }
-                    }
-                    __syncwarp();
-                    for (int i = 0, count = __popc(reach) * n; i < count; i += 32) {
-                        Candidate e{-INFINITY, INT_MAX};
-                        if (i + lane < count) {
-                            e.v = columns[warp][i + lane];
-                            e.id = col(from_lane[warp][(i + lane) / n], (i + lane) % n);
-                        }
-                        const bool in = e.v >= floor_v && e.v > -INFINITY && better(e.v, e.id, last_v, last_id);
-                        unsigned who = __ballot_sync(0xffffffffu, in);
-                        if (!who) continue;
-                        if (__popc(who) > 6) {
-                            best.merge(in ? e.v : -INFINITY, in ? e.id : INT_MAX, lane);
-                        } else {
-                            for (; who; who &= who - 1) {
-                                const int src = __ffs(who) - 1;
-                                best.insert(__shfl_sync(0xffffffffu, e.v, src), __shfl_sync(0xffffffffu, e.id, src), lane);
-                            }
-                        }
-                        last_v = __shfl_sync(0xffffffffu, best.v, a.top - 1);
-                        last_id = __shfl_sync(0xffffffffu, best.id, a.top - 1);
-                    }
-                    __syncwarp();
-                }
-            }
         };
         auto allowed = [&](int col) { return !MASK || (mask[col >> 5] >> (col & 31) & 1); };
 
-        auto load = [&](int p, uint4(&raw)[U], uint32_t(&bits)[U]) {
+        for (int p = row.p0; p < row.p1; p += THREADS * U) {
+            cp_async_wait<DEPTH - 1>();
+            float v[U * VEC], top = -INFINITY;
+            // what lies outside the row, or is masked, is -infinity; neither test costs a whole,
+            // unmasked chunk anything
+            const bool whole = p + THREADS * U <= row.p1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int at = p + u * THREADS + (int)threadIdx.x;
-                if (at < p1) raw[u] = __ldg(body + at);
-                if (MASK && at < p1) bits[u] = mask_bits(mask, head + at * VEC, VEC, a.V);
-            }
-        };
-        uint4 raw[U];
-        uint32_t bits[U];
-        load(p0, raw, bits);
-        int round = 0;
-        for (int p = p0; p < p1; p += THREADS * U) {
-            float v[U * VEC];
-            const bool whole = p + THREADS * U <= p1;
+                const int place = (slot * U + u) * THREADS + threadIdx.x;
+                const uint4 raw = ring[place];
+                unpack16<DT>(raw, v + u * VEC);
+                if (MASK || !whole) {
+                    const int at = p + u * THREADS + (int)threadIdx.x;
+                    uint32_t bits = ~0u;
+                    if (MASK) {
+                        const uint2 w = reinterpret_cast<const uint2 *>(ring + DEPTH * U * THREADS)[place];
+                        bits = __funnelshift_r(w.x, w.y, (head + at * VEC) & 31);
+                    }
+                    if (at >= row.p1) bits = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                unpack16<DT>(raw[u], v + u * VEC);
-                if (MASK) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (!(bits[u] >> e & 1)) v[u * VEC + e] = -INFINITY;
-                }
-                if (!whole && p + u * THREADS + (int)threadIdx.x >= p1) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[u * VEC + e] = -INFINITY;
+                    for (int e = 0; e < VEC; ++e) {
+                        if (!(bits >> e & 1)) v[u * VEC + e] = -INFINITY;
+                        top = fmaxf(top, v[u * VEC + e]);
+                    }
+                } else {
+                    top = fmaxf(top, max16<DT>(raw));
                 }
             }
-            if (p + THREADS * U < p1) load(p + THREADS * U, raw, bits);
-            chunk(v, std::integral_constant<int, U * VEC>{}, round++, [&](int src, int i) {
-                return head + (p + (i / VEC) * THREADS + warp * 32 + src) * VEC + i % VEC;
-            });
+            copy(slot);
+            slot = slot + 1 == DEPTH ? 0 : slot + 1;
+            add(v, top, std::integral_constant<int, U * VEC>{});
         }
-        if (part == parts - 1) {
-            // fewer than 2 * VEC columns outside the pieces: one a lane of the first warp
-            const int outside = head + a.V - tail0;
-            if (warp == 0 && outside > 0) {
-                auto column = [&](int l, int) { return l < head ? l : tail0 + l - head; };
-                float v = -INFINITY;
-                if (lane < outside && allowed(column(lane, 0))) v = E::to_float(z[column(lane, 0)]);
-                chunk(&v, std::integral_constant<int, 1>{}, -1, column);
+        const float thread_max = st.m;  // of the thread's pieces
+        // fewer than 2 * VEC columns lie outside the pieces: one a lane of the last block's first warp
+        Candidate outside{-INFINITY, INT_MAX};
+        if (part == parts - 1 && warp == 0 && lane < head + a.V - tail0) {
+            const int col = lane < head ? lane : tail0 + lane - head;
+            if (allowed(col)) outside = {E::to_float(z[col]), col};
+            add(&outside.v, outside.v, std::integral_constant<int, 1>{});
+        }
+
+        if constexpr (TOP) {
+            // At least `top` columns reach the top-th largest of the maxima of the block's 32 groups
+            // of threads, so only threads whose own maximum does have columns to look at again: a
+            // handful, unless many logits are equal.  Their pieces, one a lane, come from L2.
+            float g = thread_max;
+#pragma unroll
+            for (int o = 32 / WARPS; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+            if (lane < 32 / WARPS) group_max[warp * (32 / WARPS) + lane] = g;
+            if (threadIdx.x == 0) found.count = again_count = 0;
+            if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
+            __syncthreads();
+            const float floor_v = warp_kth_largest(group_max[lane], a.top, lane);
+            if (thread_max >= floor_v && thread_max > -INFINITY) again[atomicAdd(&again_count, 1)] = (uint8_t)threadIdx.x;
+            if (outside.v >= floor_v && outside.v > -INFINITY) found.push(outside.v, outside.id);
+            __syncthreads();
+            // the columns of one of those threads, 32 pieces at a time
+            auto columns = [&](int thread, auto take) {
+                for (int p = row.p0 + thread; p < row.p1; p += THREADS * 32) {
+                    const int at = p + lane * THREADS, col = head + at * VEC;
+                    const bool in = at < row.p1;
+                    float v[VEC];
+                    unpack16<DT>(in ? __ldg(reinterpret_cast<const uint4 *>(z + head) + at) : make_uint4(0, 0, 0, 0), v);
+                    const uint32_t bits = !in ? 0u : MASK ? mask_bits(mask, col, VEC, a.V) : ~0u;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) take((bits >> e & 1) && v[e] >= floor_v && v[e] > -INFINITY, v[e], col + e);
+                }
+            };
+            const int n_again = again_count;
+            for (int i = warp; i < n_again; i += WARPS)
+                columns(again[i], [&](bool in, float v, int id) {
+                    if (in) found.push(v, id);
+                });
+            __syncthreads();
+            if (found.count > kTopBuffer) {
+                // too many (equal logits): every warp keeps the best of its share in order instead
+                WarpTop best;
+                float last_v = -INFINITY;
+                int last_id = INT_MAX;
+                auto offer = [&](bool in, float v, int id) {
+                    in = in && better(v, id, last_v, last_id);
+                    unsigned who = __ballot_sync(0xffffffffu, in);
+                    if (!who) return;
+                    if (__popc(who) > 6) {
+                        best.merge(in ? v : -INFINITY, in ? id : INT_MAX, lane);
+                    } else {
+                        for (; who; who &= who - 1) {
+                            const int src = __ffs(who) - 1;
+                            best.insert(__shfl_sync(0xffffffffu, v, src), __shfl_sync(0xffffffffu, id, src), lane);
+                        }
+                    }
+                    last_v = __shfl_sync(0xffffffffu, best.v, a.top - 1);
+                    last_id = __shfl_sync(0xffffffffu, best.id, a.top - 1);
+                };
+                for (int i = warp; i < n_again; i += WARPS) columns(again[i], offer);
+                offer(outside.v >= floor_v && outside.v > -INFINITY, outside.v, outside.id);
+                __syncthreads();
+                if (threadIdx.x == 0) found.count = 0;
+                __syncthreads();
+                if (lane < a.top && best.v > -INFINITY) found.push(best.v, best.id);
+                __syncthreads();
             }
+            found.best(a.top, block_list);
         }
 
         // ---- join the lanes, the warps, and the cluster's blocks
-        st.template join_lanes<16>(c);
+        st.join_lanes(c);
         if (lane == 0) {
             warp_state[0][warp] = st.m;
             warp_state[1][warp] = st.s;
@@ -390,17 +462,17 @@ __global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 :
         if (warp == 0) {
             if (lane < WARPS) {
                 all.m = warp_state[0][lane];
+                all.M = SoftmaxState::reference(all.m, c);
                 all.s = warp_state[1][lane];
                 all.s1 = warp_state[2][lane];
             }
-            all.template join_lanes<WARPS / 2>(c);
+            all.join_lanes(c);
             if (parts > 1 && lane == 0) {
                 block_state[0] = all.m;
                 block_state[1] = all.s;
                 block_state[2] = all.s1;
             }
         }
-        if constexpr (TOP) top_join.run(best.v, best.id, a.top, block_list);
         if (parts > 1) {
             __syncthreads();
             cluster_sync();
@@ -410,30 +482,35 @@ __global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 :
                     if (lane < parts) {
                         const uint32_t s = dsmem_map(smem_addr(block_state), (uint32_t)lane);
                         all.m = __uint_as_float(dsmem_ld_u32(s));
+                        all.M = SoftmaxState::reference(all.m, c);
                         all.s = __uint_as_float(dsmem_ld_u32(s + 4));
                         all.s1 = __uint_as_float(dsmem_ld_u32(s + 8));
                     }
-                    all.template join_lanes<4>(c);
+                    all.join_lanes(c);
                 }
                 if constexpr (TOP) {
-                    Candidate e{-INFINITY, INT_MAX};
-                    if (warp < parts) {
+                    if (threadIdx.x == 0) found.count = 0;
+                    __syncthreads();
+                    if (warp < parts && lane < a.top) {
                         const uint32_t l = dsmem_map(smem_addr(&block_list[lane]), (uint32_t)warp);
-                        e.v = __uint_as_float(dsmem_ld_u32(l));
-                        e.id = (int)dsmem_ld_u32(l + 4);
+                        const float v = __uint_as_float(dsmem_ld_u32(l));
+                        if (v > -INFINITY) found.push(v, (int)dsmem_ld_u32(l + 4));
                     }
                     __syncthreads();  // block 0's own list has been read before it is written
-                    top_join.run(e.v, e.id, a.top, block_list);
+                    if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
+                    __syncthreads();
+                    found.best(a.top, block_list);
+                    __syncthreads();
                 }
             }
         }
         if (part == 0 && warp == 0) {
-            all.m = __shfl_sync(0xffffffffu, all.m, 0);
-            all.s = __shfl_sync(0xffffffffu, all.s, 0);
             const bool none = all.m == -INFINITY && !(all.s != all.s);
-            const float log_s = logf(all.s);
+            // ln of the sum relative to exactly m
+            const float off = fabsf(all.m) < SoftmaxState::kLarge ? -fmaf(all.m, c, -all.M) : 0.f;
+            const float log_s = logf(all.s), log_sum = fmaf(kLn2, off, log_s);
             if (lane == 0) {
-                if (a.lse) a.lse[t] = none ? -INFINITY : fmaf(all.m, a.scale, log_s);
+                if (a.lse) a.lse[t] = none ? -INFINITY : fmaf(all.m, a.scale, log_sum);
                 if (a.entropy) a.entropy[t] = none ? 0.f : log_s - kLn2 * (all.s1 / all.s);
                 if (a.logprob) {
                     const int64_t y = a.target[t];
@@ -442,7 +519,7 @@ __global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 :
                         lp = NAN;
                     } else if (y >= 0) {
                         const float zy = allowed((int)y) ? E::to_float(z[y]) : -INFINITY;
-                        lp = none ? -INFINITY : fmaf(zy - all.m, a.scale, -log_s);
+                        lp = none ? -INFINITY : fmaf(zy - all.m, a.scale, -log_sum);
                     }
                     a.logprob[t] = lp;
                 }
@@ -452,7 +529,7 @@ __global__ void __launch_bounds__(kLogprobThreads, U * Elem<DT>::VEC == 16 ? 3 :
                     const Candidate e = block_list[lane];
                     const bool bad = all.s != all.s;
                     const bool has = e.v > -INFINITY && !bad;
-                    a.top_logprob[t * a.top + lane] = bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_s) : -INFINITY;
+                    a.top_logprob[t * a.top + lane] = bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_sum) : -INFINITY;
                     a.top_id[t * a.top + lane] = has ? e.id : -1;
                 }
             }
@@ -475,39 +552,88 @@ struct LogprobGradArgs {
     int64_t lddz;
 };
 
-// dz_j = scale (g ([j = y] - p_j) - g_H p_j (log p_j + H)) for one column:
-// p_j (A + B log p_j) with A = -scale (g + g_H H), B = -scale g_H, and the
+// dz_j = scale (g ([j = y] - p_j) - g_H p_j (log p_j + H)) for the columns of a
+// row: p_j (A + B log p_j) with A = -scale (g + g_H H), B = -scale g_H, and the
 // target's scale g on top.
 struct LogprobGradRow {
     float scale, lse, A, B, hit;
-    int64_t target;
+    int target;  // -1: none
+    bool usual;  // lse is finite and its products with log2(e) are
     __device__ LogprobGradRow(const LogprobGradArgs &a, int64_t t) {
         scale = a.scale;
         lse = a.lse[t];
-        target = a.target[t];
-        float g = target >= 0 ? a.g_logprob[t] : 0.f;
-        if (target >= a.V) g = NAN;
+        const int64_t y = a.target[t];
+        float g = y >= 0 ? a.g_logprob[t] : 0.f;
+        if (y >= a.V) g = NAN;
+        target = y >= 0 && y < a.V ? (int)y : -1;
         const float gh = a.g_entropy ? a.g_entropy[t] : 0.f;
         A = -a.scale * (a.g_entropy ? fmaf(gh, a.entropy[t], g) : g);
         B = -a.scale * gh;
         hit = a.scale * g;
+        usual = fabsf(lse) < 1e29f;
+    }
+    __device__ float one(float z) const {
+        const float logp = fmaf(z, scale, -lse), p = exp2_approx(logp * kLog2e);
+        // p = 0 leaves nothing of B log p (log p may be -infinity there)
+        return lse == -INFINITY ? 0.f : p * fmaf(B, fmaxf(logp, -1000.f), A);
     }
     // the N columns from `col` on; bits: which of them the mask allows
     template <int N>
     __device__ void apply(float *v, uint32_t bits, int col) const {
-        const bool near = target >= col && target < (int64_t)col + N;
+        const int at = target - col;
+        const bool hits = at >= 0 && at < N;
+        float target_z = -INFINITY;
+        if (hits)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float logp = fmaf(v[e], scale, -lse), p = exp2_approx(logp * kLog2e);
-            // p = 0 leaves nothing of B log p (log p may be -infinity there)
-            float d = p * fmaf(B, fmaxf(logp, -1000.f), A);
-            if (near && target - col == e && v[e] > -INFINITY) d += hit;
-            v[e] = !(bits >> e & 1) ? 0.f : d;
-        }
-        if (lse == -INFINITY) {
+            for (int e = 0; e < N; ++e)
+                if (at == e) target_z = v[e];
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = 0.f;
+        for (int e = 0; e < N; ++e) v[e] = bits >> e & 1 ? one(v[e]) : 0.f;
+        if (hits && (bits >> at & 1) && target_z > -INFINITY && lse > -INFINITY)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (at == e) v[e] += hit;
+    }
+    // the same for 8 columns of 16 bits, in packed pairs and in powers of 2: log2 p is off by
+    // 2^-24 of the largest of its terms, far below what the result's 16 bits hold
+    template <int DT>
+    __device__ uint4 apply16(uint4 raw, uint32_t bits, int col) const {
+        float v[8];
+        if (!usual || (unsigned)(target - col) < 8u) {
+            unpack16<DT>(raw, v);
+            apply<8>(v, bits, col);
+            return pack16<DT>(v);
         }
+        // no -infinity, whose logarithm times a p of 0 would not be 0
+        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == SGEMM_BF16) {
+                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&w[i]), __float2bfloat162_rn(-1e30f));
+                w[i] = *reinterpret_cast<const uint32_t *>(&m);
+            } else {
+                const __half2 m = __hmax2(*reinterpret_cast<__half2 *>(&w[i]), __float2half2_rn(-65504.f));
+                w[i] = *reinterpret_cast<const uint32_t *>(&m);
+            }
+        }
+        unpack16<DT>(make_uint4(w[0], w[1], w[2], w[3]), v);
+        const F2 c(scale * kLog2e), off(-lse * kLog2e), a(A), b(B * kLn2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 t = fma(F2(v[2 * i], v[2 * i + 1]), c, off);
+            const float2 x = t.both();
+            const float2 d = (F2(exp2_approx(x.x), exp2_approx(x.y)) * fma(b, t, a)).both();
+            v[2 * i] = d.x;
+            v[2 * i + 1] = d.y;
+        }
+        uint4 out = pack16<DT>(v);
+        if (bits != 0xffu) {
+            uint32_t *o = &out.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] &= (bits >> (2 * i) & 1 ? 0xffffu : 0u) | (bits >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+        }
+        return out;
     }
 };
 
@@ -543,11 +669,15 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(const LogprobGra
         for (int u = 0; u < U; ++u) {
             const int at = base + u * THREADS + (int)threadIdx.x;
             if (at >= pieces) continue;
-            float v[VW];
-            P::unpack(raw[u], v);
             const int col = head + at * VW;
-            row.template apply<VW>(v, bits[u], col);
-            P::store(dz + col, v);
+            if constexpr (VW == 8) {
+                *reinterpret_cast<uint4 *>(dz + col) = row.template apply16<DT>(raw[u], bits[u] & 0xffu, col);
+            } else {
+                float v[VW];
+                P::unpack(raw[u], v);
+                row.template apply<VW>(v, bits[u], col);
+                P::store(dz + col, v);
+            }
         }
         if (VW > 1 && blockIdx.x == gridDim.x - 1 && (int)threadIdx.x < head + a.V - tail0) {
             const int col = (int)threadIdx.x < head ? (int)threadIdx.x : tail0 + (int)threadIdx.x - head;

@@ -68,6 +68,32 @@ __device__ __forceinline__ void f32x2_fma(uint64_t &d, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(d) : "l"(a), "l"(b));
 }
 
+// The same as a value type: two FP32 numbers on which one instruction works.
+struct F2 {
+    uint64_t v;
+    F2() = default;
+    __device__ F2(float a) : v(f32x2_dup(a)) {}
+    __device__ F2(float a, float b) : v(f32x2_pair(a, b)) {}
+    __device__ float2 both() const { return f32x2_unpack(v); }
+    __device__ float sum() const {
+        const float2 f = both();
+        return f.x + f.y;
+    }
+    __device__ friend F2 operator+(F2 a, F2 b) {
+        a.v = f32x2_add(a.v, b.v);
+        return a;
+    }
+    __device__ friend F2 operator*(F2 a, F2 b) {
+        a.v = f32x2_mul(a.v, b.v);
+        return a;
+    }
+    // a * b + c, rounded once
+    __device__ friend F2 fma(F2 a, F2 b, F2 c) {
+        f32x2_fma(c.v, a.v, b.v);
+        return c;
+    }
+};
+
 // ---------------------------------------------------------------- thread-block clusters (sm_90+)
 
 // Rank of this CTA in its cluster, and the cluster's CTA count (1 and 0 when

@@ -108,43 +108,65 @@ __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_s
 // Sums and maxima over the threads that share a row: a warp (warps == 1), the
 // block's warps through shared memory, or those of a cluster of `ranks` blocks
 // of up to 16 warps through distributed shared memory; in an order that the
-// numbers of warps and ranks fix, so every thread has the same bits.  Calls
-// alternate between two sets of slots, so one barrier a call is enough.
-// (Blocks of a cluster meet once more before they leave.)
+// numbers of warps and ranks fix, so every thread has the same bits.  Up to
+// three sums are taken together.  Calls alternate between two sets of slots, so
+// one barrier a call is enough.  (Blocks of a cluster meet once more before
+// they leave.)
 struct RowReducer {
-    float *slots;  // 2 x 32 floats of shared memory
+    static constexpr int SLOTS = 2 * 3 * 32;
+    float *slots;  // SLOTS floats of shared memory
     int warps, ranks = 1, turn = 0;
-    template <class Join>
-    __device__ uint32_t all(uint32_t v, uint32_t none, Join join) {
-        float *s = slots + 32 * turn;
+    template <int N, class Join>
+    __device__ void all(uint32_t (&v)[N], uint32_t none, Join join) {
+        float *s = slots + 96 * turn;
         turn ^= 1;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) s[warp] = __uint_as_float(v);
-        uint32_t got = none;
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[32 * i + warp] = __uint_as_float(v[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = none;
         if (ranks == 1) {
             __syncthreads();
-            if (lane < warps) got = __float_as_uint(s[lane]);
+            if (lane < warps)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = __float_as_uint(s[32 * i + lane]);
         } else {
             __syncwarp();
             cluster_sync();
             const int w = lane & 15;
             if (w < warps)
                 for (int r = lane >> 4; r < ranks; r += 2)
-                    got = join(got, dsmem_ld_u32(dsmem_map(smem_addr(s + w), (uint32_t)r)));
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        v[i] = join(v[i], dsmem_ld_u32(dsmem_map(smem_addr(s + 32 * i + w), (uint32_t)r)));
         }
-        return got;
+    }
+    template <int N>
+    __device__ void sum(float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if (warps == 1 && ranks == 1) return;
+        uint32_t bits[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) bits[i] = __float_as_uint(v[i]);
+        all(bits, 0u, [](uint32_t a, uint32_t b) {
+            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+        });
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(__uint_as_float(bits[i]));
     }
     __device__ float sum(float v) {
-        v = warp_sum(v);
-        if (warps == 1 && ranks == 1) return v;
-        return warp_sum(__uint_as_float(all(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
-            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-        })));
+        float one[1] = {v};
+        sum(one);
+        return one[0];
     }
     __device__ uint32_t max(uint32_t v) {
         v = warp_max(v);
         if (warps == 1 && ranks == 1) return v;
-        return warp_max(all(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; }));
+        uint32_t one[1] = {v};
+        all(one, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        return warp_max(one[0]);
     }
 };
 
