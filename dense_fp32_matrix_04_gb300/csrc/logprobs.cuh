@@ -401,21 +401,20 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             if (thread_max >= floor_v && thread_max > -INFINITY) again[atomicAdd(&again_count, 1)] = (uint8_t)threadIdx.x;
             if (outside.v >= floor_v && outside.v > -INFINITY) found.push(outside.v, outside.id);
             __syncthreads();
-            // the columns of one of those threads, 32 pieces at a time
-            auto columns = [&](int thread, auto take) {
-                for (int p = row.p0 + thread; p < row.p1; p += THREADS * 32) {
-                    const int at = p + lane * THREADS, col = head + at * VEC;
-                    const bool in = at < row.p1;
-                    float v[VEC];
-                    unpack16<DT>(in ? __ldg(reinterpret_cast<const uint4 *>(z + head) + at) : make_uint4(0, 0, 0, 0), v);
-                    const uint32_t bits = !in ? 0u : MASK ? mask_bits(mask, col, VEC, a.V) : ~0u;
+            // the columns of a piece
+            auto columns = [&](int at, auto take) {
+                const bool in = at < row.p1;
+                const int col = head + at * VEC;
+                float v[VEC];
+                unpack16<DT>(in ? __ldg(reinterpret_cast<const uint4 *>(z + head) + at) : make_uint4(0, 0, 0, 0), v);
+                const uint32_t bits = !in ? 0u : MASK ? mask_bits(mask, col, VEC, a.V) : ~0u;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) take((bits >> e & 1) && v[e] >= floor_v && v[e] > -INFINITY, v[e], col + e);
-                }
+                for (int e = 0; e < VEC; ++e) take((bits >> e & 1) && v[e] >= floor_v && v[e] > -INFINITY, v[e], col + e);
             };
-            const int n_again = again_count;
-            for (int i = warp; i < n_again; i += WARPS)
-                columns(again[i], [&](bool in, float v, int id) {
+            // all pieces of all those threads, one a thread
+            const int n_again = again_count, per = (row.p1 - row.p0 + THREADS - 1) / THREADS;
+            for (int i = threadIdx.x; i < n_again * per; i += THREADS)
+                columns(row.p0 + again[i / per] + (i % per) * THREADS, [&](bool in, float v, int id) {
                     if (in) found.push(v, id);
                 });
             __syncthreads();
@@ -439,7 +438,9 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
                     last_v = __shfl_sync(0xffffffffu, best.v, a.top - 1);
                     last_id = __shfl_sync(0xffffffffu, best.id, a.top - 1);
                 };
-                for (int i = warp; i < n_again; i += WARPS) columns(again[i], offer);
+                for (int i = warp; i < n_again; i += WARPS)
+                    for (int j = 0; j < per; j += 32)
+                        columns(j + lane < per ? row.p0 + again[i] + (j + lane) * THREADS : row.p1, offer);
                 offer(outside.v >= floor_v && outside.v > -INFINITY, outside.v, outside.id);
                 __syncthreads();
                 if (threadIdx.x == 0) found.count = 0;
@@ -491,11 +492,19 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
                 if constexpr (TOP) {
                     if (threadIdx.x == 0) found.count = 0;
                     __syncthreads();
+                    // no column below the largest of the lists' last can be among the best
+                    float v = -INFINITY;
+                    int id = INT_MAX;
                     if (warp < parts && lane < a.top) {
                         const uint32_t l = dsmem_map(smem_addr(&block_list[lane]), (uint32_t)warp);
-                        const float v = __uint_as_float(dsmem_ld_u32(l));
-                        if (v > -INFINITY) found.push(v, (int)dsmem_ld_u32(l + 4));
+                        v = __uint_as_float(dsmem_ld_u32(l));
+                        id = (int)dsmem_ld_u32(l + 4);
                     }
+                    if (lane == a.top - 1) group_max[warp] = v;
+                    __syncthreads();
+                    float floor_v = -INFINITY;
+                    for (int w = 0; w < WARPS; ++w) floor_v = fmaxf(floor_v, group_max[w]);
+                    if (v > -INFINITY && v >= floor_v) found.push(v, id);
                     __syncthreads();  // block 0's own list has been read before it is written
                     if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
                     __syncthreads();

@@ -12,6 +12,7 @@ torch operation; what a call allocates itself is marked as used on its stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 _I, _F, _P, _S = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -30,106 +31,117 @@ SIGNATURES = {
     "sgemm_logprobs_backward": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
 }
 
-_codes = None
-_lib = None
+# Set on the first call: torch, the library, the codes of the element types.
+# What a call costs on the host is a few microseconds, which a decoding step
+# sees, so the checks below ask a tensor as little as they can.
+_torch = _lib = None
+_codes = {}
+_raw_stream = None
 
 
-def _library():
-    global _lib
-    if _lib is None:
-        from . import load
-        _lib = load()
-    return _lib
+def _start():
+    global _torch, _lib, _raw_stream
+    import torch
+
+    from . import load
+    _lib = load()
+    _codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _torch = torch
 
 
 def _check(status, where):
-    if status:
-        from . import SgemmError
-        raise SgemmError(status, where)
+    from . import SgemmError
+    raise SgemmError(status, where)
 
 
-def _dtype(t, name):
-    """The library's code of a tensor's element type."""
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    code = _codes.get(t if not hasattr(t, "dtype") else t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    return code
+def _first(t, name, dtypes=None):
+    """(element type, device index, shape) of a call's first tensor, a 2-D CUDA one."""
+    if _torch is None:
+        _start()
+    dtype = t.dtype
+    if dtype not in (_codes if dtypes is None else dtypes):
+        raise TypeError(f"{name} must be {'float32, bfloat16 or float16' if dtypes is None else dtypes[0]}")
+    index = t.get_device()
+    if index < 0 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D CUDA tensor")
+    return dtype, index, t.shape
 
 
-def _matrix(t, name, dtype, rows=None, cols=None, device=None):
-    """(pointer, leading dimension) of a 2-D CUDA tensor with unit column stride."""
-    shape = t.shape
-    if len(shape) != 2 or not t.is_cuda or t.dtype != dtype:
+def _matrix(t, name, dtype, index, shape=None, cols=None):
+    """(pointer, leading dimension) of a 2-D CUDA tensor with unit column stride, of
+    this shape, or of this many columns."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+        if t.dtype is dtype and t.dim() == 2 and t.get_device() >= 0:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
         raise TypeError(f"{name} must be a 2-D {dtype} CUDA tensor")
-    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} is {tuple(shape)}, not ({rows}, {cols})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    rows, n = t.shape
+    if (shape is not None and (rows != shape[0] or n != shape[1])) or (cols is not None and n != cols):
+        raise ValueError(f"{name} is ({rows}, {n}), not {tuple(shape) if shape is not None else ('any', cols)}")
+    if t.is_contiguous():
+        return t.data_ptr(), n or 1
     s0, s1 = t.stride()
-    if shape[1] > 1 and s1 != 1:
+    if n > 1 and s1 != 1:
         raise ValueError(f"{name} must have unit column stride")
-    if shape[0] > 1:
-        if s0 < shape[1]:
+    if rows > 1:
+        if s0 < n:
             raise ValueError(f"{name} has rows that overlap")
-        return t.data_ptr(), max(s0, 1)
-    return t.data_ptr(), max(shape[1], 1)
+        return t.data_ptr(), s0 or 1
+    return t.data_ptr(), n or 1
 
 
-def _vector(t, name, n, dtypes, device):
+def _vector(t, name, n, dtypes, index):
     """Pointer of a dense 1-D CUDA tensor of n elements."""
-    if t.dtype not in dtypes or not t.is_cuda or t.dim() != 1:
+    if t.dtype not in dtypes or t.get_device() < 0 or t.dim() != 1:
         raise TypeError(f"{name} must be a 1-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
     if t.shape[0] != n:
         raise ValueError(f"{name} has {t.shape[0]} elements, not {n}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if n > 1 and t.stride(0) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be dense")
     return t.data_ptr()
 
 
-class _Call:
-    """The device and stream of a call: makes the tensors' device current, and
-    marks what the call allocated as used on a stream that is not torch's."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.torch, self.device = torch, device
-        self.other = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-            self.guard.__enter__()
-        else:
-            self.guard = None
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
-        else:
-            self.handle = stream if isinstance(stream, int) else int(stream.cuda_stream)
-            if self.handle != torch._C._cuda_getCurrentRawStream(device.index):
-                self.other = (stream if not isinstance(stream, int)
-                              else torch.cuda.ExternalStream(stream, device=device))
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *_):
-        if self.guard is not None:
-            self.guard.__exit__(None, None, None)
-
-    def empty(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            # allocated on torch's current stream, used on another
-            self.other.wait_stream(self.torch.cuda.current_stream(self.device))
-            t.record_stream(self.other)
-        return t
+def _on(index, stream):
+    """The raw handle of the stream that a call on the current device runs on."""
+    if stream is None:
+        return _raw_stream(index)
+    return stream if isinstance(stream, int) else int(stream.cuda_stream)
 
 
-def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantize=False, out=None, stream=None):
+def _foreign(fn):
+    """Runs a call whose tensors are on another device than the current one, or whose
+    stream is not torch's: with the device made current, and with what the call
+    allocates (on torch's stream) ordered before and marked as used on its stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **more):
+        if _torch is None:
+            _start()
+        index = first.get_device() if hasattr(first, "get_device") else -1
+        if stream is None and (index < 0 or index == _torch._C._cuda_getDevice()):
+            return fn(first, *args, **more)
+        if index < 0:
+            return fn(first, *args, stream=stream, **more)  # refuses it
+        with _torch.cuda.device(index):
+            handle = _on(index, stream)
+            if handle == _raw_stream(index):
+                return fn(first, *args, **more)
+            other = _torch.cuda.ExternalStream(handle, device=index) if isinstance(stream, int) else stream
+            # the inputs are the caller's to order; what is allocated here may have been freed by
+            # work that is still queued on torch's stream
+            other.wait_stream(_torch.cuda.current_stream(index))
+            kept = []
+            got = fn(first, *args, stream=stream, keep=kept, **more)
+            for t in kept:
+                t.record_stream(other)
+            return got
+    return call
+
+
+@_foreign
+def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantize=False, out=None, stream=None,
+               keep=None):
     """The step from one block's output ``y`` and the residual stream ``x`` (T x D)
     to the next block's input:
 
@@ -141,201 +153,218 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     8-bit integers with a scale per row.  ``rstd`` (2 x T) is for the backward
     pass.  ``out`` receives r; it may be x.
     """
-    import torch
-    dt, dev = x.dtype, x.device
-    T, D = x.shape
-    px, ldx = _matrix(x, "x", dt)
-    py, ldy = _matrix(y, "y", dt, T, D, dev)
-    code = _dtype(x, "x")
-    weights = (torch.float32, dt)
-    p_pre = _vector(w_pre, "w_pre", D, weights, dev)
-    p_post = _vector(w_post, "w_post", D, (w_pre.dtype,), dev) if w_post is not None else 0
+    dt, dev, shape = _first(x, "x")
+    f32, empty, where = _torch.float32, _torch.empty, x.device
+    T, D = shape
+    px, ldx = _matrix(x, "x", dt, dev)
+    py, ldy = _matrix(y, "y", dt, dev, shape)
+    wt = w_pre.dtype
+    p_pre = _vector(w_pre, "w_pre", D, (f32, dt), dev)
+    p_post = _vector(w_post, "w_post", D, (wt,), dev) if w_post is not None else 0
     pg, ldg, G = 0, 1, 0
     if gate is not None:
-        pg, ldg = _matrix(gate, "gate", dt, None, D, dev)
+        pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
-    with _Call(dev, stream) as c:
-        r = c.empty((T, D), dt) if out is None else out
-        pr, ldr = _matrix(r, "out", dt, T, D, dev)
-        rstd = c.empty((2, T), torch.float32)
-        n = q = s = None
-        if quantize:
-            q, s = c.empty((T, D), torch.int8), c.empty((T,), torch.float32)
-        else:
-            n = c.empty((T, D), dt)
-        _check(_library().sgemm_block_norm(
-            T, D, code, px, ldx, py, ldy, p_pre, p_post, _dtype(w_pre, "w_pre"), pg, ldg, G, scale, eps, pr, ldr,
-            n.data_ptr() if n is not None else 0, max(D, 1), q.data_ptr() if quantize else 0, max(D, 1),
-            s.data_ptr() if quantize else 0, rstd.data_ptr(), c.handle), "sgemm_block_norm")
-    return (r, q, s, rstd) if quantize else (r, n, rstd)
+    r = empty(shape, dtype=dt, device=where) if out is None else out
+    pr, ldr = _matrix(r, "out", dt, dev, shape) if out is not None else (r.data_ptr(), D or 1)
+    rstd = empty((2, T), dtype=f32, device=where)
+    if quantize:
+        q, s = empty(shape, dtype=_torch.int8, device=where), empty((T,), dtype=f32, device=where)
+        made, pn, pq, ps = (r, q, s, rstd), 0, q.data_ptr(), s.data_ptr()
+    else:
+        n = empty(shape, dtype=dt, device=where)
+        made, pn, pq, ps = (r, n, rstd), n.data_ptr(), 0, 0
+    status = _lib.sgemm_block_norm(T, D, _codes[dt], px, ldx, py, ldy, p_pre, p_post, _codes[wt], pg, ldg, G, scale, eps,
+                                   pr, ldr, pn, D or 1, pq, D or 1, ps, rstd.data_ptr(), _on(dev, stream))
+    if status:
+        _check(status, "sgemm_block_norm")
+    if keep is not None:
+        keep += made
+    return made
 
 
-def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, scale=1.0, stream=None):
+@_foreign
+def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, scale=1.0, stream=None, keep=None):
     """Gradients ``(dx, dy, dw_pre, dw_post, dgate)`` of ``block_norm`` from those of
     its n and r (``dr`` None: zero); ``dw_post`` and ``dgate`` are None where there is
     no such input."""
-    import torch
-    dt, dev = x.dtype, x.device
-    T, D = x.shape
-    px, ldx = _matrix(x, "x", dt)
-    py, ldy = _matrix(y, "y", dt, T, D, dev)
-    pn, ldn = _matrix(dn, "dn", dt, T, D, dev)
-    pr, ldr = _matrix(dr, "dr", dt, T, D, dev) if dr is not None else (0, max(D, 1))
-    code = _dtype(x, "x")
-    p_pre = _vector(w_pre, "w_pre", D, (torch.float32, dt), dev)
-    p_post = _vector(w_post, "w_post", D, (w_pre.dtype,), dev) if w_post is not None else 0
-    if rstd.dtype != torch.float32 or tuple(rstd.shape) != (2, T) or not rstd.is_contiguous() or rstd.device != dev:
+    dt, dev, shape = _first(x, "x")
+    f32, empty, where = _torch.float32, _torch.empty, x.device
+    T, D = shape
+    px, ldx = _matrix(x, "x", dt, dev)
+    py, ldy = _matrix(y, "y", dt, dev, shape)
+    pn, ldn = _matrix(dn, "dn", dt, dev, shape)
+    pr, ldr = _matrix(dr, "dr", dt, dev, shape) if dr is not None else (0, D or 1)
+    wt = w_pre.dtype
+    p_pre = _vector(w_pre, "w_pre", D, (f32, dt), dev)
+    p_post = _vector(w_post, "w_post", D, (wt,), dev) if w_post is not None else 0
+    if rstd.dtype is not f32 or rstd.shape != (2, T) or not rstd.is_contiguous() or rstd.get_device() != dev:
         raise ValueError("rstd must be the (2, T) float32 tensor that block_norm returned")
     pg, ldg, G = 0, 1, 0
     if gate is not None:
-        pg, ldg = _matrix(gate, "gate", dt, None, D, dev)
+        pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
-    with _Call(dev, stream) as c:
-        dx, dy = c.empty((T, D), dt), c.empty((T, D), dt)
-        dw_pre = c.empty((D,), w_pre.dtype)
-        dw_post = c.empty((D,), w_pre.dtype) if w_post is not None else None
-        dgate = c.empty((G, D), dt) if gate is not None else None
-        lib = _library()
-        need = lib.sgemm_block_norm_backward_workspace_size(T, D)
-        ws = c.empty((need,), torch.uint8)
-        _check(lib.sgemm_block_norm_backward(
-            T, D, code, px, ldx, py, ldy, p_pre, p_post, _dtype(w_pre, "w_pre"), pg, ldg, G, scale, rstd.data_ptr(),
-            pn, ldn, pr, ldr, dx.data_ptr(), max(D, 1), dy.data_ptr(), max(D, 1), dw_pre.data_ptr(),
-            dw_post.data_ptr() if dw_post is not None else 0, dgate.data_ptr() if dgate is not None else 0,
-            max(D, 1), ws.data_ptr(), need, c.handle), "sgemm_block_norm_backward")
-    return dx, dy, dw_pre, dw_post, dgate
+    dx, dy = empty(shape, dtype=dt, device=where), empty(shape, dtype=dt, device=where)
+    dw_pre = empty((D,), dtype=wt, device=where)
+    dw_post = empty((D,), dtype=wt, device=where) if w_post is not None else None
+    dgate = empty((G, D), dtype=dt, device=where) if gate is not None else None
+    need = _lib.sgemm_block_norm_backward_workspace_size(T, D)
+    ws = empty((need,), dtype=_torch.uint8, device=where)
+    status = _lib.sgemm_block_norm_backward(
+        T, D, _codes[dt], px, ldx, py, ldy, p_pre, p_post, _codes[wt], pg, ldg, G, scale, rstd.data_ptr(), pn, ldn, pr,
+        ldr, dx.data_ptr(), D or 1, dy.data_ptr(), D or 1, dw_pre.data_ptr(),
+        dw_post.data_ptr() if dw_post is not None else 0, dgate.data_ptr() if dgate is not None else 0, D or 1,
+        ws.data_ptr(), need, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_block_norm_backward")
+    made = (dx, dy, dw_pre, dw_post, dgate)
+    if keep is not None:
+        keep += [t for t in (*made, ws) if t is not None]
+    return made
 
 
-def quantize_i8(x, stream=None):
+@_foreign
+def quantize_i8(x, stream=None, keep=None):
     """``(q, scale)``: the rows of x (M x K) as 8-bit integers, scale = max|row| / 127
     and q = rint(row * (127 / max|row|)).  For activations a scale per token, for
     weights (N x K) one per output channel."""
-    import torch
-    code = _dtype(x, "x")
-    px, ldx = _matrix(x, "x", x.dtype)
-    M, K = x.shape
-    with _Call(x.device, stream) as c:
-        q, s = c.empty((M, K), torch.int8), c.empty((M,), torch.float32)
-        _check(_library().sgemm_quantize_i8(M, K, code, px, ldx, q.data_ptr(), max(K, 1), s.data_ptr(), c.handle),
-               "sgemm_quantize_i8")
+    dt, dev, shape = _first(x, "x")
+    px, ldx = _matrix(x, "x", dt, dev)
+    M, K = shape
+    q = _torch.empty(shape, dtype=_torch.int8, device=x.device)
+    s = _torch.empty((M,), dtype=_torch.float32, device=x.device)
+    status = _lib.sgemm_quantize_i8(M, K, _codes[dt], px, ldx, q.data_ptr(), K or 1, s.data_ptr(), _on(dev, stream))
+    if status:
+        _check(status, "sgemm_quantize_i8")
+    if keep is not None:
+        keep += [q, s]
     return q, s
 
 
-def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
-    """``a_scale[m] * w_scale[n] * sum_k a[m, k] w[n, k] + bias[n]`` for 8-bit integers
-    a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise)."""
-    import torch
-    dev = a.device
-    pa, lda = _matrix(a, "a", torch.int8)
-    M, K = a.shape
-    pw, ldw = _matrix(w, "w", torch.int8, None, K, dev)
-    N = w.shape[0]
-    f32 = (torch.float32,)
-    ps, pt = _vector(a_scale, "a_scale", M, f32, dev), _vector(w_scale, "w_scale", N, f32, dev)
-    pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
-    with _Call(dev, stream) as c:
-        if out is None:
-            out = c.empty((M, N), out_dtype or torch.float32)
-        code = _dtype(out, "out")
-        po, ldo = _matrix(out, "out", out_dtype or out.dtype, M, N, dev)
-        lib = _library()
-        need = lib.sgemm_i8_workspace_size(M, N, K, pw, ldw)
-        if workspace is None and need:
-            workspace = c.empty((need,), torch.uint8)
-        size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.sgemm_i8(M, N, K, pa, lda, ps, pw, ldw, pt, pb, po, ldo, code,
-                            workspace.data_ptr() if size else 0, size, c.handle), "sgemm_i8")
-    return out
-
-
-def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
-    """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
-    quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise."""
-    import torch
-    dev = x.device
-    xcode = _dtype(x, "x")
-    px, ldx = _matrix(x, "x", x.dtype)
+def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, stream, keep, size_of):
+    """What matmul_i8 and linear_i8 share: the weights, the output and the workspace."""
+    dev = x.get_device()
     M, K = x.shape
-    pw, ldw = _matrix(w, "w", torch.int8, None, K, dev)
+    pw, ldw = _matrix(w, "w", _torch.int8, dev, None, K)
     N = w.shape[0]
-    f32 = (torch.float32,)
+    f32 = (_torch.float32,)
     pt = _vector(w_scale, "w_scale", N, f32, dev)
     pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
-    with _Call(dev, stream) as c:
-        if out is None:
-            out = c.empty((M, N), out_dtype or x.dtype)
-        code = _dtype(out, "out")
-        po, ldo = _matrix(out, "out", out_dtype or out.dtype, M, N, dev)
-        lib = _library()
-        need = lib.sgemm_linear_i8_workspace_size(M, N, K, pw, ldw)
-        if workspace is None and need:
-            workspace = c.empty((need,), torch.uint8)
-        size = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.sgemm_linear_i8(M, N, K, xcode, px, ldx, pw, ldw, pt, pb, po, ldo, code,
-                                   workspace.data_ptr() if size else 0, size, c.handle), "sgemm_linear_i8")
+    if out is None:
+        if out_dtype not in _codes:
+            raise TypeError("out_dtype must be float32, bfloat16 or float16")
+        out = _torch.empty((M, N), dtype=out_dtype, device=x.device)
+        po, ldo = out.data_ptr(), N or 1
+        if keep is not None:
+            keep.append(out)
+    else:
+        out_dtype = out.dtype
+        if out_dtype not in _codes:
+            raise TypeError("out must be float32, bfloat16 or float16")
+        po, ldo = _matrix(out, "out", out_dtype, dev, (M, N))
+    pws = size = 0
+    if workspace is not None:
+        pws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        size = size_of(M, N, K, pw, ldw)
+        if size:
+            workspace = _torch.empty((size,), dtype=_torch.uint8, device=x.device)
+            pws = workspace.data_ptr()
+            if keep is not None:
+                keep.append(workspace)
+    status = call(M, N, K, *head, pw, ldw, pt, pb, po, ldo, _codes[out_dtype], pws, size, _on(dev, stream))
+    if status:
+        _check(status, where)
     return out
 
 
-def _mask(mask, T, V, device):
+@_foreign
+def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, keep=None):
+    """``a_scale[m] * w_scale[n] * sum_k a[m, k] w[n, k] + bias[n]`` for 8-bit integers
+    a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise)."""
+    if _torch is None:
+        _start()
+    _, dev, shape = _first(a, "a", (_torch.int8,))
+    pa, lda = _matrix(a, "a", _torch.int8, dev)
+    ps = _vector(a_scale, "a_scale", shape[0], (_torch.float32,), dev)
+    return _linear(_lib.sgemm_i8, "sgemm_i8", a, (pa, lda, ps), w, w_scale, bias, out_dtype or _torch.float32, out,
+                   workspace, stream, keep, _lib.sgemm_i8_workspace_size)
+
+
+@_foreign
+def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, keep=None):
+    """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
+    quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise."""
+    dt, dev, _ = _first(x, "x")
+    px, ldx = _matrix(x, "x", dt, dev)
+    return _linear(_lib.sgemm_linear_i8, "sgemm_linear_i8", x, (_codes[dt], px, ldx), w, w_scale, bias, out_dtype or dt,
+                   out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)
+
+
+def _mask(mask, T, V, index):
     """(pointer, words between rows, rows) of a mask of ceil(V / 32) words a row."""
-    import torch
     if mask is None:
         return 0, 0, 0
-    pm, ldm = _matrix(mask, "mask", torch.int32, None, (V + 31) // 32, device)
-    if mask.shape[0] not in (1, T):
-        raise ValueError(f"mask has {mask.shape[0]} rows, not 1 or {T}")
-    return pm, ldm, mask.shape[0]
+    pm, ldm = _matrix(mask, "mask", _torch.int32, index, None, (V + 31) // 32)
+    rows = mask.shape[0]
+    if rows not in (1, T):
+        raise ValueError(f"mask has {rows} rows, not 1 or {T}")
+    return pm, ldm, rows
 
 
-def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None):
+@_foreign
+def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, keep=None):
     """``(logprob, entropy, lse)`` per row of ``softmax(scale * logits)`` (T x V), and with
     ``top`` > 0 also ``(top_logprob, top_id)`` (T x top), most likely first.
 
     ``target``: T int64 columns; a negative one is not scored (logprob 0).
     ``mask``: int32 words, 1 or T rows of ceil(V / 32), bit j % 32 of word j // 32 set
     where column j is allowed."""
-    import torch
-    code = _dtype(logits, "logits")
-    dev = logits.device
-    pz, ldz = _matrix(logits, "logits", logits.dtype)
-    T, V = logits.shape
-    py = _vector(target, "target", T, (torch.int64,), dev)
+    dt, dev, (T, V) = _first(logits, "logits")
+    pz, ldz = _matrix(logits, "logits", dt, dev)
+    py = _vector(target, "target", T, (_torch.int64,), dev)
     pm, ldm, rows = _mask(mask, T, V, dev)
-    with _Call(dev, stream) as c:
-        three = c.empty((3, T), torch.float32)
-        p = three.data_ptr()
-        got = three.unbind(0)
-        pv = pi = 0
-        if top:
-            values, ids = c.empty((T, top), torch.float32), c.empty((T, top), torch.int32)
-            pv, pi = values.data_ptr(), ids.data_ptr()
-            got = (*got, values, ids)
-        _check(_library().sgemm_logprobs(T, V, code, pz, ldz, scale, pm, ldm, rows, py, p, p + 4 * T, p + 8 * T, top,
-                                         pv, pi, c.handle), "sgemm_logprobs")
+    empty, f32, where = _torch.empty, _torch.float32, logits.device
+    got = (empty((T,), dtype=f32, device=where), empty((T,), dtype=f32, device=where),
+           empty((T,), dtype=f32, device=where))
+    pv = pi = 0
+    if top > 0:
+        got += (empty((T, top), dtype=f32, device=where), empty((T, top), dtype=_torch.int32, device=where))
+        pv, pi = got[3].data_ptr(), got[4].data_ptr()
+    status = _lib.sgemm_logprobs(T, V, _codes[dt], pz, ldz, scale, pm, ldm, rows, py, got[0].data_ptr(),
+                                 got[1].data_ptr(), got[2].data_ptr(), top, pv, pi, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_logprobs")
+    if keep is not None:
+        keep += got
     return got
 
 
+@_foreign
 def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, scale=1.0, mask=None, out=None,
-                      stream=None):
+                      stream=None, keep=None):
     """The gradient with respect to the logits of ``logprobs``' logprob and entropy, from
     theirs (``g_entropy`` None: no gradient reaches the entropy).  ``out`` may be the
     logits themselves."""
-    import torch
-    code = _dtype(logits, "logits")
-    dev = logits.device
-    pz, ldz = _matrix(logits, "logits", logits.dtype)
-    T, V = logits.shape
-    py = _vector(target, "target", T, (torch.int64,), dev)
-    f32 = (torch.float32,)
+    dt, dev, shape = _first(logits, "logits")
+    T, V = shape
+    pz, ldz = _matrix(logits, "logits", dt, dev)
+    py = _vector(target, "target", T, (_torch.int64,), dev)
+    f32 = (_torch.float32,)
     pl = _vector(lse, "lse", T, f32, dev)
     ph = _vector(entropy, "entropy", T, f32, dev) if entropy is not None else 0
     pg = _vector(g_logprob, "g_logprob", T, f32, dev)
     pe = _vector(g_entropy, "g_entropy", T, f32, dev) if g_entropy is not None else 0
     pm, ldm, rows = _mask(mask, T, V, dev)
-    with _Call(dev, stream) as c:
-        if out is None:
-            out = c.empty((T, V), logits.dtype)
-        po, ldo = _matrix(out, "out", logits.dtype, T, V, dev)
-        _check(_library().sgemm_logprobs_backward(T, V, code, pz, ldz, scale, pm, ldm, rows, py, pl, ph, pg, pe, po,
-                                                  ldo, c.handle), "sgemm_logprobs_backward")
+    if out is None:
+        out = _torch.empty(shape, dtype=dt, device=logits.device)
+        po, ldo = out.data_ptr(), V or 1
+        if keep is not None:
+            keep.append(out)
+    else:
+        po, ldo = _matrix(out, "out", dt, dev, shape)
+    status = _lib.sgemm_logprobs_backward(T, V, _codes[dt], pz, ldz, scale, pm, ldm, rows, py, pl, ph, pg, pe, po, ldo,
+                                          _on(dev, stream))
+    if status:
+        _check(status, "sgemm_logprobs_backward")
     return out
