@@ -33,7 +33,10 @@ int launch_quantize(int M, int K, const void *x, int ldx, Code *q, int64_t ldq, 
     const int threads = std::max(1, (K + 511) / 512) * 32;  // 16 elements a thread
     const dim3 block(threads, threads == 32 ? 4 : 1);
     const int64_t groups = ((int64_t)M + block.y - 1) / block.y;
-    const int64_t most = (int64_t)dev.sms * std::max(1, 2048 / (int)(block.x * block.y));
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, quantize_i8_kernel<DT, VW, NV, Code>, (int)(block.x * block.y), 0);
+    if (!fit) return SGEMM_ERR_LAUNCH;
+    const int64_t most = (int64_t)dev.sms * fit;
     const int q_vec = aligned(q, VW > 1 ? VW : 1) && ldq % VW == 0;
     return launch(quantize_i8_kernel<DT, VW, NV, Code>, dim3((unsigned)std::min(groups, most)), block, 0, stream, 1, M,
                   K, static_cast<const type *>(x), (int64_t)ldx, q, ldq, s, q_vec);
@@ -123,15 +126,18 @@ struct StreamPlan {
         static constexpr struct {
             int tok, bk;
             double step;
-        } kSteps[] = {{16, 128, 760}, {32, 128, 770}, {64, 128, 850}, {128, 128, 1050}, {256, 64, 680}};
+        } kSteps[] = {{16, 128, 760}, {32, 128, 770}, {64, 128, 850}, {128, 128, 1050},
+                      {192, 64, 560}, {208, 64, 590}, {224, 64, 620}, {240, 64, 650}, {256, 64, 680}};
         double best = 1e300;
         for (const auto &c : kSteps) {
             const int steps = (K + c.bk - 1) / c.bk;
             const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + 127) / 128);
             for (int s = 1; s <= 16 && s <= (steps + 3) / 4; ++s) {
                 const int64_t rounds = (tiles * s + sms - 1) / sms;
-                double t = (double)rounds * (((steps + s - 1) / s) * c.step + 12 * c.tok) + 2000;
-                if (s > 1) t += 5000 + (double)s * M * N * 8 / 2500;
+                // a tile's drain shows where there is no second accumulator
+                const double drain = c.tok <= 192 ? 1000 : 14. * c.tok;
+                double t = (double)rounds * (((steps + s - 1) / s) * c.step + drain) + 2000;
+                if (s > 1) t += 5000 + (double)s * M * N * 8 / 1500;
                 if (t < best) best = t, tok = c.tok, splits = s;
             }
             if (M <= c.tok) break;
@@ -174,6 +180,10 @@ int stream_product(I8Args p, const __half *x, int8_t *rows, float *partials, con
         case 32: st = launch_stream<32>(p, x, plan, partials, dev, stream); break;
         case 64: st = launch_stream<64>(p, x, plan, partials, dev, stream); break;
         case 128: st = launch_stream<128>(p, x, plan, partials, dev, stream); break;
+        case 192: st = launch_stream<192>(p, x, plan, partials, dev, stream); break;
+        case 208: st = launch_stream<208>(p, x, plan, partials, dev, stream); break;
+        case 224: st = launch_stream<224>(p, x, plan, partials, dev, stream); break;
+        case 240: st = launch_stream<240>(p, x, plan, partials, dev, stream); break;
         default: st = launch_stream<256>(p, x, plan, partials, dev, stream);
     }
     if (st != SGEMM_OK || plan.splits == 1) return st;

@@ -43,14 +43,25 @@ __global__ void __launch_bounds__(1024)
     RowReducer red{slots, (int)(blockDim.x >> 5)};
     const int threads = blockDim.x;
     const int step = gridDim.x * blockDim.y;
-    for (int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; m < M; m += step) {
-        float v[NV * VW];
-        uint32_t top = 0;
+    // the next row is on its way while this one is reduced and written (rows of single elements,
+    // and FP32 ones, have no registers for that)
+    constexpr bool AHEAD = VW == 8;
+    typename P::raw next[NV];
+    auto load = [&](int64_t m) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * threads + (int)threadIdx.x) * VW;
-            P::unpack(c < K ? P::load(x + m * ldx + c) : P::zero(), v + i * VW);
+            next[i] = m < M && c < K ? P::load(x + m * ldx + c) : P::zero();
         }
+    };
+    if (AHEAD) load((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
+    for (int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; m < M; m += step) {
+        float v[NV * VW];
+        uint32_t top = 0;
+        if (!AHEAD) load(m);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) P::unpack(next[i], v + i * VW);
+        if (AHEAD) load(m + step);
 #pragma unroll
         for (int i = 0; i < NV * VW; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
         const I8Scale s(red.max(top));

@@ -12,7 +12,7 @@
 // B as FP16 in shared memory would be beyond it.
 //
 // One block per SM walks units (tile, k-split): one thread copies by TMA into a
-// ring, sixteen warps convert, one thread issues the products, four warps drain
+// ring, eight warps convert, one thread issues the products, four warps drain
 // the accumulator, apply the scales and the bias and store.  Every wait is
 // bounded; a block that gives up records an error code, stores nothing more and
 // frees its tensor memory.
@@ -36,12 +36,12 @@ struct I8StreamTile {
     static constexpr int BK = TOK <= 128 ? 128 : 64;
     // warps: 0 copies, 1 products, then SETS sets of four that convert every SETS-th k-step, and
     // four that drain
-    static constexpr int SETS = 4, CONVERT = 4, DRAIN = CONVERT + 4 * SETS, THREADS = 32 * (DRAIN + 4);
+    static constexpr int SETS = 2, CONVERT = 4, DRAIN = CONVERT + 4 * SETS, THREADS = 32 * (DRAIN + 4);
     static constexpr int W_BYTES = ROWS * BK, X_BOX = TOK * 128, X_BYTES = X_BOX * (BK / 64), STAGE = W_BYTES + X_BYTES;
     // a stage is shared memory for both operands and BK / 2 columns of tensor memory for the codes of B
     static constexpr int A_COLS = BK / 2;
     // accumulators: two where tensor memory has room for both beside four stages
-    static constexpr int ACCS = TOK <= 128 ? 2 : 1;
+    static constexpr int ACCS = TOK <= 192 ? 2 : 1;
     static constexpr int ACC_COLS = TOK < 32 ? 32 : TOK;
     static constexpr int FIT_SMEM = (227 * 1024 - 1024 - 256) / STAGE, FIT_TMEM = (512 - ACCS * ACC_COLS) / A_COLS;
     static constexpr int STAGES = FIT_SMEM < FIT_TMEM ? FIT_SMEM : FIT_TMEM;
@@ -171,27 +171,41 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
             prefetch_tensor_map(&tmW);
             prefetch_tensor_map(&tmX);
         }
-        // the tokens may come from the kernel before, which B does not
+        // Copies of step k of a unit into the ring's next stage: B's part, which announces both, and
+        // the tokens'.
+        auto copy_b = [&](uint32_t at, int k, int n0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(full0 + 8 * at, T::STAGE);
+                tma_load_2d(w_base + at * T::W_BYTES, &tmW, k * T::BK, n0, full0 + 8 * at);
+            }
+        };
+        auto copy_tokens = [&](uint32_t at, int k, int m0) {
+            if (elect_one())
+#pragma unroll
+                for (int h = 0; h < T::BK / 64; ++h)
+                    tma_load_2d(base + at * T::X_BYTES + h * T::X_BOX, &tmX, k * T::BK + 64 * h, m0, full0 + 8 * at);
+        };
+        // the tokens may come from the kernel before, which B does not: the first unit's first stages
+        // of B are on their way before that kernel is waited for
+        int ahead = 0, m0, n0, k0, n;
+        if (!(debug & 1) && (int)blockIdx.x < units) {
+            unit(blockIdx.x, m0, n0, k0, n);
+            for (ahead = min(n, T::STAGES); issued < ahead; ++issued) copy_b(issued, k0 + issued, n0);
+        }
         griddep_wait();
+        for (int k = 0; k < ahead; ++k, s.next()) copy_tokens(k, k0 + k, m0);
         bool ok = true;
         for (int u = blockIdx.x; ok && !(debug & 1) && u < units; u += gridDim.x) {
-            int m0, n0, k0, n;
             unit(u, m0, n0, k0, n);
-            for (int k = k0; k < k0 + n; ++k) {
+            for (int k = k0 + (u == (int)blockIdx.x ? ahead : 0); k < k0 + n; ++k) {
                 if (issued >= T::STAGES) ok = mbar_wait_polite(empty0 + 8 * s.at, s.round ^ 1, wait_limit_ns, 0);
                 if (!__all_sync(0xffffffffu, ok)) {
                     *abort_flag = 1;
                     ok = false;
                     break;
                 }
-                if (elect_one()) {
-                    const uint32_t bar = full0 + 8 * s.at, x = base + s.at * T::X_BYTES;
-                    mbar_arrive_expect_tx(bar, T::STAGE);
-                    tma_load_2d(w_base + s.at * T::W_BYTES, &tmW, k * T::BK, n0, bar);
-#pragma unroll
-                    for (int h = 0; h < T::BK / 64; ++h)
-                        tma_load_2d(x + h * T::X_BOX, &tmX, k * T::BK + 64 * h, m0, bar);
-                }
+                copy_b(s.at, k, n0);
+                copy_tokens(s.at, k, m0);
                 __syncwarp();
                 ++issued;
                 s.next();
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
             const float bias = in && splits == 1 && p.bias ? p.bias[col] : 0.f;
             float *slab = splits > 1 ? partials + (int64_t)(u / tiles) * p.M * ldp : nullptr;
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b.at * T::ACC_COLS;
-            constexpr int CHUNK = TOK < 32 ? 16 : 32;
+            constexpr int CHUNK = TOK % 32 ? 16 : 32;
 #pragma unroll 1
             for (int c0 = 0; c0 < TOK; c0 += CHUNK) {
                 float v[32];
