@@ -37,7 +37,7 @@ struct Rows {
 int row_threads(int D, int per) { return ((D + per - 1) / per + 31) / 32 * 32; }
 
 constexpr int kMaxRows = 1 << 30;
-constexpr int kMaxWidth = 24576;  // eight blocks of 3072: FP32 rows with every input fit their rings
+constexpr int kMaxWidth = 24576;  // over a cluster of eight blocks, FP32 rows with every input fit their rings
 
 bool finite(float v) { return std::isfinite(v); }
 
@@ -57,7 +57,7 @@ struct RowPlan {
             width = ranks == 1 ? D : ((D + ranks - 1) / ranks + vec - 1) / vec * vec;
             const int threads = row_threads(width, per);
             block = dim3(threads, threads == 32 && ranks == 1 ? 4 : 1);
-            smem = (size_t)slots * row_pieces(width, size) * 16 * block.y;
+            smem = (size_t)slots * row_pieces(threads, per, size) * 16 * block.y;
             if (ranks == 8 || (threads <= most && smem <= 225 * 1024)) break;
         }
     }
@@ -94,25 +94,34 @@ int norm_by_width(const BlockNormArgs &a, const Device &dev, cudaStream_t stream
 // narrow rows a warp each.  Every one writes its own partial sums, so there are
 // no more than the SMs hold at once, 512 threads of 128 registers each; this is
 // the most there can be for any type and alignment.
-int most_grad_runners(int T, int D, int sms) { return std::min(T, std::max(1, 512 * sms / row_threads(D, 8))); }
+int most_grad_runners(int T, int D, int sms) { return std::min(T, std::max(1, 512 * sms / row_threads(D, 16))); }
 
-template <int DT, bool ALIGNED>
+template <int DT, bool ALIGNED, bool TOKEN, int PER>
 int launch_norm_grad(BlockNormGradArgs a, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
     constexpr int most = ALIGNED ? 512 : 480;  // single elements take more registers
-    const auto kernel = block_norm_grad_kernel<DT, ALIGNED, 8 / Elem<DT>::VEC, most, 1>;
+    const auto kernel = block_norm_grad_kernel<DT, ALIGNED, PER / Elem<DT>::VEC, TOKEN, most>;
     constexpr int size = sizeof(typename Elem<DT>::type);
-    const RowPlan plan(a.D, size, kNormGradStages * (3 + (a.gate_period == 1) + (a.dr != nullptr)), 8, most);
+    const RowPlan plan(a.D, size, kNormGradStages * (3 + TOKEN + (a.dr != nullptr)), PER, most);
     a.ranks = plan.ranks;
     a.width = plan.width;
     if (!sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem)) return SGEMM_ERR_LAUNCH;
     const int fit = std::max(1, std::min(512 / plan.threads(), 226 * 1024 / (int)(plan.smem + 2048)));
-    a.runners = std::min(a.T, std::max(1, dev.sms * fit / plan.ranks) * (int)plan.block.y);
+    a.runners = std::min(most_grad_runners(a.T, a.D, dev.sms), std::max(1, dev.sms * fit / plan.ranks) * (int)plan.block.y);
     const unsigned groups = (a.runners + plan.block.y - 1) / plan.block.y;
     const int st = launch(kernel, dim3(groups * plan.ranks), plan.block, plan.smem, stream, (unsigned)plan.ranks, a);
     if (st != SGEMM_OK) return st;
     const int gates = a.gate_period > 1 ? std::min({a.T / a.gate_period, a.runners - 1, 16}) : 0;
-    return launch<true>(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, 2 + gates), dim3(32, 32), 0, stream, 1, a);
+    return launch<true>(block_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, 2 + gates), dim3(32, kNormJoinSlices), 0, stream, 1, a);
+}
+
+template <int DT>
+int norm_grad_by_layout(const BlockNormGradArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
+    if (a.gate_period == 1)
+        return vec ? launch_norm_grad<DT, true, true, 8>(a, dev, stream) : launch_norm_grad<DT, false, true, 8>(a, dev, stream);
+    // 16 elements a thread halve what a row costs beside them; of FP32, which unpacks nothing, 8
+    constexpr int PER = DT == SGEMM_F32 ? 8 : 16;
+    return vec ? launch_norm_grad<DT, true, false, PER>(a, dev, stream) : launch_norm_grad<DT, false, false, 8>(a, dev, stream);
 }
 
 // Checks that the forward and the backward pass share.
@@ -273,7 +282,7 @@ int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
                      aligned(w_post, 16);
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        return vec ? launch_norm_grad<DT, true>(a, dev, stream) : launch_norm_grad<DT, false>(a, dev, stream);
+        return norm_grad_by_layout<DT>(a, vec, dev, stream);
     });
 }
 

@@ -142,8 +142,37 @@ struct RowReducer {
                         v[i] = join(v[i], dsmem_ld_u32(dsmem_map(smem_addr(s + 32 * i + w), (uint32_t)r)));
         }
     }
+    // Three sums within a block: a quarter of the lanes (the last two quarters the same) carries
+    // one each, which halves the shuffles.
+    __device__ void sum3(float (&v)[3]) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 3;
+        const bool hi = lane & 16, odd = lane & 8;
+        float a = hi ? v[2] : v[0], b = v[1];
+        a += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+        b += __shfl_xor_sync(0xffffffffu, v[1], 16);
+        // lanes 0-15 hold the first two sums, 16-31 the third
+        const float got = __shfl_xor_sync(0xffffffffu, hi || odd ? a : b, 8);
+        a = (hi || !odd ? a : b) + got;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (warps > 1) {
+            float *s = slots + 96 * turn;
+            turn ^= 1;
+            const int sum = min(q, 2), w = lane & 7;
+            if (w == 0 && q < 3) s[32 * sum + warp] = a;
+            __syncthreads();
+            a = w < warps ? s[32 * sum + w] : 0.f;
+            if (warps > 8 && w + 8 < warps) a += s[32 * sum + w + 8];
+#pragma unroll
+            for (int o = 4; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(0xffffffffu, a, 8 * i);
+    }
     template <int N>
     __device__ void sum(float (&v)[N]) {
+        if constexpr (N == 3)
+            if (ranks == 1) return sum3(v);  // of up to 16 warps
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
         if (warps == 1 && ranks == 1) return;
