@@ -9,6 +9,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "i8_quantize.cuh"
 #include "ptx.cuh"
@@ -68,159 +69,159 @@ __device__ __forceinline__ void store_weight(void *w, int w_f32, int64_t c, floa
 //
 // The threads that share a row copy the next rows' inputs into shared memory
 // (cp.async, whole 16-byte pieces) while they work on this one, so what is in
-// flight does not depend on how many blocks fit an SM.  With ALIGNED rows
-// (16-byte aligned and a whole number of pieces) each thread copies the pieces
-// it will read itself and needs no barrier, and its pieces past the row's end
-// are zeros that no copy touches, so that what it reads needs no test (a test
-// a piece had made half of the gradient's instructions branches and their
-// bookkeeping); any other row is copied as the
-// pieces that enclose it (up to 15 bytes in front and behind are read and
-// never used), a barrier lets the row's threads see each other's copies, and
-// they read single elements.
+// flight does not depend on how many blocks fit an SM.
+//
+// With ALIGNED rows (16-byte aligned and a whole number of pieces) a warp takes
+// NV pieces a lane beside each other, so that one address serves all of them.
+// Each thread copies the pieces it will read itself and needs no barrier; its
+// pieces past the row's end are zeros that no copy touches, so that what it
+// reads needs no test.  (With a test a piece, and with addresses of their own,
+// two thirds of the gradient's instructions were addresses and branches.)
+//
+// Any other row is copied as the pieces that enclose it (up to 15 bytes in
+// front and behind are read and never used), a barrier lets the row's threads
+// see each other's copies, and they read single elements, i-th at column
+// i * threads + thread.
+// 16-byte pieces of the slot of one input of a row, for `threads` threads of `per` elements each
+// (the last piece for a row that does not start on one).
+__host__ __device__ constexpr int row_pieces(int threads, int per, int size) { return threads * per * size / 16 + 1; }
+
 template <int DT, bool ALIGNED, int NV>
 struct RowLayout {
     using type = typename Elem<DT>::type;
     static constexpr int VEC = Elem<DT>::VEC, N = NV * VEC;  // elements a thread
-    // column of this thread's element i
-    __device__ static int col(int i, int threads, int tx) {
-        return ALIGNED ? ((i / VEC) * threads + tx) * VEC + i % VEC : i * threads + tx;
+    static constexpr int NEXT = 32 * VEC;                    // columns from a thread's piece to its next
+    int D, threads, tx;
+    int col, left;  // ALIGNED: this thread's first column, and the columns from there to the row's end
+
+    __device__ explicit RowLayout(int D) : D(D), threads(blockDim.x), tx(threadIdx.x) {
+        col = ALIGNED ? ((tx & ~31) * NV + (tx & 31)) * VEC : 0;
+        left = D - col;
     }
-    // starts the copies of a row into `slot`
-    __device__ static void copy(uint4 *slot, const type *row, int D, int threads, int tx) {
+    // pieces of the slot of one input, and a thread's place in the ring of `rows` slots
+    __device__ int pieces() const { return ALIGNED ? NV * 32 : row_pieces(threads, N, sizeof(type)); }
+    __device__ uint4 *place(uint4 *ring, int rows) const {
+        if constexpr (ALIGNED) {
+            const int warp = (threadIdx.y * threads + tx) >> 5;
+            return ring + warp * rows * pieces() + (tx & 31);
+        } else {
+            return ring + threadIdx.y * rows * pieces();
+        }
+    }
+    __device__ bool has(int e) const { return left > e / VEC * NEXT; }  // ALIGNED: the piece of element e
+    __device__ static int at(int e) { return e / VEC * NEXT + e % VEC; }
+    // zeros past the row's end
+    __device__ void clear(uint4 *place, int rows) const {
+        if constexpr (ALIGNED) {
+            if (has(N - 1)) return;
+            for (int k = 0; k < rows; ++k)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    if (!has(v * VEC)) place[(k * NV + v) * 32] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    // The functions below take rows from this thread's first column (ALIGNED) or their start, and
+    // slots from this thread's place.
+    __device__ void copy(uint4 *slot, const type *row) const {
         if constexpr (ALIGNED) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int p = v * threads + tx;
-                if (p * VEC < D) cp_async_16(smem_addr(slot + p), row + p * VEC, 16);
-            }
+            for (int v = 0; v < NV; ++v)
+                if (has(v * VEC)) cp_async_16(smem_addr(slot + v * 32), row + v * NEXT, 16);
         } else {
             const uintptr_t lo = reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15;
-            const int pieces = (int)((reinterpret_cast<uintptr_t>(row + D) + 15 - lo) >> 4);
-            for (int p = tx; p < pieces; p += threads)
+            const int n = (int)((reinterpret_cast<uintptr_t>(row + D) + 15 - lo) >> 4);
+            for (int p = tx; p < n; p += threads)
                 cp_async_16(smem_addr(slot + p), reinterpret_cast<const void *>(lo + 16 * (uintptr_t)p), 16);
         }
     }
-    // zeros past the end of `rows` slots of `pieces` each
-    __device__ static void clear(uint4 *slot, int rows, int pieces, int D, int threads, int tx) {
-        if (!ALIGNED || D == N * threads) return;
-        for (int k = 0; k < rows; ++k)
-            for (int p = tx; p < NV * threads; p += threads)
-                if (p * VEC >= D) slot[k * pieces + p] = make_uint4(0, 0, 0, 0);
-    }
-    // this thread's elements of the row that was copied from `row`; 0 past its end
-    __device__ static void read(const uint4 *slot, const type *row, int D, int threads, int tx, float *out) {
-        if constexpr (ALIGNED) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                unpack16<DT>(slot[v * threads + tx], out + v * VEC);
-            }
+    template <int COUNT>
+    __device__ static void unpack(const type *p, F2 (&out)[COUNT / 2]) {
+        float f[8];
+        if constexpr (sizeof(type) * COUNT == 16) {
+            unpack16<DT>(*reinterpret_cast<const uint4 *>(p), f);
         } else {
-            const type *e = reinterpret_cast<const type *>(slot) + (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(type);
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            unpack16<DT>(make_uint4(w.x, w.y, 0, 0), f);
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) out[i] = i * threads + tx < D ? Elem<DT>::to_float(e[i * threads + tx]) : 0.f;
+        for (int i = 0; i < COUNT / 2; ++i) out[i] = F2(f[2 * i], f[2 * i + 1]);
+    }
+    // COUNT elements (a piece, or four of one) from this thread's e-th of the row that was copied
+    // from `row`; 0 past its end
+    template <int COUNT>
+    __device__ void read(const uint4 *slot, const type *row, int e, F2 (&out)[COUNT / 2]) const {
+        if constexpr (ALIGNED) {
+            unpack<COUNT>(reinterpret_cast<const type *>(slot + e / VEC * 32) + e % VEC, out);
+        } else {
+            const type *q = reinterpret_cast<const type *>(slot) + (reinterpret_cast<uintptr_t>(row) & 15) / sizeof(type);
+            auto one = [&](int i) { return i * threads + tx < D ? Elem<DT>::to_float(q[i * threads + tx]) : 0.f; };
+#pragma unroll
+            for (int i = 0; i < COUNT; i += 2) out[i / 2] = F2(one(e + i), one(e + i + 1));
         }
     }
-    __device__ static void store(type *row, int D, int threads, int tx, const float *v) {
+    // the same of weights (from the block's first column); ALIGNED weights start on 16 bytes
+    template <int COUNT>
+    __device__ void weights(const void *w, int w_f32, int e, F2 (&out)[COUNT / 2]) const {
         if constexpr (ALIGNED) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int p = k * threads + tx;
-                if (p * VEC < D) *reinterpret_cast<uint4 *>(row + p * VEC) = pack16<DT>(v + k * VEC);
+            for (int i = 0; i < COUNT / 2; ++i) out[i] = F2(0.f);
+            if (w_f32) {
+#pragma unroll
+                for (int i = 0; i < COUNT; i += 4)
+                    if (has(e)) {
+                        const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + col + at(e + i)));
+                        out[i / 2] = F2(f.x, f.y), out[i / 2 + 1] = F2(f.z, f.w);
+                    }
+            } else if (has(e)) {
+                unpack<COUNT>(static_cast<const type *>(w) + col + at(e), out);
             }
         } else {
+            auto one = [&](int i) { return i * threads + tx < D ? load_weight<DT>(w, w_f32, i * threads + tx) : 0.f; };
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i * threads + tx < D) row[i * threads + tx] = Elem<DT>::from_float(v[i]);
+            for (int i = 0; i < COUNT; i += 2) out[i / 2] = F2(one(e + i), one(e + i + 1));
         }
     }
-    // the same, two elements to a register pair
-    __device__ static void read(const uint4 *slot, const type *row, int D, int threads, int tx, F2 *out) {
-        float v[N];
-        read(slot, row, D, threads, tx, v);
+    // a piece from this thread's e-th element on
+    __device__ void store(type *row, int e, const F2 *v) const {
+        float f[VEC];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) out[i] = F2(v[2 * i], v[2 * i + 1]);
-    }
-    __device__ static void store(type *row, int D, int threads, int tx, const F2 *v) {
-        float f[N];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
+        for (int i = 0; i < VEC / 2; ++i) {
             const float2 b = v[i].both();
             f[2 * i] = b.x;
             f[2 * i + 1] = b.y;
         }
-        store(row, D, threads, tx, f);
-    }
-    __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, F2 *out) {
-        float v[N];
-        weights(w, w_f32, c0, D, threads, tx, v);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) out[i] = F2(v[2 * i], v[2 * i + 1]);
-    }
-    // 0 past the row's end; ALIGNED weights start on 16 bytes
-    __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, float *out) {
         if constexpr (ALIGNED) {
+            if (has(e)) *reinterpret_cast<uint4 *>(row + at(e)) = pack16<DT>(f);
+        } else {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int at = (v * threads + tx) * VEC, c = at < D ? at : 0;
-                if (w_f32) {
+            for (int i = 0; i < VEC; ++i)
+                if ((e + i) * threads + tx < D) row[(e + i) * threads + tx] = Elem<DT>::from_float(f[i]);
+        }
+    }
+    // the same of FP32 sums, four columns to a store where a thread has them beside each other
+    // (single floats would write every sector eight times)
+    __device__ void put(float *row, int e, const F2 *v, bool add) const {
+        if constexpr (ALIGNED) {
+            if (has(e))
 #pragma unroll
-                    for (int e = 0; e < VEC; e += 4) {
-                        const float4 q = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c0 + c + e));
-                        out[v * VEC + e] = q.x, out[v * VEC + e + 1] = q.y;
-                        out[v * VEC + e + 2] = q.z, out[v * VEC + e + 3] = q.w;
+                for (int i = 0; i < VEC / 2; i += 2) {
+                    float4 *p = reinterpret_cast<float4 *>(row + at(e + 2 * i));
+                    const float2 f = v[i].both(), g = v[i + 1].both();
+                    float4 s = make_float4(f.x, f.y, g.x, g.y);
+                    if (add) {
+                        const float4 o = *p;
+                        s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
                     }
-                } else {
-                    unpack16<DT>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const type *>(w) + c0 + c)), out + v * VEC);
+                    *p = s;
                 }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) out[v * VEC + e] = at < D ? out[v * VEC + e] : 0.f;
-            }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                out[i] = i * threads + tx < D ? load_weight<DT>(w, w_f32, c0 + i * threads + tx) : 0.f;
-        }
-    }
-};
-
-// Four elements at a time of an ALIGNED thread's row (its elements 4 q to 4 q + 3), where the
-// registers hold no more than that of several rows beside each other; a whole piece of any other.
-template <int DT, bool ALIGNED>
-struct RowPart {
-    using One = RowLayout<DT, ALIGNED, 1>;
-    using type = typename One::type;
-    static constexpr int VEC = One::VEC, N = ALIGNED ? 4 : VEC, PER = VEC / N;
-    __device__ static void unpack(const type *p, F2 (&out)[N / 2]) {
-        if constexpr (DT == SGEMM_F32) {
-            const float4 f = *reinterpret_cast<const float4 *>(p);
-            out[0] = F2(f.x, f.y), out[1] = F2(f.z, f.w);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p);
-            float f[8];
-            unpack16<DT>(make_uint4(w.x, w.y, 0, 0), f);
-            out[0] = F2(f[0], f[1]), out[1] = F2(f[2], f[3]);
-        }
-    }
-    __device__ static int col(int q, int threads, int tx) { return (q / PER * threads + tx) * VEC + q % PER * N; }
-    __device__ static void read(const uint4 *slot, const type *row, int D, int threads, int tx, int q, F2 (&out)[N / 2]) {
-        if constexpr (ALIGNED) {
-            unpack(reinterpret_cast<const type *>(slot) + col(q, threads, tx), out);
-        } else {
-            One::read(slot, row, D, threads, q * N * threads + tx, out);
-        }
-    }
-    __device__ static void weights(const void *w, int w_f32, int c0, int D, int threads, int tx, int q, F2 (&out)[N / 2]) {
-        if constexpr (ALIGNED) {
-            const int at = col(q, threads, tx), c = at < D ? at : 0;
-            if (w_f32) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c0 + c));
-                out[0] = F2(f.x, f.y), out[1] = F2(f.z, f.w);
-            } else {
-                unpack(static_cast<const type *>(w) + c0 + c, out);
+            for (int i = 0; i < VEC / 2; ++i) {
+                const float2 f = v[i].both();
+                const int c = (e + 2 * i) * threads + tx, c1 = c + threads;
+                if (c < D) row[c] = add ? row[c] + f.x : f.x;
+                if (c1 < D) row[c1] = add ? row[c1] + f.y : f.y;
             }
-            if (at >= D) out[0] = out[1] = F2(0.f);
-        } else {
-            One::weights(w, w_f32, c0, D, threads, q * N * threads + tx, out);
         }
     }
 };
@@ -228,10 +229,6 @@ struct RowPart {
 // Rows a thread keeps on their way (and the one it works on).
 constexpr int kNormStages = 4;
 constexpr int kNormGradStages = 3;
-
-// 16-byte pieces of the slot of one input of a row, for `threads` threads of `per` elements each
-// (the last piece for a row that does not start on one).
-__host__ __device__ constexpr int row_pieces(int threads, int per, int size) { return threads * per * size / 16 + 1; }
 
 // The barrier of the threads that share a row.
 __device__ __forceinline__ void row_sync(int warps) {
@@ -246,34 +243,45 @@ template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormArgs a) {
     using L = RowLayout<DT, ALIGNED, NV>;
     using type = typename L::type;
-    constexpr int N = L::N, S = kNormStages;
+    constexpr int N = L::N, V = L::VEC, H = V / 2, S = kNormStages;  // H pairs a piece
     extern __shared__ uint4 ring[];
     __shared__ float slots[RowReducer::SLOTS];
     RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
-    const int threads = blockDim.x, tx = threadIdx.x;
     const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
-    const int c0 = rank * a.width, D = min(a.width, a.D - c0);  // this block's columns
+    const int c0 = rank * a.width;  // this block's columns
+    const L l(min(a.width, a.D - c0));
+    const int cols = c0 + l.col;
     const float inv_d = 1.f / (float)a.D;
     const bool token_gate = a.gate_period == 1;
-    const int arrays = token_gate ? 3 : 2, pieces = row_pieces(threads, N, sizeof(type));
-    uint4 *mine = ring + threadIdx.y * S * arrays * pieces;
-    L::clear(mine, S * arrays, pieces, D, threads, tx);
+    const int arrays = token_gate ? 3 : 2, pieces = l.pieces();
+    uint4 *mine = l.place(ring, S * arrays);
+    l.clear(mine, S * arrays);
 
-    float w_pre[N], w_post[N];
-    L::weights(a.w_pre, a.w_f32, c0, D, threads, tx, w_pre);
-    if (a.w_post) L::weights(a.w_post, a.w_f32, c0, D, threads, tx, w_post);
+    auto weights = [&](const void *w, int v, F2 (&out)[H]) {
+        l.template weights<V>(static_cast<const char *>(w) + (int64_t)c0 * (a.w_f32 ? 4 : (int)sizeof(type)), a.w_f32, v * V, out);
+    };
+    F2 w_pre[NV][H], w_post[NV][H];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        weights(a.w_pre, v, w_pre[v]);
+        if (a.w_post) weights(a.w_post, v, w_post[v]);
+    }
 
     const int64_t first = (int64_t)group_id * blockDim.y + threadIdx.y;
     const int64_t step = (int64_t)(gridDim.x / (unsigned)a.ranks) * blockDim.y;
-    auto x_row = [&](int64_t t) { return static_cast<const type *>(a.x) + t * a.ldx + c0; };
-    auto y_row = [&](int64_t t) { return static_cast<const type *>(a.y) + t * a.ldy + c0; };
-    auto g_row = [&](int64_t t) { return static_cast<const type *>(a.gate) + (int64_t)((unsigned)t / (unsigned)a.gate_period) * a.ldg + c0; };
+    // rows are numbered below 2^30 and leading dimensions are 32-bit: one multiplication
+    auto row = [&](const void *p, int64_t ld, int64_t t) {
+        return static_cast<const type *>(p) + ((int64_t)(int)t * (int)ld + cols);
+    };
+    auto x_row = [&](int64_t t) { return row(a.x, a.ldx, t); };
+    auto y_row = [&](int64_t t) { return row(a.y, a.ldy, t); };
+    auto g_row = [&](int64_t t) { return row(a.gate, a.ldg, (unsigned)t / (unsigned)a.gate_period); };
     auto fetch = [&](int64_t t, int stage) {
         if (t < a.T) {
             uint4 *slot = mine + stage * arrays * pieces;
-            L::copy(slot, x_row(t), D, threads, tx);
-            L::copy(slot + pieces, y_row(t), D, threads, tx);
-            if (token_gate) L::copy(slot + 2 * pieces, g_row(t), D, threads, tx);
+            l.copy(slot, x_row(t));
+            l.copy(slot + pieces, y_row(t));
+            if (token_gate) l.copy(slot + 2 * pieces, g_row(t));
         }
         cp_async_commit();
     };
@@ -285,79 +293,83 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormA
         cp_async_wait<S - 2>();
         if (!ALIGNED) row_sync(red.warps);
         const uint4 *slot = mine + stage * arrays * pieces;
-        float h[N], r[N];
-        L::read(slot + pieces, y_row(t), D, threads, tx, h);
+        F2 h[NV][H], r[NV][H];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) l.template read<V>(slot + pieces, y_row(t), v * V, h[v]);
         float rho = 1.f;
         if (a.w_post) {
-            float ss = 0.f;
+            F2 ss(0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) ss = fmaf(h[i], h[i], ss);
-            rho = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < N; ++i) h[i] *= rho * w_post[i];
+                for (int i = 0; i < H; ++i) ss = fma(h[v][i], h[v][i], ss);
+            rho = rsqrtf(fmaf(red.sum(ss.sum()), inv_d, a.eps));
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < H; ++i) h[v][i] = h[v][i] * (F2(rho) * w_post[v][i]);
         }
         if (a.gate_period) {
-            float g[N];
-            if (token_gate) {
-                L::read(slot + 2 * pieces, g_row(t), D, threads, tx, g);
-            } else if constexpr (ALIGNED) {
-                const type *row = g_row(t);  // the same for many rows: from L1
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int c = (v * threads + tx) * L::VEC;
-                    unpack16<DT>(c < D ? __ldg(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0, 0, 0, 0),
-                                 g + v * L::VEC);
-                }
-            } else {
-                const type *row = g_row(t);
+            for (int v = 0; v < NV; ++v) {
+                F2 g[H];
+                if (token_gate) l.template read<V>(slot + 2 * pieces, g_row(t), v * V, g);
+                else l.template weights<V>(g_row(t) - l.col, 0, v * V, g);  // the same for many rows: from L1
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    g[i] = i * threads + tx < D ? Elem<DT>::to_float(row[i * threads + tx]) : 0.f;
+                for (int i = 0; i < H; ++i) h[v][i] = h[v][i] * g[i];
             }
-#pragma unroll
-            for (int i = 0; i < N; ++i) h[i] *= g[i];
         }
         // the slot that the previous row was read from takes the row after the next ones
         fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
         stage = stage == S - 1 ? 0 : stage + 1;
-        L::read(slot, x_row(t), D, threads, tx, r);
-        float ss = 0.f;
+        F2 ss(0.f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r[i] = fmaf(a.scale, h[i], r[i]);
-            ss = fmaf(r[i], r[i], ss);
+        for (int v = 0; v < NV; ++v) {
+            l.template read<V>(slot, x_row(t), v * V, r[v]);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                r[v][i] = fma(F2(a.scale), h[v][i], r[v][i]);
+                ss = fma(r[v][i], r[v][i], ss);
+            }
+            l.store(const_cast<type *>(row(a.r, a.ldr, t)), v * V, r[v]);
         }
-        L::store(static_cast<type *>(a.r) + t * a.ldr + c0, D, threads, tx, r);
-        const float rho2 = rsqrtf(fmaf(red.sum(ss), inv_d, a.eps));
-        if (a.rstd && tx == 0 && rank == 0) {
+        const float rho2 = rsqrtf(fmaf(red.sum(ss.sum()), inv_d, a.eps));
+        if (a.rstd && threadIdx.x == 0 && rank == 0) {
             a.rstd[t] = rho;
             a.rstd[a.T + t] = rho2;
         }
-        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            r[i] *= rho2 * w_pre[i];
-            top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) r[v][i] = r[v][i] * (F2(rho2) * w_pre[v][i]);
+            if (a.n) l.store(const_cast<type *>(row(a.n, a.ldn, t)), v * V, r[v]);
         }
-        if (a.n) L::store(static_cast<type *>(a.n) + t * a.ldn + c0, D, threads, tx, r);
         if (a.q) {
+            uint32_t top = 0;
+            float n[N];
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 f = r[i / V][i % V / 2].both();
+                n[i] = f.x;
+                n[i + 1] = f.y;
+                top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+            }
             const I8Scale q(red.max(top));
-            if (tx == 0 && rank == 0) a.q_scale[t] = q.scale;
-            int8_t *out = a.q + t * a.ldq + c0;
+            if (threadIdx.x == 0 && rank == 0) a.q_scale[t] = q.scale;
+            int8_t *out = a.q + t * a.ldq + cols;
             if constexpr (ALIGNED) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int c = (v * threads + tx) * L::VEC;
-                    if (c >= D) continue;
-                    int8_t b[L::VEC];
+                    if (!l.has(v * V)) continue;
+                    int8_t b[V];
 #pragma unroll
-                    for (int e = 0; e < L::VEC; ++e) b[e] = q(r[v * L::VEC + e]);
-                    store_bytes(out + c, b, a.q_vec);
+                    for (int e = 0; e < V; ++e) b[e] = q(n[v * V + e]);
+                    store_bytes(out + l.at(v * V), b, a.q_vec);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (i * threads + tx < D) out[i * threads + tx] = q(r[i]);
+                    if (i * l.threads + l.tx < l.D) out[i * l.threads + l.tx] = q(n[i]);
             }
         }
     }
@@ -396,45 +408,47 @@ struct RowRuns {
 template <int DT, bool ALIGNED, int NV, bool TOKEN, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNormGradArgs a) {
     using L = RowLayout<DT, ALIGNED, NV>;
-    using E = Elem<DT>;
     using type = typename L::type;
-    using One = RowLayout<DT, ALIGNED, 1>;  // a piece of a thread's row
-    using Part = RowPart<DT, ALIGNED>;
-    constexpr int H = L::N / 2, P = One::N / 2, Q = Part::N / 2, S = kNormGradStages;  // pairs of elements
+    constexpr int N = L::N, V = L::VEC, P = V / 2, S = kNormGradStages;  // P pairs a piece
+    // elements at a time of the first pass, where the registers hold no more of four rows
+    constexpr int Q = ALIGNED ? 4 : V;
     extern __shared__ uint4 ring[];
     __shared__ float slots[RowReducer::SLOTS];
     RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
-    const int threads = blockDim.x, tx = threadIdx.x;
-    auto first = [&](int v) { return tx + v * (ALIGNED ? 1 : One::N) * threads; };  // as One sees piece v
     const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
-    const int c0 = rank * a.width, D = min(a.width, a.D - c0);  // this block's columns
+    const int c0 = rank * a.width;  // this block's columns
+    const L l(min(a.width, a.D - c0));
+    const int cols = c0 + l.col;
     const float inv_d = 1.f / (float)a.D;
     const int runner = group_id * blockDim.y + threadIdx.y;
     if (runner >= a.runners) return;  // only where a warp is a runner: no barrier spans warps
     const RowRuns runs(a.T, a.runners);
     const int begin = runs.first(runner), end = runs.first(runner + 1);
-    const int pieces = row_pieces(threads, L::N, sizeof(type));
-    const int dr_at = (TOKEN ? 4 : 3) * pieces;
-    const int stride = dr_at + (a.dr ? pieces : 0);
-    uint4 *mine = ring + threadIdx.y * S * stride;
-    L::clear(mine, S * stride / pieces, pieces, D, threads, tx);
+    constexpr int DR = TOKEN ? 4 : 3;  // slots of a row: x, y, dn, with TOKEN the gate, dr if there is one
+    const int pieces = l.pieces(), stride = (a.dr ? DR + 1 : DR) * pieces;
+    uint4 *mine = l.place(ring, S * (a.dr ? DR + 1 : DR));
+    l.clear(mine, S * (a.dr ? DR + 1 : DR));
     // the runner's four sums of a.D columns
-    auto partial = [&](int k) { return a.partial + (((int64_t)runner * 4 + k) * a.D + c0); };
+    auto partial = [&](int k) { return a.partial + (((int64_t)runner * 4 + k) * a.D + cols); };
 
-    // gate: m above, but w_post alone with TOKEN; s: dw_post with TOKEN
-    F2 m[H], dw_pre[H], s[H];
-    auto post = [&](int v, F2 *out) {
+    // m: as above, but w_post alone with TOKEN; s: dw_post with TOKEN
+    F2 m[N / 2], dw_pre[N / 2], s[N / 2];
+    auto weights = [&](const void *w, auto count, int e, auto &out) {
+        l.template weights<decltype(count)::value>(static_cast<const char *>(w) + (int64_t)c0 * (a.w_f32 ? 4 : (int)sizeof(type)),
+                                                   a.w_f32, e, out);
+    };
+    auto post = [&](int v, F2 (&out)[P]) {
         if (a.w_post) {
-            One::weights(a.w_post, a.w_f32, c0, D, threads, first(v), out);
+            weights(a.w_post, std::integral_constant<int, V>{}, v * V, out);
         } else {
 #pragma unroll
             for (int i = 0; i < P; ++i) out[i] = F2(1.f);
         }
     };
     // a g for a gate row: read from L1 where it is the same for many rows
-    auto gate_row = [&](int group, int v, F2 *out) {
+    auto gate_row = [&](int group, int v, F2 (&out)[P]) {
         if (a.gate_period) {
-            One::weights(static_cast<const type *>(a.gate) + group * a.ldg, 0, c0, D, threads, first(v), out);
+            l.template weights<V>(static_cast<const type *>(a.gate) + (group * a.ldg + c0), 0, v * V, out);
 #pragma unroll
             for (int i = 0; i < P; ++i) out[i] = out[i] * F2(a.scale);
         } else {
@@ -445,53 +459,25 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
     auto take_gate = [&](int group) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            F2 g[P];
-            post(v, m + v * P);
-            if (TOKEN) continue;
-            gate_row(group, v, g);
+            F2 g[P], w[P];
+            post(v, w);
+            if (!TOKEN) gate_row(group, v, g);
 #pragma unroll
-            for (int i = 0; i < P; ++i) m[v * P + i] = m[v * P + i] * g[i];
-        }
-    };
-    // four columns to a store where a thread has four beside each other (single floats would write
-    // every sector eight times)
-    auto put = [&](float *to, int v, const F2 *q, bool add) {
-        if constexpr (ALIGNED) {
-            const int c = One::col(0, threads, first(v));
-            if (c < D)
-#pragma unroll
-                for (int i = 0; i < P; i += 2) {
-                    float4 *p = reinterpret_cast<float4 *>(to + c + 2 * i);
-                    const float2 f = q[i].both(), g = q[i + 1].both();
-                    float4 s = make_float4(f.x, f.y, g.x, g.y);
-                    if (add) {
-                        const float4 o = *p;
-                        s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
-                    }
-                    *p = s;
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 f = q[i].both();
-                const int c = One::col(2 * i, threads, first(v)), c1 = One::col(2 * i + 1, threads, first(v));
-                if (c < D) to[c] = add ? to[c] + f.x : f.x;
-                if (c1 < D) to[c1] = add ? to[c1] + f.y : f.y;
-            }
+            for (int i = 0; i < P; ++i) m[v * P + i] = TOKEN ? w[i] : w[i] * g[i];
         }
     };
 
     // row t: leading dimensions are 32-bit, so this is one multiplication, and no register holds it
-    auto at = [&](const void *p, int64_t ld, int t) { return static_cast<const type *>(p) + ((int64_t)t * (int)ld + c0); };
-    auto to = [&](void *p, int64_t ld, int t) { return static_cast<type *>(p) + ((int64_t)t * (int)ld + c0); };
+    auto at = [&](const void *p, int64_t ld, int t) { return static_cast<const type *>(p) + ((int64_t)t * (int)ld + cols); };
+    auto to = [&](void *p, int64_t ld, int t) { return static_cast<type *>(p) + ((int64_t)t * (int)ld + cols); };
     auto fetch = [&](int t, int stage) {
         if (t < end) {
             uint4 *slot = mine + stage * stride;
-            L::copy(slot, at(a.x, a.ldx, t), D, threads, tx);
-            L::copy(slot + pieces, at(a.y, a.ldy, t), D, threads, tx);
-            L::copy(slot + 2 * pieces, at(a.dn, a.lddn, t), D, threads, tx);
-            if (TOKEN) L::copy(slot + 3 * pieces, at(a.gate, a.ldg, t), D, threads, tx);
-            if (a.dr) L::copy(slot + dr_at, at(a.dr, a.lddr, t), D, threads, tx);
+            l.copy(slot, at(a.x, a.ldx, t));
+            l.copy(slot + pieces, at(a.y, a.ldy, t));
+            l.copy(slot + 2 * pieces, at(a.dn, a.lddn, t));
+            if (TOKEN) l.copy(slot + 3 * pieces, at(a.gate, a.ldg, t));
+            if (a.dr) l.copy(slot + DR * pieces, at(a.dr, a.lddr, t));
         }
         cp_async_commit();
     };
@@ -503,7 +489,7 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
     if (!TOKEN && a.gate_period) last = (begin / a.gate_period + 1) * a.gate_period;
     take_gate(!TOKEN && a.gate_period ? begin / a.gate_period : 0);
 #pragma unroll
-    for (int i = 0; i < H; ++i) dw_pre[i] = s[i] = F2(0.f);
+    for (int i = 0; i < N / 2; ++i) dw_pre[i] = s[i] = F2(0.f);
 
     int stage = 0;
     for (int t = begin; t < end; ++t) {
@@ -513,48 +499,40 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
         fetch(t + S - 1, stage == 0 ? S - 1 : stage - 1);
         stage = stage == S - 1 ? 0 : stage + 1;
         const float rho = a.w_post ? a.rstd[t] : 1.f, rho2 = a.rstd[a.T + t];
-        // What the second half needs again is kept (or, y and the gate, read again): a piece at a time
-        // the rest fits registers.
-        F2 r[H], w[H], part[3] = {F2(0.f), F2(0.f), F2(0.f)};
-        auto read_y = [&](int v, F2 *out) {
-            One::read(slot + pieces, ALIGNED ? nullptr : at(a.y, a.ldy, t), D, threads, first(v), out);
-        };
-        auto read_gate = [&](int v, F2 *out) {
-            One::read(slot + 3 * pieces, ALIGNED ? nullptr : at(a.gate, a.ldg, t), D, threads, first(v), out);
+        // What the second half needs again is kept (or, y and the gate, read again): a few elements
+        // at a time the rest fits registers.
+        F2 r[N / 2], w[N / 2], part[3] = {F2(0.f), F2(0.f), F2(0.f)};
 #pragma unroll
-            for (int i = 0; i < P; ++i) out[i] = out[i] * F2(a.scale);
-        };
-#pragma unroll
-        for (int q = 0; q < H / Q; ++q) {
-            F2 xx[Q], yy[Q], u[Q], d[Q], w_pre[Q], g[Q];
-            Part::read(slot, ALIGNED ? nullptr : at(a.x, a.ldx, t), D, threads, tx, q, xx);
-            Part::read(slot + pieces, ALIGNED ? nullptr : at(a.y, a.ldy, t), D, threads, tx, q, yy);
+        for (int e = 0; e < N; e += Q) {
+            F2 xx[Q / 2], yy[Q / 2], u[Q / 2], d[Q / 2], w_pre[Q / 2], g[Q / 2];
+            l.template read<Q>(slot, at(a.x, a.ldx, t), e, xx);
+            l.template read<Q>(slot + pieces, at(a.y, a.ldy, t), e, yy);
             if constexpr (TOKEN) {
-                Part::read(slot + 3 * pieces, ALIGNED ? nullptr : at(a.gate, a.ldg, t), D, threads, tx, q, g);
+                l.template read<Q>(slot + 3 * pieces, at(a.gate, a.ldg, t), e, g);
 #pragma unroll
-                for (int i = 0; i < Q; ++i) g[i] = g[i] * F2(a.scale);
+                for (int i = 0; i < Q / 2; ++i) g[i] = g[i] * F2(a.scale);
             }
-            Part::read(slot + 2 * pieces, ALIGNED ? nullptr : at(a.dn, a.lddn, t), D, threads, tx, q, u);
+            l.template read<Q>(slot + 2 * pieces, at(a.dn, a.lddn, t), e, u);
             if (a.dr) {
-                Part::read(slot + dr_at, ALIGNED ? nullptr : at(a.dr, a.lddr, t), D, threads, tx, q, d);
+                l.template read<Q>(slot + DR * pieces, at(a.dr, a.lddr, t), e, d);
             } else {
 #pragma unroll
-                for (int i = 0; i < Q; ++i) d[i] = F2(0.f);
+                for (int i = 0; i < Q / 2; ++i) d[i] = F2(0.f);
             }
-            Part::weights(a.w_pre, a.w_f32, c0, D, threads, tx, q, w_pre);  // again for each row, from L1
+            weights(a.w_pre, std::integral_constant<int, Q>{}, e, w_pre);  // again for each row, from L1
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                const int e = q * Q + i;
-                F2 my = yy[i] * m[e];
+            for (int i = 0; i < Q / 2; ++i) {
+                const int k = e / 2 + i;
+                F2 my = yy[i] * m[k];
                 if constexpr (TOKEN) my = my * g[i];
-                r[e] = fma(my, F2(rho), xx[i]);
+                r[k] = fma(my, F2(rho), xx[i]);
                 u[i] = u[i] * F2(rho2);
-                dw_pre[e] = fma(u[i], r[e], dw_pre[e]);
+                dw_pre[k] = fma(u[i], r[k], dw_pre[k]);
                 u[i] = u[i] * w_pre[i];
-                w[e] = d[i] + u[i];
-                part[0] = fma(u[i], r[e], part[0]);
-                part[1] = fma(my, w[e], part[1]);
-                part[2] = fma(my, r[e], part[2]);
+                w[k] = d[i] + u[i];
+                part[0] = fma(u[i], r[k], part[0]);
+                part[1] = fma(my, w[k], part[1]);
+                part[2] = fma(my, r[k], part[2]);
             }
         }
         float sums[3] = {part[0].sum(), part[1].sum(), part[2].sum()};
@@ -565,14 +543,15 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             F2 yy[P], g[P];
-            read_y(v, yy);
-            if constexpr (TOKEN) read_gate(v, g);
+            l.template read<V>(slot + pieces, at(a.y, a.ldy, t), v * V, yy);
+            if constexpr (TOKEN) l.template read<V>(slot + 3 * pieces, at(a.gate, a.ldg, t), v * V, g);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const int e = v * P + i;
                 r[e] = fma(r[e], F2(-c), w[e]);
                 F2 d = r[e] * F2(rho);
                 if constexpr (TOKEN) {
+                    g[i] = g[i] * F2(a.scale);
                     const F2 dy = d * yy[i];
                     s[e] = fma(dy, g[i], s[e]);
                     d = d * (m[e] * g[i]);
@@ -583,9 +562,9 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
                 }
                 w[e] = fma(yy[i], F2(-k), d);
             }
-            One::store(to(a.dx, a.lddx, t), D, threads, first(v), r + v * P);
-            One::store(to(a.dy, a.lddy, t), D, threads, first(v), w + v * P);
-            if constexpr (TOKEN) One::store(to(a.dgate, a.lddg, t), D, threads, first(v), g);
+            l.store(to(a.dx, a.lddx, t), v * V, r + v * P);
+            l.store(to(a.dy, a.lddy, t), v * V, w + v * P);
+            if constexpr (TOKEN) l.store(to(a.dgate, a.lddg, t), v * V, g);
         }
         if (!TOKEN && (t + 1 == last || t + 1 == end)) {
             // a gate row's sum is whole when all of its rows are this runner's, otherwise one of the
@@ -600,14 +579,14 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
                     gate_row(group, v, q);
 #pragma unroll
                     for (int i = 0; i < P; ++i) q[i] = q[i] * s[v * P + i];
-                    put(partial(1), v, q, a.gate_period && later);
+                    l.put(partial(1), v * V, q, a.gate_period && later);
                 }
                 if (a.gate_period) {
                     post(v, q);
 #pragma unroll
                     for (int i = 0; i < P; ++i) q[i] = q[i] * s[v * P + i] * F2(a.scale);
-                    if (whole) One::store(to(a.dgate, a.lddg, group), D, threads, first(v), q);
-                    else put(partial(later ? 3 : 2), v, q, false);
+                    if (whole) l.store(to(a.dgate, a.lddg, group), v * V, q);
+                    else l.put(partial(later ? 3 : 2), v * V, q, false);
                 }
 #pragma unroll
                 for (int i = 0; i < P; ++i) s[v * P + i] = F2(0.f);
@@ -618,8 +597,8 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        put(partial(0), v, dw_pre + v * P, false);
-        if (TOKEN) put(partial(1), v, s + v * P, false);
+        l.put(partial(0), v * V, dw_pre + v * P, false);
+        if (TOKEN) l.put(partial(1), v * V, s + v * P, false);
     }
     if (a.ranks > 1) cluster_sync();
 }
