@@ -1,7 +1,8 @@
 // Rows quantised to 8-bit integers with one scale each: s = max|x| / 127,
 // q = rint(x (127 / max|x|)).  The row is read once into registers (or, when
 // it is too wide for them, a second time from L2) and written as bytes: the
-// kernel is bound by memory.
+// kernel is bound by memory.  Blocks walk several rows and read the next one
+// before they reduce this one's maximum.
 #pragma once
 
 #include <cstdint>

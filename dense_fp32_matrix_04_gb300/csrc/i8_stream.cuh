@@ -11,6 +11,18 @@
 // tokens written and read once: below the 128 bytes a cycle it can move, where
 // B as FP16 in shared memory would be beyond it.
 //
+// Measured, with the kernel that quantises the tokens and, where K is split, the
+// one that adds the splits: 24 x 16384 x 4096 18.2 us (3.7 TB/s of operands; two
+// launches, one round of 128 tiles on 152 SMs, and the copies, the conversion
+// and the products of a tile's first and last steps one after another);
+// 4096 x 4096 x 4096 103 us; 8192 x 8192 x 8192 705 us, 1559 TFLOP/s, 80 % of what
+// FP16 products reach: 48 us quantise, then the tensor pipe is 72 % busy, held
+// up by the issue of a step's products (680 cycles a step, 512 of them the
+// pipe's; two steps to a round of that loop took 731 us) and by drains that 256
+// columns leave no second accumulator to hide.  3001 x 4999 x 2047 in FP32
+// takes 75.7 us: about 12 for quantising rows of single floats, 4 rounds of
+// tiles, and 60 MB of results that all SMs store at the same time.
+//
 // One block per SM walks units (tile, k-split): one thread copies by TMA into a
 // ring, eight warps convert, one thread issues the products, four warps drain
 // the accumulator, apply the scales and the bias and store.  Every wait is
@@ -308,16 +320,25 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
         for (int u = blockIdx.x; u < units; u += gridDim.x, b.next()) {
             int m0, n0, k0, n;
             unit(u, m0, n0, k0, n);
+            const int col = n0 + 32 * q + lane;
+            const bool in = col < p.N;
+            // the scales are here before the accumulator is: lane l holds those of tokens l, l + 32, ...
+            float scale = 1.f, bias = 0.f, token_scales[(TOK + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (TOK + 31) / 32; ++i) {
+                const int m = m0 + 32 * i + lane;
+                token_scales[i] = splits == 1 && m < p.M ? p.a_scale[m] : 0.f;
+            }
+            if (in && splits == 1) {
+                scale = p.b_scale[col];
+                if (p.bias) bias = p.bias[col];
+            }
             // a finished tile is stored whatever another role decided since
             if (!mbar_wait_warp(acc_full0 + 8 * b.at, b.round, wait_limit_ns, 200)) {
                 if (lane == 0) *abort_flag = 1;
                 break;
             }
             tc_fence_after_sync();
-            const int col = n0 + 32 * q + lane;
-            const bool in = col < p.N;
-            const float scale = in && splits == 1 ? p.b_scale[col] : 1.f;
-            const float bias = in && splits == 1 && p.bias ? p.bias[col] : 0.f;
             float *slab = splits > 1 ? partials + (int64_t)(u / tiles) * p.M * ldp : nullptr;
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b.at * T::ACC_COLS;
             constexpr int CHUNK = TOK % 32 ? 16 : 32;
@@ -341,10 +362,13 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
                             if (j < count) slab[(int64_t)(m + j) * ldp + col] = v[j];
                     continue;
                 }
-                const float token_scale = lane < count ? p.a_scale[m + lane] : 0.f;
+                float token_scale = token_scales[0];
+#pragma unroll
+                for (int i = 1; i < (TOK + 31) / 32; ++i)
+                    if (c0 / 32 == i) token_scale = token_scales[i];
 #pragma unroll
                 for (int j = 0; j < CHUNK; ++j) {
-                    const float s = __shfl_sync(0xffffffffu, token_scale, j);
+                    const float s = __shfl_sync(0xffffffffu, token_scale, c0 % 32 + j);
                     v[j] = fmaf(v[j] * s, scale, bias);
                 }
                 if (in) {

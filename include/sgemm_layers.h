@@ -12,7 +12,8 @@
  * and its leading dimension are never written.  Any alignment of rows that the
  * element type allows is accepted.  The calls launch kernels only, so after
  * one call on a device they can be captured into a CUDA graph.  Results are
- * the same bits on every run.
+ * the same bits on every run.  (A backward pass over no rows, T == 0, clears the
+ * weights' gradients by cudaMemsetAsync instead of a kernel.)
  */
 #ifndef SGEMM_LAYERS_H
 #define SGEMM_LAYERS_H
@@ -87,7 +88,8 @@ int sgemm_block_norm_backward(int T, int D, int dtype,
                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Workspace bytes of sgemm_block_norm_backward on the current device (0 if
- * the device cannot be queried or T or D is 0). */
+ * the device cannot be queried or T or D is 0): 16 D for each block, or for
+ * narrow rows each warp, that sums over rows, of which an SM holds 1 to 16. */
 size_t sgemm_block_norm_backward_workspace_size(int T, int D);
 
 /*
@@ -106,14 +108,18 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx,
  * C = diag(a_scale) A B^T diag(b_scale) + bias, with A (M x K) and B (N x K,
  * as a linear layer stores its weights) 8-bit integers:
  *     C[m][n] = a_scale[m] * b_scale[n] * sum_k A[m][k] B[n][k] + bias[n]
- * The sum is exact while its partial sums stay below 2^24 in magnitude (always
- * for K <= 1024) and an FP32 sum otherwise; the scales and the bias are
- * applied in FP32 and the result is rounded once to ctype.
+ * For M <= 4 the sum is an exact integer.  For more rows it is exact while its partial
+ * sums stay below 2^24 in magnitude (always for K <= 1024) and an FP32 sum
+ * otherwise; the scales and the bias are applied in FP32 and the result is
+ * rounded once to ctype.
  *   bias: N FP32 values or NULL.  K <= 131071.
- *   workspace: sgemm_i8_workspace_size(M, N, K) bytes, 16-byte aligned, with
- *       contents that do not matter; calls that share one must not overlap on
- *       the GPU.
+ *   workspace: sgemm_i8_workspace_size(M, N, K, B, ldb) bytes, 16-byte aligned,
+ *       with contents that do not matter; calls that share one must not
+ *       overlap on the GPU.  M <= 4 needs none; rows of B that are not 16-byte
+ *       aligned need N K bytes of it.
  * K == 0: every sum is empty (C = bias, or 0).
+ * The kernel for more than four rows waits for its own copies, with a limit:
+ * one that runs out is reported by sgemm_device_status, and C is unspecified.
  */
 int sgemm_i8(int M, int N, int K,
              const signed char *A, int lda, const float *a_scale,
@@ -159,7 +165,8 @@ size_t sgemm_linear_i8_workspace_size(int M, int N, int K, const signed char *B,
  *       log probability -infinity.
  * A row without any allowed finite column has lse -infinity, entropy 0 and
  * logprob -infinity.  A row whose allowed logits hold a NaN or +infinity has
- * NaN for all its numbers and -1 for its alternatives.
+ * NaN for all its numbers and -1 for its alternatives.  A row that is not
+ * scored has logprob 0 in either case.
  */
 int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float scale,
                    const int32_t *mask, int ldm, int mask_rows, const int64_t *target,
