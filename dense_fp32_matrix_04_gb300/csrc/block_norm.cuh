@@ -9,13 +9,15 @@
 // Memory bounds the forward pass: four elements moved for about ten operations.
 // 8192 x 5120 BF16 takes 58.6 us, 5.7 TB/s of the 6.8 that a copy reaches; a
 // row's two barriers are what is left.  Rows are walked by blocks that stay, so
-// that copies of the next three rows are always on their way (blocks of a row
-// each took 72 us).  Seven rows of 4096 take 3.8 us, a launch and two memory
-// latencies.  The gradient moves six elements for about 25 operations: 8192 x
-// 4096 BF16 takes 88 us (4.6 TB/s), FP32 4096 x 4096, half the arithmetic for
-// the same bytes, 79; 9 us of it are the launch, the runners' first row and the
-// joining of their sums.  Rows of single elements (not 16-byte aligned, or of
-// odd width) run at two thirds of that: 2047 x 1111 FP32 takes 24 us.
+// that copies of the next three rows are always on their way (a test and an
+// address for each piece took 63 us).  Seven rows of 4096 take 3.8 us, a launch
+// and two memory latencies.
+//
+// The gradient moves six elements for about 25 operations: 8192 x 4096 BF16
+// takes 87 us (4.6 TB/s), FP32 4096 x 4096, half the arithmetic for the same
+// bytes, 79; 9 us of it are the launch, the runners' first row and the joining
+// of their sums.  Rows of single elements (not 16-byte aligned, or of odd width)
+// run at two thirds of that: 2047 x 1111 FP32 takes 24 us.
 #pragma once
 
 #include <cstdint>
