@@ -36,17 +36,17 @@ SIGNATURES = {
 # sees, so the checks below ask a tensor as little as they can.
 _torch = _lib = None
 _codes = {}
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _start():
-    global _torch, _lib, _raw_stream
+    global _torch, _lib, _raw_stream, _current_device
     import torch
 
     from . import load
     _lib = load()
     _codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _torch = torch
 
 
@@ -56,7 +56,8 @@ def _check(status, where):
 
 
 def _first(t, name, dtypes=None):
-    """(element type, device index, shape) of a call's first tensor, a 2-D CUDA one."""
+    """(element type, device index, shape, pointer, leading dimension) of a call's first
+    tensor, a 2-D CUDA one."""
     if _torch is None:
         _start()
     dtype = t.dtype
@@ -65,19 +66,12 @@ def _first(t, name, dtypes=None):
     index = t.get_device()
     if index < 0 or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D CUDA tensor")
-    return dtype, index, t.shape
+    shape = t.shape
+    return (dtype, index, shape, *_rows(t, name, *shape))
 
 
-def _matrix(t, name, dtype, index, shape=None, cols=None):
-    """(pointer, leading dimension) of a 2-D CUDA tensor with unit column stride, of
-    this shape, or of this many columns."""
-    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
-        if t.dtype is dtype and t.dim() == 2 and t.get_device() >= 0:
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-        raise TypeError(f"{name} must be a 2-D {dtype} CUDA tensor")
-    rows, n = t.shape
-    if (shape is not None and (rows != shape[0] or n != shape[1])) or (cols is not None and n != cols):
-        raise ValueError(f"{name} is ({rows}, {n}), not {tuple(shape) if shape is not None else ('any', cols)}")
+def _rows(t, name, rows, n):
+    """(pointer, leading dimension) of a matrix with unit column stride."""
     if t.is_contiguous():
         return t.data_ptr(), n or 1
     s0, s1 = t.stride()
@@ -90,13 +84,27 @@ def _matrix(t, name, dtype, index, shape=None, cols=None):
     return t.data_ptr(), n or 1
 
 
+def _matrix(t, name, dtype, index, shape=None, cols=None):
+    """(pointer, leading dimension) of a 2-D CUDA tensor with unit column stride, of
+    this shape, or of this many columns."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+        if t.dtype is dtype and t.dim() == 2 and t.get_device() >= 0:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+        raise TypeError(f"{name} must be a 2-D {dtype} CUDA tensor")
+    rows, n = t.shape
+    if (shape is not None and (rows != shape[0] or n != shape[1])) or (cols is not None and n != cols):
+        raise ValueError(f"{name} is ({rows}, {n}), not {tuple(shape) if shape is not None else ('any', cols)}")
+    return _rows(t, name, rows, n)
+
+
 def _vector(t, name, n, dtypes, index):
     """Pointer of a dense 1-D CUDA tensor of n elements."""
-    if t.dtype not in dtypes or t.get_device() < 0 or t.dim() != 1:
+    on = t.get_device()
+    if t.dtype not in dtypes or on < 0 or t.dim() != 1:
         raise TypeError(f"{name} must be a 1-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    if t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} elements, not {n}")
-    if t.get_device() != index:
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    if on != index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be dense")
@@ -118,8 +126,8 @@ def _foreign(fn):
     def call(first, *args, stream=None, **more):
         if _torch is None:
             _start()
-        index = first.get_device() if hasattr(first, "get_device") else -1
-        if stream is None and (index < 0 or index == _torch._C._cuda_getDevice()):
+        index = first.get_device() if isinstance(first, _torch.Tensor) else -1
+        if stream is None and (index < 0 or index == _current_device()):
             return fn(first, *args, **more)
         if index < 0:
             return fn(first, *args, stream=stream, **more)  # refuses it
@@ -153,10 +161,9 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     8-bit integers with a scale per row.  ``rstd`` (2 x T) is for the backward
     pass.  ``out`` receives r; it may be x.
     """
-    dt, dev, shape = _first(x, "x")
+    dt, dev, shape, px, ldx = _first(x, "x")
     f32, empty, where = _torch.float32, _torch.empty, x.device
     T, D = shape
-    px, ldx = _matrix(x, "x", dt, dev)
     py, ldy = _matrix(y, "y", dt, dev, shape)
     wt = w_pre.dtype
     p_pre = _vector(w_pre, "w_pre", D, (f32, dt), dev)
@@ -188,10 +195,9 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
     """Gradients ``(dx, dy, dw_pre, dw_post, dgate)`` of ``block_norm`` from those of
     its n and r (``dr`` None: zero); ``dw_post`` and ``dgate`` are None where there is
     no such input."""
-    dt, dev, shape = _first(x, "x")
+    dt, dev, shape, px, ldx = _first(x, "x")
     f32, empty, where = _torch.float32, _torch.empty, x.device
     T, D = shape
-    px, ldx = _matrix(x, "x", dt, dev)
     py, ldy = _matrix(y, "y", dt, dev, shape)
     pn, ldn = _matrix(dn, "dn", dt, dev, shape)
     pr, ldr = _matrix(dr, "dr", dt, dev, shape) if dr is not None else (0, D or 1)
@@ -228,8 +234,7 @@ def quantize_i8(x, stream=None, keep=None):
     """``(q, scale)``: the rows of x (M x K) as 8-bit integers, scale = max|row| / 127
     and q = rint(row * (127 / max|row|)).  For activations a scale per token, for
     weights (N x K) one per output channel."""
-    dt, dev, shape = _first(x, "x")
-    px, ldx = _matrix(x, "x", dt, dev)
+    dt, dev, shape, px, ldx = _first(x, "x")
     M, K = shape
     q = _torch.empty(shape, dtype=_torch.int8, device=x.device)
     s = _torch.empty((M,), dtype=_torch.float32, device=x.device)
@@ -284,8 +289,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, works
     a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise)."""
     if _torch is None:
         _start()
-    _, dev, shape = _first(a, "a", (_torch.int8,))
-    pa, lda = _matrix(a, "a", _torch.int8, dev)
+    _, dev, shape, pa, lda = _first(a, "a", (_torch.int8,))
     ps = _vector(a_scale, "a_scale", shape[0], (_torch.float32,), dev)
     return _linear(_lib.sgemm_i8, "sgemm_i8", a, (pa, lda, ps), w, w_scale, bias, out_dtype or _torch.float32, out,
                    workspace, stream, keep, _lib.sgemm_i8_workspace_size)
@@ -295,8 +299,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, works
 def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, keep=None):
     """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
     quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise."""
-    dt, dev, _ = _first(x, "x")
-    px, ldx = _matrix(x, "x", dt, dev)
+    dt, _, _, px, ldx = _first(x, "x")
     return _linear(_lib.sgemm_linear_i8, "sgemm_linear_i8", x, (_codes[dt], px, ldx), w, w_scale, bias, out_dtype or dt,
                    out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)
 
@@ -320,8 +323,7 @@ def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, keep=None
     ``target``: T int64 columns; a negative one is not scored (logprob 0).
     ``mask``: int32 words, 1 or T rows of ceil(V / 32), bit j % 32 of word j // 32 set
     where column j is allowed."""
-    dt, dev, (T, V) = _first(logits, "logits")
-    pz, ldz = _matrix(logits, "logits", dt, dev)
+    dt, dev, (T, V), pz, ldz = _first(logits, "logits")
     py = _vector(target, "target", T, (_torch.int64,), dev)
     pm, ldm, rows = _mask(mask, T, V, dev)
     empty, f32, where = _torch.empty, _torch.float32, logits.device
@@ -346,9 +348,8 @@ def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, s
     """The gradient with respect to the logits of ``logprobs``' logprob and entropy, from
     theirs (``g_entropy`` None: no gradient reaches the entropy).  ``out`` may be the
     logits themselves."""
-    dt, dev, shape = _first(logits, "logits")
+    dt, dev, shape, pz, ldz = _first(logits, "logits")
     T, V = shape
-    pz, ldz = _matrix(logits, "logits", dt, dev)
     py = _vector(target, "target", T, (_torch.int64,), dev)
     f32 = (_torch.float32,)
     pl = _vector(lse, "lse", T, f32, dev)
