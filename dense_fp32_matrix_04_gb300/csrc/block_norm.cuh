@@ -14,14 +14,13 @@
 // and two memory latencies.
 //
 // The gradient moves six elements for about 25 operations: 8192 x 4096 BF16
-// takes 87 us (4.6 TB/s), FP32 4096 x 4096, half the arithmetic for the same
+// takes 84 us (4.8 TB/s), FP32 4096 x 4096, half the arithmetic for the same
 // bytes, 79; 9 us of it are the launch, the runners' first row and the joining
 // of their sums.  Rows of single elements (not 16-byte aligned, or of odd width)
 // run at two thirds of that: 2047 x 1111 FP32 takes 24 us.
 #pragma once
 
 #include <cstdint>
-#include <type_traits>
 
 #include "i8_quantize.cuh"
 #include "ptx.cuh"
@@ -86,8 +85,8 @@ __device__ __forceinline__ void store_weight(void *w, int w_f32, int64_t c, floa
 // With ALIGNED rows (16-byte aligned and a whole number of pieces) a warp takes
 // NV pieces a lane beside each other, so that one address serves all of them.
 // Each thread copies the pieces it will read itself and needs no barrier; its
-// pieces past the row's end are zeros that no copy touches, so that what it
-// reads needs no test.  (With a test a piece, and with addresses of their own,
+// pieces past the row's end are copies of nothing, zeros, so that what it reads
+// needs no test.  (With a test a piece, and with addresses of their own,
 // two thirds of the gradient's instructions were addresses and branches.)
 //
 // Any other row is copied as the pieces that enclose it (up to 15 bytes in
@@ -122,23 +121,13 @@ struct RowLayout {
     }
     __device__ bool has(int e) const { return left > e / VEC * NEXT; }  // ALIGNED: the piece of element e
     __device__ static int at(int e) { return e / VEC * NEXT + e % VEC; }
-    // zeros past the row's end
-    __device__ void clear(uint4 *place, int rows) const {
-        if constexpr (ALIGNED) {
-            if (has(N - 1)) return;
-            for (int k = 0; k < rows; ++k)
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (!has(v * VEC)) place[(k * NV + v) * 32] = make_uint4(0, 0, 0, 0);
-        }
-    }
     // The functions below take rows from this thread's first column (ALIGNED) or their start, and
     // slots from this thread's place.
     __device__ void copy(uint4 *slot, const type *row) const {
         if constexpr (ALIGNED) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                if (has(v * VEC)) cp_async_16(smem_addr(slot + v * 32), row + v * NEXT, 16);
+                cp_async_16(smem_addr(slot + v * 32), row + v * NEXT, has(v * VEC) ? 16 : 0);
         } else {
             const uintptr_t lo = reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15;
             const int n = (int)((reinterpret_cast<uintptr_t>(row + D) + 15 - lo) >> 4);
@@ -171,10 +160,22 @@ struct RowLayout {
             for (int i = 0; i < COUNT; i += 2) out[i / 2] = F2(one(e + i), one(e + i + 1));
         }
     }
-    // the same of weights (from the block's first column); ALIGNED weights start on 16 bytes
-    template <int COUNT>
+    // the same of weights (from the block's first column); ALIGNED weights start on 16 bytes.
+    // FOR_ZEROS: they meet only zeros past the row's end, and are the row's last ones there.
+    template <int COUNT, bool FOR_ZEROS = false>
     __device__ void weights(const void *w, int w_f32, int e, F2 (&out)[COUNT / 2]) const {
-        if constexpr (ALIGNED) {
+        if constexpr (ALIGNED && FOR_ZEROS) {
+            const int c = (has(e) ? col + e / VEC * NEXT : D - VEC) + e % VEC;
+            if (w_f32) {
+#pragma unroll
+                for (int i = 0; i < COUNT; i += 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c + i));
+                    out[i / 2] = F2(f.x, f.y), out[i / 2 + 1] = F2(f.z, f.w);
+                }
+            } else {
+                unpack<COUNT>(static_cast<const type *>(w) + c, out);
+            }
+        } else if constexpr (ALIGNED) {
 #pragma unroll
             for (int i = 0; i < COUNT / 2; ++i) out[i] = F2(0.f);
             if (w_f32) {
@@ -267,7 +268,6 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const BlockNormA
     const bool token_gate = a.gate_period == 1;
     const int arrays = token_gate ? 3 : 2, pieces = l.pieces();
     uint4 *mine = l.place(ring, S * arrays);
-    l.clear(mine, S * arrays);
 
     auto weights = [&](const void *w, int v, F2 (&out)[H]) {
         l.template weights<V>(static_cast<const char *>(w) + (int64_t)c0 * (a.w_f32 ? 4 : (int)sizeof(type)), a.w_f32, v * V, out);
@@ -439,19 +439,15 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
     constexpr int DR = TOKEN ? 4 : 3;  // slots of a row: x, y, dn, with TOKEN the gate, dr if there is one
     const int pieces = l.pieces(), stride = (a.dr ? DR + 1 : DR) * pieces;
     uint4 *mine = l.place(ring, S * (a.dr ? DR + 1 : DR));
-    l.clear(mine, S * (a.dr ? DR + 1 : DR));
     // the runner's four sums of a.D columns
     auto partial = [&](int k) { return a.partial + (((int64_t)runner * 4 + k) * a.D + cols); };
 
     // m: as above, but w_post alone with TOKEN; s: dw_post with TOKEN
     F2 m[N / 2], dw_pre[N / 2], s[N / 2];
-    auto weights = [&](const void *w, auto count, int e, auto &out) {
-        l.template weights<decltype(count)::value>(static_cast<const char *>(w) + (int64_t)c0 * (a.w_f32 ? 4 : (int)sizeof(type)),
-                                                   a.w_f32, e, out);
-    };
+    const int wsize = a.w_f32 ? 4 : (int)sizeof(type);
     auto post = [&](int v, F2 (&out)[P]) {
         if (a.w_post) {
-            weights(a.w_post, std::integral_constant<int, V>{}, v * V, out);
+            l.template weights<V>(static_cast<const char *>(a.w_post) + c0 * wsize, a.w_f32, v * V, out);
         } else {
 #pragma unroll
             for (int i = 0; i < P; ++i) out[i] = F2(1.f);
@@ -531,7 +527,8 @@ __global__ void __launch_bounds__(MAXT, 1) block_norm_grad_kernel(const BlockNor
 #pragma unroll
                 for (int i = 0; i < Q / 2; ++i) d[i] = F2(0.f);
             }
-            weights(a.w_pre, std::integral_constant<int, Q>{}, e, w_pre);  // again for each row, from L1
+            // again for each row, from L1
+            l.template weights<Q, true>(static_cast<const char *>(a.w_pre) + c0 * wsize, a.w_f32, e, w_pre);
 #pragma unroll
             for (int i = 0; i < Q / 2; ++i) {
                 const int k = e / 2 + i;
