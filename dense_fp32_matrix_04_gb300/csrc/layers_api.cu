@@ -160,6 +160,9 @@ int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t str
     // alternatives 91 -> 81 us; with five alternatives 106 -> 112 us)
     if (parts == 1 && !a.top) return launch_logprobs<DT, 64, false, MASK>(a, 1, dev, stream);
     if (parts == 1 && a.V < 16384) return launch_logprobs<DT, 64, true, MASK>(a, 1, dev, stream);
+    // four warps for longer rows with alternatives, where there are two for each block that the SMs
+    // hold (4096 x 50001 106 -> 91 us; 2000 x 32000 with 20 alternatives 44 -> 48 us)
+    if (parts == 1 && a.T >= 2 * 8 * dev.sms) return launch_logprobs<DT, 128, true, MASK>(a, 1, dev, stream);
     return a.top ? launch_logprobs<DT, 256, true, MASK>(a, parts, dev, stream)
                  : launch_logprobs<DT, 256, false, MASK>(a, parts, dev, stream);
 }

@@ -17,10 +17,9 @@
 // column, a handful, have theirs looked at again, and the few columns that
 // reach it are inserted into a list over a warp's lanes.
 //
-// Of 16-bit logits the pass is bound by the issue of instructions (about 14 an
+// Of 16-bit logits the pass is bound by the issue of instructions (about 13 an
 // element, one of them the exponential, which alone would take 44 us at 4096 x
-// 50001): 106 us there, 3.9 TB/s, against 60.5 for the bytes.  FP32 logits come
-// close to memory.  Three rows of 131072 with 20 alternatives, shared by 24
+// 50001): 91 us there, 4.5 TB/s, against 60.5 for the bytes.  Three rows of 131072 with 20 alternatives, shared by 24
 // blocks, take 13 us: a latency to read, one to join a cluster, and the sorted
 // list.  The gradient reads and writes once: 4096 x 32000 FP32 149 us, 511 x
 // 128001 BF16 49 us (5.4 TB/s).
@@ -258,8 +257,9 @@ constexpr int kLogprobPieces = 16 / Elem<DT>::VEC;
 template <int DT, int THREADS, bool MASK>
 constexpr int kLogprobRing = kLogprobDepth * kLogprobPieces<DT> * THREADS * (MASK ? 24 : 16);
 
-// THREADS: 256, or 64 for rows so short that what a row costs a warp beside its
-// columns counts.  Registers for 1024 threads an SM (768 where it takes more).
+// THREADS: 256, or fewer where a row gives a thread so few columns that what a
+// row costs a warp beside them counts.  Registers for 1024 threads an SM (768
+// where it takes more).
 template <int DT, int THREADS, bool TOP, bool MASK>
 __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !TOP ? 768 : 1024) / THREADS)
     logprobs_kernel(const LogprobArgs a) {

@@ -348,3 +348,46 @@ def test_python_refusals(sg):
     with pytest.raises(sg.SgemmError):
         sg.logprobs_backward(z, target, torch.zeros(4, device="cuda"), None, torch.zeros(4, device="cuda"),
                              torch.zeros(4, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,masked", [("f32", False), ("bf16", True)])
+def test_many_long_rows(sg, dtype, masked):
+    """Thousands of rows of tens of thousands of columns, which blocks of four warps walk.  As
+    above, with runs of at most V / 128 + 64; a logit's own log probability adds 4 u |scale z|."""
+    import torch
+    T, V, top, scale = 2600, 16411, 5, 0.75
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    z = (3 * torch.randn(T, V, generator=g, device="cuda")).to(td(dtype))
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    target[::9] = -1
+    mask = allowed = None
+    if masked:
+        rng = np.random.RandomState(3)
+        rows = rng.rand(1, V) < 0.6
+        mask, allowed = torch.from_numpy(pack(rows)).cuda(), torch.from_numpy(rows).cuda()
+    got = sg.logprobs(z, target, scale=scale, mask=mask, top=top)
+    for r0 in range(0, T, 650):
+        rows = slice(r0, r0 + 650)
+        d = z[rows].double() * scale
+        if masked:
+            d = d.masked_fill(~allowed, -float("inf"))
+        lse = torch.logsumexp(d, 1)
+        lp = d - lse[:, None]
+        p = lp.exp()
+        h = -torch.where(p > 0, p * lp, 0.0).sum(1)
+        m = d.max(1).values
+        et = torch.where(p > 0, p * (d - m[:, None]).abs(), 0.0).sum(1) / np.log(2)
+        tol_s = (V / 128 + 80) * U + 4 * U * et
+        tol = tol_s + 4 * U * (m.abs() + (lse - m).abs())
+        assert bool(((got[2][rows].double() - lse).abs() <= tol).all())
+        assert bool(((got[1][rows].double() - h).abs() <= tol + (tol_s + 8 * U) * et).all())
+        y = target[rows].clamp(min=0)[:, None]
+        want = torch.where(target[rows] >= 0, lp.gather(1, y)[:, 0], 0.0)
+        own = tol + 4 * U * d.gather(1, y)[:, 0].abs().nan_to_num(posinf=0.0)
+        same = (got[0][rows].double() == want) | ((got[0][rows].double() - want).abs() <= own)
+        assert bool(same.all())
+        best, ids = torch.sort(d, dim=1, descending=True, stable=True)
+        assert torch.equal(got[4][rows].long(), ids[:, :top])
+        own = tol[:, None] + 4 * U * best[:, :top].abs()
+        assert bool(((got[3][rows].double() - (best[:, :top] - lse[:, None])).abs() <= own).all())
