@@ -83,11 +83,13 @@ int launch_norm(BlockNormArgs a, const Device &dev, cudaStream_t stream) {
 template <int DT, bool ALIGNED>
 int norm_by_width(const BlockNormArgs &a, const Device &dev, cudaStream_t stream) {
     constexpr int VEC = Elem<DT>::VEC;
-    // narrow rows take 8 elements a thread, so that a block has warps to hide its barriers; wide
-    // ones 16, so that a row needs fewer of them
+    // 16 elements a thread (32768 x 1024 BF16 48 us, with 8 58): two blocks an SM while 320 threads
+    // are enough (6553 x 5120 49 us, one block of up to 512 threads 69); rows of single elements,
+    // whose addresses and tests take the registers, 8 while they are narrow
     if (a.D > 5120) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
-    if (a.D > 2048) return launch_norm<DT, ALIGNED, 16 / VEC, 320, ALIGNED ? 2 : 1>(a, dev, stream);
-    return launch_norm<DT, ALIGNED, 8 / VEC, 256, 3>(a, dev, stream);
+    if constexpr (!ALIGNED)
+        if (a.D <= 2048) return launch_norm<DT, false, 8 / VEC, 256, 3>(a, dev, stream);
+    return launch_norm<DT, ALIGNED, 16 / VEC, 320, ALIGNED ? 2 : 1>(a, dev, stream);
 }
 
 // Runners of the gradient's rows: a block (or a cluster of blocks) each, or for
@@ -119,7 +121,8 @@ template <int DT>
 int norm_grad_by_layout(const BlockNormGradArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
     if (a.gate_period == 1)
         return vec ? launch_norm_grad<DT, true, true, 8>(a, dev, stream) : launch_norm_grad<DT, false, true, 8>(a, dev, stream);
-    // 16 elements a thread halve what a row costs beside them; of FP32, which unpacks nothing, 8
+    // 16 elements a thread halve what a row costs beside them (8192 x 4096 BF16: 120 us with 8, 115
+    // with 16); FP32, which unpacks nothing, does with 8, and 16 spill
     constexpr int PER = DT == SGEMM_F32 ? 8 : 16;
     return vec ? launch_norm_grad<DT, true, false, PER>(a, dev, stream) : launch_norm_grad<DT, false, false, 8>(a, dev, stream);
 }
@@ -161,8 +164,11 @@ int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t str
     if (parts == 1 && !a.top) return launch_logprobs<DT, 64, false, MASK>(a, 1, dev, stream);
     if (parts == 1 && a.V < 16384) return launch_logprobs<DT, 64, true, MASK>(a, 1, dev, stream);
     // four warps for longer rows with alternatives, where there are two for each block that the SMs
-    // hold (4096 x 50001 106 -> 91 us; 2000 x 32000 with 20 alternatives 44 -> 48 us)
-    if (parts == 1 && a.T >= 2 * 8 * dev.sms) return launch_logprobs<DT, 128, true, MASK>(a, 1, dev, stream);
+    // hold (4096 x 50001 106 -> 91 us; 2000 x 32000 with 20 alternatives 44 -> 48 us), and while
+    // the columns that may be alternatives are few, which grows with top and with what a thread
+    // sees of a row (4096 x 100001 with 5 alternatives 180 -> 167 us, with 20 211 -> 254 us)
+    if (parts == 1 && a.T >= 2 * 8 * dev.sms && (int64_t)a.top * a.V <= 1 << 20)
+        return launch_logprobs<DT, 128, true, MASK>(a, 1, dev, stream);
     return a.top ? launch_logprobs<DT, 256, true, MASK>(a, parts, dev, stream)
                  : launch_logprobs<DT, 256, false, MASK>(a, parts, dev, stream);
 }
