@@ -108,9 +108,9 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx,
  * C = diag(a_scale) A B^T diag(b_scale) + bias, with A (M x K) and B (N x K,
  * as a linear layer stores its weights) 8-bit integers:
  *     C[m][n] = a_scale[m] * b_scale[n] * sum_k A[m][k] B[n][k] + bias[n]
- * For M <= 4 the sum is an exact integer.  For more rows it is exact while its partial
- * sums stay below 2^24 in magnitude (always for K <= 1024) and an FP32 sum
- * otherwise; the scales and the bias are applied in FP32 and the result is
+ * For M <= 4 the sum is an exact integer.  For more rows it is exact while its
+ * partial sums stay below 2^24 in magnitude (always for K <= 1024) and an FP32
+ * sum otherwise; the scales and the bias are applied in FP32 and the result is
  * rounded once to ctype.
  *   bias: N FP32 values or NULL.  K <= 131071.
  *   workspace: sgemm_i8_workspace_size(M, N, K, B, ldb) bytes, 16-byte aligned,
