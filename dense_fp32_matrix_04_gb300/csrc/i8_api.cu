@@ -148,8 +148,8 @@ struct StreamPlan {
 };
 
 template <int TOK>
-int launch_stream(const I8Args &p, const __half *x, const StreamPlan &plan, float *partials, const Device &dev,
-                  cudaStream_t stream) {
+int launch_stream(const I8Args &p, const __half *x, bool laid_out, const StreamPlan &plan, float *partials,
+                  const Device &dev, cudaStream_t stream) {
     using T = I8StreamTile<TOK>;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
     const auto kernel = i8_stream_kernel<TOK>;
@@ -160,7 +160,7 @@ int launch_stream(const I8Args &p, const __half *x, const StreamPlan &plan, floa
         return SGEMM_ERR_LAUNCH;
     const int64_t units = (int64_t)((p.M + TOK - 1) / TOK) * ((p.N + 127) / 128) * plan.splits;
     return launch<true>(kernel, dim3((unsigned)std::min<int64_t>(units, dev.sms)), dim3(T::THREADS), T::SMEM_BYTES,
-                        stream, 1, tw, tx, p, plan.splits, partials, plan.ldp(p.N), dev.err_word,
+                        stream, 1, tw, tx, p, plan.splits, partials, plan.ldp(p.N), (int)laid_out, dev.err_word,
                         sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
 }
 
@@ -169,22 +169,23 @@ int launch_stream(const I8Args &p, const __half *x, const StreamPlan &plan, floa
 int stream_product(I8Args p, const __half *x, int8_t *rows, float *partials, const StreamPlan &plan, const Device &dev,
                    cudaStream_t stream) {
     int st = SGEMM_OK;
-    if (!rows16(p.B, p.ldb)) {
+    const bool laid_out = !rows16(p.B, p.ldb);
+    if (laid_out) {
         st = lay_out<true>(p.N, p.K, p.B, p.ldb, rows, ld16(p.K), dev, stream);
         if (st != SGEMM_OK) return st;
         p.B = rows;
         p.ldb = ld16(p.K);
     }
     switch (plan.tok) {
-        case 16: st = launch_stream<16>(p, x, plan, partials, dev, stream); break;
-        case 32: st = launch_stream<32>(p, x, plan, partials, dev, stream); break;
-        case 64: st = launch_stream<64>(p, x, plan, partials, dev, stream); break;
-        case 128: st = launch_stream<128>(p, x, plan, partials, dev, stream); break;
-        case 192: st = launch_stream<192>(p, x, plan, partials, dev, stream); break;
-        case 208: st = launch_stream<208>(p, x, plan, partials, dev, stream); break;
-        case 224: st = launch_stream<224>(p, x, plan, partials, dev, stream); break;
-        case 240: st = launch_stream<240>(p, x, plan, partials, dev, stream); break;
-        default: st = launch_stream<256>(p, x, plan, partials, dev, stream);
+        case 16: st = launch_stream<16>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 32: st = launch_stream<32>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 64: st = launch_stream<64>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 128: st = launch_stream<128>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 192: st = launch_stream<192>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 208: st = launch_stream<208>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 224: st = launch_stream<224>(p, x, laid_out, plan, partials, dev, stream); break;
+        case 240: st = launch_stream<240>(p, x, laid_out, plan, partials, dev, stream); break;
+        default: st = launch_stream<256>(p, x, laid_out, plan, partials, dev, stream);
     }
     if (st != SGEMM_OK || plan.splits == 1) return st;
     return join(p, plan.splits, partials, plan.ldp(p.N), stream);

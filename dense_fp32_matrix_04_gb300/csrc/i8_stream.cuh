@@ -118,12 +118,13 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // within groups of eight tiles of rows, so that blocks at work together share
 // both operands in L2.  With splits > 1 each unit writes its raw sums to its
 // own M x ldp slab of `partials` and i8_join_kernel adds the slabs in order and
-// applies the scales.  debug: the test-only switches (bit 0: no copies, so that
-// the waits run out).
+// applies the scales.  laid_out: the kernel before writes B too, not the tokens'
+// codes alone.  debug: the test-only switches (bit 0: no copies, so that the
+// waits run out).
 template <int TOK>
 __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
     i8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8Args p,
-                     int splits, float *__restrict__ partials, int64_t ldp, int *__restrict__ err_word,
+                     int splits, float *__restrict__ partials, int64_t ldp, int laid_out, int *__restrict__ err_word,
                      unsigned long long wait_limit_ns, int debug) {
     using T = I8StreamTile<TOK>;
     extern __shared__ unsigned char smem_raw[];
@@ -197,10 +198,11 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
                 for (int h = 0; h < T::BK / 64; ++h)
                     tma_load_2d(base + at * T::X_BYTES + h * T::X_BOX, &tmX, k * T::BK + 64 * h, m0, full0 + 8 * at);
         };
-        // the tokens may come from the kernel before, which B does not: the first unit's first stages
-        // of B are on their way before that kernel is waited for
+        // The tokens' codes come from the kernel before, and B too where its rows had to be laid out.
+        // The caller's own B does not: the first unit's first stages of it are on their way before
+        // that kernel is waited for.
         int ahead = 0, m0, n0, k0, n;
-        if (!(debug & 1) && (int)blockIdx.x < units) {
+        if (!laid_out && !(debug & 1) && (int)blockIdx.x < units) {
             unit(blockIdx.x, m0, n0, k0, n);
             for (ahead = min(n, T::STAGES); issued < ahead; ++issued) copy_b(issued, k0 + issued, n0);
         }
