@@ -254,9 +254,12 @@ int sgemm_block_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
     if ((w_post != nullptr) != (dw_post != nullptr) || (gate != nullptr) != (dgate != nullptr))
         return SGEMM_ERR_INVALID_ARG;
     if (T == 0) {
-        // sums over no rows
+        // sums over no rows; the gaps between the gate's rows stay as they are
+        const bool gates = dgate && gate_rows > 0;
+        if (gates && !DG.ok(D, size)) return SGEMM_ERR_INVALID_ARG;
         if (cudaMemsetAsync(dw_pre, 0, (size_t)D * wsize, stream) != cudaSuccess ||
-            (dw_post && cudaMemsetAsync(dw_post, 0, (size_t)D * wsize, stream) != cudaSuccess)) {
+            (dw_post && cudaMemsetAsync(dw_post, 0, (size_t)D * wsize, stream) != cudaSuccess) ||
+            (gates && cudaMemset2DAsync(dgate, (size_t)lddg * size, 0, (size_t)D * size, (size_t)gate_rows, stream) != cudaSuccess)) {
             (void)cudaGetLastError();
             return SGEMM_ERR_LAUNCH;
         }

@@ -13,7 +13,8 @@
  * element type allows is accepted.  The calls launch kernels only, so after
  * one call on a device they can be captured into a CUDA graph.  Results are
  * the same bits on every run.  (A backward pass over no rows, T == 0, clears the
- * weights' gradients by cudaMemsetAsync instead of a kernel.)
+ * gradients of the weights and the gate by cudaMemsetAsync and cudaMemset2DAsync
+ * instead of a kernel.)
  */
 #ifndef SGEMM_LAYERS_H
 #define SGEMM_LAYERS_H

@@ -1,0 +1,28 @@
+"""More of include/sgemm_layers.h without a GPU: what is refused on the host before
+any CUDA call."""
+
+import pytest
+
+import dense_fp32_matrix_04_gb300 as sg
+from dense_fp32_matrix_04_gb300 import build
+
+BAD, ALIAS, OK = sg.SGEMM_ERR_INVALID_ARG, sg.SGEMM_ERR_ALIAS, sg.SGEMM_OK
+F32, BF16, F16 = 0, 1, 2
+#: device-looking addresses, 16-byte aligned and far apart; never dereferenced
+P = [0x7F0000000000 + (i << 36) for i in range(24)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return sg.load()
+
+
+@pytest.mark.parametrize("change", [dict(lddg=63), dict(dgate=P[14] + 1), dict(dgate=0), dict(dw_post=0), dict(dw_pre=0)])
+def test_block_norm_backward_over_no_rows_refuses(lib, change):
+    a = dict(T=0, D=64, dtype=BF16, x=P[0], ldx=64, y=P[1], ldy=64, w_pre=P[2], w_post=P[3], wdtype=F32, gate=P[4],
+             ldg=64, gate_rows=2, scale=1.0, rstd=P[7], dn=P[8], lddn=64, dr=P[9], lddr=64, dx=P[10], lddx=64,
+             dy=P[11], lddy=64, dw_pre=P[12], dw_post=P[13], dgate=P[14], lddg=64, ws=P[15], ws_bytes=1 << 30,
+             stream=None)
+    a.update(change)
+    assert lib.sgemm_block_norm_backward(*a.values()) == BAD
