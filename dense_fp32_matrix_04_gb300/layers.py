@@ -159,7 +159,8 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
 
     Returns ``(r, n, rstd)``, or with ``quantize`` ``(r, q, q_scale, rstd)``: n as
     8-bit integers with a scale per row.  ``rstd`` (2 x T) is for the backward
-    pass.  ``out`` receives r; it may be x.
+    pass.  ``out`` receives r; it may be x.  Rows of no columns (D = 0) have NaN for
+    the means' roots and 0 for the scale.
     """
     dt, dev, shape, px, ldx = _first(x, "x")
     f32, empty, where = _torch.float32, _torch.empty, x.device
@@ -185,9 +186,23 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
                                    pr, ldr, pn, D or 1, pq, D or 1, ps, rstd.data_ptr(), _on(dev, stream))
     if status:
         _check(status, "sgemm_block_norm")
+    if D == 0 and T:
+        _no_columns(rstd, w_post is not None, s if quantize else None, dev, stream)
     if keep is not None:
         keep += made
     return made
+
+
+def _no_columns(rstd, post, q_scale, index, stream):
+    """What a row of no elements has beside them, which the library does not launch a kernel
+    for: the mean of nothing is NaN, the largest of nothing 0."""
+    with _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                            _torch.cuda.ExternalStream(_on(index, stream), device=index)):
+        rstd.fill_(float("nan"))
+        if not post:
+            rstd[0].fill_(1.0)
+        if q_scale is not None:
+            q_scale.zero_()
 
 
 @_foreign

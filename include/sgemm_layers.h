@@ -55,7 +55,8 @@ typedef enum {
  *   rstd: 2 x T FP32: rsqrt(mean(y^2) + eps) of each row (1 without w_post),
  *       then rsqrt(mean(r^2) + eps); the backward pass reads them.  May be
  *       NULL.
- * T <= 2^30, D <= 24576.
+ * T <= 2^30, D <= 24576.  Without rows or columns (T == 0 or D == 0) nothing is
+ * launched and nothing written, rstd and q_scale included.
  */
 int sgemm_block_norm(int T, int D, int dtype,
                      const void *x, int ldx, const void *y, int ldy,

@@ -50,3 +50,24 @@ def test_the_gaps_between_the_gates_rows_stay(sg):
                                            torch.cuda.current_stream().cuda_stream)
     assert status == sg.SGEMM_OK
     assert bool((dw_pre == 0).all()) and bool((dgate[:, :D] == 0).all()) and bool((dgate[:, D:] == 5).all())
+
+
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("side", [False, True])
+def test_rows_of_no_columns(sg, post, side):
+    import torch
+    T = 700
+    x, w = torch.empty(T, 0, device="cuda"), torch.empty(0, device="cuda")
+    stream = torch.cuda.Stream() if side else None
+    torch.full((2, T), 5.0, device="cuda")          # what the call allocates has been somebody else's before
+    torch.full((T,), 5.0, device="cuda")
+    r, n, rstd = sg.block_norm(x, x, w, w if post else None, stream=stream)
+    torch.cuda.synchronize()
+    assert r.shape == n.shape == (T, 0)
+    want = (x.square().mean(1) + 1e-6).rsqrt()      # the mean of nothing
+    assert torch.equal(torch.isnan(rstd[1]), torch.isnan(want)) and bool(torch.isnan(rstd[1]).all())
+    assert bool(torch.isnan(rstd[0]).all()) if post else bool((rstd[0] == 1).all())
+    r, q, scale, rstd = sg.block_norm(x, x, w, w if post else None, quantize=True, stream=stream)
+    torch.cuda.synchronize()
+    assert q.shape == (T, 0) and torch.equal(scale, sg.quantize_i8(x)[1]) and bool((scale == 0).all())
+    assert bool(torch.isnan(rstd[1]).all())
