@@ -66,12 +66,8 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------- up to four tokens
 
-// Whether the kernel that reads whole rows takes the product: its tokens' codes
-// have to fit shared memory beside three other blocks'.
-bool takes_rows(int M, int K) {
-    const int tokens = M <= 1 ? 1 : M <= 2 ? 2 : 4;
-    return M <= kRowsTokens && K > 0 && tokens * rows_pitch(K) <= 52 * 1024;
-}
+// Up to four tokens go to the kernel that reads whole rows, whatever K.
+bool takes_rows(int M, int K) { return M <= kRowsTokens && K > 0; }
 
 template <int MT, int XT, bool ALIGNED>
 int launch_rows(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
@@ -85,16 +81,34 @@ int launch_rows(const I8Args &p, const void *X, int64_t ldx, const Device &dev, 
     return launch(kernel, dim3(blocks), dim3(kRowsThreads), smem, stream, 1, p, X, ldx);
 }
 
+// As many tokens at a time as shared memory holds the codes of: all four up to
+// K = 57344, two up to 114688, one of any K.  B is read once for each of those.
 template <int XT>
-int rows_product(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
-    auto by_alignment = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value;
-        return rows16(p.B, p.ldb) ? launch_rows<MT, XT, true>(p, X, ldx, dev, stream)
-                                  : launch_rows<MT, XT, false>(p, X, ldx, dev, stream);
-    };
-    if (p.M <= 1) return by_alignment(std::integral_constant<int, 1>{});
-    if (p.M <= 2) return by_alignment(std::integral_constant<int, 2>{});
-    return by_alignment(std::integral_constant<int, 4>{});
+int rows_product(const I8Args &all, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    int most = kRowsTokens;
+    while (most * rows_pitch(all.K) > kRowsCodes) most /= 2;
+    for (int m = 0; m < all.M; m += most) {
+        I8Args p = all;
+        p.M = std::min(most, all.M - m);
+        p.C = static_cast<char *>(all.C) + m * all.ldc * dtype_size(all.ctype);
+        const void *x = X;
+        if constexpr (XT < 0) {
+            p.A += m * all.lda;
+            p.a_scale += m;
+        } else {
+            x = static_cast<const typename Elem<XT < 0 ? 0 : XT>::type *>(X) + m * ldx;
+        }
+        auto by_alignment = [&](auto mt) {
+            constexpr int MT = decltype(mt)::value;
+            return rows16(p.B, p.ldb) ? launch_rows<MT, XT, true>(p, x, ldx, dev, stream)
+                                      : launch_rows<MT, XT, false>(p, x, ldx, dev, stream);
+        };
+        const int st = p.M <= 1   ? by_alignment(std::integral_constant<int, 1>{})
+                       : p.M <= 2 ? by_alignment(std::integral_constant<int, 2>{})
+                                  : by_alignment(std::integral_constant<int, 4>{});
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
 }
 
 // ---------------------------------------------------------------- more tokens
@@ -254,16 +268,16 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx, signed ch
 
 // Bytes of a workspace without k-splits, which depend on the device.
 static size_t least_workspace(int M, int N, int K, const signed char *B, int ldb) {
-    if (M <= 0 || N <= 0 || K < 0 || takes_rows(M, K)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || takes_rows(M, K)) return 0;
     return (size_t)Workspace(M, N, K, !rows16(reinterpret_cast<const int8_t *>(B), ldb), StreamPlan()).bytes;
 }
 
 // One workspace serves both entry points: with 8-bit tokens the place of their
 // scales stays unused.
 size_t sgemm_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb) {
-    if (M <= 0 || N <= 0 || K < 0) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || takes_rows(M, K)) return 0;
     const int sms = device_sms();
-    if (!sms || takes_rows(M, K)) return 0;
+    if (!sms) return 0;
     return (size_t)Workspace(M, N, K, !rows16(reinterpret_cast<const int8_t *>(B), ldb), StreamPlan(M, N, K, sms)).bytes;
 }
 
@@ -295,8 +309,7 @@ int sgemm_i8(int M, int N, int K, const signed char *A, int lda, const float *a_
 }
 
 size_t sgemm_linear_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb) {
-    // K = 0 quantises rows of nothing, for their scales
-    return K == 0 && M > 0 && N > 0 ? (size_t)up256(4 * (int64_t)M) : sgemm_i8_workspace_size(M, N, K, B, ldb);
+    return sgemm_i8_workspace_size(M, N, K, B, ldb);
 }
 
 int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx, const signed char *B, int ldb,
@@ -317,6 +330,7 @@ int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx, cons
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     float *s = reinterpret_cast<float *>(ws);
     const I8Args p{M, N, K, nullptr, reinterpret_cast<const int8_t *>(B), 0, ldb, s, b_scale, bias, C, ldc, ctype};
+    if (K == 0) return join(p, 0, nullptr, 0, stream);
     if (takes_rows(M, K))
         return by_dtype(xtype, [&](auto xt) { return rows_product<decltype(xt)::value>(p, X, ldx, dev, stream); });
     const StreamPlan plan(M, N, K, dev.sms);
@@ -324,7 +338,6 @@ int sgemm_linear_i8(int M, int N, int K, int xtype, const void *X, int ldx, cons
     __half *codes = reinterpret_cast<__half *>(ws + at.codes);
     st = quantize(M, K, xtype, X, ldx, codes, ld8(K), s, dev, stream);
     if (st != SGEMM_OK) return st;
-    if (K == 0) return join(p, 0, nullptr, 0, stream);
     return stream_product(p, codes, reinterpret_cast<int8_t *>(ws + at.rows), reinterpret_cast<float *>(ws + at.partials),
                           plan, dev, stream);
 }

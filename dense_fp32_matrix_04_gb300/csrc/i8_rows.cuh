@@ -13,6 +13,11 @@
 // the rest a launch, the quantised row and the last loads' latency.  From five
 // tokens on the byte products, 273 a cycle and SM, would set the pace, and the
 // tensor cores are faster (i8_stream.cuh; 11.4 us there for five tokens).
+//
+// The sums are exact for every K, so long rows stay here: four tokens' codes fit
+// shared memory up to K = 57344 (4 x 5120 x 28672 about 58 us, 54 for five tokens
+// on the tensor cores); beyond, two or one at a time read B once for each
+// (4 x 4096 x 65536 178 us, 100 for five).
 #pragma once
 
 #include <cstdint>
@@ -24,6 +29,8 @@ namespace sgemm {
 
 constexpr int kRowsTokens = 4, kRowsThreads = 256;
 constexpr int kRowsPieces = 8;  // loads of 16 bytes a lane has in flight
+
+constexpr int kRowsCodes = 224 * 1024;  // shared memory that a block's tokens' codes may take
 
 // Bytes of a token's codes in shared memory: whole rounds of loads.
 __host__ __device__ constexpr int rows_pitch(int K) { return (K + 511) / 512 * 512; }
@@ -48,9 +55,19 @@ __global__ void __launch_bounds__(kRowsThreads, MT < 4 && ALIGNED ? 4 : 3)
     load(w, from, 0);
 
     if constexpr (XT < 0) {
+        // 16 codes at a time; those past the row's end are 0
         for (int m = 0; m < MT; ++m)
-            for (int k = tid; k < pitch; k += kRowsThreads)
-                smem[m * pitch + k] = k < K && m < p.M ? (unsigned char)p.A[m * p.lda + k] : 0;
+#pragma unroll 4
+            for (int k = 16 * tid; k < pitch; k += 16 * kRowsThreads) {
+                const uint4 c = load_codes<false>(p.A + m * p.lda, k, m < p.M ? K : 0);
+                uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int left = K - k - 4 * i;
+                    word[i] = left >= 4 ? word[i] : left > 0 ? word[i] & ((1u << 8 * left) - 1) : 0u;
+                }
+                *reinterpret_cast<uint4 *>(smem + m * pitch + k) = make_uint4(word[0], word[1], word[2], word[3]);
+            }
         if (tid < MT) scales[tid] = tid < p.M ? p.a_scale[tid] : 0.f;
     } else {
         // the block's warps are shared out to the tokens, which are quantised side by side

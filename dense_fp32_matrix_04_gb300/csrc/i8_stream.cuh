@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(I8StreamTile<TOK>::THREADS, 1)
 }
 
 // Adds the k-splits' slabs in order and applies the scales and the bias (with
-// no split at all, K = 0, the sums are empty).  blockIdx.y (+ gridDim.y, ...):
+// no split at all, K = 0, the sums are empty and the scales, which may not be
+// finite or not exist, are not read).  blockIdx.y (+ gridDim.y, ...):
 // rows of C; a thread four columns, whose sums lie on 16 bytes (ldp is a
 // multiple of 4 and the slabs' rows are padded to it).
 constexpr int kJoinThreads = 128;
@@ -435,12 +436,13 @@ __global__ void __launch_bounds__(kJoinThreads)
             const float4 v = *reinterpret_cast<const float4 *>(partials + ((int64_t)k * p.M + m) * ldp + n);
             s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-        const float sums[4] = {s.x, s.y, s.z, s.w}, scale = p.a_scale[m];
+        const float sums[4] = {s.x, s.y, s.z, s.w}, scale = splits ? p.a_scale[m] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < p.N)
-                store_c(p.C, m * p.ldc + n + i, p.ctype,
-                        fmaf(sums[i] * scale, p.b_scale[n + i], p.bias ? p.bias[n + i] : 0.f));
+        for (int i = 0; i < 4; ++i) {
+            if (n + i >= p.N) break;
+            const float bias = p.bias ? p.bias[n + i] : 0.f;
+            store_c(p.C, m * p.ldc + n + i, p.ctype, splits ? fmaf(sums[i] * scale, p.b_scale[n + i], bias) : bias);
+        }
     }
 }
 

@@ -117,9 +117,9 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx,
  *   bias: N FP32 values or NULL.  K <= 131071.
  *   workspace: sgemm_i8_workspace_size(M, N, K, B, ldb) bytes, 16-byte aligned,
  *       with contents that do not matter; calls that share one must not
- *       overlap on the GPU.  M <= 4 needs none; rows of B that are not 16-byte
- *       aligned need N K bytes of it.
- * K == 0: every sum is empty (C = bias, or 0).
+ *       overlap on the GPU.  M <= 4 and K == 0 need none; rows of B that are not
+ *       16-byte aligned need N K bytes of it.
+ * K == 0: every sum is empty (C = bias, or 0, whatever the scales).
  * The kernel for more than four rows waits for its own copies, with a limit:
  * one that runs out is reported by sgemm_device_status, and C is unspecified.
  */
