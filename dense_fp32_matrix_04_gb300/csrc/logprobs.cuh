@@ -612,34 +612,22 @@ struct LogprobGradRow {
                 if (at == e) v[e] += hit;
     }
     // the same for 8 columns of 16 bits, in packed pairs and in powers of 2: log2 p is off by
-    // 2^-24 of the largest of its terms, far below what the result's 16 bits hold
+    // 2^-24 of the largest of its terms, about what the rounding of lse costs it anyhow
     template <int DT>
     __device__ uint4 apply16(uint4 raw, uint32_t bits, int col) const {
         float v[8];
+        unpack16<DT>(raw, v);
         if (!usual || (unsigned)(target - col) < 8u) {
-            unpack16<DT>(raw, v);
             apply<8>(v, bits, col);
             return pack16<DT>(v);
         }
-        // no -infinity, whose logarithm times a p of 0 would not be 0
-        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (DT == SGEMM_BF16) {
-                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&w[i]), __float2bfloat162_rn(-1e30f));
-                w[i] = *reinterpret_cast<const uint32_t *>(&m);
-            } else {
-                const __half2 m = __hmax2(*reinterpret_cast<__half2 *>(&w[i]), __float2half2_rn(-65504.f));
-                w[i] = *reinterpret_cast<const uint32_t *>(&m);
-            }
-        }
-        unpack16<DT>(make_uint4(w[0], w[1], w[2], w[3]), v);
         const F2 c(scale * kLog2e), off(-lse * kLog2e), a(A), b(B * kLn2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const F2 t = fma(F2(v[2 * i], v[2 * i + 1]), c, off);
-            const float2 x = t.both();
-            const float2 d = (F2(exp2_approx(x.x), exp2_approx(x.y)) * fma(b, t, a)).both();
+            // p is 0 below, and a logarithm of -infinity times it would not be
+            const float2 t = fma(F2(v[2 * i], v[2 * i + 1]), c, off).both();
+            const float x = fmaxf(t.x, -1000.f), y = fmaxf(t.y, -1000.f);
+            const float2 d = (F2(exp2_approx(x), exp2_approx(y)) * fma(b, F2(x, y), a)).both();
             v[2 * i] = d.x;
             v[2 * i + 1] = d.y;
         }
