@@ -5,11 +5,12 @@
 // t_j = z_j c - M (one fused operation), the pass keeps
 //     s = sum 2^t_j   and   s1 = sum 2^t_j t_j,
 // which a larger M' turns into f s and f (s1 + s d), d = M - M', f = 2^d: the
-// rounding of M is the same for every term, so it costs no accuracy.  At the end
+// rounding of M is the same for every term, so it costs no accuracy while it is
+// below 1/2 (|M| < 2^24; the 2^128 that FP32 ends at is one of 128).  At the end
 // lse = ln 2 M + ln s, taken as scale m + ln s + ln 2 (M - m c) with an exact
 // difference; entropy = ln s - ln 2 s1 / s; log p_y = scale (z_y - m) - ln s -
-// ln 2 (M - m c).  Logits beyond 1e37, whose products with c could overflow
-// (masks of the type's lowest value), take t_j = (z_j - m) c instead.
+// ln 2 (M - m c).  Where m c is larger (rows of nothing but mask values, large
+// scales), t_j = (z_j - m) c instead.
 //
 // The alternatives cost the pass nothing: each thread knows the largest logit it
 // has met, and at the row's end at least `top` columns reach the top-th largest
@@ -95,13 +96,15 @@ __device__ __forceinline__ bool better(float v, int id, float v2, int id2) {
 // The running sums of a thread, or of several joined.
 struct SoftmaxState {
     float m = -INFINITY, M = -INFINITY, s = 0.f, s1 = 0.f;
-    static constexpr float kLarge = 1e37f;
     // (a product of its own: fused into a difference it would not be the M that the terms saw)
-    __device__ static float reference(float m, float c) { return fabsf(m) < kLarge ? __fmul_rn(m, c) : m; }
-    // log2 of the factor from one maximum to another; far below 0, 2^d is 0 and the bound on d
-    // keeps products with it from being 0 times infinity
+    __device__ static float reference(float m, float c) { return __fmul_rn(m, c); }
+    // whether terms are taken relative to the product M, rather than to m before it is scaled
+    __device__ static bool usual(float M) { return fabsf(M) < 0x1p24f; }
+    // log2 of the factor from one maximum to another, each as its terms see it; far below 0, 2^d
+    // is 0 and the bound on d keeps products with it from being 0 times infinity
     __device__ static float step(float m, float M, float m2, float M2, float c) {
-        return fabsf(m) < kLarge && fabsf(m2) < kLarge ? M - M2 : (m - m2) * c;
+        const bool from = usual(M), to = usual(M2);
+        return from && to ? M - M2 : from ? -fmaf(m2, c, -M) : to ? fmaf(m, c, -M2) : (m - m2) * c;
     }
     // raises the maximum to at least m2
     __device__ void raise(float m2, float c) {
@@ -116,7 +119,7 @@ struct SoftmaxState {
     // adds the N logits v, none of them above m, two at a time (N is 1 or even)
     template <int N>
     __device__ void add(const float *v, float c) {
-        if (N > 1 && fabsf(m) < kLarge) {
+        if (N > 1 && usual(M)) {
             F2 sum(s, 0.f), sum1(s1, 0.f);
             const F2 cc(c), MM(-M);
 #pragma unroll
@@ -137,7 +140,7 @@ struct SoftmaxState {
         // a term of 0 times -infinity (a logit of -infinity), a NaN, or large logits
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float t = fabsf(m) < kLarge ? fmaf(v[j], c, -M) : (v[j] - m) * c, e = exp2_approx(t);
+            const float t = usual(M) ? fmaf(v[j], c, -M) : (v[j] - m) * c, e = exp2_approx(t);
             s += e;
             s1 = fmaf(e, fmaxf(t, -1000.f), s1);
         }
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         if (part == 0 && warp == 0) {
             const bool none = all.m == -INFINITY && !(all.s != all.s);
             // ln of the sum relative to exactly m
-            const float off = fabsf(all.m) < SoftmaxState::kLarge ? -fmaf(all.m, c, -all.M) : 0.f;
+            const float off = SoftmaxState::usual(all.M) ? -fmaf(all.m, c, -all.M) : 0.f;
             const float log_s = logf(all.s), log_sum = fmaf(kLn2, off, log_s);
             if (lane == 0) {
                 if (a.lse) a.lse[t] = none ? -INFINITY : fmaf(all.m, a.scale, log_sum);
