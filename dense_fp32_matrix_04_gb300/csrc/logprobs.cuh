@@ -58,6 +58,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return r;
 }
 
+// The same with results below 2^-126, which exp2_approx takes as 0.
+__device__ __forceinline__ float exp2_small(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Bits of the mask's row for columns c .. c + n - 1 (n <= 8), lowest first;
 // columns from V on read as 0.
 __device__ __forceinline__ uint32_t mask_bits(const int32_t *row, int c, int n, int V) {
@@ -593,8 +600,9 @@ struct LogprobGradRow {
         usual = fabsf(lse) < 1e29f;
     }
     __device__ float one(float z) const {
-        const float logp = fmaf(z, scale, -lse), p = exp2_approx(logp * kLog2e);
-        // p = 0 leaves nothing of B log p (log p may be -infinity there)
+        // p below 2^-126 counts: its product with B log p may be above.  p = 0 leaves nothing of it
+        // (log p may be -infinity there).
+        const float logp = fmaf(z, scale, -lse), p = exp2_small(logp * kLog2e);
         return lse == -INFINITY ? 0.f : p * fmaf(B, fmaxf(logp, -1000.f), A);
     }
     // the N columns from `col` on; bits: which of them the mask allows
