@@ -585,7 +585,7 @@ struct LogprobGradArgs {
 struct LogprobGradRow {
     float scale, lse, A, B, hit;
     int target;  // -1: none
-    bool usual;  // lse is finite and its products with log2(e) are
+    bool usual;  // lse is a number that the packed path below is exact enough for
     __device__ LogprobGradRow(const LogprobGradArgs &a, int64_t t) {
         scale = a.scale;
         lse = a.lse[t];
@@ -597,7 +597,7 @@ struct LogprobGradRow {
         A = -a.scale * (a.g_entropy ? fmaf(gh, a.entropy[t], g) : g);
         B = -a.scale * gh;
         hit = a.scale * g;
-        usual = fabsf(lse) < 1e29f;
+        usual = fabsf(lse) < 256.f;
     }
     __device__ float one(float z) const {
         // p below 2^-126 counts: its product with B log p may be above.  p = 0 leaves nothing of it
@@ -622,8 +622,10 @@ struct LogprobGradRow {
             for (int e = 0; e < N; ++e)
                 if (at == e) v[e] += hit;
     }
-    // the same for 8 columns of 16 bits, in packed pairs and in powers of 2: log2 p is off by
-    // 2^-24 of the largest of its terms, about what the rounding of lse costs it anyhow
+    // the same for 8 columns of 16 bits, in packed pairs and in powers of 2.  Its terms scale z
+    // log2(e) and lse log2(e) are each rounded before they cancel, so p is off by 2^-24 (|scale z| +
+    // |lse|) relative: at the limit of 256 2^-15, a sixteenth of FP16's half unit.  Rows beyond it
+    // take the path above, which rounds their difference once.
     template <int DT>
     __device__ uint4 apply16(uint4 raw, uint32_t bits, int col) const {
         float v[8];

@@ -182,6 +182,7 @@ int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float s
  * for the columns that the mask allows, and 0 for the others.
  *   lse, entropy: what the forward pass wrote (entropy may be NULL when
  *       g_entropy is NULL).  g_entropy NULL: no gradient reaches the entropy.
+ *       lse is FP32, so beside everything else p_j is off by 2^-24 |lse| relative.
  *       Rows with target < 0 have no gradient from logprob.
  *   dz: T x V, of the logits' type; may be the logits themselves (same pointer
  *       and leading dimension).

@@ -97,3 +97,42 @@ def test_a_maximum_that_rises_past_the_limit(sg):
     assert float(((got[0].double() - lp).abs() - 4 * U * lp.abs()).max()) <= tol
     h = want - (p * a).sum(1)
     assert float((got[1].double() - h).abs().max()) <= tol * (2 + 4 * et)
+
+
+@pytest.mark.parametrize("dtype,base,spread,scale", [c for c in CASES if (abs(c[1]) + 4 * c[2]) * c[3] < 3e8] + [
+    ("bf16", 300.0, 3.0, 1.0), ("f16", -400.0, 2.0, 1.0), ("bf16", 1e6, 0.0, 1.0), ("f16", 6e4, 30.0, 1.0),
+    ("bf16", 240.0, 1.0, 1.0), ("f16", 240.0, 1.0, 1.0)])
+@pytest.mark.parametrize("T,V", [(2, 5), (3, 1111), (2, 9001)])
+def test_gradients_moved_together(sg, T, V, dtype, base, spread, scale):
+    """lse enters the formula as the forward pass rounded it (beyond 3e8 that rounding is all that is
+    left of p, and p need not be finite).  Then p is off by 8 u (|log p| + 2) +
+    2^-20 relative, and for 16 bits while |lse| < 256 by another 600 u; the result by its half unit."""
+    import torch
+    half = {"f32": U, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    rng = np.random.RandomState(V)
+    z = np.float64(base) + spread * rng.randn(T, V)
+    z = torch.from_numpy(np.clip(z, -3.4e38, 3.4e38).astype(np.float32)).to(td(dtype))
+    z = z.clamp(torch.finfo(td(dtype)).min, torch.finfo(td(dtype)).max).cuda()
+    target = torch.from_numpy(rng.randint(0, V, T)).cuda()
+    target[0] = -1
+    _, H, lse = sg.logprobs(z, target, scale=scale)[:3]
+    g, gh = rng.randn(T).astype(np.float32), rng.randn(T).astype(np.float32)
+    dz = sg.logprobs_backward(z, target, lse, H, torch.from_numpy(g).cuda(), torch.from_numpy(gh).cuda(), scale=scale)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    s, got, l64, h64 = float(np.float32(scale)), f(dz), f(lse), f(H)
+    logp = s * f(z) - l64[:, None]
+    p = np.exp(logp)
+    logp = np.where(p > 0, logp, 0)
+    y = target.cpu().numpy()
+    gl = np.where(y >= 0, g, 0).astype(np.float64)
+    hit = np.zeros((T, V))
+    hit[np.arange(T), np.maximum(y, 0)] = gl
+    e = gh.astype(np.float64)[:, None]
+    with np.errstate(over="ignore"):
+        want = s * (hit - gl[:, None] * p - e * p * (logp + h64[:, None]))
+        size = p * (np.abs(gl[:, None]) + np.abs(e) * (np.abs(logp) + np.abs(h64[:, None])))
+        rel = 8 * U * (np.abs(logp) + 2) + 2.0 ** -20 + (600 * U if dtype != "f32" else 0)
+        tol = s * (size * rel + 4 * U * np.abs(hit)) + half * np.abs(want) * 1.01 + (2.0 ** -25 if dtype == "f16" else 2.0 ** -126)
+        top = torch.finfo(td(dtype)).max
+        same = (np.abs(got - want) <= tol) | ((np.abs(want) > top) & np.isinf(got) & (np.sign(got) == np.sign(want)))
+        assert same.all(), f"{got[~same][:4]} against {want[~same][:4]}"
