@@ -186,7 +186,8 @@ int launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t stream) {
 bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, const int32_t *mask, int ldm,
                        int mask_rows) {
     if (T < 0 || V < 0 || T > kMaxRows || V > kMaxRows || !dtype_ok(dtype)) return false;
-    if (!finite(scale) || !(scale > 0.f) || mask_rows < 0) return false;
+    // (a larger scale's product with log2(e) would not be finite)
+    if (!(scale > 0.f && scale <= 0x1p127f) || mask_rows < 0) return false;
     if (T == 0) return true;
     if (V > 0 && !z.ok(V, dtype_size(dtype))) return false;
     if ((mask != nullptr) != (mask_rows > 0)) return false;

@@ -151,7 +151,7 @@ size_t sgemm_linear_i8_workspace_size(int M, int N, int K, const signed char *B,
  *     top      the `top` most likely columns, most likely first, equal logits
  *              by the lowest column, with their log probabilities
  * read from the logits in one pass.
- *   scale: finite and > 0 (one over the temperature).
+ *   scale: > 0 and at most 2^127 (one over the temperature).
  *   mask: mask_rows x ceil(V / 32) words, bit j % 32 of word j / 32 set where
  *       column j is allowed; mask_rows is T or 1 (one mask for all rows), ldm
  *       words between rows.  NULL (mask_rows 0): every column is allowed.  What

@@ -26,3 +26,11 @@ def test_block_norm_backward_over_no_rows_refuses(lib, change):
              stream=None)
     a.update(change)
     assert lib.sgemm_block_norm_backward(*a.values()) == BAD
+
+
+@pytest.mark.parametrize("scale,want", [(2.0 ** 127 * (1 + 2.0 ** -23), BAD), (3.4e38, BAD), (2.0 ** 127, OK), (1e-45, OK)])
+def test_logprobs_scales(lib, scale, want):
+    # no rows: nothing is launched for what is accepted
+    assert lib.sgemm_logprobs(0, 100, F32, P[0], 100, scale, 0, 0, 0, P[2], P[3], P[4], P[5], 0, 0, 0, None) == want
+    assert lib.sgemm_logprobs_backward(0, 100, F32, P[0], 100, scale, 0, 0, 0, P[2], P[3], P[4], P[5], P[6], P[7], 100,
+                                       None) == want

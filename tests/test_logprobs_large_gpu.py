@@ -136,3 +136,17 @@ def test_gradients_moved_together(sg, T, V, dtype, base, spread, scale):
         top = torch.finfo(td(dtype)).max
         same = (np.abs(got - want) <= tol) | ((np.abs(want) > top) & np.isinf(got) & (np.sign(got) == np.sign(want)))
         assert same.all(), f"{got[~same][:4]} against {want[~same][:4]}"
+
+
+def test_the_largest_scale(sg):
+    import torch
+    z = torch.tensor([[0.0, 0.0, -1e-38, 0.0], [1.0, 0.5, -1.0, 0.0]], device="cuda")
+    target = torch.tensor([1, 0], device="cuda")
+    scale = 2.0 ** 127
+    logprob, entropy, lse = sg.logprobs(z, target, scale=scale)
+    a = torch.logsumexp(z[0].double() * scale, 0)
+    p = torch.exp(z[0].double() * scale - a)
+    # (three columns of 1, one of 2^-2.4: sums and logarithms of numbers near 1, ten roundings and 2^-21)
+    assert abs(float(lse[0]) - float(a)) < 2.0 ** -19 and abs(float(logprob[0]) + float(a)) < 2.0 ** -19
+    assert abs(float(entropy[0]) + float((p * p.log()).sum())) < 2.0 ** -18
+    assert float(logprob[1]) == 0 and float(entropy[1]) == 0
