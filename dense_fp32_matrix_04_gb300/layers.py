@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 
 _I, _F, _P, _S = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -122,25 +123,28 @@ def _foreign(fn):
     """Runs a call whose tensors are on another device than the current one, or whose
     stream is not torch's: with the device made current, and with what the call
     allocates (on torch's stream) ordered before and marked as used on its stream."""
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **more):
+    def call(*args, stream=None, **more):
         if _torch is None:
             _start()
+        first = args[0] if args else more.get(name)
         index = first.get_device() if isinstance(first, _torch.Tensor) else -1
         if stream is None and (index < 0 or index == _current_device()):
-            return fn(first, *args, **more)
+            return fn(*args, **more)
         if index < 0:
-            return fn(first, *args, stream=stream, **more)  # refuses it
+            return fn(*args, stream=stream, **more)  # refuses it
         with _torch.cuda.device(index):
             handle = _on(index, stream)
             if handle == _raw_stream(index):
-                return fn(first, *args, **more)
+                return fn(*args, **more)
             other = _torch.cuda.ExternalStream(handle, device=index) if isinstance(stream, int) else stream
             # the inputs are the caller's to order; what is allocated here may have been freed by
             # work that is still queued on torch's stream
             other.wait_stream(_torch.cuda.current_stream(index))
             kept = []
-            got = fn(first, *args, stream=stream, keep=kept, **more)
+            got = fn(*args, stream=stream, keep=kept, **more)
             for t in kept:
                 t.record_stream(other)
             return got

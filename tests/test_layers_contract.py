@@ -34,3 +34,18 @@ def test_logprobs_scales(lib, scale, want):
     assert lib.sgemm_logprobs(0, 100, F32, P[0], 100, scale, 0, 0, 0, P[2], P[3], P[4], P[5], 0, 0, 0, None) == want
     assert lib.sgemm_logprobs_backward(0, 100, F32, P[0], 100, scale, 0, 0, 0, P[2], P[3], P[4], P[5], P[6], P[7], 100,
                                        None) == want
+
+
+def test_first_argument_by_name():
+    """Every call takes its first tensor by the name that its signature shows."""
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(2, 8), torch.ones(8)
+    y = torch.zeros(2, dtype=torch.int64)
+    for call in (lambda: sg.block_norm(x=x, y=x, w_pre=w), lambda: sg.quantize_i8(x=x),
+                 lambda: sg.block_norm_backward(x=x, y=x, w_pre=w, rstd=x, dn=x), lambda: sg.logprobs(logits=x, target=y),
+                 lambda: sg.linear_i8(x=x, w=x, w_scale=w), lambda: sg.matmul_i8(a=x.to(torch.int8), a_scale=w, w=x, w_scale=w),
+                 lambda: sg.logprobs_backward(logits=x, target=y, lse=w, entropy=w, g_logprob=w)):
+        with pytest.raises(TypeError, match="must be a 2-D CUDA tensor"):
+            call()
+    with pytest.raises(TypeError, match="missing"):
+        sg.quantize_i8()
