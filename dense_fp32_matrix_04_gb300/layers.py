@@ -122,13 +122,17 @@ def _on(index, stream):
 def _foreign(fn):
     """Runs a call whose tensors are on another device than the current one, or whose
     stream is not torch's: with the device made current, and with what the call
-    allocates (on torch's stream) ordered before and marked as used on its stream."""
-    name = next(iter(inspect.signature(fn).parameters))
+    allocates (on torch's stream) ordered before and marked as used on its stream.  The
+    stream is seen by name or by place."""
+    names = list(inspect.signature(fn).parameters)
+    name, at = names[0], names.index("stream")
 
     @functools.wraps(fn)
     def call(*args, stream=None, **more):
         if _torch is None:
             _start()
+        if len(args) == at + 1 and stream is None:
+            stream, args = args[at], args[:at]
         first = args[0] if args else more.get(name)
         index = first.get_device() if isinstance(first, _torch.Tensor) else -1
         if stream is None and (index < 0 or index == _current_device()):
@@ -153,7 +157,7 @@ def _foreign(fn):
 
 @_foreign
 def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantize=False, out=None, stream=None,
-               keep=None):
+               *, keep=None):
     """The step from one block's output ``y`` and the residual stream ``x`` (T x D)
     to the next block's input:
 
@@ -210,7 +214,7 @@ def _no_columns(rstd, post, q_scale, index, stream):
 
 
 @_foreign
-def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, scale=1.0, stream=None, keep=None):
+def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, scale=1.0, stream=None, *, keep=None):
     """Gradients ``(dx, dy, dw_pre, dw_post, dgate)`` of ``block_norm`` from those of
     its n and r (``dr`` None: zero); ``dw_post`` and ``dgate`` are None where there is
     no such input."""
@@ -249,7 +253,7 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
 
 
 @_foreign
-def quantize_i8(x, stream=None, keep=None):
+def quantize_i8(x, stream=None, *, keep=None):
     """``(q, scale)``: the rows of x (M x K) as 8-bit integers, scale = max|row| / 127
     and q = rint(row * (127 / max|row|)).  For activations a scale per token, for
     weights (N x K) one per output channel."""
@@ -303,7 +307,7 @@ def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, s
 
 
 @_foreign
-def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, keep=None):
+def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
     """``a_scale[m] * w_scale[n] * sum_k a[m, k] w[n, k] + bias[n]`` for 8-bit integers
     a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise)."""
     if _torch is None:
@@ -315,7 +319,7 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, works
 
 
 @_foreign
-def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, keep=None):
+def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
     """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
     quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise."""
     dt, _, _, px, ldx = _first(x, "x")
@@ -335,7 +339,7 @@ def _mask(mask, T, V, index):
 
 
 @_foreign
-def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, keep=None):
+def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, *, keep=None):
     """``(logprob, entropy, lse)`` per row of ``softmax(scale * logits)`` (T x V), and with
     ``top`` > 0 also ``(top_logprob, top_id)`` (T x top), most likely first.
 
@@ -363,7 +367,7 @@ def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, keep=None
 
 @_foreign
 def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, scale=1.0, mask=None, out=None,
-                      stream=None, keep=None):
+                      stream=None, *, keep=None):
     """The gradient with respect to the logits of ``logprobs``' logprob and entropy, from
     theirs (``g_entropy`` None: no gradient reaches the entropy).  ``out`` may be the
     logits themselves."""

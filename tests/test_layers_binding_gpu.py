@@ -36,3 +36,52 @@ def test_first_argument_by_name(sg, side):
             [sg.matmul_i8(q, s, q, s)], lp, [sg.logprobs_backward(x, target, lp[2], lp[1], w[:6])]]
     for a, b in zip(got, want):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("by_name", [True, False])
+@pytest.mark.parametrize("handle", [True, False])
+def test_a_call_on_another_stream_waits_for_the_memory_it_is_given(sg, by_name, handle):
+    """What a call allocates may have been freed by work that torch's stream still has queued:
+    here a wait and then a fill, which must not land after the call's results."""
+    import torch
+    x, w = torch.randn(500, 640, device="cuda"), torch.ones(640, device="cuda")
+    q, s = sg.quantize_i8(torch.randn(300, 640, device="cuda"))
+    target = torch.arange(500, device="cuda")
+    norm, lp = sg.block_norm(x, x, w), sg.logprobs(x, target)
+    g = torch.ones(500, device="cuda")
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    named = dict(stream=stream) if by_name else {}
+    calls = [
+        lambda on: sg.block_norm(x, x, w, None, None, 1.0, 1e-6, False, None, *on[0], **on[1]),
+        lambda on: sg.block_norm(x, x, w, None, None, 1.0, 1e-6, True, None, *on[0], **on[1]),
+        lambda on: sg.block_norm_backward(x, x, w, norm[2], x, None, None, None, 1.0, *on[0], **on[1]),
+        lambda on: sg.quantize_i8(x, *on[0], **on[1]),
+        lambda on: [sg.linear_i8(x, q, s, None, None, None, None, *on[0], **on[1])],
+        lambda on: [sg.matmul_i8(q, s, q, s, None, None, None, None, *on[0], **on[1])],
+        lambda on: sg.logprobs(x, target, 1.0, None, 4, *on[0], **on[1]),
+        lambda on: [sg.logprobs_backward(x, target, lp[2], lp[1], g, g, 1.0, None, None, *on[0], **on[1])],
+    ]
+    for call in calls:
+        want = call(((), {}))
+        shapes = [(t.shape, t.dtype) for t in want if t is not None]
+        torch.cuda.synchronize()
+        held = [torch.empty(sh, dtype=dt, device="cuda") for sh, dt in shapes for _ in range(2)]
+        torch.cuda._sleep(20_000_000)                 # about 10 ms
+        for t in held:
+            t.fill_(77)
+        del held, t
+        got = call(((), named) if by_name else ((stream,), {}))
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert same(got, want)
+
+
+def test_a_stream_given_twice_or_out_of_place(sg):
+    import torch
+    x = torch.randn(4, 64, device="cuda")
+    side = torch.cuda.Stream()
+    with pytest.raises(TypeError):
+        sg.quantize_i8(x, side, stream=side)
+    with pytest.raises(TypeError):
+        sg.quantize_i8(x, side, [])
