@@ -292,6 +292,13 @@ def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, s
         po, ldo = _matrix(out, "out", out_dtype, dev, (M, N))
     pws = size = 0
     if workspace is not None:
+        on = workspace.get_device()
+        if on < 0:
+            raise TypeError("workspace must be a CUDA tensor")
+        if on != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on cuda:{dev}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be dense")
         pws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
         size = size_of(M, N, K, pw, ldw)
@@ -321,7 +328,9 @@ def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, works
 @_foreign
 def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
     """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
-    quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise."""
+    quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise.
+    ``workspace``, here and in ``matmul_i8``: a dense tensor of any type with the bytes that
+    ``sgemm_linear_i8_workspace_size`` or ``sgemm_i8_workspace_size`` gives; allocated if None."""
     dt, _, _, px, ldx = _first(x, "x")
     return _linear(_lib.sgemm_linear_i8, "sgemm_linear_i8", x, (_codes[dt], px, ldx), w, w_scale, bias, out_dtype or dt,
                    out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)

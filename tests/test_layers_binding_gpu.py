@@ -85,3 +85,25 @@ def test_a_stream_given_twice_or_out_of_place(sg):
         sg.quantize_i8(x, side, stream=side)
     with pytest.raises(TypeError):
         sg.quantize_i8(x, side, [])
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_workspaces_that_are_refused(sg, M):
+    import torch
+    x = torch.randn(M, 64, device="cuda")
+    q, s = sg.quantize_i8(x)
+    w, ws = sg.quantize_i8(torch.randn(48, 64, device="cuda"))
+    need = max(int(sg.load().sgemm_linear_i8_workspace_size(M, 48, 64, w.data_ptr(), 64)), 256)
+    whole = torch.full((2 * need,), 9, dtype=torch.uint8, device="cuda")
+    bad = [(torch.empty(need, dtype=torch.uint8), TypeError), (torch.empty(need, dtype=torch.uint8).share_memory_(), TypeError),
+           (whole[::2], ValueError), (whole[:1].expand(need), ValueError),
+           (torch.empty(need, dtype=torch.uint8, device="meta"), TypeError)]
+    for workspace, error in bad:
+        with pytest.raises(error, match="workspace"):
+            sg.linear_i8(x, w, ws, workspace=workspace)
+        with pytest.raises(error, match="workspace"):
+            sg.matmul_i8(q, s, w, ws, workspace=workspace)
+    assert bool((whole == 9).all())
+    # any type and shape that is dense
+    ok = torch.empty(2, (need + 7) // 8, device="cuda")
+    assert torch.equal(sg.linear_i8(x, w, ws, workspace=ok), sg.linear_i8(x, w, ws))
