@@ -71,8 +71,13 @@ def _first(t, name, dtypes=None):
     return (dtype, index, shape, *_rows(t, name, *shape))
 
 
+_MOST = 2 ** 31 - 1  # what the library's sizes and leading dimensions can be
+
+
 def _rows(t, name, rows, n):
     """(pointer, leading dimension) of a matrix with unit column stride."""
+    if rows > _MOST or n > _MOST:
+        raise ValueError(f"{name} is ({rows}, {n}): rows and columns must be below 2^31")
     if t.is_contiguous():
         return t.data_ptr(), n or 1
     s0, s1 = t.stride()
@@ -81,6 +86,8 @@ def _rows(t, name, rows, n):
     if rows > 1:
         if s0 < n:
             raise ValueError(f"{name} has rows that overlap")
+        if s0 > _MOST:
+            raise ValueError(f"{name} has rows {s0} elements apart: they must be below 2^31")
         return t.data_ptr(), s0 or 1
     return t.data_ptr(), n or 1
 
@@ -362,6 +369,8 @@ def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, *, keep=N
     got = (empty((T,), dtype=f32, device=where), empty((T,), dtype=f32, device=where),
            empty((T,), dtype=f32, device=where))
     pv = pi = 0
+    if not -_MOST <= top <= _MOST:
+        raise ValueError(f"top is {top}: it must be 0 .. 32")
     if top > 0:
         got += (empty((T, top), dtype=f32, device=where), empty((T, top), dtype=_torch.int32, device=where))
         pv, pi = got[3].data_ptr(), got[4].data_ptr()

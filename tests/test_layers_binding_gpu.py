@@ -107,3 +107,21 @@ def test_workspaces_that_are_refused(sg, M):
     # any type and shape that is dense
     ok = torch.empty(2, (need + 7) // 8, device="cuda")
     assert torch.equal(sg.linear_i8(x, w, ws, workspace=ok), sg.linear_i8(x, w, ws))
+
+
+def test_rows_too_far_apart_are_refused(sg):
+    """Rows 2^32 + 64 elements apart, whose lower 32 bits are a dense row's."""
+    import torch
+    buf = torch.zeros(2 ** 32 + 128, dtype=torch.int8, device="cuda")
+    w = buf.as_strided((2, 64), (2 ** 32 + 64, 1))
+    w[1] = 5
+    one = torch.ones(2, device="cuda")
+    a = torch.ones(3, 64, dtype=torch.int8, device="cuda")
+    with pytest.raises(ValueError, match="2\\^31"):
+        sg.matmul_i8(a, torch.ones(3, device="cuda"), w, one)
+    with pytest.raises(ValueError, match="2\\^31"):
+        sg.quantize_i8(torch.empty(2 ** 32 + 1, 1, dtype=torch.bfloat16, device="cuda"))
+    z = torch.zeros(1, 8, device="cuda")
+    for top in (2 ** 32 + 1, -2 ** 32 + 1):
+        with pytest.raises(ValueError, match="top"):
+            sg.logprobs(z, torch.zeros(1, dtype=torch.int64, device="cuda"), top=top)

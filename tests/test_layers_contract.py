@@ -49,3 +49,19 @@ def test_first_argument_by_name():
             call()
     with pytest.raises(TypeError, match="missing"):
         sg.quantize_i8()
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    """ctypes drops the upper half of such a number without a word; tensors without storage show it."""
+    torch = pytest.importorskip("torch")
+    from dense_fp32_matrix_04_gb300 import layers
+
+    def rows(shape, stride):
+        return layers._rows(torch.empty_strided(shape, stride, device="meta"), "x", *shape)
+
+    assert rows((2, 8), (2 ** 31 - 1, 1))[1] == 2 ** 31 - 1
+    assert rows((1, 8), (2 ** 40, 1))[1] == 8            # one row: its stride does not matter
+    for shape, stride in (((2, 8), (2 ** 31, 1)), ((2, 8), (2 ** 32 + 8, 1)), ((2 ** 31, 1), (1, 1)), ((2 ** 32 + 3, 1), (1, 1)),
+                          ((2 ** 32, 4), (8, 1)), ((1, 2 ** 31), (2 ** 31, 1)), ((1, 2 ** 32 + 5), (2 ** 32 + 5, 1))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            rows(shape, stride)
