@@ -188,6 +188,8 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     if gate is not None:
         pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
+        if G == 0 and T:
+            raise ValueError(f"gate has no rows for the {T} of x")
     r = empty(shape, dtype=dt, device=where) if out is None else out
     pr, ldr = _matrix(r, "out", dt, dev, shape) if out is not None else (r.data_ptr(), D or 1)
     rstd = empty((2, T), dtype=f32, device=where)
@@ -240,6 +242,8 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
     if gate is not None:
         pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
+        if G == 0 and T:
+            raise ValueError(f"gate has no rows for the {T} of x")
     dx, dy = empty(shape, dtype=dt, device=where), empty(shape, dtype=dt, device=where)
     dw_pre = empty((D,), dtype=wt, device=where)
     dw_post = empty((D,), dtype=wt, device=where) if w_post is not None else None

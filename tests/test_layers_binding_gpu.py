@@ -125,3 +125,19 @@ def test_rows_too_far_apart_are_refused(sg):
     for top in (2 ** 32 + 1, -2 ** 32 + 1):
         with pytest.raises(ValueError, match="top"):
             sg.logprobs(z, torch.zeros(1, dtype=torch.int64, device="cuda"), top=top)
+
+
+def test_a_gate_without_rows(sg):
+    """The library knows no gate by its null pointer, which a tensor without rows has."""
+    import torch
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    none = torch.empty(0, 64, device="cuda")
+    rstd = sg.block_norm(x, x, w)[2]
+    with pytest.raises(ValueError, match="gate"):
+        sg.block_norm(x, x, w, gate=none)
+    with pytest.raises(ValueError, match="gate"):
+        sg.block_norm_backward(x, x, w, rstd, x, gate=none)
+    # no rows of x, one gate a token: none is what there is
+    r, n, rstd = sg.block_norm(none, none, w, gate=none)
+    assert r.shape == (0, 64)
+    assert sg.block_norm_backward(none, none, w, rstd, none, gate=none)[4].shape == (0, 64)
