@@ -23,6 +23,7 @@ using sgemm_host::launch;
 using sgemm_host::Range;
 
 constexpr int kMaxK = 131071;  // 2^14 K < 2^31: a sum of 8-bit products fits 32 bits
+constexpr int kMaxRows = 1 << 30;  // of tokens and of weights: the kernels' row numbers and a round of them fit 32 bits
 
 // Codes as 8-bit integers (Code int8_t) or as FP16 values on padded rows (__half).
 template <int DT, int VW, class Code>
@@ -211,8 +212,8 @@ struct Workspace {
     int64_t codes, rows, partials, bytes;
     Workspace(int M, int N, int K, bool lay_out_rows, const StreamPlan &plan) {
         codes = up256(4 * (int64_t)M);
-        rows = codes + up256(2 * M * ld8(K));
-        partials = rows + (lay_out_rows ? up256(N * ld16(K)) : 0);
+        rows = codes + up256(2 * (int64_t)M * ld8(K));
+        partials = rows + (lay_out_rows ? up256((int64_t)N * ld16(K)) : 0);
         bytes = partials + plan.partial_bytes(M, N);
     }
 };
@@ -225,7 +226,7 @@ int device_sms() {
 
 bool output_ok(int M, int N, int K, const signed char *B, int ldb, const float *b_scale, const float *bias,
                const void *C, int ldc, int ctype) {
-    if (M < 0 || N < 0 || K < 0 || K > kMaxK || !dtype_ok(ctype)) return false;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxK || !dtype_ok(ctype)) return false;
     if (ldb < std::max(K, 1) || ldc < std::max(N, 1)) return false;
     if (M == 0 || N == 0) return true;
     if ((K > 0 && !B) || !b_scale || !C || !aligned(b_scale, 4) || !aligned(bias, 4)) return false;
@@ -275,7 +276,7 @@ static size_t least_workspace(int M, int N, int K, const signed char *B, int ldb
 // One workspace serves both entry points: with 8-bit tokens the place of their
 // scales stays unused.
 size_t sgemm_i8_workspace_size(int M, int N, int K, const signed char *B, int ldb) {
-    if (M <= 0 || N <= 0 || K <= 0 || takes_rows(M, K)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > kMaxRows || K > kMaxK || takes_rows(M, K)) return 0;
     const int sms = device_sms();
     if (!sms) return 0;
     return (size_t)Workspace(M, N, K, !rows16(reinterpret_cast<const int8_t *>(B), ldb), StreamPlan(M, N, K, sms)).bytes;

@@ -114,7 +114,7 @@ int sgemm_quantize_i8(int M, int K, int dtype, const void *x, int ldx,
  * partial sums stay below 2^24 in magnitude (always for K <= 1024) and an FP32
  * sum otherwise; the scales and the bias are applied in FP32 and the result is
  * rounded once to ctype.
- *   bias: N FP32 values or NULL.  K <= 131071.
+ *   bias: N FP32 values or NULL.  M, N <= 2^30, K <= 131071.
  *   workspace: sgemm_i8_workspace_size(M, N, K, B, ldb) bytes, 16-byte aligned,
  *       with contents that do not matter; calls that share one must not
  *       overlap on the GPU.  M <= 4 and K == 0 need none; rows of B that are not

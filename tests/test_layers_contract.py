@@ -65,3 +65,16 @@ def test_binding_refuses_sizes_beyond_32_bits():
                           ((2 ** 32, 4), (8, 1)), ((1, 2 ** 31), (2 ** 31, 1)), ((1, 2 ** 32 + 5), (2 ** 32 + 5, 1))):
         with pytest.raises(ValueError, match="2\\^31"):
             rows(shape, stride)
+
+
+@pytest.mark.parametrize("change", [dict(M=2 ** 30 + 1), dict(N=2 ** 30 + 1, ldc=2 ** 30 + 1), dict(M=2 ** 31 - 1),
+                                    dict(N=2 ** 31 - 1, ldc=2 ** 31 - 1), dict(K=131072, lda=131072, ldb=131072)])
+def test_i8_sizes_are_bounded(lib, change):
+    a = dict(M=40, N=8, K=64, A=P[0], lda=64, a_scale=P[1], B=P[2], ldb=64, b_scale=P[3], bias=P[4], C=P[5], ldc=8,
+             ctype=F32, ws=P[6], ws_bytes=1 << 30, stream=None)
+    a.update(change)
+    assert lib.sgemm_i8(*a.values()) == BAD
+    assert lib.sgemm_i8_workspace_size(a["M"], a["N"], a["K"], a["B"], a["ldb"]) == 0
+    del a["a_scale"]
+    b = list(a.values())
+    assert lib.sgemm_linear_i8(*b[:3], BF16, *b[3:]) == BAD
