@@ -71,7 +71,9 @@ def _first(t, name, dtypes=None):
     return (dtype, index, shape, *_rows(t, name, *shape))
 
 
-_MOST = 2 ** 31 - 1  # what the library's sizes and leading dimensions can be
+# What the library's sizes and leading dimensions can be: ctypes would drop the upper half of a
+# larger number without a word.
+_MOST = 2 ** 31 - 1
 
 
 def _rows(t, name, rows, n):
@@ -130,32 +132,35 @@ def _foreign(fn):
     """Runs a call whose tensors are on another device than the current one, or whose
     stream is not torch's: with the device made current, and with what the call
     allocates (on torch's stream) ordered before and marked as used on its stream.  The
-    stream is seen by name or by place."""
+    first tensor and the stream are seen by place or by name."""
     names = list(inspect.signature(fn).parameters)
-    name, at = names[0], names.index("stream")
+    name, more_than = names[0], names.index("stream") - 1
 
     @functools.wraps(fn)
-    def call(*args, stream=None, **more):
+    def call(first=None, /, *args, stream=None, **more):
         if _torch is None:
             _start()
-        if len(args) == at + 1 and stream is None:
-            stream, args = args[at], args[:at]
-        first = args[0] if args else more.get(name)
+        if first is None:
+            if name not in more:
+                return fn(*args, **more)  # refuses it
+            first = more.pop(name)
+        if len(args) > more_than and stream is None:
+            stream, args = args[more_than], args[:more_than] + args[more_than + 1:]
         index = first.get_device() if isinstance(first, _torch.Tensor) else -1
         if stream is None and (index < 0 or index == _current_device()):
-            return fn(*args, **more)
+            return fn(first, *args, **more)
         if index < 0:
-            return fn(*args, stream=stream, **more)  # refuses it
+            return fn(first, *args, stream=stream, **more)  # refuses it
         with _torch.cuda.device(index):
             handle = _on(index, stream)
             if handle == _raw_stream(index):
-                return fn(*args, **more)
+                return fn(first, *args, **more)
             other = _torch.cuda.ExternalStream(handle, device=index) if isinstance(stream, int) else stream
             # the inputs are the caller's to order; what is allocated here may have been freed by
             # work that is still queued on torch's stream
             other.wait_stream(_torch.cuda.current_stream(index))
             kept = []
-            got = fn(*args, stream=stream, keep=kept, **more)
+            got = fn(first, *args, stream=stream, keep=kept, **more)
             for t in kept:
                 t.record_stream(other)
             return got
@@ -188,7 +193,7 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     if gate is not None:
         pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
-        if G == 0 and T:
+        if not G and T:
             raise ValueError(f"gate has no rows for the {T} of x")
     r = empty(shape, dtype=dt, device=where) if out is None else out
     pr, ldr = _matrix(r, "out", dt, dev, shape) if out is not None else (r.data_ptr(), D or 1)
@@ -203,7 +208,7 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
                                    pr, ldr, pn, D or 1, pq, D or 1, ps, rstd.data_ptr(), _on(dev, stream))
     if status:
         _check(status, "sgemm_block_norm")
-    if D == 0 and T:
+    if not D and T:
         _no_columns(rstd, w_post is not None, s if quantize else None, dev, stream)
     if keep is not None:
         keep += made
@@ -242,7 +247,7 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
     if gate is not None:
         pg, ldg = _matrix(gate, "gate", dt, dev, None, D)
         G = gate.shape[0]
-        if G == 0 and T:
+        if not G and T:
             raise ValueError(f"gate has no rows for the {T} of x")
     dx, dy = empty(shape, dtype=dt, device=where), empty(shape, dtype=dt, device=where)
     dw_pre = empty((D,), dtype=wt, device=where)
