@@ -7,6 +7,9 @@ library's kernels.  A call runs on ``stream`` (a ``torch.cuda.Stream``, a raw
 handle, or None: torch's current stream).  Tensors that are used on a stream
 other than the one they were made on are the caller's to order, as with any
 torch operation; what a call allocates itself is marked as used on its stream.
+
+No call is recorded by torch's autograd: what comes back does not require a
+gradient, whatever the inputs do, and the gradients are calls of their own.
 """
 
 from __future__ import annotations
@@ -180,7 +183,8 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     Returns ``(r, n, rstd)``, or with ``quantize`` ``(r, q, q_scale, rstd)``: n as
     8-bit integers with a scale per row.  ``rstd`` (2 x T) is for the backward
     pass.  ``out`` receives r; it may be x.  Rows of no columns (D = 0) have NaN for
-    the means' roots and 0 for the scale.
+    the means' roots and 0 for the scale.  Autograd does not see the call: its gradient
+    is ``block_norm_backward``.
     """
     dt, dev, shape, px, ldx = _first(x, "x")
     f32, empty, where = _torch.float32, _torch.empty, x.device
@@ -272,7 +276,7 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
 def quantize_i8(x, stream=None, *, keep=None):
     """``(q, scale)``: the rows of x (M x K) as 8-bit integers, scale = max|row| / 127
     and q = rint(row * (127 / max|row|)).  For activations a scale per token, for
-    weights (N x K) one per output channel."""
+    weights (N x K) one per output channel.  Has no gradient, and autograd does not see it."""
     dt, dev, shape, px, ldx = _first(x, "x")
     M, K = shape
     q = _torch.empty(shape, dtype=_torch.int8, device=x.device)
@@ -332,7 +336,8 @@ def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, s
 @_foreign
 def matmul_i8(a, a_scale, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
     """``a_scale[m] * w_scale[n] * sum_k a[m, k] w[n, k] + bias[n]`` for 8-bit integers
-    a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise)."""
+    a (M x K) and w (N x K), in ``out_dtype`` (float32 unless said otherwise).  For inference:
+    autograd does not see it."""
     if _torch is None:
         _start()
     _, dev, shape, pa, lda = _first(a, "a", (_torch.int8,))
@@ -346,7 +351,8 @@ def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None
     """``matmul_i8`` on the rows of x (M x K, float32, bfloat16 or float16), which are
     quantised first as ``quantize_i8`` does it; ``out_dtype`` is x's unless said otherwise.
     ``workspace``, here and in ``matmul_i8``: a dense tensor of any type with the bytes that
-    ``sgemm_linear_i8_workspace_size`` or ``sgemm_i8_workspace_size`` gives; allocated if None."""
+    ``sgemm_linear_i8_workspace_size`` or ``sgemm_i8_workspace_size`` gives; allocated if None.
+    For inference: autograd does not see the call."""
     dt, _, _, px, ldx = _first(x, "x")
     return _linear(_lib.sgemm_linear_i8, "sgemm_linear_i8", x, (_codes[dt], px, ldx), w, w_scale, bias, out_dtype or dt,
                    out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)
@@ -370,7 +376,8 @@ def logprobs(logits, target, scale=1.0, mask=None, top=0, stream=None, *, keep=N
 
     ``target``: T int64 columns; a negative one is not scored (logprob 0).
     ``mask``: int32 words, 1 or T rows of ceil(V / 32), bit j % 32 of word j // 32 set
-    where column j is allowed."""
+    where column j is allowed.  Autograd does not see the call: its gradient is
+    ``logprobs_backward``."""
     dt, dev, (T, V), pz, ldz = _first(logits, "logits")
     py = _vector(target, "target", T, (_torch.int64,), dev)
     pm, ldm, rows = _mask(mask, T, V, dev)
