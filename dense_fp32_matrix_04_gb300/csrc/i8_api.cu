@@ -70,16 +70,22 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 // Up to four tokens go to the kernel that reads whole rows, whatever K.
 bool takes_rows(int M, int K) { return M <= kRowsTokens && K > 0; }
 
-template <int MT, int XT, bool ALIGNED>
-int launch_rows(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
+template <int MT, int XT, bool ALIGNED, int THREADS>
+int launch_rows(const I8Args &p, const void *X, int64_t ldx, int smem, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = i8_rows_kernel<MT, XT, ALIGNED>;
-    const int smem = MT * rows_pitch(p.K);
-    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, kRowsThreads, smem);
+    const auto kernel = i8_rows_kernel<MT, XT, ALIGNED, THREADS>;
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, THREADS, smem);
     if (!fit) return SGEMM_ERR_LAUNCH;
-    constexpr int warps = kRowsThreads / 32;
+    constexpr int warps = THREADS / 32;
     const int blocks = std::min((p.N + warps - 1) / warps, dev.sms * fit);
-    return launch(kernel, dim3(blocks), dim3(kRowsThreads), smem, stream, 1, p, X, ldx);
+    return launch(kernel, dim3(blocks), dim3(THREADS), smem, stream, 1, p, X, ldx);
+}
+
+template <int MT, int XT, bool ALIGNED>
+int rows_by_width(const I8Args &p, const void *X, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    const int smem = MT * rows_pitch(p.K);
+    return smem > kRowsWide ? launch_rows<MT, XT, ALIGNED, kRowsWideThreads>(p, X, ldx, smem, dev, stream)
+                            : launch_rows<MT, XT, ALIGNED, kRowsThreads>(p, X, ldx, smem, dev, stream);
 }
 
 // As many tokens at a time as shared memory holds the codes of: all four up to
@@ -101,8 +107,8 @@ int rows_product(const I8Args &all, const void *X, int64_t ldx, const Device &de
         }
         auto by_alignment = [&](auto mt) {
             constexpr int MT = decltype(mt)::value;
-            return rows16(p.B, p.ldb) ? launch_rows<MT, XT, true>(p, x, ldx, dev, stream)
-                                      : launch_rows<MT, XT, false>(p, x, ldx, dev, stream);
+            return rows16(p.B, p.ldb) ? rows_by_width<MT, XT, true>(p, x, ldx, dev, stream)
+                                      : rows_by_width<MT, XT, false>(p, x, ldx, dev, stream);
         };
         const int st = p.M <= 1   ? by_alignment(std::integral_constant<int, 1>{})
                        : p.M <= 2 ? by_alignment(std::integral_constant<int, 2>{})

@@ -15,9 +15,9 @@
 // tensor cores are faster (i8_stream.cuh; 11.4 us there for five tokens).
 //
 // The sums are exact for every K, so long rows stay here: four tokens' codes fit
-// shared memory up to K = 57344 (4 x 5120 x 28672 about 58 us, 54 for five tokens
-// on the tensor cores); beyond, two or one at a time read B once for each
-// (4 x 4096 x 65536 178 us, 100 for five).
+// shared memory up to K = 57344 (4 x 5120 x 28672 42.4 us, 50.9 for five tokens on
+// the tensor cores; with codes that come quantised 39.4 and 34.9); beyond, two or
+// one at a time read B once for each (4 x 4096 x 65536 130 us, 92 for five).
 #pragma once
 
 #include <cstdint>
@@ -27,24 +27,29 @@
 
 namespace sgemm {
 
-constexpr int kRowsTokens = 4, kRowsThreads = 256;
+constexpr int kRowsTokens = 4;
+constexpr int kRowsThreads = 256, kRowsWideThreads = 768;  // a block's; see kRowsWide
 constexpr int kRowsPieces = 8;  // loads of 16 bytes a lane has in flight
 
 constexpr int kRowsCodes = 224 * 1024;  // shared memory that a block's tokens' codes may take
+// Codes of more than this leave room for too few blocks of 256 threads, and so for
+// too few loads on their way: one block of 768 then (4 x 5120 x 28672 53.9 -> 42.4
+// us, 2 x 5120 x 28672 37.6 -> 32.1, 4 x 4096 x 14336 23.5 and 23.8).
+constexpr int kRowsWide = 52 * 1024;
 
 // Bytes of a token's codes in shared memory: whole rounds of loads.
 __host__ __device__ constexpr int rows_pitch(int K) { return (K + 511) / 512 * 512; }
 
 // XT: the tokens are codes (-1) or values of that element type.
-template <int MT, int XT, bool ALIGNED>
-__global__ void __launch_bounds__(kRowsThreads, MT < 4 && ALIGNED ? 4 : 3)
+template <int MT, int XT, bool ALIGNED, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > kRowsThreads ? 1 : MT < 4 && ALIGNED ? 4 : 3)
     i8_rows_kernel(const I8Args p, const void *__restrict__ X, int64_t ldx) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float slots[kRowsThreads / 32], scales[MT];
+    __shared__ float slots[THREADS / 32], scales[MT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
     const int pitch = rows_pitch(K);
-    const int warps = gridDim.x * (kRowsThreads / 32);
-    int row = blockIdx.x * (kRowsThreads / 32) + warp;
+    const int warps = gridDim.x * (THREADS / 32);
+    int row = blockIdx.x * (THREADS / 32) + warp;
 
     auto load = [&](uint4 (&w)[kRowsPieces], const int8_t *from, int k0) {
 #pragma unroll
@@ -58,7 +63,7 @@ __global__ void __launch_bounds__(kRowsThreads, MT < 4 && ALIGNED ? 4 : 3)
         // 16 codes at a time; those past the row's end are 0
         for (int m = 0; m < MT; ++m)
 #pragma unroll 4
-            for (int k = 16 * tid; k < pitch; k += 16 * kRowsThreads) {
+            for (int k = 16 * tid; k < pitch; k += 16 * THREADS) {
                 const uint4 c = load_codes<false>(p.A + m * p.lda, k, m < p.M ? K : 0);
                 uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -72,7 +77,7 @@ __global__ void __launch_bounds__(kRowsThreads, MT < 4 && ALIGNED ? 4 : 3)
     } else {
         // the block's warps are shared out to the tokens, which are quantised side by side
         using E = Elem<XT < 0 ? 0 : XT>;
-        constexpr int SHARE = kRowsThreads / 32 / MT, VEC = E::VEC;
+        constexpr int SHARE = THREADS / 32 / MT, VEC = E::VEC;
         const int m = warp / SHARE, first = (warp % SHARE) * 32 + lane, step = SHARE * 32;
         const typename E::type *x = static_cast<const typename E::type *>(X) + min(m, p.M - 1) * ldx;
         const int pieces = (reinterpret_cast<uintptr_t>(x) & 15) == 0 ? K / VEC : 0;
