@@ -17,7 +17,8 @@
 // takes 84 us (4.8 TB/s), FP32 4096 x 4096, half the arithmetic for the same
 // bytes, 79; 9 us of it are the launch, the runners' first row and the joining
 // of their sums.  Rows of single elements (not 16-byte aligned, or of odd width)
-// run at two thirds of that: 2047 x 1111 FP32 takes 24 us.
+// run at half of that and less: 2047 x 1111 FP32 takes 24.6 us, the forward pass of
+// 8192 x 1111 BF16 37.6 (1112 columns 21.4), of 8192 x 5121 133 (5120 58.6).
 #pragma once
 
 #include <cstdint>

@@ -12,15 +12,15 @@
 // B as FP16 in shared memory would be beyond it.
 //
 // Measured, with the kernel that quantises the tokens and, where K is split, the
-// one that adds the splits: 24 x 16384 x 4096 18.2 us (3.7 TB/s of operands; two
+// one that adds the splits: 24 x 16384 x 4096 18.5 us (3.7 TB/s of operands; two
 // launches, one round of 128 tiles on 152 SMs, and the copies, the conversion
 // and the products of a tile's first and last steps one after another);
-// 4096 x 4096 x 4096 103 us; 8192 x 8192 x 8192 705 us, 1559 TFLOP/s, 80 % of what
+// 4096 x 4096 x 4096 103 us; 8192 x 8192 x 8192 713 us, 1541 TFLOP/s, 79 % of what
 // FP16 products reach: 48 us quantise, then the tensor pipe is 72 % busy, held
 // up by the issue of a step's products (680 cycles a step, 512 of them the
 // pipe's; two steps to a round of that loop took 731 us) and by drains that 256
 // columns leave no second accumulator to hide.  3001 x 4999 x 2047 in FP32
-// takes 75.7 us: about 12 for quantising rows of single floats, 4 rounds of
+// takes 76.2 us: about 12 for quantising rows of single floats, 4 rounds of
 // tiles, and 60 MB of results that all SMs store at the same time.
 //
 // One block per SM walks units (tile, k-split): one thread copies by TMA into a

@@ -121,7 +121,7 @@ template <int DT>
 int norm_grad_by_layout(const BlockNormGradArgs &a, bool vec, const Device &dev, cudaStream_t stream) {
     if (a.gate_period == 1)
         return vec ? launch_norm_grad<DT, true, true, 8>(a, dev, stream) : launch_norm_grad<DT, false, true, 8>(a, dev, stream);
-    // 16 elements a thread halve what a row costs beside them (8192 x 4096 BF16: 120 us with 8, 115
+    // 16 elements a thread halve what a row costs beside them (8192 x 4096 BF16: 88 us with 8, 82
     // with 16); FP32, which unpacks nothing, does with 8, and 16 spill
     constexpr int PER = DT == SGEMM_F32 ? 8 : 16;
     return vec ? launch_norm_grad<DT, true, false, PER>(a, dev, stream) : launch_norm_grad<DT, false, false, 8>(a, dev, stream);
@@ -159,14 +159,14 @@ int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t str
     unsigned parts = 1;
     while (parts < 8 && (int64_t)a.T * parts * 2 <= 2 * dev.sms && a.V / (int)(parts * 2) >= 2048) parts *= 2;
     // two warps a row where a row is short, or nothing but its sums is wanted: what a row costs a
-    // warp beside its columns weighs less (64000 x 1000 298 -> 82 us, 4096 x 50001 without
-    // alternatives 91 -> 81 us; with five alternatives 106 -> 112 us)
+    // warp beside its columns weighs less (64000 x 1000 302 -> 81 us, 4096 x 50001 without
+    // alternatives 91 -> 80 us; with five alternatives 104 -> 110 us)
     if (parts == 1 && !a.top) return launch_logprobs<DT, 64, false, MASK>(a, 1, dev, stream);
     if (parts == 1 && a.V < 16384) return launch_logprobs<DT, 64, true, MASK>(a, 1, dev, stream);
     // four warps for longer rows with alternatives, where there are two for each block that the SMs
-    // hold (4096 x 50001 106 -> 91 us; 2000 x 32000 with 20 alternatives 44 -> 48 us), and while
+    // hold (4096 x 50001 104 -> 89 us; 2000 x 32000 with 20 alternatives 44 -> 49 us), and while
     // the columns that may be alternatives are few, which grows with top and with what a thread
-    // sees of a row (4096 x 100001 with 5 alternatives 180 -> 167 us, with 20 211 -> 254 us)
+    // sees of a row (4096 x 100001 with 5 alternatives 173 -> 171 us, with 20 205 -> 256 us)
     if (parts == 1 && a.T >= 2 * 8 * dev.sms && (int64_t)a.top * a.V <= 1 << 20)
         return launch_logprobs<DT, 128, true, MASK>(a, 1, dev, stream);
     return a.top ? launch_logprobs<DT, 256, true, MASK>(a, parts, dev, stream)

@@ -12,18 +12,23 @@
 // ln 2 (M - m c).  Where m c is larger (rows of nothing but mask values, large
 // scales), t_j = (z_j - m) c instead.
 //
-// The alternatives cost the pass nothing: each thread knows the largest logit it
-// has met, and at the row's end at least `top` columns reach the top-th largest
-// of the maxima of 32 groups of threads.  Only the threads that have such a
-// column, a handful, have theirs looked at again, and the few columns that
-// reach it are inserted into a list over a warp's lanes.
+// The alternatives cost the pass no instruction a column: each thread knows the
+// largest logit it has met, and at the row's end at least `top` columns reach the
+// top-th largest of the maxima of 32 groups of threads.  Only the threads that
+// have such a column, a handful, have theirs looked at again, and the few columns
+// that reach it are ranked against each other.  That is a dozen barriers and a
+// second look at a part of the row, which grows with top and V: 4096 x 50001 takes
+// 80 us without alternatives and 89 with five, 4096 x 100001 205 with twenty.
 //
-// Of 16-bit logits the pass is bound by the issue of instructions (about 13 an
+// Of 16-bit logits the pass is bound by the issue of instructions (about 12 an
 // element, one of them the exponential, which alone would take 44 us at 4096 x
-// 50001): 91 us there, 4.5 TB/s, against 60.5 for the bytes.  Three rows of 131072 with 20 alternatives, shared by 24
-// blocks, take 13 us: a latency to read, one to join a cluster, and the sorted
-// list.  The gradient reads and writes once: 4096 x 32000 FP32 149 us, 511 x
-// 128001 BF16 49 us (5.4 TB/s).
+// 50001): 89 us there, 4.6 TB/s, against 60.5 for the bytes.  A masked column is
+// -infinity, whose term 0 times -infinity is NaN, so a chunk with one is added a
+// second time, column by column: 4096 x 50001 takes 181 us with a mask, FP32 4096
+// x 32000 115 against 92.  Three rows of 131072 with 20 alternatives, shared by 24
+// blocks, take 13 us: a latency to read, one to join a cluster, and the row's end.
+// The gradient reads and writes once: 4096 x 32000 FP32 151 us, 511 x 128001 BF16
+// 49 us (5.4 TB/s).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -366,8 +371,8 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         for (int p = row.p0; p < row.p1; p += THREADS * U) {
             cp_async_wait<DEPTH - 1>();
             float v[U * VEC], top = -INFINITY;
-            // what lies outside the row, or is masked, is -infinity; neither test costs a whole,
-            // unmasked chunk anything
+            // what lies outside the row, or is masked, is -infinity; neither test costs a whole chunk
+            // of a call without a mask anything
             const bool whole = p + THREADS * U <= row.p1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
