@@ -590,7 +590,18 @@ struct LogprobGradArgs {
 struct LogprobGradRow {
     float scale, lse, A, B, hit;
     int target;  // -1: none
-    bool usual;  // lse is a number that the packed path below is exact enough for
+    bool usual;  // what the packed path below takes
+    // the lowest value that the packed path sees of 16-bit logits; -infinity counts as it
+    template <int DT>
+    static constexpr float kLowest = DT == SGEMM_F16 ? -65504.f : -1e30f;
+    template <int DT>
+    __device__ static LogprobGradRow load(const LogprobGradArgs &a, int64_t t) {
+        LogprobGradRow r(a, t);
+        // all from there down has p = 0, and B log p is a number
+        const float logp = fmaf(kLowest<DT>, r.scale, -r.lse);
+        r.usual = logp < -128.f && fabsf(r.B * logp) < 1e37f;
+        return r;
+    }
     __device__ LogprobGradRow(const LogprobGradArgs &a, int64_t t) {
         scale = a.scale;
         lse = a.lse[t];
@@ -602,7 +613,6 @@ struct LogprobGradRow {
         A = -a.scale * (a.g_entropy ? fmaf(gh, a.entropy[t], g) : g);
         B = -a.scale * gh;
         hit = a.scale * g;
-        usual = fabsf(lse) < 256.f;
     }
     __device__ float one(float z) const {
         // p below 2^-126 counts: its product with B log p may be above.  p = 0 leaves nothing of it
@@ -627,25 +637,36 @@ struct LogprobGradRow {
             for (int e = 0; e < N; ++e)
                 if (at == e) v[e] += hit;
     }
-    // the same for 8 columns of 16 bits, in packed pairs and in powers of 2.  Its terms scale z
-    // log2(e) and lse log2(e) are each rounded before they cancel, so p is off by 2^-24 (|scale z| +
-    // |lse|) relative: at the limit of 256 2^-15, a sixteenth of FP16's half unit.  Rows beyond it
-    // take the path above, which rounds their difference once.
+    // the same for 8 columns of 16 bits, in packed pairs.  scale z - lse is rounded once, after they
+    // cancel: the entropy's gradient needs log p itself where p is near 1.  The exponential is
+    // taken 2^24 times too large, so that p counts down to 2^-150.
     template <int DT>
     __device__ uint4 apply16(uint4 raw, uint32_t bits, int col) const {
         float v[8];
-        unpack16<DT>(raw, v);
         if (!usual || (unsigned)(target - col) < 8u) {
+            unpack16<DT>(raw, v);
             apply<8>(v, bits, col);
             return pack16<DT>(v);
         }
-        const F2 c(scale * kLog2e), off(-lse * kLog2e), a(A), b(B * kLn2);
+        // no -infinity, whose logarithm times a p of 0 would not be 0
+        uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // p is 0 below, and a logarithm of -infinity times it would not be
-            const float2 t = fma(F2(v[2 * i], v[2 * i + 1]), c, off).both();
-            const float x = fmaxf(t.x, -1000.f), y = fmaxf(t.y, -1000.f);
-            const float2 d = (F2(exp2_approx(x), exp2_approx(y)) * fma(b, F2(x, y), a)).both();
+            if constexpr (DT == SGEMM_BF16) {
+                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&w[i]), __float2bfloat162_rn(kLowest<DT>));
+                w[i] = *reinterpret_cast<const uint32_t *>(&m);
+            } else {
+                const __half2 m = __hmax2(*reinterpret_cast<__half2 *>(&w[i]), __float2half2_rn(kLowest<DT>));
+                w[i] = *reinterpret_cast<const uint32_t *>(&m);
+            }
+        }
+        unpack16<DT>(make_uint4(w[0], w[1], w[2], w[3]), v);
+        const F2 c(scale), off(-lse), a(A * 0x1p-24f), b(B * 0x1p-24f), log2e(kLog2e), up(24.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 logp = fma(F2(v[2 * i], v[2 * i + 1]), c, off);
+            const float2 t = fma(logp, log2e, up).both();
+            const float2 d = (F2(exp2_approx(t.x), exp2_approx(t.y)) * fma(b, logp, a)).both();
             v[2 * i] = d.x;
             v[2 * i + 1] = d.y;
         }
@@ -671,7 +692,7 @@ __global__ void __launch_bounds__(THREADS) logprobs_grad_kernel(const LogprobGra
         const type *z = static_cast<const type *>(a.z) + t * a.ldz;
         type *dz = static_cast<type *>(a.dz) + t * a.lddz;
         const int32_t *mask = MASK ? a.mask + t * a.ldm : nullptr;
-        const LogprobGradRow row(a, t);
+        const LogprobGradRow row = LogprobGradRow::load<DT>(a, t);
         // 16-byte pieces need both rows at the same distance from a 16-byte boundary
         const int off = VW > 1 ? (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(type)) : 0;
         const int head = min(off ? VW - off : 0, a.V);
