@@ -366,6 +366,8 @@ def _mask(mask, T, V, index):
     rows = mask.shape[0]
     if rows not in (1, T):
         raise ValueError(f"mask has {rows} rows, not 1 or {T}")
+    if not V:
+        return 0, 0, 0  # no words, and no pointer to them
     return pm, ldm, rows
 
 

@@ -141,3 +141,17 @@ def test_a_gate_without_rows(sg):
     r, n, rstd = sg.block_norm(none, none, w, gate=none)
     assert r.shape == (0, 64)
     assert sg.block_norm_backward(none, none, w, rstd, none, gate=none)[4].shape == (0, 64)
+
+
+@pytest.mark.parametrize("T", [0, 3])
+@pytest.mark.parametrize("mask_rows", [None, 1, 3])
+def test_a_vocabulary_of_nothing(sg, T, mask_rows):
+    import torch
+    z = torch.empty(T, 0, device="cuda")
+    target = torch.tensor([-1, 0, 7], device="cuda")[:T]
+    mask = None if mask_rows is None else torch.empty(min(mask_rows, max(T, 1)), 0, dtype=torch.int32, device="cuda")
+    logprob, entropy, lse, top_logprob, top_id = sg.logprobs(z, target, mask=mask, top=2)
+    assert bool((entropy == 0).all()) and bool((lse == float("-inf")).all())
+    assert bool((top_id == -1).all()) and bool((top_logprob == float("-inf")).all())
+    assert bool((logprob[:1] == 0).all()) and bool(torch.isnan(logprob[1:]).all())     # no column is below V
+    assert sg.logprobs_backward(z, target, lse, entropy, entropy, entropy, mask=mask).shape == (T, 0)
