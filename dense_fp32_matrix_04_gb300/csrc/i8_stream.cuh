@@ -12,7 +12,7 @@
 // B as FP16 in shared memory would be beyond it.
 //
 // Measured, with the kernel that quantises the tokens and, where K is split, the
-// one that adds the splits: 24 x 16384 x 4096 18.5 us (3.7 TB/s of operands; two
+// one that adds the splits: 24 x 16384 x 4096 18.5 - 19.4 us (3.6 TB/s of operands; two
 // launches, one round of 128 tiles on 152 SMs, and the copies, the conversion
 // and the products of a tile's first and last steps one after another);
 // 4096 x 4096 x 4096 103 us; 8192 x 8192 x 8192 713 us, 1541 TFLOP/s, 79 % of what

@@ -28,7 +28,7 @@
 // x 32000 115 against 92.  Three rows of 131072 with 20 alternatives, shared by 24
 // blocks, take 13 us: a latency to read, one to join a cluster, and the row's end.
 // The gradient reads and writes once: 4096 x 32000 FP32 151 us, 511 x 128001 BF16
-// 49 us (5.4 TB/s).
+// 50 us (5.2 TB/s).
 #pragma once
 
 #include <cuda_runtime.h>
