@@ -1,0 +1,267 @@
+// The C interface of the products with 4-bit weights: argument checks, kernel
+// choice and launch.  The contract is in include/sgemm_layers.h.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fp4_mma.cuh"
+#include "fp4_quantize.cuh"
+#include "host.h"
+
+namespace {
+
+using namespace sgemm;
+using sgemm_host::aligned;
+using sgemm_host::by_dtype;
+using sgemm_host::Device;
+using sgemm_host::dtype_ok;
+using sgemm_host::dtype_size;
+using sgemm_host::launch;
+using sgemm_host::Range;
+
+constexpr int kMaxSize = 1 << 30;  // of rows and columns: row numbers and a round of them fit 32 bits
+
+bool block_ok(int block) { return block == 16 || block == 32; }
+int64_t code_bytes(int K) { return ((int64_t)K + 1) / 2; }
+int64_t code_pitch(int K) { return (code_bytes(K) + 15) / 16 * 16; }
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t tile_bytes(int rows, int K, int block) {
+    return rows > 0 && K > 0 ? ((int64_t)rows + 127) / 128 * fp4_tiles(K, block) * kFp4TileBytes : 0;
+}
+
+// Calls f(std::integral_constant<int, block>).
+template <class F>
+int by_block(int block, F &&f) {
+    return block == 16 ? f(std::integral_constant<int, 16>{}) : f(std::integral_constant<int, 32>{});
+}
+
+// ---------------------------------------------------------------- quantising
+
+template <int DT, int VW, int BLOCK>
+int launch_quantize(const Fp4Rows &a, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    using type = typename Elem<DT>::type;
+    const type *from = static_cast<const type *>(x);
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    if (a.K > 16384) {
+        const auto kernel = quantize_fp4_wide_kernel<DT, VW, BLOCK>;
+        const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, 1024, 0);
+        if (!fit) return SGEMM_ERR_LAUNCH;
+        return launch(kernel, dim3((unsigned)std::min(a.rows, dev.sms * fit)), dim3(1024), 0, stream, 1, a, from, ldx);
+    }
+    const auto kernel = quantize_fp4_kernel<DT, VW, BLOCK>;
+    const int threads = (a.K + 511) / 512 * 32;  // 16 columns a thread
+    const dim3 block(threads, threads == 32 ? 4 : 1);
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, (int)(block.x * block.y), 0);
+    if (!fit) return SGEMM_ERR_LAUNCH;
+    const int64_t groups = ((int64_t)a.rows + block.y - 1) / block.y;
+    return launch(kernel, dim3((unsigned)std::min<int64_t>(groups, (int64_t)dev.sms * fit)), block, 0, stream, 1, a, from, ldx);
+}
+
+int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value, VEC = Elem<DT>::VEC;
+        const bool vec = a.K % VEC == 0 && aligned(x, 16) && ldx % VEC == 0;
+        return by_block(block, [&](auto b) {
+            constexpr int BLOCK = decltype(b)::value;
+            return vec ? launch_quantize<DT, VEC, BLOCK>(a, x, ldx, dev, stream)
+                       : launch_quantize<DT, 1, BLOCK>(a, x, ldx, dev, stream);
+        });
+    });
+}
+
+// ---------------------------------------------------------------- the product
+
+// Tokens a tile, and the blocks that share one: the smallest estimate, in cycles, of
+// rounds over the SMs times the length of one.
+struct Fp4Plan {
+    int tok = 256, splits = 1;
+    Fp4Plan(int M, int N, int K, int sms) {
+        static constexpr struct {
+            int tok;
+            double step;
+        } kSteps[] = {{16, 420}, {32, 430}, {64, 450}, {128, 500}, {192, 560}, {256, 700}};
+        double best = 1e300;
+        const int steps = (K + 255) / 256;
+        for (const auto &c : kSteps) {
+            if (c.tok < 64 && M > c.tok) continue;  // see Fp4Tile
+            const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + 127) / 128);
+            for (int s = 1; s <= 8 && s <= steps; s *= 2) {
+                if (s > 1 && tiles * s > 2 * sms) break;
+                const int64_t rounds = (tiles * s + sms - 1) / sms;
+                const double drain = c.tok <= 192 ? 600 : 14. * c.tok;
+                double t = (double)rounds * (((steps + s - 1) / s) * c.step + drain) + 3000 + 14. * c.tok;
+                if (s > 1) t += 2000 + 20. * c.tok;
+                if (t < best) best = t, tok = c.tok, splits = s;
+            }
+            if (M <= c.tok) break;
+        }
+    }
+};
+
+struct Fp4Operands {
+    const uint8_t *A, *B;
+    int64_t lda, ldb;
+};
+
+template <int TOK, int BLOCK>
+int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, const Device &dev, cudaStream_t stream) {
+    using T = Fp4Tile<TOK, BLOCK>;
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = fp4_mma_kernel<TOK, BLOCK>;
+    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, T::THREADS, T::SMEM_BYTES)) return SGEMM_ERR_LAUNCH;
+    CUtensorMap tw, tx;
+    if (!sgemm_host::encode_i8(&tw, o.B, p.N, code_bytes(p.K), o.ldb, T::ROWS, T::BYTES) ||
+        !sgemm_host::encode_i8(&tx, o.A, p.M, code_bytes(p.K), o.lda, TOK, T::BYTES))
+        return SGEMM_ERR_LAUNCH;
+    const int64_t units = (int64_t)((p.M + TOK - 1) / TOK) * ((p.N + T::ROWS - 1) / T::ROWS) * splits;
+    return launch<true>(kernel, dim3((unsigned)(splits > 1 ? units : std::min<int64_t>(units, dev.sms))), dim3(T::THREADS),
+                        T::SMEM_BYTES, stream, (unsigned)splits, tw, tx, p, splits, dev.err_word, sgemm_host::wait_limit_ns(),
+                        sgemm_host::test_flags());
+}
+
+int product(const Fp4Args &p, const Fp4Operands &o, int block, const Device &dev, cudaStream_t stream) {
+    const Fp4Plan plan(p.M, p.N, p.K, dev.sms);
+    return by_block(block, [&](auto b) {
+        constexpr int BLOCK = decltype(b)::value;
+        switch (plan.tok) {
+            case 16: return launch_mma<16, BLOCK>(p, o, plan.splits, dev, stream);
+            case 32: return launch_mma<32, BLOCK>(p, o, plan.splits, dev, stream);
+            case 64: return launch_mma<64, BLOCK>(p, o, plan.splits, dev, stream);
+            case 128: return launch_mma<128, BLOCK>(p, o, plan.splits, dev, stream);
+            case 192: return launch_mma<192, BLOCK>(p, o, plan.splits, dev, stream);
+            default: return launch_mma<256, BLOCK>(p, o, plan.splits, dev, stream);
+        }
+    });
+}
+
+int empty_product(const Fp4Args &p, const Device &dev, cudaStream_t stream) {
+    const int64_t blocks = ((int64_t)p.M * p.N + 255) / 256;
+    return launch(fp4_empty_kernel, dim3((unsigned)std::min<int64_t>(blocks, dev.sms * 8)), dim3(256), 0, stream, 1, p);
+}
+
+// Rows of codes, which start on 16 bytes, with their scales.
+bool codes_ok(const unsigned char *q, int ld, const unsigned char *tiles, const float *scale, int K) {
+    if (K > 0 && (!q || !tiles || !aligned(q, 16) || ld % 16 != 0 || !aligned(tiles, 16))) return false;
+    return aligned(scale, 4);
+}
+
+bool shapes_ok(int M, int N, int K, int block, int ldb, int ldc, int ctype) {
+    if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return false;
+    return block_ok(block) && dtype_ok(ctype) && ldb >= std::max<int64_t>(code_bytes(K), 1) && ldc >= std::max(N, 1);
+}
+
+bool output_ok(const void *C, int ctype, const float *bias) {
+    return C && aligned(C, (unsigned)dtype_size(ctype)) && aligned(bias, 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sgemm_fp4_scales_size(int rows, int K, int block) {
+    if (rows < 0 || K < 0 || rows > kMaxSize || K > kMaxSize || !block_ok(block)) return 0;
+    return (size_t)tile_bytes(rows, K, block);
+}
+
+int sgemm_quantize_fp4(int M, int K, int dtype, const void *x, int ldx, int block, unsigned char *q, int ldq,
+                       unsigned char *block_scale, float *scale, cudaStream_t stream) {
+    if (M < 0 || K < 0 || M > kMaxSize || K > kMaxSize || !dtype_ok(dtype) || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
+    if (ldx < std::max(K, 1) || ldq < std::max<int64_t>(code_bytes(K), 1)) return SGEMM_ERR_INVALID_ARG;
+    if ((block == 16) != (scale != nullptr) && M > 0) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0) return SGEMM_OK;
+    const int size = dtype_size(dtype);
+    if (!aligned(scale, 4)) return SGEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!x || !aligned(x, (unsigned)size) || !codes_ok(q, ldq, block_scale, nullptr, K))) return SGEMM_ERR_INVALID_ARG;
+    const int64_t n = tile_bytes(M, K, block);
+    const Range in(x, M, K, ldx, size);
+    const Range out[3] = {Range(q, M, code_bytes(K), ldq, 1), Range(block_scale, 1, n, n, 1), Range(scale, 1, M, M, 4)};
+    for (int o = 0; o < 3; ++o) {
+        if (out[o].overlaps(in)) return SGEMM_ERR_ALIAS;
+        for (int i = 0; i < o; ++i)
+            if (out[o].overlaps(out[i])) return SGEMM_ERR_ALIAS;
+    }
+    if (K == 0) {
+        if (scale && cudaMemsetAsync(scale, 0, (size_t)M * sizeof(float), stream) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return SGEMM_ERR_LAUNCH;
+        }
+        return SGEMM_OK;
+    }
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    return quantize({M, (M + 127) / 128 * 128, K, q, ldq, block_scale, scale}, dtype, block, x, ldx, dev, stream);
+}
+
+int sgemm_fp4_lay_out_scales(int rows, int K, int block, const unsigned char *s, int lds, unsigned char *tiles,
+                             cudaStream_t stream) {
+    if (rows < 0 || K < 0 || rows > kMaxSize || K > kMaxSize || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
+    if (rows == 0 || K == 0) return SGEMM_OK;
+    const int blocks = fp4_blocks(K, block);
+    if (!s || lds < blocks || !tiles || !aligned(tiles, 16)) return SGEMM_ERR_INVALID_ARG;
+    const int64_t n = tile_bytes(rows, K, block);
+    if (Range(tiles, 1, n, n, 1).overlaps(Range(s, rows, blocks, lds, 1))) return SGEMM_ERR_ALIAS;
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    const int64_t most = (n / 4 + 255) / 256;
+    return launch(fp4_lay_out_scales_kernel, dim3((unsigned)std::min<int64_t>(most, dev.sms * 8)), dim3(256), 0, stream, 1,
+                  rows, blocks, s, (int64_t)lds, tiles);
+}
+
+int sgemm_fp4(int M, int N, int K, int block, const unsigned char *A, int lda, const unsigned char *a_block,
+              const float *a_scale, const unsigned char *B, int ldb, const unsigned char *b_block, const float *b_scale,
+              const float *bias, void *C, int ldc, int ctype, cudaStream_t stream) {
+    if (!shapes_ok(M, N, K, block, ldb, ldc, ctype) || lda < std::max<int64_t>(code_bytes(K), 1)) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (!output_ok(C, ctype, bias) || !codes_ok(A, lda, a_block, a_scale, K) || !codes_ok(B, ldb, b_block, b_scale, K))
+        return SGEMM_ERR_INVALID_ARG;
+    const int64_t na = tile_bytes(M, K, block), nb = tile_bytes(N, K, block);
+    const Range c(C, M, N, ldc, dtype_size(ctype));
+    for (const Range &in : {Range(A, M, code_bytes(K), lda, 1), Range(a_block, 1, na, na, 1), Range(a_scale, 1, M, M, 4),
+                            Range(B, N, code_bytes(K), ldb, 1), Range(b_block, 1, nb, nb, 1), Range(b_scale, 1, N, N, 4),
+                            Range(bias, 1, N, N, 4)})
+        if (c.overlaps(in)) return SGEMM_ERR_ALIAS;
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    const Fp4Args p{M, N, K, a_block, b_block, a_scale, b_scale, bias, C, ldc, ctype};
+    if (K == 0) return empty_product(p, dev, stream);
+    return product(p, {A, B, lda, ldb}, block, dev, stream);
+}
+
+// The tokens' codes, their block scales, their scales.
+size_t sgemm_linear_fp4_workspace_size(int M, int K, int block) {
+    if (M <= 0 || K <= 0 || M > kMaxSize || K > kMaxSize || !block_ok(block)) return 0;
+    return (size_t)(up256((int64_t)M * code_pitch(K)) + up256(tile_bytes(M, K, block)) + (block == 16 ? up256((int64_t)M * 4) : 0));
+}
+
+int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int block, const unsigned char *B, int ldb,
+                     const unsigned char *b_block, const float *b_scale, const float *bias, void *C, int ldc, int ctype,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!shapes_ok(M, N, K, block, ldb, ldc, ctype) || !dtype_ok(xtype) || ldx < std::max(K, 1)) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    const int size = dtype_size(xtype);
+    if (!output_ok(C, ctype, bias) || !codes_ok(B, ldb, b_block, b_scale, K) || (K > 0 && (!X || !aligned(X, (unsigned)size))))
+        return SGEMM_ERR_INVALID_ARG;
+    const size_t need = sgemm_linear_fp4_workspace_size(M, K, block);
+    if (!aligned(workspace, 16) || (need && (!workspace || workspace_bytes < need))) return SGEMM_ERR_INVALID_ARG;
+    const int64_t nb = tile_bytes(N, K, block);
+    const Range c(C, M, N, ldc, dtype_size(ctype)), ws(workspace, 1, (int64_t)need, (int64_t)need, 1);
+    for (const Range &in : {Range(X, M, K, ldx, size), Range(B, N, code_bytes(K), ldb, 1), Range(b_block, 1, nb, nb, 1),
+                            Range(b_scale, 1, N, N, 4), Range(bias, 1, N, N, 4)})
+        if (c.overlaps(in) || ws.overlaps(in)) return SGEMM_ERR_ALIAS;
+    if (c.overlaps(ws)) return SGEMM_ERR_ALIAS;
+    Device dev;
+    if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
+    Fp4Args p{M, N, K, nullptr, b_block, nullptr, b_scale, bias, C, ldc, ctype};
+    if (K == 0) return empty_product(p, dev, stream);
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *tiles = codes + up256((int64_t)M * code_pitch(K));
+    float *scale = block == 16 ? reinterpret_cast<float *>(tiles + up256(tile_bytes(M, K, block))) : nullptr;
+    const int st = quantize({M, M, K, codes, code_pitch(K), tiles, scale}, xtype, block, X, ldx, dev, stream);
+    if (st != SGEMM_OK) return st;
+    p.a_tiles = tiles;
+    p.a_scale = scale;
+    return product(p, {codes, B, code_pitch(K), ldb}, block, dev, stream);
+}
+
+}  // extern "C"

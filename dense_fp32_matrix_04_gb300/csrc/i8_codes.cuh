@@ -64,12 +64,6 @@ struct I8Args {
     int ctype;
 };
 
-__device__ __forceinline__ void store_c(void *C, int64_t at, int ctype, float v) {
-    if (ctype == SGEMM_F32) static_cast<float *>(C)[at] = v;
-    else if (ctype == SGEMM_BF16) static_cast<__nv_bfloat16 *>(C)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(C)[at] = __float2half_rn(v);
-}
-
 // Rows of 8-bit integers written out on padded, 16-byte aligned rows: as FP16
 // (Code __half, ld a multiple of 8) or as they are (int8_t, ld a multiple of
 // 16).  Elements between K and ld are not read by what follows.

@@ -65,25 +65,6 @@ struct I8StreamTile {
     static_assert(STAGES >= 4 && STAGES >= SETS, "a ring that hides the copies, and no set two rounds ahead of another");
 };
 
-// A place in a ring of N, and the parity of the rounds made.
-template <int N>
-struct RingPlace {
-    uint32_t at = 0, round = 0;
-    __device__ void next() {
-        if (++at == N) {
-            at = 0;
-            round ^= 1;
-        }
-    }
-};
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
-    return p != 0;
-}
-
 // D[tmem] (+)= A[tmem] * B[smem desc]^T with FP16 inputs and FP32 accumulation.
 __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -93,12 +74,6 @@ __device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// Descriptor of a K-major operand in 128-byte swizzled rows (8 rows = 1024 bytes).
-__device__ __forceinline__ uint64_t umma_desc_128b(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
 // 32 columns of this thread's lane of tensor memory.

@@ -37,6 +37,13 @@ struct Elem<SGEMM_F16> {
     __device__ static __half from_float(float v) { return __float2half_rn(v); }
 };
 
+// One element of a matrix of type `ctype`, rounded once.
+__device__ __forceinline__ void store_c(void *C, int64_t at, int ctype, float v) {
+    if (ctype == SGEMM_F32) static_cast<float *>(C)[at] = v;
+    else if (ctype == SGEMM_BF16) static_cast<__nv_bfloat16 *>(C)[at] = __float2bfloat16_rn(v);
+    else static_cast<__half *>(C)[at] = __float2half_rn(v);
+}
+
 // 16 bytes of elements as FP32 values.
 template <int DT>
 __device__ __forceinline__ void unpack16(const uint4 &raw, float *out) {

@@ -13,6 +13,25 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
+// A place in a ring of N, and the parity of the rounds made.
+template <int N>
+struct RingPlace {
+    uint32_t at = 0, round = 0;
+    __device__ void next() {
+        if (++at == N) {
+            at = 0;
+            round ^= 1;
+        }
+    }
+};
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- tcgen05 (5th-gen tensor cores, TMEM)
 
 // Allocate `ncols` TMEM columns (power of two >= 32) for this CTA; the whole
@@ -44,6 +63,12 @@ __device__ __forceinline__ void umma_tf32(uint32_t d_tmem, uint64_t a_desc, uint
         "tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// Descriptor of a K-major operand in 128-byte swizzled rows (8 rows = 1024 bytes).
+__device__ __forceinline__ uint64_t umma_desc_128b(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
 // Arrive once on the mbarrier when every MMA this thread issued so far is done.

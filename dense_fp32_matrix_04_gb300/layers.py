@@ -31,6 +31,12 @@ SIGNATURES = {
     "sgemm_i8_workspace_size": (_S, [_I, _I, _I, _P, _I]),
     "sgemm_linear_i8": (_I, [_I, _I, _I, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _P, _S, _P]),
     "sgemm_linear_i8_workspace_size": (_S, [_I, _I, _I, _P, _I]),
+    "sgemm_quantize_fp4": (_I, [_I, _I, _I, _P, _I, _I, _P, _I, _P, _P, _P]),
+    "sgemm_fp4_scales_size": (_S, [_I, _I, _I]),
+    "sgemm_fp4_lay_out_scales": (_I, [_I, _I, _I, _P, _I, _P, _P]),
+    "sgemm_fp4": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _P]),
+    "sgemm_linear_fp4": (_I, [_I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
+    "sgemm_linear_fp4_workspace_size": (_S, [_I, _I, _I]),
     "sgemm_logprobs": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
     "sgemm_logprobs_backward": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
 }
@@ -40,6 +46,7 @@ SIGNATURES = {
 # sees, so the checks below ask a tensor as little as they can.
 _torch = _lib = None
 _codes = {}
+_blocks = {}
 _raw_stream = _current_device = None
 
 
@@ -50,6 +57,7 @@ def _start():
     from . import load
     _lib = load()
     _codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    _blocks.update({torch.float8_e4m3fn: 16, torch.float8_e8m0fnu: 32})
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _torch = torch
 
@@ -289,6 +297,20 @@ def quantize_i8(x, stream=None, *, keep=None):
     return q, s
 
 
+def _workspace(t, index):
+    """(pointer, bytes) of a workspace that the caller gives, or (0, 0)."""
+    if t is None:
+        return 0, 0
+    on = t.get_device()
+    if on < 0:
+        raise TypeError("workspace must be a CUDA tensor")
+    if on != index:
+        raise ValueError(f"workspace is on {t.device}, not on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be dense")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, stream, keep, size_of):
     """What matmul_i8 and linear_i8 share: the weights, the output and the workspace."""
     dev = x.get_device()
@@ -310,17 +332,8 @@ def _linear(call, where, x, head, w, w_scale, bias, out_dtype, out, workspace, s
         if out_dtype not in _codes:
             raise TypeError("out must be float32, bfloat16 or float16")
         po, ldo = _matrix(out, "out", out_dtype, dev, (M, N))
-    pws = size = 0
-    if workspace is not None:
-        on = workspace.get_device()
-        if on < 0:
-            raise TypeError("workspace must be a CUDA tensor")
-        if on != dev:
-            raise ValueError(f"workspace is on {workspace.device}, not on cuda:{dev}")
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be dense")
-        pws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
+    pws, size = _workspace(workspace, dev)
+    if workspace is None:
         size = size_of(M, N, K, pw, ldw)
         if size:
             workspace = _torch.empty((size,), dtype=_torch.uint8, device=x.device)
@@ -356,6 +369,155 @@ def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None
     dt, _, _, px, ldx = _first(x, "x")
     return _linear(_lib.sgemm_linear_i8, "sgemm_linear_i8", x, (_codes[dt], px, ldx), w, w_scale, bias, out_dtype or dt,
                    out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)
+
+
+def _fp4_tiles(rows, K, block):
+    """Shape of the tiles that hold the block scales of rows x K columns."""
+    return ((rows + 127) // 128, ((K + block - 1) // block + 3) // 4 * 512)
+
+
+def _block_scales(t, name, rows, K, index):
+    """(pointer, block) of the tiles of block scales of rows x K columns."""
+    block = _blocks.get(t.dtype)
+    if block is None or t.get_device() < 0 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D CUDA tensor of float8_e4m3fn (blocks of 16) or float8_e8m0fnu (of 32)")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    want = _fp4_tiles(rows, K, block)
+    if t.shape != want:
+        raise ValueError(f"{name} is {tuple(t.shape)}, not the {want} of tiles for {rows} rows of {K}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be dense")
+    return t.data_ptr(), block
+
+
+def _fp4_rows(t, name, index, shape=None, cols=None):
+    """(pointer, bytes between rows) of packed codes."""
+    p, ld = _matrix(t, name, _torch.uint8, index, shape, cols)
+    rows, n = t.shape
+    if rows > 1 and ld % 16:
+        raise ValueError(f"{name} has rows {ld} bytes apart: they must be a multiple of 16, as quantize_fp4 lays them out")
+    if p % 16:
+        raise ValueError(f"{name} must start on 16 bytes")
+    return p, (ld if rows > 1 else max((n + 15) // 16 * 16, 16))
+
+
+@_foreign
+def quantize_fp4(x, block=16, stream=None, *, keep=None):
+    """``(q, block_scale, scale)``: the rows of x (M x K) as 4-bit floating point, for
+    ``linear_fp4`` and ``matmul_fp4``.  With ``block`` 16, blocks of 16 columns have e4m3 scales
+    and rows an FP32 scale; with 32, blocks of 32 have powers of two (e8m0) and ``scale`` is None.
+
+    ``q`` (M x ceil(K / 2), uint8) holds two codes a byte, the even column in the low half, on
+    rows a multiple of 16 bytes apart; ``block_scale`` is in tiles of 128 rows by 4 blocks (one row of
+    tiles a row of the tensor), with the format's type.  Has no gradient, and autograd does not
+    see it."""
+    dt, dev, (M, K), px, ldx = _first(x, "x")
+    if block not in (16, 32):
+        raise ValueError(f"block is {block}: it must be 16 or 32")
+    empty, where = _torch.empty, x.device
+    pitch = max((K + 31) // 32 * 16, 16)
+    whole = empty((M, pitch), dtype=_torch.uint8, device=where)
+    tiles = empty(_fp4_tiles(M, K, block), dtype=_torch.uint8, device=where)
+    scale = empty((M,), dtype=_torch.float32, device=where) if block == 16 else None
+    status = _lib.sgemm_quantize_fp4(M, K, _codes[dt], px, ldx, block, whole.data_ptr(), pitch, tiles.data_ptr(),
+                                     scale.data_ptr() if block == 16 else 0, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_quantize_fp4")
+    if keep is not None:
+        keep += [whole, tiles] + ([scale] if block == 16 else [])
+    return whole[:, :(K + 1) // 2], tiles.view(_torch.float8_e4m3fn if block == 16 else _torch.float8_e8m0fnu), scale
+
+
+@_foreign
+def lay_out_fp4_scales(s, stream=None, *, keep=None):
+    """Block scales (rows x blocks, float8_e4m3fn of blocks of 16 or float8_e8m0fnu of blocks of
+    32) in the tiles that ``matmul_fp4`` and ``linear_fp4`` take, for weights quantised elsewhere."""
+    if _torch is None:
+        _start()
+    dt, dev, (rows, blocks), ps, lds = _first(s, "s", tuple(_blocks))
+    block = _blocks[dt]
+    shape = _fp4_tiles(rows, blocks * block, block)
+    if blocks * block > 1 << 30:
+        raise ValueError(f"s has {blocks} blocks of {block}: more than 2^30 columns")
+    tiles = _torch.empty(shape, dtype=_torch.uint8, device=s.device)
+    status = _lib.sgemm_fp4_lay_out_scales(rows, blocks * block, block, ps, lds, tiles.data_ptr(), _on(dev, stream))
+    if status:
+        _check(status, "sgemm_fp4_lay_out_scales")
+    if keep is not None:
+        keep.append(tiles)
+    return tiles.view(dt)
+
+
+def _output(out, out_dtype, M, N, index, where, keep):
+    """(tensor, pointer, leading dimension, type's code) of a product's output."""
+    if out is None:
+        if out_dtype not in _codes:
+            raise TypeError("out_dtype must be float32, bfloat16 or float16")
+        out = _torch.empty((M, N), dtype=out_dtype, device=where)
+        if keep is not None:
+            keep.append(out)
+        return out, out.data_ptr(), N or 1, _codes[out_dtype]
+    if out.dtype not in _codes:
+        raise TypeError("out must be float32, bfloat16 or float16")
+    return (out, *_matrix(out, "out", out.dtype, index, (M, N)), _codes[out.dtype])
+
+
+@_foreign
+def matmul_fp4(a, a_block, a_scale, w, w_block, w_scale, bias=None, out_dtype=None, out=None, stream=None, *, keep=None):
+    """The product of the matrices that 4-bit codes and their scales stand for, a (M x K) times
+    the transpose of w (N x K), plus ``bias``, in ``out_dtype`` (float32 unless said otherwise).
+    Codes and scales are as ``quantize_fp4`` returns them, of the same block; ``a_scale`` and
+    ``w_scale`` may be None (1).  For inference: autograd does not see it."""
+    if _torch is None:
+        _start()
+    _, dev, (M, n), _, _ = _first(a, "a", (_torch.uint8,))
+    pa, lda = _fp4_rows(a, "a", dev)
+    N, K = w.shape[0], 2 * n  # the half behind an odd number of columns is 0
+    pw, ldw = _fp4_rows(w, "w", dev, None, n)
+    pab, block = _block_scales(a_block, "a_block", M, K, dev)
+    pwb, w_is = _block_scales(w_block, "w_block", N, K, dev)
+    if w_is != block:
+        raise ValueError(f"a has blocks of {block}, w of {w_is}")
+    f32 = (_torch.float32,)
+    ps = _vector(a_scale, "a_scale", M, f32, dev) if a_scale is not None else 0
+    pt = _vector(w_scale, "w_scale", N, f32, dev) if w_scale is not None else 0
+    pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
+    out, po, ldo, code = _output(out, out_dtype or _torch.float32, M, N, dev, a.device, keep)
+    status = _lib.sgemm_fp4(M, N, K, block, pa, lda, pab, ps, pw, ldw, pwb, pt, pb, po, ldo, code, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_fp4")
+    return out
+
+
+@_foreign
+def linear_fp4(x, w, w_block, w_scale=None, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
+    """``matmul_fp4`` on the rows of x (M x K, float32, bfloat16 or float16), which are quantised
+    first as ``quantize_fp4`` does it, in the blocks of ``w_block``; ``out_dtype`` is x's unless said
+    otherwise.  ``workspace``: a dense tensor of any type with the bytes that
+    ``sgemm_linear_fp4_workspace_size`` gives; allocated if None.  For inference: autograd does
+    not see the call."""
+    dt, dev, (M, K), px, ldx = _first(x, "x")
+    pw, ldw = _fp4_rows(w, "w", dev, None, (K + 1) // 2)
+    N = w.shape[0]
+    pwb, block = _block_scales(w_block, "w_block", N, K, dev)
+    f32 = (_torch.float32,)
+    pt = _vector(w_scale, "w_scale", N, f32, dev) if w_scale is not None else 0
+    pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
+    out, po, ldo, code = _output(out, out_dtype or dt, M, N, dev, x.device, keep)
+    pws, size = _workspace(workspace, dev)
+    if workspace is None:
+        size = _lib.sgemm_linear_fp4_workspace_size(M, K, block)
+        if size:
+            workspace = _torch.empty((size,), dtype=_torch.uint8, device=x.device)
+            pws = workspace.data_ptr()
+            if keep is not None:
+                keep.append(workspace)
+    status = _lib.sgemm_linear_fp4(M, N, K, _codes[dt], px, ldx, block, pw, ldw, pwb, pt, pb, po, ldo, code, pws, size,
+                                   _on(dev, stream))
+    if status:
+        _check(status, "sgemm_linear_fp4")
+    return out
 
 
 def _mask(mask, T, V, index):

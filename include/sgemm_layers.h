@@ -195,6 +195,82 @@ int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz
                             const float *g_logprob, const float *g_entropy,
                             void *dz, int lddz, cudaStream_t stream);
 
+/*
+ * Rows quantised to 4-bit floating point.  A code is a sign bit and three bits
+ * for 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1); `block` columns share a scale:
+ *   block 16: each row has a scale S = max|row| / 2688 (FP32), each block one of
+ *       8 bits, s = e4m3(max|y| / 6) with y = x (2688 / max|row|); the codes are
+ *       e2m1(y (1 / s)), and a column stands for code * s * S.
+ *   block 32: each block has a power of two, s = the smallest with
+ *       max|x| / s <= 6, as its exponent + 127 in 8 bits (e8m0); the codes are
+ *       e2m1(x / s), a column stands for code * s, and there is no row scale
+ *       (scale is NULL).
+ * All by FP32 operations each rounded once (1 / 6 is the FP32 number next to it), to
+ * nearest with ties to even, so codes and scales are defined to the bit.  Blocks whose
+ * scale comes out as 0 have codes 0.  A row (block 16), or a block (block 32), that
+ * holds an infinity or a NaN gets codes 0 and a scale that is not finite, so that its
+ * products are NaN and not silently wrong.
+ *   q: M x ceil(K / 2) bytes, ldq bytes between rows: column k in the low half of
+ *       byte k / 2 where k is even, in the high half where it is odd; the half
+ *       behind an odd K is 0.  q must be 16-byte aligned and ldq a multiple of
+ *       16, here and in the products.
+ *   block_scale: sgemm_fp4_scales_size(M, K, block) bytes, 16-byte aligned: the
+ *       blocks' scales in tiles of 128 rows by 4 blocks.  The scale of row r and
+ *       block j is byte 16 (r % 32) + 4 (r / 32 % 4) + j % 4 of the 512 of tile
+ *       (r / 128, j / 4); tiles of the same rows follow each other.  Scales of
+ *       blocks and rows behind the matrix are 0.
+ *   scale: M FP32 values (block 16).
+ * M, K <= 2^30.  Serves for activations and for weights stored N x K.
+ */
+int sgemm_quantize_fp4(int M, int K, int dtype, const void *x, int ldx, int block,
+                       unsigned char *q, int ldq, unsigned char *block_scale, float *scale,
+                       cudaStream_t stream);
+
+/* Bytes of the tiles that hold the blocks' scales of rows x K columns. */
+size_t sgemm_fp4_scales_size(int rows, int K, int block);
+
+/*
+ * Block scales from rows of plain bytes (s: rows x ceil(K / block), lds between
+ * rows) to tiles, for weights that were quantised elsewhere.
+ */
+int sgemm_fp4_lay_out_scales(int rows, int K, int block, const unsigned char *s, int lds,
+                             unsigned char *tiles, cudaStream_t stream);
+
+/*
+ * C = A B^T + bias for the matrices that codes and scales stand for (A: M x K, B:
+ * N x K, both quantised with the same block, as sgemm_quantize_fp4 lays them out):
+ * the products of a block and its scales are exact, the sums over K are FP32, in an
+ * order fixed by the shape; the rows' scales and the bias are applied in FP32 and the
+ * result is rounded once to ctype.
+ *   a_scale, b_scale: M and N FP32 values, or NULL (1).  Beside weights that were
+ *       quantised elsewhere b_scale can hold whatever scale they have beyond their
+ *       blocks', repeated for each row.
+ *   bias: N FP32 values or NULL.  M, N, K <= 2^30.
+ *   Scales of rows behind the matrix do not matter; those of blocks behind K must be
+ *   finite.
+ * K == 0: every sum is empty (C = bias, or 0, whatever the scales).
+ * The kernel waits for its own copies, with a limit: one that runs out is reported by
+ * sgemm_device_status, and C is unspecified.
+ */
+int sgemm_fp4(int M, int N, int K, int block,
+              const unsigned char *A, int lda, const unsigned char *a_block, const float *a_scale,
+              const unsigned char *B, int ldb, const unsigned char *b_block, const float *b_scale,
+              const float *bias, void *C, int ldc, int ctype, cudaStream_t stream);
+
+/*
+ * The linear layer with 4-bit weights on activations that are not quantised yet:
+ * sgemm_quantize_fp4 of the M x K rows of X (xtype), then sgemm_fp4.
+ *   workspace: sgemm_linear_fp4_workspace_size(M, K, block) bytes, 16-byte aligned,
+ *       with contents that do not matter; calls that share one must not overlap on
+ *       the GPU.
+ */
+int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int block,
+                     const unsigned char *B, int ldb, const unsigned char *b_block, const float *b_scale,
+                     const float *bias, void *C, int ldc, int ctype,
+                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+size_t sgemm_linear_fp4_workspace_size(int M, int K, int block);
+
 #ifdef __cplusplus
 }
 #endif

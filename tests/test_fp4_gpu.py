@@ -1,0 +1,196 @@
+"""Rows quantised to 4-bit floating point, and the product of such operands.
+
+Codes and scales are defined to the bit by FP32 operations (numpy repeats them, with
+its own roundings to 4 and 8 bits).  The products of codes and block scales are exact,
+their sum over K is held to the library's 2 K u sum |a||b|; the rows' scales and the
+bias then add three roundings, 4 u (|v| + |bias|), and the output type's."""
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF_UNIT = {"f32": U, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+LEVELS = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6], np.float64)
+# every value of e4m3 up to its largest, 448, by its bits
+E4M3 = np.array([(m / 8) * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for e in range(16) for m in range(8)][:127])
+
+
+def td(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+@pytest.fixture(scope="module")
+def sg(cuda_device, lib):
+    import dense_fp32_matrix_04_gb300 as sg
+    return sg
+
+
+def nearest(table, v):
+    """Indexes of the nearest entries, of two the even one; values beyond the last go to it."""
+    v = np.minimum(v.astype(np.float64), table[-1])
+    low = np.clip(np.searchsorted(table, v, side="right") - 1, 0, len(table) - 1)
+    high = np.minimum(low + 1, len(table) - 1)
+    up, down = table[high] - v, v - table[low]
+    return np.where((up < down) | ((up == down) & (low % 2 == 1)), high, low)
+
+
+def quantized(x, block):
+    """(codes, bits of the blocks' scales, rows' scales) of the definition, in FP32 steps."""
+    x = x.astype(np.float32)
+    M, K = x.shape
+    n = -(-K // block)
+    b = np.zeros((M, n * block), np.float32)
+    b[:, :K] = x
+    b = b.reshape(M, n, block)
+    with np.errstate(all="ignore"):
+        if block == 16:
+            top = np.abs(b).max((1, 2))
+            pre = np.where(top < 2.0 ** -100, np.float32(2.0 ** 64), np.float32(1))
+            t = np.where(top > 0, np.float32(2688) / (top * pre), np.float32(0)).astype(np.float32)
+            y = b * pre[:, None, None] * t[:, None, None]
+            bits = nearest(E4M3, np.abs(y).max(2) * (np.float32(1) / np.float32(6)))
+            s = E4M3[bits].astype(np.float32)
+            inv = np.where(s > 0, np.float32(1) / s, np.float32(0)).astype(np.float32)
+            v = y * inv[:, :, None]
+            rows = top / np.float32(2688)
+        else:
+            f, e = np.frexp(np.abs(b).max(2))
+            e = np.where(f == 0, -127, np.clip(np.where(f <= 0.75, e - 3, e - 2), -127, 127))
+            bits, rows = e + 127, None
+            v = np.ldexp(b.astype(np.float64), -e[:, :, None])
+    code = nearest(LEVELS, np.abs(v)) + 8 * (np.signbit(v))
+    return code.reshape(M, -1)[:, :K], bits, rows
+
+
+def codes_of(q, K):
+    q = q.cpu().numpy()
+    return np.stack([q & 15, q >> 4], 2).reshape(q.shape[0], -1)[:, :K]
+
+
+def tile_bytes(s):
+    import torch
+    return s.view(torch.uint8).cpu().numpy()
+
+
+def bits_of(s, rows, blocks):
+    r, j = np.arange(rows)[:, None], np.arange(blocks)[None]
+    return tile_bytes(s)[r // 128, j // 4 * 512 + r % 32 * 16 + r % 128 // 32 * 4 + j % 4]
+
+
+def values_of(q, s, K, block):
+    """What codes and block scales stand for, in 64 bits."""
+    code = codes_of(q, K)
+    bits = bits_of(s, code.shape[0], -(-K // block))
+    if block == 16:
+        with_nan = np.append(E4M3, np.nan)
+        scale = with_nan[np.minimum(bits, 127)]
+    else:
+        scale = np.where(bits == 255, np.nan, np.ldexp(1.0, bits.astype(np.int64) - 127))
+    return LEVELS[code % 8] * np.where(code >= 8, -1.0, 1.0) * np.repeat(scale, block, 1)[:, :K]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,K,pad,offset", [(1, 1, 0, 0), (3, 5, 0, 1), (1, 4096, 0, 0), (130, 512, 8, 8), (9, 1111, 0, 0),
+                                            (2, 16384, 0, 0), (2, 16392, 0, 0), (3, 40017, 0, 0), (70, 264, 3, 1),
+                                            (2000, 64, 0, 0), (33, 528, 0, 0)])
+def test_codes_are_defined_to_the_bit(sg, M, K, pad, offset, block, dtype):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    buf = torch.full((M * (K + pad) + offset,), float("nan"), dtype=td(dtype), device="cuda")
+    x = buf[offset:].view(M, K + pad)[:, :K]
+    x.copy_(torch.randn(M, K, generator=g, device="cuda") * torch.exp(2 * torch.randn(M, 1, generator=g, device="cuda")))
+    x[:, :K // 3] *= 2.0 ** -9                  # blocks whose scale is small, or comes out as 0
+    if M > 1:
+        x[1] = 0
+    q, s, rows = sg.quantize_fp4(x, block)
+    code, bits, want_rows = quantized(x.float().cpu().numpy(), block)
+    got = codes_of(q, K)
+    n = -(-K // block)
+    assert np.array_equal(bits_of(s, M, n), bits)
+    # a zero may carry either sign
+    assert np.array_equal(np.where(got == 8, 0, got), np.where(code == 8, 0, code))
+    if block == 16:
+        assert np.array_equal(rows.cpu().numpy(), want_rows)
+    else:
+        assert rows is None
+    if K % 2:
+        assert not (q[:, -1] >> 4).any()
+    # nothing but zeros behind the matrix
+    assert np.count_nonzero(tile_bytes(s)) == np.count_nonzero(bits)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_halves_go_to_the_even_code(sg, block):
+    import torch
+    x = torch.zeros(1, 64, device="cuda")
+    # 6 as the largest of every block: scales of 448 (times 6 / 2688) and of 1
+    x[0] = torch.tensor([6.0, .25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, -.25, -.75, -1.25, -1.75, -2.5, -3.5, -5.0, -6.0]).repeat(4)
+    q, _, _ = sg.quantize_fp4(x, block)
+    assert codes_of(q, 16)[0].tolist() == [7, 0, 2, 2, 4, 4, 6, 6, 8, 10, 10, 12, 12, 14, 14, 15]
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_codes_of_extreme_rows(sg, block):
+    import torch
+    x = torch.zeros(6, 64, device="cuda")
+    x[0, 3], x[0, 5] = 1e-44, -5e-45          # below the smallest normal number
+    x[1, 3], x[1, 5] = 3.4e38, -1.7e38
+    x[2, 3] = float("inf")
+    x[3, 3] = float("nan")
+    x[4, 3], x[4, 4] = float("-inf"), float("nan")
+    q, s, rows = sg.quantize_fp4(x, block)
+    code = codes_of(q, 64)
+    # the largest is 6 steps of its scale in the one format; in the other it is 3.997 times 2^126
+    assert not code[2:].any() and code[1, 3] == (7 if block == 16 else 6) and not code[:2, 6:].any()
+    if block == 16:
+        rows = rows.cpu().numpy()
+        assert code[0, 3] == 7 and np.isinf(rows[2]) and np.isnan(rows[3]) and np.isnan(rows[4]) and rows[5] == 0
+    else:
+        # 2^127 is the largest power of two the codes can be scaled by: 1e-44 2^127 is 0
+        bits = bits_of(s, 6, 2)
+        assert not (code[0] % 8).any() and bits[0].tolist() == [0, 0] and (bits[2:5, 0] == 255).all() and bits[5, 0] == 0
+        assert values_of(q, s, 64, 32)[1, 3] == pytest.approx(3.4e38, rel=0.25)
+
+
+def operands(sg, M, N, K, seed, block, dtype="f32"):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn(M, K, generator=g, device="cuda") * torch.exp(torch.randn(M, 1, generator=g, device="cuda"))).to(td(dtype))
+    w = torch.randn(N, K, generator=g, device="cuda")
+    return x, sg.quantize_fp4(w, block), torch.randn(N, generator=g, device="cuda") * 10
+
+
+def check(got, a, w, K, block, bias, out):
+    A, B = values_of(a[0], a[1], K, block), values_of(w[0], w[1], K, block)
+    s = 1.0
+    if block == 16:
+        s = np.outer(a[2].double().cpu().numpy(), w[2].double().cpu().numpy())
+    extra = bias.double().cpu().numpy() if bias is not None else 0.0
+    v, size = A @ B.T * s, np.abs(A) @ np.abs(B).T * s
+    want = v + extra
+    tol = 2 * K * U * size + 4 * U * (np.abs(v) + np.abs(extra)) + HALF_UNIT[out] * np.abs(want) * (1 + 2.0 ** -7) + 2.0 ** -126
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"worst {(err / tol).max():.3g} of the bound, {np.count_nonzero(~(err <= tol))} of {err.size}"
+
+
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1000, 4096), (2, 129, 300), (3, 4, 5), (5, 257, 1024), (8, 512, 8192), (9, 130, 77),
+          (15, 96, 2048), (16, 1024, 4096), (17, 200, 1040), (24, 384, 4096), (31, 65, 129), (33, 300, 640), (64, 256, 512),
+          (65, 130, 2047), (127, 257, 100), (128, 512, 1024), (129, 1025, 513), (200, 136, 8192), (256, 256, 256),
+          (257, 129, 1033), (300, 4999, 64), (513, 640, 2048), (1030, 260, 530), (2050, 4100, 300)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("block", [16, 32])
+def test_product(sg, M, N, K, block):
+    out = ["f32", "bf16", "f16"][(M + N + K) % 3]
+    x, w, bias = operands(sg, M, N, K, M + N + K, block)
+    use_bias = bias if (M + N) % 2 else None
+    a = sg.quantize_fp4(x, block)
+    got = sg.matmul_fp4(*a, *w, use_bias, out_dtype=td(out))
+    check(got, a, w, K, block, use_bias, out)
+    # the layer quantises the same codes itself
+    assert bool((sg.linear_fp4(x, *w, bias=use_bias, out_dtype=td(out)) == got).all())
