@@ -409,5 +409,5 @@ def matmul(A, B, out=None, stream=None):
     return out
 
 
-from .layers import (block_norm, block_norm_backward, lay_out_fp4_scales, linear_fp4, linear_i8, logprobs,  # noqa: E402
-                     logprobs_backward, matmul_fp4, matmul_i8, quantize_fp4, quantize_i8)
+from .layers import (block_norm, block_norm_backward, lay_out_fp4_scales, layer_norm, layer_norm_backward,  # noqa: E402
+                     linear_fp4, linear_i8, logprobs, logprobs_backward, matmul_fp4, matmul_i8, quantize_fp4, quantize_i8)

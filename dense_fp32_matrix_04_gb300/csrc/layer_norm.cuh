@@ -1,0 +1,290 @@
+// The norm of rows about their mean, after the sum of the residual stream and a
+// block's output, and its gradient:
+//     r = x + a                       (rounded to the rows' type, and handed on)
+//     n = (r - mean) rstd w + b,      rstd = rsqrt(mean((r - mean)^2) + eps)
+// What is normalised is the r that is handed on, so that the gradient needs r alone.
+// A row is read once into registers and walked as in block_norm.cuh; its two moments
+// are each warp's own, about its own mean, joined with one barrier.
+#pragma once
+
+#include <cstdint>
+
+#include "ptx.cuh"
+#include "row_ring.cuh"
+#include "rows.cuh"
+
+namespace sgemm {
+
+struct LayerNormArgs {
+    int T, D;
+    const void *x, *add;
+    int64_t ldx, lda;
+    const void *w, *b;
+    int w_f32;         // the weights are FP32 (otherwise of the rows' type)
+    float eps;
+    void *r, *n;
+    int64_t ldr, ldn;
+    float *stats;      // 2 x T: mean, rstd
+    int ranks, width;  // blocks that share a row, and the columns of each
+};
+
+struct LayerNormGradArgs {
+    int T, D;
+    const void *x, *dn, *dr;
+    int64_t ldx, lddn, lddr;
+    const void *w;
+    int w_f32;
+    const float *stats;
+    void *dx;
+    int64_t lddx;
+    void *dw, *db;
+    float *partial;    // runners x 2 x D: dw, db
+    int runners;
+    int ranks, width;
+};
+
+constexpr int kLayerNormStages = 4;
+constexpr int kLayerNormGradStages = 3;
+
+// The threads of a row: as in block_norm_kernel.
+template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const LayerNormArgs a) {
+    using L = RowLayout<DT, ALIGNED, NV>;
+    using type = typename L::type;
+    constexpr int V = L::VEC, H = V / 2, S = kLayerNormStages;  // H pairs a piece
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[RowReducer::SLOTS];
+    RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
+    const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
+    const int c0 = rank * a.width;  // this block's columns
+    const L l(min(a.width, a.D - c0));
+    const int cols = c0 + l.col;
+    const float inv_d = 1.f / (float)a.D;
+    const int arrays = a.add ? 2 : 1, pieces = l.pieces();
+    uint4 *mine = l.place(ring, S * arrays);
+
+    F2 w[NV][H], b[NV][H];
+    const int wsize = a.w_f32 ? 4 : (int)sizeof(type);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        l.template weights<V>(static_cast<const char *>(a.w) + (int64_t)c0 * wsize, a.w_f32, v * V, w[v]);
+        if (a.b) {
+            l.template weights<V>(static_cast<const char *>(a.b) + (int64_t)c0 * wsize, a.w_f32, v * V, b[v]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < H; ++i) b[v][i] = F2(0.f);
+        }
+    }
+    const float count = l.warp_columns(), inv_count = count > 0.f ? 1.f / count : 0.f;
+
+    const int64_t first = (int64_t)group_id * blockDim.y + threadIdx.y;
+    const int64_t step = (int64_t)(gridDim.x / (unsigned)a.ranks) * blockDim.y;
+    // rows are numbered below 2^30 and leading dimensions are 32-bit: one multiplication
+    auto row = [&](const void *p, int64_t ld, int64_t t) {
+        return static_cast<const type *>(p) + ((int64_t)(int)t * (int)ld + cols);
+    };
+    auto fetch = [&](int64_t t, int stage) {
+        if (t < a.T) {
+            uint4 *slot = mine + stage * arrays * pieces;
+            l.copy(slot, row(a.x, a.ldx, t));
+            if (a.add) l.copy(slot + pieces, row(a.add, a.lda, t));
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) fetch(first + s * step, s);
+
+    int stage = 0;
+    for (int64_t t = first; t < a.T; t += step) {
+        cp_async_wait<S - 2>();
+        if (!ALIGNED) row_sync(red.warps);
+        const uint4 *slot = mine + stage * arrays * pieces;
+        F2 r[NV][H], sum(0.f), square(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            l.template read<V>(slot, row(a.x, a.ldx, t), v * V, r[v]);
+            if (a.add) {
+                F2 y[H];
+                l.template read<V>(slot + pieces, row(a.add, a.lda, t), v * V, y);
+#pragma unroll
+                for (int i = 0; i < H; ++i) r[v][i] = r[v][i] + y[i];
+                l.store(const_cast<type *>(row(a.r, a.ldr, t)), v * V, r[v]);
+                L::rounded(r[v]);
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) sum = sum + r[v][i];
+        }
+        // the slot that the previous row was read from takes the row after the next ones
+        fetch(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        float mean, var;
+        // sum of squares about `about`, of this thread's columns
+        auto squares = [&](float about) {
+            F2 ss(0.f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    F2 d = r[v][i] + F2(-about);
+                    l.only_inside(v * V + 2 * i, d);
+                    ss = fma(d, d, ss);
+                }
+            return ss.sum();
+        };
+        if (a.ranks > 1) {
+            mean = red.sum(sum.sum()) * inv_d;
+            var = red.sum(squares(mean)) * inv_d;
+        } else {
+            const float s = warp_sum(sum.sum());
+            red.moments(count, s, warp_sum(squares(s * inv_count)), inv_d, mean, var);
+        }
+        const float rstd = rsqrtf(var + a.eps);
+        if (a.stats && threadIdx.x == 0 && rank == 0) {
+            a.stats[t] = mean;
+            a.stats[a.T + t] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) r[v][i] = fma((r[v][i] + F2(-mean)) * F2(rstd), w[v][i], b[v][i]);
+            l.store(const_cast<type *>(row(a.n, a.ldn, t)), v * V, r[v]);
+        }
+    }
+    if (a.ranks > 1) cluster_sync();
+}
+
+// With h = (x - mean) rstd and u = dn w the gradient of a row is
+//     dx = dr + rstd (u - mean(u) - h mean(u h)),
+// two sums, taken at once, so a row costs one barrier.  dw = sum dn h and db = sum dn
+// over a runner's rows stay in registers; what a runner has of them goes to `partial`,
+// where a second kernel adds the runners in order.
+template <int DT, bool ALIGNED, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNormGradArgs a) {
+    using L = RowLayout<DT, ALIGNED, NV>;
+    using type = typename L::type;
+    constexpr int N = L::N, V = L::VEC, P = V / 2, S = kLayerNormGradStages;  // P pairs a piece
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[RowReducer::SLOTS];
+    RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
+    const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
+    const int c0 = rank * a.width;  // this block's columns
+    const L l(min(a.width, a.D - c0));
+    const int cols = c0 + l.col;
+    const float inv_d = 1.f / (float)a.D;
+    const int runner = group_id * blockDim.y + threadIdx.y;
+    if (runner >= a.runners) return;  // only where a warp is a runner: no barrier spans warps
+    const RowRuns runs(a.T, a.runners);
+    const int begin = runs.first(runner), end = runs.first(runner + 1);
+    const int arrays = a.dr ? 3 : 2, pieces = l.pieces(), stride = arrays * pieces;
+    uint4 *mine = l.place(ring, S * arrays);
+
+    F2 w[N / 2], dw[N / 2], db[N / 2];
+    const int wsize = a.w_f32 ? 4 : (int)sizeof(type);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        F2 f[P];
+        l.template weights<V>(static_cast<const char *>(a.w) + (int64_t)c0 * wsize, a.w_f32, v * V, f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) w[v * P + i] = f[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) dw[i] = db[i] = F2(0.f);
+
+    auto at = [&](const void *p, int64_t ld, int t) { return static_cast<const type *>(p) + ((int64_t)t * (int)ld + cols); };
+    auto fetch = [&](int t, int stage) {
+        if (t < end) {
+            uint4 *slot = mine + stage * stride;
+            l.copy(slot, at(a.x, a.ldx, t));
+            l.copy(slot + pieces, at(a.dn, a.lddn, t));
+            if (a.dr) l.copy(slot + 2 * pieces, at(a.dr, a.lddr, t));
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) fetch(begin + k, k);
+
+    int stage = 0;
+    for (int t = begin; t < end; ++t) {
+        cp_async_wait<S - 2>();
+        if (!ALIGNED) row_sync(red.warps);
+        const uint4 *slot = mine + stage * stride;
+        fetch(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        const float mean = a.stats[t], rstd = a.stats[a.T + t];
+        F2 h[N / 2], u[N / 2], part[2] = {F2(0.f), F2(0.f)};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            F2 xx[P], d[P];
+            l.template read<V>(slot, at(a.x, a.ldx, t), v * V, xx);
+            l.template read<V>(slot + pieces, at(a.dn, a.lddn, t), v * V, d);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                // (past the row's end dn is 0)
+                const int k = v * P + i;
+                h[k] = (xx[i] + F2(-mean)) * F2(rstd);
+                dw[k] = fma(d[i], h[k], dw[k]);
+                db[k] = db[k] + d[i];
+                u[k] = d[i] * w[k];
+                part[0] = part[0] + u[k];
+                part[1] = fma(u[k], h[k], part[1]);
+            }
+        }
+        float sums[2] = {part[0].sum(), part[1].sum()};
+        red.sum(sums);
+        const float c1 = sums[0] * inv_d * rstd, c2 = sums[1] * inv_d * rstd;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            F2 d[P];
+            if (a.dr) {
+                l.template read<V>(slot + 2 * pieces, at(a.dr, a.lddr, t), v * V, d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) d[i] = F2(0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int k = v * P + i;
+                d[i] = d[i] + fma(h[k], F2(-c2), fma(u[k], F2(rstd), F2(-c1)));
+            }
+            l.store(static_cast<type *>(a.dx) + ((int64_t)t * (int)a.lddx + cols), v * V, d);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float *p = a.partial + ((int64_t)runner * 2 * a.D + cols);
+        l.put(p, v * V, dw + v * P, false);
+        if (a.db) l.put(p + a.D, v * V, db + v * P, false);
+    }
+    if (a.ranks > 1) cluster_sync();
+}
+
+// Adds the runners' partial sums, blockIdx.y 0 of dw and 1 of db: 32 columns by
+// kLayerNormJoinSlices slices of the runners, each added in order with LOADS loads on
+// their way, then the slices in order.
+constexpr int kLayerNormJoinSlices = 16;
+template <int DT>
+__global__ void __launch_bounds__(32 * kLayerNormJoinSlices) layer_norm_grad_join_kernel(const LayerNormGradArgs a) {
+    constexpr int LOADS = 16, SLICES = kLayerNormJoinSlices;
+    __shared__ float part[SLICES][32];
+    const int c = blockIdx.x * 32 + threadIdx.x, k = blockIdx.y;
+    griddep_wait();
+    float s = 0.f;
+    if (c < a.D)
+        for (int b = threadIdx.y; b < a.runners; b += LOADS * SLICES) {
+            float v[LOADS];
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                v[i] = b + i * SLICES < a.runners ? __ldcg(a.partial + ((int64_t)(b + i * SLICES) * 2 + k) * a.D + c) : 0.f;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) s += v[i];
+        }
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < a.D) {
+#pragma unroll
+        for (int i = 1; i < SLICES; ++i) s += part[i][threadIdx.x];
+        store_weight<DT>(k ? a.db : a.dw, a.w_f32, c, s);
+    }
+}
+
+}  // namespace sgemm

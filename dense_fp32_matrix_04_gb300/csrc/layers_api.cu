@@ -10,6 +10,7 @@
 #include "block_norm.cuh"
 #include "host.h"
 #include "logprobs.cuh"
+#include "row_host.h"
 
 namespace {
 
@@ -20,49 +21,17 @@ using sgemm_host::Device;
 using sgemm_host::dtype_ok;
 using sgemm_host::dtype_size;
 using sgemm_host::launch;
+using sgemm_host::kMaxWidth;
+using sgemm_host::most_grad_runners;
 using sgemm_host::Range;
-
-// A matrix of rows as an operator sees it.
-struct Rows {
-    const void *p;
-    int ld;
-    // 16-byte pieces: aligned base and rows
-    bool vec(int size) const { return !p || (aligned(p, 16) && (int64_t)ld * size % 16 == 0); }
-    bool ok(int cols, int size) const { return p && aligned(p, (unsigned)size) && ld >= std::max(cols, 1); }
-    Range range(int64_t rows, int cols, int size) const { return Range(p, rows, cols, ld, size); }
-    bool same(const Rows &o) const { return p == o.p && ld == o.ld; }
-};
-
-// The threads that share a row of D elements, `per` of them each: whole warps.
-int row_threads(int D, int per) { return ((D + per - 1) / per + 31) / 32 * 32; }
+using sgemm_host::row_threads;
+using sgemm_host::RowPlan;
+using sgemm_host::Rows;
 
 constexpr int kMaxRows = 1 << 30;
-constexpr int kMaxWidth = 24576;  // over a cluster of eight blocks, FP32 rows with every input fit their rings
-
 bool finite(float v) { return std::isfinite(v); }
 
 // ---------------------------------------------------------------- block norm
-
-// How a row is shared out: `ranks` blocks of a cluster with `width` columns
-// each, in pieces that no 16 bytes span; `per` elements a thread.  A block
-// takes at most `most` threads, and its ring of `slots` rows at most 225 KB.
-// Where a warp is enough for a row, a block has four.
-struct RowPlan {
-    int ranks = 1, width;
-    dim3 block;
-    size_t smem;
-    RowPlan(int D, int size, int slots, int per, int most) : width(D) {
-        for (;; ranks *= 2) {
-            const int vec = 16 / size;
-            width = ranks == 1 ? D : ((D + ranks - 1) / ranks + vec - 1) / vec * vec;
-            const int threads = row_threads(width, per);
-            block = dim3(threads, threads == 32 && ranks == 1 ? 4 : 1);
-            smem = (size_t)slots * row_pieces(threads, per, size) * 16 * block.y;
-            if (ranks == 8 || (threads <= most && smem <= 225 * 1024)) break;
-        }
-    }
-    int threads() const { return (int)(block.x * block.y); }
-};
 
 template <int DT, bool ALIGNED, int NV, int MAXT, int MINB>
 int launch_norm(BlockNormArgs a, const Device &dev, cudaStream_t stream) {
@@ -91,12 +60,6 @@ int norm_by_width(const BlockNormArgs &a, const Device &dev, cudaStream_t stream
         if (a.D <= 2048) return launch_norm<DT, false, 8 / VEC, 256, 3>(a, dev, stream);
     return launch_norm<DT, ALIGNED, 16 / VEC, 320, ALIGNED ? 2 : 1>(a, dev, stream);
 }
-
-// Runners of the gradient's rows: a block (or a cluster of blocks) each, or for
-// narrow rows a warp each.  Every one writes its own partial sums, so there are
-// no more than the SMs hold at once, 512 threads of 128 registers each; this is
-// the most there can be for any type and alignment.
-int most_grad_runners(int T, int D, int sms) { return std::min(T, std::max(1, 512 * sms / row_threads(D, 16))); }
 
 template <int DT, bool ALIGNED, bool TOKEN, int PER>
 int launch_norm_grad(BlockNormGradArgs a, const Device &dev, cudaStream_t stream) {

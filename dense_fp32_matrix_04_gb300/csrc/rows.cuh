@@ -197,6 +197,31 @@ struct RowReducer {
         sum(one);
         return one[0];
     }
+    // Mean and variance of a row within a block from each warp's count of columns, sum, and sum of
+    // squares about its own mean: joined without a difference of large numbers, and with one
+    // barrier.  (Of one warp: what it has.)
+    __device__ void moments(float n, float s, float m2, float inv_d, float &mean, float &var) {
+        if (warps > 1) {
+            float *p = slots + 96 * turn;
+            turn ^= 1;
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+            if (lane == 0) {
+                p[warp] = n;
+                p[32 + warp] = s;
+                p[64 + warp] = m2;
+            }
+            __syncthreads();
+            n = lane < warps ? p[lane] : 0.f;
+            s = lane < warps ? p[32 + lane] : 0.f;
+            m2 = lane < warps ? p[64 + lane] : 0.f;
+            mean = warp_sum(s) * inv_d;
+            const float d = n > 0.f ? s / n - mean : 0.f;
+            var = warp_sum(fmaf(n * d, d, m2)) * inv_d;
+        } else {
+            mean = s * inv_d;
+            var = m2 * inv_d;
+        }
+    }
     __device__ uint32_t max(uint32_t v) {
         v = warp_max(v);
         if (warps == 1 && ranks == 1) return v;

@@ -26,6 +26,9 @@ SIGNATURES = {
     "sgemm_block_norm_backward": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _F, _P, _P, _I, _P, _I,
                                        _P, _I, _P, _I, _P, _P, _P, _I, _P, _S, _P]),
     "sgemm_block_norm_backward_workspace_size": (_S, [_I, _I]),
+    "sgemm_layer_norm": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P, _I, _F, _P, _I, _P, _I, _P, _P]),
+    "sgemm_layer_norm_backward": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _S, _P]),
+    "sgemm_layer_norm_backward_workspace_size": (_S, [_I, _I]),
     "sgemm_quantize_i8": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P]),
     "sgemm_i8": (_I, [_I, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, _I, _I, _P, _S, _P]),
     "sgemm_i8_workspace_size": (_S, [_I, _I, _I, _P, _I]),
@@ -227,11 +230,16 @@ def block_norm(x, y, w_pre, w_post=None, gate=None, scale=1.0, eps=1e-6, quantiz
     return made
 
 
+def _stream_of(index, stream):
+    """The context in which torch's own calls run on the stream of a call."""
+    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                              _torch.cuda.ExternalStream(_on(index, stream), device=index))
+
+
 def _no_columns(rstd, post, q_scale, index, stream):
     """What a row of no elements has beside them, which the library does not launch a kernel
     for: the mean of nothing is NaN, the largest of nothing 0."""
-    with _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
-                            _torch.cuda.ExternalStream(_on(index, stream), device=index)):
+    with _stream_of(index, stream):
         rstd.fill_(float("nan"))
         if not post:
             rstd[0].fill_(1.0)
@@ -278,6 +286,79 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
     if keep is not None:
         keep += [t for t in (*made, ws) if t is not None]
     return made
+
+
+@_foreign
+def layer_norm(x, w, bias=None, add=None, eps=1e-5, out=None, stream=None, *, keep=None):
+    """The norm of the rows of x (T x D) about their mean, after the sum with ``add``:
+
+        r = x + add                                  (rounded to x's type; r is x without ``add``)
+        n = (r - mean) * rstd * w + bias,            rstd = rsqrt(mean((r - mean)^2) + eps)
+
+    Returns ``(r, n, stats)``, of which ``stats`` (2 x T: mean, rstd) and r are for the backward
+    pass.  ``out`` receives r; it may be x or add.  Rows of no columns (D = 0) have NaN for their
+    statistics.  Autograd does not see the call: its gradient is ``layer_norm_backward``.
+    """
+    dt, dev, shape, px, ldx = _first(x, "x")
+    f32, empty, where = _torch.float32, _torch.empty, x.device
+    T, D = shape
+    wt = w.dtype
+    pw = _vector(w, "w", D, (f32, dt), dev)
+    pb = _vector(bias, "bias", D, (wt,), dev) if bias is not None else 0
+    stats, n = empty((2, T), dtype=f32, device=where), empty(shape, dtype=dt, device=where)
+    made = [n, stats]
+    if add is None:
+        if out is not None:
+            raise ValueError("out is for the sum with add, which is not given")
+        r, pa, lda, pr, ldr = x, 0, D or 1, 0, D or 1
+    else:
+        pa, lda = _matrix(add, "add", dt, dev, shape)
+        if out is None:
+            r = empty(shape, dtype=dt, device=where)
+            made.append(r)
+            pr, ldr = r.data_ptr(), D or 1
+        else:
+            r = out
+            pr, ldr = _matrix(out, "out", dt, dev, shape)
+    status = _lib.sgemm_layer_norm(T, D, _codes[dt], px, ldx, pa, lda, pw, pb, _codes[wt], eps, pr, ldr, n.data_ptr(), D or 1,
+                                   stats.data_ptr(), _on(dev, stream))
+    if status:
+        _check(status, "sgemm_layer_norm")
+    if not D and T:
+        with _stream_of(dev, stream):
+            stats.fill_(float("nan"))
+    if keep is not None:
+        keep += made
+    return r, n, stats
+
+
+@_foreign
+def layer_norm_backward(x, w, stats, dn, dr=None, bias=True, stream=None, *, keep=None):
+    """Gradients ``(dx, dw, db)`` of ``layer_norm`` from those of its n and r (``dr`` None: zero);
+    ``x`` is the r that it returned, and ``dx`` the gradient of x and of ``add``.  ``bias`` False: db
+    is not computed, and None."""
+    dt, dev, shape, px, ldx = _first(x, "x")
+    f32, empty, where = _torch.float32, _torch.empty, x.device
+    T, D = shape
+    pn, ldn = _matrix(dn, "dn", dt, dev, shape)
+    pr, ldr = _matrix(dr, "dr", dt, dev, shape) if dr is not None else (0, D or 1)
+    wt = w.dtype
+    pw = _vector(w, "w", D, (f32, dt), dev)
+    if stats.dtype is not f32 or stats.shape != (2, T) or not stats.is_contiguous() or stats.get_device() != dev:
+        raise ValueError("stats must be the (2, T) float32 tensor that layer_norm returned")
+    dx = empty(shape, dtype=dt, device=where)
+    dw = empty((D,), dtype=wt, device=where)
+    db = empty((D,), dtype=wt, device=where) if bias else None
+    need = _lib.sgemm_layer_norm_backward_workspace_size(T, D)
+    ws = empty((need,), dtype=_torch.uint8, device=where)
+    status = _lib.sgemm_layer_norm_backward(T, D, _codes[dt], px, ldx, pw, _codes[wt], stats.data_ptr(), pn, ldn, pr, ldr,
+                                            dx.data_ptr(), D or 1, dw.data_ptr(), db.data_ptr() if bias else 0,
+                                            ws.data_ptr(), need, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_layer_norm_backward")
+    if keep is not None:
+        keep += [t for t in (dx, dw, db, ws) if t is not None]
+    return dx, dw, db
 
 
 @_foreign

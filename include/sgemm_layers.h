@@ -95,6 +95,51 @@ int sgemm_block_norm_backward(int T, int D, int dtype,
 size_t sgemm_block_norm_backward_workspace_size(int T, int D);
 
 /*
+ * The norm of rows about their mean, of T rows of width D, after an optional sum:
+ *     r = x + add                                  (r = x without add)
+ *     n = (r - mean) rstd w + b,   mean = mean(r), rstd = rsqrt(mean((r - mean)^2) + eps)
+ * The sum is rounded to dtype, once, and what is normalised is the r that is written,
+ * so the backward pass needs r alone; everything else is FP32, and n is rounded once.
+ * The squares are summed about means of parts of the row, so a mean that is large beside
+ * the deviation costs nothing more than what rounded inputs hold.
+ *   dtype: the type of x, add, r and n.  r is needed exactly when add is given; it may be
+ *       x or add (same pointer and leading dimension).
+ *   w, b: D weights each, of type wdtype (FP32, or the same as dtype); b may be NULL (0).
+ *   stats: 2 x T FP32, the means, then the rstd of all rows, for the backward pass.  May be
+ *       NULL.
+ * T <= 2^30, D <= 24576.  Without rows or columns nothing is launched and nothing written.
+ */
+int sgemm_layer_norm(int T, int D, int dtype,
+                     const void *x, int ldx, const void *add, int lda,
+                     const void *w, const void *b, int wdtype, float eps,
+                     void *r, int ldr, void *n, int ldn, float *stats, cudaStream_t stream);
+
+/*
+ * The gradient of sgemm_layer_norm with respect to r, whose gradient add and the forward
+ * pass's x share, to w and to b.  With h = (x - mean) rstd and u = dn w, of each row:
+ *     dx = dr + rstd (u - mean(u) - h mean(u h)),   dw = sum dn h,   db = sum dn
+ *   x: the r of the forward pass (its x, where nothing was added).  stats: what the forward
+ *       pass wrote.  dn, dr: the gradients of n and of r (dr NULL: zero).
+ *   dx (dtype) may be dn, dr or x (same pointer and leading dimension); dw and db have
+ *       type wdtype; db NULL: not wanted.
+ * Sums over rows are FP32, in an order fixed by the shape, and rounded once.
+ *   workspace: sgemm_layer_norm_backward_workspace_size(T, D) bytes, 16-byte aligned; its
+ *       contents on entry do not matter.  Calls that share one must not overlap on the
+ *       GPU.
+ * Over no rows (T == 0) dw and db are cleared.
+ */
+int sgemm_layer_norm_backward(int T, int D, int dtype,
+                              const void *x, int ldx, const void *w, int wdtype, const float *stats,
+                              const void *dn, int lddn, const void *dr, int lddr,
+                              void *dx, int lddx, void *dw, void *db,
+                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of sgemm_layer_norm_backward on the current device (0 if the device
+ * cannot be queried or T or D is 0): 8 D for each block, or for narrow rows each warp, that
+ * sums over rows, of which an SM holds 1 to 16. */
+size_t sgemm_layer_norm_backward_workspace_size(int T, int D);
+
+/*
  * Rows quantised to 8-bit integers: for each of M rows of K elements
  *     s = max|x| / 127,   q = rint(x * (127 / max|x|))   in [-127, 127]
  * with FP32 operations each rounded once, so q is defined to the bit.  A row
