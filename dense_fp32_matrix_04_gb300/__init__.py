@@ -409,5 +409,6 @@ def matmul(A, B, out=None, stream=None):
     return out
 
 
-from .layers import (block_norm, block_norm_backward, lay_out_fp4_scales, layer_norm, layer_norm_backward,  # noqa: E402
-                     linear_fp4, linear_i8, logprobs, logprobs_backward, matmul_fp4, matmul_i8, quantize_fp4, quantize_i8)
+from .layers import (beam_reorder, beam_step, block_norm, block_norm_backward, lay_out_fp4_scales,  # noqa: E402
+                     layer_norm, layer_norm_backward, linear_fp4, linear_i8, logprobs, logprobs_backward, matmul_fp4,
+                     matmul_i8, quantize_fp4, quantize_i8)

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libsgemm.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["sgemm_api.cu", "layers_api.cu", "i8_api.cu", "fp4_api.cu", "layer_norm_api.cu"]
+SOURCES = ["sgemm_api.cu", "layers_api.cu", "i8_api.cu", "fp4_api.cu", "layer_norm_api.cu", "beam_api.cu"]
 
 
 def _nvcc() -> str:

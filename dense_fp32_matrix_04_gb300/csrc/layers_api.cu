@@ -10,6 +10,7 @@
 #include "block_norm.cuh"
 #include "host.h"
 #include "logprobs.cuh"
+#include "logprobs_host.h"
 #include "row_host.h"
 
 namespace {
@@ -160,6 +161,18 @@ bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, cons
 
 }  // namespace
 
+int sgemm_host::logprobs(const LogprobArgs &a, int dtype, const Device &dev, cudaStream_t stream) {
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return a.mask ? logprobs_by_length<DT, true>(a, dev, stream) : logprobs_by_length<DT, false>(a, dev, stream);
+    });
+}
+
+bool sgemm_host::logprobs_shape_ok(int T, int V, int dtype, const void *z, int ldz, float scale, const int32_t *mask, int ldm,
+                                   int mask_rows) {
+    return ::logprobs_shape_ok(T, V, dtype, Rows{z, ldz}, scale, mask, ldm, mask_rows);
+}
+
 extern "C" {
 
 int sgemm_block_norm(int T, int D, int dtype, const void *x, int ldx, const void *y, int ldy, const void *w_pre,
@@ -286,11 +299,8 @@ int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float s
     Device dev;
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     const LogprobArgs a{T, V, logits, ldz, scale, mask, mask_rows > 1 ? ldm : 0, target, logprob, entropy, lse, top,
-                        top_logprob, top_id};
-    return by_dtype(dtype, [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        return mask ? logprobs_by_length<DT, true>(a, dev, stream) : logprobs_by_length<DT, false>(a, dev, stream);
-    });
+                        top_logprob, top_id, nullptr, nullptr, nullptr};
+    return sgemm_host::logprobs(a, dtype, dev, stream);
 }
 
 int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz, float scale, const int32_t *mask,

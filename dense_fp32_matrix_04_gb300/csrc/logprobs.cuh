@@ -55,7 +55,18 @@ struct LogprobArgs {
     int top;
     float *top_logprob;
     int32_t *top_id;
+    // For beams (beam.cuh): rows that take no part are passed over, top_logprob receives the
+    // logits themselves, and `reference` each row's largest logit m and its sum s.  Null otherwise.
+    const float *score;
+    const uint8_t *finished;
+    float2 *reference;
 };
+
+// Whether a beam of this score goes on over the vocabulary: a score that is not finite is that of a
+// beam that does not exist.
+__device__ __forceinline__ bool row_takes_part(float score, const uint8_t *finished) {
+    return fabsf(score) < INFINITY && !(finished && *finished);
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
@@ -311,12 +322,16 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         r.p1 = (int)((int64_t)r.pieces * (part + 1) >> log_parts);
         return r;
     };
+    auto passed_over = [&](int64_t t) {
+        return a.score && !row_takes_part(a.score[t], a.finished ? a.finished + t : nullptr);
+    };
     // the chunk that is copied next: of row `ahead_t`, from piece `ahead_p` on
     int64_t ahead_t = blockIdx.y;
     Row ahead;
     int ahead_p = 0;
     auto next_row = [&](int64_t t) {
         for (ahead_t = t; ahead_t < a.T; ahead_t += gridDim.y) {
+            if (passed_over(ahead_t)) continue;
             ahead = row_of(ahead_t);
             ahead_p = ahead.p0;
             if (ahead.p0 < ahead.p1) break;
@@ -348,6 +363,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
     int slot = 0;
 
     for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
+        if (passed_over(t)) continue;
         const Row row = row_of(t);
         const type *z = row.z;
         const int32_t *mask = row.mask;
@@ -542,6 +558,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             const float off = SoftmaxState::usual(all.M) ? -fmaf(all.m, c, -all.M) : 0.f;
             const float log_s = logf(all.s), log_sum = fmaf(kLn2, off, log_s);
             if (lane == 0) {
+                if (a.reference) a.reference[t] = make_float2(all.m, all.s);
                 if (a.lse) a.lse[t] = none ? -INFINITY : fmaf(all.m, a.scale, log_sum);
                 if (a.entropy) a.entropy[t] = none ? 0.f : log_s - kLn2 * (all.s1 / all.s);
                 if (a.logprob) {
@@ -561,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
                     const Candidate e = block_list[lane];
                     const bool bad = all.s != all.s;
                     const bool has = e.v > -INFINITY && !bad;
-                    a.top_logprob[t * a.top + lane] = bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_sum) : -INFINITY;
+                    a.top_logprob[t * a.top + lane] = a.reference ? e.v : bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_sum) : -INFINITY;
                     a.top_id[t * a.top + lane] = has ? e.id : -1;
                 }
             }

@@ -18,7 +18,7 @@ import ctypes
 import functools
 import inspect
 
-_I, _F, _P, _S = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_I, _L, _F, _P, _S = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
 SIGNATURES = {
     "sgemm_block_norm": (_I, [_I, _I, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I, _F, _F, _P, _I, _P, _I, _P, _I, _P,
@@ -41,6 +41,9 @@ SIGNATURES = {
     "sgemm_linear_fp4": (_I, [_I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
     "sgemm_linear_fp4_workspace_size": (_S, [_I, _I, _I]),
     "sgemm_logprobs": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
+    "sgemm_beam_step": (_I, [_I, _I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _S, _P]),
+    "sgemm_beam_step_workspace_size": (_S, [_I, _I, _I]),
+    "sgemm_beam_reorder": (_I, [_I, _I, _I, _L, _L, _P, _L, _L, _P, _P, _L, _L, _P]),
     "sgemm_logprobs_backward": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _P, _P, _I, _P]),
 }
 
@@ -670,4 +673,117 @@ def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, s
                                           _on(dev, stream))
     if status:
         _check(status, "sgemm_logprobs_backward")
+    return out
+
+
+def _beams(t, name, dtypes, index, shape=None):
+    """Pointer of a dense 2-D CUDA tensor with an entry for each beam."""
+    on = t.get_device()
+    if t.dtype not in dtypes or on < 0 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if on != index:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be dense")
+    return t.data_ptr()
+
+
+@_foreign
+def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=0, stream=None, *, keep=None):
+    """The best continuations of B groups of W beams: ``(score, parent, token)``, each B x top,
+    best first, from ``logits`` ((B W) x V; row b W + w is beam w of group b) and the beams' scores
+    so far (B x W, float32; -infinity for a beam that does not exist).
+
+    A continuation's score is the beam's plus the log probability of its column in
+    ``softmax(scale * logits)`` over the columns that ``mask`` allows (as in ``logprobs``).  Equal ones go
+    by the lower beam, then the lower column.  ``top`` is W unless said otherwise.  ``finished`` (B x W,
+    bool or uint8): such a beam goes on as it is, with column ``end``.  Where there are fewer than
+    ``top`` continuations the rest have score -infinity, parent -1 and token -1.
+    Has no gradient, and autograd does not see it."""
+    dt, dev, (T, V), pz, ldz = _first(logits, "logits")
+    ps = _beams(score, "score", (_torch.float32,), dev)
+    B, W = score.shape
+    if B * W != T:
+        raise ValueError(f"score is ({B}, {W}), logits has {T} rows")
+    if top is None:
+        top = W
+    if not (1 <= top <= 32 and 1 <= W <= 32):
+        raise ValueError(f"{W} beams and the best {top}: they must be 1 .. 32")
+    pf = _beams(finished, "finished", (_torch.bool, _torch.uint8), dev, score.shape) if finished is not None else 0
+    if not 0 <= end <= _MOST:
+        raise ValueError(f"end is {end}: it must be a column")
+    pm, ldm, rows = _mask(mask, T, V, dev)
+    empty, where = _torch.empty, logits.device
+    got = (empty((B, top), dtype=_torch.float32, device=where), empty((B, top), dtype=_torch.int32, device=where),
+           empty((B, top), dtype=_torch.int32, device=where))
+    size = _lib.sgemm_beam_step_workspace_size(B, W, top)
+    ws = empty((size,), dtype=_torch.uint8, device=where)
+    status = _lib.sgemm_beam_step(B, W, V, _codes[dt], pz, ldz, scale, pm, ldm, rows, ps, pf, end, top, got[0].data_ptr(),
+                                  got[1].data_ptr(), got[2].data_ptr(), ws.data_ptr(), size, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_beam_step")
+    if keep is not None:
+        keep += [*got, ws]
+    return got
+
+
+def _runs(a, b):
+    """(outer, inner, run of a, run of b): rows of a and b, tensors of the same shape behind the
+    first dimension, as `outer` runs of `inner` elements, which are runs apart in each."""
+    dims = []  # (size, stride in a, stride in b), the first ones outermost, merged where both follow on
+    for n, s, t in zip(a.shape[1:], a.stride()[1:], b.stride()[1:]):
+        if n == 1:
+            continue
+        if dims and dims[-1][1] == n * s and dims[-1][2] == n * t:
+            n *= dims.pop()[0]
+        dims.append((n, s, t))
+    if not dims or dims[-1][1:] != (1, 1):
+        dims.append((1, 1, 1))
+    if len(dims) > 2:
+        raise ValueError("rows of states must be one dense run, or runs at one distance from each other")
+    outer, s, t = dims[0] if len(dims) == 2 else (1, 0, 0)
+    return outer, dims[-1][0], s, t
+
+
+@_foreign
+def beam_reorder(state, parent, out=None, stream=None, *, keep=None):
+    """Rows of ``state`` ((B W) x ..., of any type) as the beams of a step were chosen: row
+    b top + k of the result is row b W + parent[b, k] of the state, for ``parent`` (B x top, int32) as
+    ``beam_step`` returns it.  Rows whose parent is no beam are left as they are.
+
+    ``out`` receives the rows; it may be the state itself (top = W), which is then reordered
+    in place, where rows that stay cost nothing.  What belongs to a row may be one dense run or runs at
+    one distance, as in ``cache[:, :, :length]``.  Has no gradient, and autograd does not see it."""
+    if _torch is None:
+        _start()
+    dev = state.get_device()
+    if dev < 0 or state.dim() < 1:
+        raise TypeError("state must be a CUDA tensor with a row for each beam")
+    pp = _beams(parent, "parent", (_torch.int32,), dev)
+    B, top = parent.shape
+    T = state.shape[0]
+    if (T % B if B else T):
+        raise ValueError(f"state has {T} rows, which are not {B} groups of as many beams")
+    W = T // B if B else 1
+    if B and not (1 <= W <= 32 and 1 <= top <= 32):
+        raise ValueError(f"{W} beams and {top} parents: they must be 1 .. 32")
+    shape = (B * top, *state.shape[1:])
+    if out is None:
+        out = _torch.empty(shape, dtype=state.dtype, device=state.device)
+        if keep is not None:
+            keep.append(out)
+    elif out.dtype is not state.dtype or out.get_device() != dev:
+        raise TypeError(f"out must be a {state.dtype} tensor on {state.device}")
+    elif out.shape != shape:
+        raise ValueError(f"out is {tuple(out.shape)}, not {shape}")
+    if not B or not out.numel():
+        return out
+    outer, inner, run_in, run_out = _runs(state, out)
+    size = state.element_size()
+    status = _lib.sgemm_beam_reorder(B, W, top, outer, inner * size, state.data_ptr(), state.stride(0) * size, run_in * size, pp,
+                                     out.data_ptr(), out.stride(0) * size, run_out * size, _on(dev, stream))
+    if status:
+        _check(status, "sgemm_beam_reorder")
     return out

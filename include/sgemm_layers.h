@@ -316,6 +316,51 @@ int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int
 
 size_t sgemm_linear_fp4_workspace_size(int M, int K, int block);
 
+/*
+ * A step of beam search.  B groups of W beams each have logits over V columns (row
+ * b W + w is beam w of group b) and a score, their log probability so far.  Of each
+ * group's W V continuations, whose score is
+ *     score[b][w] + log softmax(scale * logits)[column]        (over the columns that the
+ *                                                               mask allows)
+ * the `top` best are written, best first: their scores, their beams (0 .. W - 1) and their
+ * columns.  Equal scores go by the lower beam, then the lower column.  The scores are
+ * compared in 64 bits (from FP32 sums) and rounded once when they are written.
+ *   logits, scale, mask: as in sgemm_logprobs.  score: B x W, dense.
+ *   finished: B x W bytes or NULL.  A beam whose byte is not 0 has one continuation, the
+ *       column `end` (>= 0) with the score it has; its logits are not read.
+ *   A beam whose score is not finite takes no part (a beam that does not exist has
+ *   -infinity), nor does one whose allowed logits hold a NaN or +infinity, or are all
+ *   -infinity.  Columns that cannot occur are no continuations.  Where fewer than `top`
+ *   are left, the rest have score -infinity, beam -1 and column -1.
+ *   out_score (FP32), parent, token (32-bit): B x top, dense.
+ *   workspace: sgemm_beam_step_workspace_size(B, W, top) bytes, 16-byte aligned; contents on
+ *       entry do not matter.  Calls that share one must not overlap on the GPU.
+ * W, top: 1 .. 32.  B W <= 2^30.
+ */
+int sgemm_beam_step(int B, int W, int V, int dtype, const void *logits, int ldz, float scale,
+                    const int32_t *mask, int ldm, int mask_rows,
+                    const float *score, const unsigned char *finished, int end,
+                    int top, float *out_score, int32_t *parent, int32_t *token,
+                    void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+size_t sgemm_beam_step_workspace_size(int B, int W, int top);
+
+/*
+ * Rows of states reordered as beams were chosen: row b top + k of out becomes row
+ * b W + parent[b][k] of in, for B groups.  A row is `outer` runs of `inner` bytes, in_outer
+ * (out_outer) bytes apart; rows are in_row (out_row) bytes apart.  A row whose parent is
+ * not 0 .. W - 1 is left as it is.
+ *   out may be in (same pointer and strides, top == W): each row then becomes what its
+ *       parent was before the call, and rows that are their own parent are neither read
+ *       nor written for themselves.
+ *   Rows of out must not overlap each other.  All sizes and strides are bytes, at most 2^44
+ *   in all; any alignment is accepted (16 bytes at a time where all allow it).
+ */
+int sgemm_beam_reorder(int B, int W, int top, int64_t outer, int64_t inner,
+                       const void *in, int64_t in_row, int64_t in_outer,
+                       const int32_t *parent, void *out, int64_t out_row, int64_t out_outer,
+                       cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
