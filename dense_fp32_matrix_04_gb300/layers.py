@@ -52,7 +52,6 @@ SIGNATURES = {
 # sees, so the checks below ask a tensor as little as they can.
 _torch = _lib = None
 _codes = {}
-_blocks = {}
 _raw_stream = _current_device = None
 
 
@@ -63,7 +62,6 @@ def _start():
     from . import load
     _lib = load()
     _codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    _blocks.update({torch.float8_e4m3fn: 16, torch.float8_e8m0fnu: 32})
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _torch = torch
 
@@ -292,79 +290,6 @@ def block_norm_backward(x, y, w_pre, rstd, dn, dr=None, w_post=None, gate=None, 
 
 
 @_foreign
-def layer_norm(x, w, bias=None, add=None, eps=1e-5, out=None, stream=None, *, keep=None):
-    """The norm of the rows of x (T x D) about their mean, after the sum with ``add``:
-
-        r = x + add                                  (rounded to x's type; r is x without ``add``)
-        n = (r - mean) * rstd * w + bias,            rstd = rsqrt(mean((r - mean)^2) + eps)
-
-    Returns ``(r, n, stats)``, of which ``stats`` (2 x T: mean, rstd) and r are for the backward
-    pass.  ``out`` receives r; it may be x or add.  Rows of no columns (D = 0) have NaN for their
-    statistics.  Autograd does not see the call: its gradient is ``layer_norm_backward``.
-    """
-    dt, dev, shape, px, ldx = _first(x, "x")
-    f32, empty, where = _torch.float32, _torch.empty, x.device
-    T, D = shape
-    wt = w.dtype
-    pw = _vector(w, "w", D, (f32, dt), dev)
-    pb = _vector(bias, "bias", D, (wt,), dev) if bias is not None else 0
-    stats, n = empty((2, T), dtype=f32, device=where), empty(shape, dtype=dt, device=where)
-    made = [n, stats]
-    if add is None:
-        if out is not None:
-            raise ValueError("out is for the sum with add, which is not given")
-        r, pa, lda, pr, ldr = x, 0, D or 1, 0, D or 1
-    else:
-        pa, lda = _matrix(add, "add", dt, dev, shape)
-        if out is None:
-            r = empty(shape, dtype=dt, device=where)
-            made.append(r)
-            pr, ldr = r.data_ptr(), D or 1
-        else:
-            r = out
-            pr, ldr = _matrix(out, "out", dt, dev, shape)
-    status = _lib.sgemm_layer_norm(T, D, _codes[dt], px, ldx, pa, lda, pw, pb, _codes[wt], eps, pr, ldr, n.data_ptr(), D or 1,
-                                   stats.data_ptr(), _on(dev, stream))
-    if status:
-        _check(status, "sgemm_layer_norm")
-    if not D and T:
-        with _stream_of(dev, stream):
-            stats.fill_(float("nan"))
-    if keep is not None:
-        keep += made
-    return r, n, stats
-
-
-@_foreign
-def layer_norm_backward(x, w, stats, dn, dr=None, bias=True, stream=None, *, keep=None):
-    """Gradients ``(dx, dw, db)`` of ``layer_norm`` from those of its n and r (``dr`` None: zero);
-    ``x`` is the r that it returned, and ``dx`` the gradient of x and of ``add``.  ``bias`` False: db
-    is not computed, and None."""
-    dt, dev, shape, px, ldx = _first(x, "x")
-    f32, empty, where = _torch.float32, _torch.empty, x.device
-    T, D = shape
-    pn, ldn = _matrix(dn, "dn", dt, dev, shape)
-    pr, ldr = _matrix(dr, "dr", dt, dev, shape) if dr is not None else (0, D or 1)
-    wt = w.dtype
-    pw = _vector(w, "w", D, (f32, dt), dev)
-    if stats.dtype is not f32 or stats.shape != (2, T) or not stats.is_contiguous() or stats.get_device() != dev:
-        raise ValueError("stats must be the (2, T) float32 tensor that layer_norm returned")
-    dx = empty(shape, dtype=dt, device=where)
-    dw = empty((D,), dtype=wt, device=where)
-    db = empty((D,), dtype=wt, device=where) if bias else None
-    need = _lib.sgemm_layer_norm_backward_workspace_size(T, D)
-    ws = empty((need,), dtype=_torch.uint8, device=where)
-    status = _lib.sgemm_layer_norm_backward(T, D, _codes[dt], px, ldx, pw, _codes[wt], stats.data_ptr(), pn, ldn, pr, ldr,
-                                            dx.data_ptr(), D or 1, dw.data_ptr(), db.data_ptr() if bias else 0,
-                                            ws.data_ptr(), need, _on(dev, stream))
-    if status:
-        _check(status, "sgemm_layer_norm_backward")
-    if keep is not None:
-        keep += [t for t in (dx, dw, db, ws) if t is not None]
-    return dx, dw, db
-
-
-@_foreign
 def quantize_i8(x, stream=None, *, keep=None):
     """``(q, scale)``: the rows of x (M x K) as 8-bit integers, scale = max|row| / 127
     and q = rint(row * (127 / max|row|)).  For activations a scale per token, for
@@ -455,155 +380,6 @@ def linear_i8(x, w, w_scale, bias=None, out_dtype=None, out=None, workspace=None
                    out, workspace, stream, keep, _lib.sgemm_linear_i8_workspace_size)
 
 
-def _fp4_tiles(rows, K, block):
-    """Shape of the tiles that hold the block scales of rows x K columns."""
-    return ((rows + 127) // 128, ((K + block - 1) // block + 3) // 4 * 512)
-
-
-def _block_scales(t, name, rows, K, index):
-    """(pointer, block) of the tiles of block scales of rows x K columns."""
-    block = _blocks.get(t.dtype)
-    if block is None or t.get_device() < 0 or t.dim() != 2:
-        raise TypeError(f"{name} must be a 2-D CUDA tensor of float8_e4m3fn (blocks of 16) or float8_e8m0fnu (of 32)")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-    want = _fp4_tiles(rows, K, block)
-    if t.shape != want:
-        raise ValueError(f"{name} is {tuple(t.shape)}, not the {want} of tiles for {rows} rows of {K}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be dense")
-    return t.data_ptr(), block
-
-
-def _fp4_rows(t, name, index, shape=None, cols=None):
-    """(pointer, bytes between rows) of packed codes."""
-    p, ld = _matrix(t, name, _torch.uint8, index, shape, cols)
-    rows, n = t.shape
-    if rows > 1 and ld % 16:
-        raise ValueError(f"{name} has rows {ld} bytes apart: they must be a multiple of 16, as quantize_fp4 lays them out")
-    if p % 16:
-        raise ValueError(f"{name} must start on 16 bytes")
-    return p, (ld if rows > 1 else max((n + 15) // 16 * 16, 16))
-
-
-@_foreign
-def quantize_fp4(x, block=16, stream=None, *, keep=None):
-    """``(q, block_scale, scale)``: the rows of x (M x K) as 4-bit floating point, for
-    ``linear_fp4`` and ``matmul_fp4``.  With ``block`` 16, blocks of 16 columns have e4m3 scales
-    and rows an FP32 scale; with 32, blocks of 32 have powers of two (e8m0) and ``scale`` is None.
-
-    ``q`` (M x ceil(K / 2), uint8) holds two codes a byte, the even column in the low half, on
-    rows a multiple of 16 bytes apart; ``block_scale`` is in tiles of 128 rows by 4 blocks (one row of
-    tiles a row of the tensor), with the format's type.  Has no gradient, and autograd does not
-    see it."""
-    dt, dev, (M, K), px, ldx = _first(x, "x")
-    if block not in (16, 32):
-        raise ValueError(f"block is {block}: it must be 16 or 32")
-    empty, where = _torch.empty, x.device
-    pitch = max((K + 31) // 32 * 16, 16)
-    whole = empty((M, pitch), dtype=_torch.uint8, device=where)
-    tiles = empty(_fp4_tiles(M, K, block), dtype=_torch.uint8, device=where)
-    scale = empty((M,), dtype=_torch.float32, device=where) if block == 16 else None
-    status = _lib.sgemm_quantize_fp4(M, K, _codes[dt], px, ldx, block, whole.data_ptr(), pitch, tiles.data_ptr(),
-                                     scale.data_ptr() if block == 16 else 0, _on(dev, stream))
-    if status:
-        _check(status, "sgemm_quantize_fp4")
-    if keep is not None:
-        keep += [whole, tiles] + ([scale] if block == 16 else [])
-    return whole[:, :(K + 1) // 2], tiles.view(_torch.float8_e4m3fn if block == 16 else _torch.float8_e8m0fnu), scale
-
-
-@_foreign
-def lay_out_fp4_scales(s, stream=None, *, keep=None):
-    """Block scales (rows x blocks, float8_e4m3fn of blocks of 16 or float8_e8m0fnu of blocks of
-    32) in the tiles that ``matmul_fp4`` and ``linear_fp4`` take, for weights quantised elsewhere."""
-    if _torch is None:
-        _start()
-    dt, dev, (rows, blocks), ps, lds = _first(s, "s", tuple(_blocks))
-    block = _blocks[dt]
-    shape = _fp4_tiles(rows, blocks * block, block)
-    if blocks * block > 1 << 30:
-        raise ValueError(f"s has {blocks} blocks of {block}: more than 2^30 columns")
-    tiles = _torch.empty(shape, dtype=_torch.uint8, device=s.device)
-    status = _lib.sgemm_fp4_lay_out_scales(rows, blocks * block, block, ps, lds, tiles.data_ptr(), _on(dev, stream))
-    if status:
-        _check(status, "sgemm_fp4_lay_out_scales")
-    if keep is not None:
-        keep.append(tiles)
-    return tiles.view(dt)
-
-
-def _output(out, out_dtype, M, N, index, where, keep):
-    """(tensor, pointer, leading dimension, type's code) of a product's output."""
-    if out is None:
-        if out_dtype not in _codes:
-            raise TypeError("out_dtype must be float32, bfloat16 or float16")
-        out = _torch.empty((M, N), dtype=out_dtype, device=where)
-        if keep is not None:
-            keep.append(out)
-        return out, out.data_ptr(), N or 1, _codes[out_dtype]
-    if out.dtype not in _codes:
-        raise TypeError("out must be float32, bfloat16 or float16")
-    return (out, *_matrix(out, "out", out.dtype, index, (M, N)), _codes[out.dtype])
-
-
-@_foreign
-def matmul_fp4(a, a_block, a_scale, w, w_block, w_scale, bias=None, out_dtype=None, out=None, stream=None, *, keep=None):
-    """The product of the matrices that 4-bit codes and their scales stand for, a (M x K) times
-    the transpose of w (N x K), plus ``bias``, in ``out_dtype`` (float32 unless said otherwise).
-    Codes and scales are as ``quantize_fp4`` returns them, of the same block; ``a_scale`` and
-    ``w_scale`` may be None (1).  For inference: autograd does not see it."""
-    if _torch is None:
-        _start()
-    _, dev, (M, n), _, _ = _first(a, "a", (_torch.uint8,))
-    pa, lda = _fp4_rows(a, "a", dev)
-    N, K = w.shape[0], 2 * n  # the half behind an odd number of columns is 0
-    pw, ldw = _fp4_rows(w, "w", dev, None, n)
-    pab, block = _block_scales(a_block, "a_block", M, K, dev)
-    pwb, w_is = _block_scales(w_block, "w_block", N, K, dev)
-    if w_is != block:
-        raise ValueError(f"a has blocks of {block}, w of {w_is}")
-    f32 = (_torch.float32,)
-    ps = _vector(a_scale, "a_scale", M, f32, dev) if a_scale is not None else 0
-    pt = _vector(w_scale, "w_scale", N, f32, dev) if w_scale is not None else 0
-    pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
-    out, po, ldo, code = _output(out, out_dtype or _torch.float32, M, N, dev, a.device, keep)
-    status = _lib.sgemm_fp4(M, N, K, block, pa, lda, pab, ps, pw, ldw, pwb, pt, pb, po, ldo, code, _on(dev, stream))
-    if status:
-        _check(status, "sgemm_fp4")
-    return out
-
-
-@_foreign
-def linear_fp4(x, w, w_block, w_scale=None, bias=None, out_dtype=None, out=None, workspace=None, stream=None, *, keep=None):
-    """``matmul_fp4`` on the rows of x (M x K, float32, bfloat16 or float16), which are quantised
-    first as ``quantize_fp4`` does it, in the blocks of ``w_block``; ``out_dtype`` is x's unless said
-    otherwise.  ``workspace``: a dense tensor of any type with the bytes that
-    ``sgemm_linear_fp4_workspace_size`` gives; allocated if None.  For inference: autograd does
-    not see the call."""
-    dt, dev, (M, K), px, ldx = _first(x, "x")
-    pw, ldw = _fp4_rows(w, "w", dev, None, (K + 1) // 2)
-    N = w.shape[0]
-    pwb, block = _block_scales(w_block, "w_block", N, K, dev)
-    f32 = (_torch.float32,)
-    pt = _vector(w_scale, "w_scale", N, f32, dev) if w_scale is not None else 0
-    pb = _vector(bias, "bias", N, f32, dev) if bias is not None else 0
-    out, po, ldo, code = _output(out, out_dtype or dt, M, N, dev, x.device, keep)
-    pws, size = _workspace(workspace, dev)
-    if workspace is None:
-        size = _lib.sgemm_linear_fp4_workspace_size(M, K, block)
-        if size:
-            workspace = _torch.empty((size,), dtype=_torch.uint8, device=x.device)
-            pws = workspace.data_ptr()
-            if keep is not None:
-                keep.append(workspace)
-    status = _lib.sgemm_linear_fp4(M, N, K, _codes[dt], px, ldx, block, pw, ldw, pwb, pt, pb, po, ldo, code, pws, size,
-                                   _on(dev, stream))
-    if status:
-        _check(status, "sgemm_linear_fp4")
-    return out
-
-
 def _mask(mask, T, V, index):
     """(pointer, words between rows, rows) of a mask of ceil(V / 32) words a row."""
     if mask is None:
@@ -676,22 +452,103 @@ def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, s
     return out
 
 
-def _beams(t, name, dtypes, index, shape=None):
-    """Pointer of a dense 2-D CUDA tensor with an entry for each beam."""
-    on = t.get_device()
-    if t.dtype not in dtypes or on < 0 or t.dim() != 2:
-        raise TypeError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    if on != index:
-        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be dense")
-    return t.data_ptr()
+
+# ---------------------------------------------------------------- through the native binding
+#
+# The operators below check and allocate in C++ (csrc/native.cpp): a call with three outputs
+# costs the host a quarter of what the ones above do.
+
+_native = None
 
 
-@_foreign
-def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=0, stream=None, *, keep=None):
+def _load_native():
+    global _native
+    if _torch is None:
+        _start()
+    try:
+        from . import _native as module
+    except ImportError as e:
+        raise RuntimeError(f"the native binding is not built ({e}): run python -m dense_fp32_matrix_04_gb300.build") from e
+    _native = module
+    return module
+
+
+def _elsewhere(fn, stream, first, *args):
+    """A call on a stream that is given: where it is not torch's own, that one is ordered
+    behind torch's, which the memory that the call allocates may still be in use on."""
+    index = first.get_device() if isinstance(first, _torch.Tensor) else -1
+    if index < 0:
+        return fn(first, *args, None)  # refuses it
+    with _torch.cuda.device(index):
+        handle = _on(index, stream)
+        if handle != _raw_stream(index):
+            other = _torch.cuda.ExternalStream(handle, device=index) if isinstance(stream, int) else stream
+            other.wait_stream(_torch.cuda.current_stream(index))
+        return fn(first, *args, handle)
+
+
+def layer_norm(x, w, bias=None, add=None, eps=1e-5, out=None, stream=None):
+    """The norm of the rows of x (T x D) about their mean, after the sum with ``add``:
+
+        r = x + add                                  (rounded to x's type; r is x without ``add``)
+        n = (r - mean) * rstd * w + bias,            rstd = rsqrt(mean((r - mean)^2) + eps)
+
+    Returns ``(r, n, stats)``, of which ``stats`` (2 x T: mean, rstd) and r are for the backward
+    pass.  ``out`` receives r; it may be x or add.  Rows of no columns (D = 0) have NaN for their
+    statistics.  Autograd does not see the call: its gradient is ``layer_norm_backward``.
+    """
+    fn = (_native or _load_native()).layer_norm
+    return fn(x, w, bias, add, eps, out, None) if stream is None else _elsewhere(fn, stream, x, w, bias, add, eps, out)
+
+
+def layer_norm_backward(x, w, stats, dn, dr=None, bias=True, stream=None):
+    """Gradients ``(dx, dw, db)`` of ``layer_norm`` from those of its n and r (``dr`` None: zero);
+    ``x`` is the r that it returned, and ``dx`` the gradient of x and of ``add``.  ``bias`` False: db
+    is not computed, and None."""
+    fn = (_native or _load_native()).layer_norm_backward
+    return fn(x, w, stats, dn, dr, bias, None) if stream is None else _elsewhere(fn, stream, x, w, stats, dn, dr, bias)
+
+
+def quantize_fp4(x, block=16, stream=None):
+    """``(q, block_scale, scale)``: the rows of x (M x K) as 4-bit floating point, for
+    ``linear_fp4`` and ``matmul_fp4``.  With ``block`` 16, blocks of 16 columns have e4m3 scales
+    and rows an FP32 scale; with 32, blocks of 32 have powers of two (e8m0) and ``scale`` is None.
+
+    ``q`` (M x ceil(K / 2), uint8) holds two codes a byte, the even column in the low half, on
+    rows a multiple of 16 bytes apart; ``block_scale`` is in tiles of 128 rows by 4 blocks (one row of
+    tiles a row of the tensor), with the format's type.  Has no gradient, and autograd does not
+    see it."""
+    fn = (_native or _load_native()).quantize_fp4
+    return fn(x, block, None) if stream is None else _elsewhere(fn, stream, x, block)
+
+
+def lay_out_fp4_scales(s, stream=None):
+    """Block scales (rows x blocks, float8_e4m3fn of blocks of 16 or float8_e8m0fnu of blocks of
+    32) in the tiles that ``matmul_fp4`` and ``linear_fp4`` take, for weights quantised elsewhere."""
+    fn = (_native or _load_native()).lay_out_fp4_scales
+    return fn(s, None) if stream is None else _elsewhere(fn, stream, s)
+
+
+def matmul_fp4(a, a_block, a_scale, w, w_block, w_scale, bias=None, out_dtype=None, out=None, stream=None):
+    """The product of the matrices that 4-bit codes and their scales stand for, a (M x K) times
+    the transpose of w (N x K), plus ``bias``, in ``out_dtype`` (float32 unless said otherwise).
+    Codes and scales are as ``quantize_fp4`` returns them, of the same block; ``a_scale`` and
+    ``w_scale`` may be None (1).  For inference: autograd does not see it."""
+    fn = (_native or _load_native()).matmul_fp4
+    return fn(a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out, None) if stream is None else _elsewhere(fn, stream, a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out)
+
+
+def linear_fp4(x, w, w_block, w_scale=None, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """``matmul_fp4`` on the rows of x (M x K, float32, bfloat16 or float16), which are quantised
+    first as ``quantize_fp4`` does it, in the blocks of ``w_block``; ``out_dtype`` is x's unless said
+    otherwise.  ``workspace``: a dense tensor of any type with the bytes that
+    ``sgemm_linear_fp4_workspace_size`` gives; allocated if None.  For inference: autograd does
+    not see the call."""
+    fn = (_native or _load_native()).linear_fp4
+    return fn(x, w, w_block, w_scale, bias, out_dtype, out, workspace, None) if stream is None else _elsewhere(fn, stream, x, w, w_block, w_scale, bias, out_dtype, out, workspace)
+
+
+def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=0, stream=None):
     """The best continuations of B groups of W beams: ``(score, parent, token)``, each B x top,
     best first, from ``logits`` ((B W) x V; row b W + w is beam w of group b) and the beams' scores
     so far (B x W, float32; -infinity for a beam that does not exist).
@@ -702,53 +559,11 @@ def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=
     bool or uint8): such a beam goes on as it is, with column ``end``.  Where there are fewer than
     ``top`` continuations the rest have score -infinity, parent -1 and token -1.
     Has no gradient, and autograd does not see it."""
-    dt, dev, (T, V), pz, ldz = _first(logits, "logits")
-    ps = _beams(score, "score", (_torch.float32,), dev)
-    B, W = score.shape
-    if B * W != T:
-        raise ValueError(f"score is ({B}, {W}), logits has {T} rows")
-    if top is None:
-        top = W
-    if not (1 <= top <= 32 and 1 <= W <= 32):
-        raise ValueError(f"{W} beams and the best {top}: they must be 1 .. 32")
-    pf = _beams(finished, "finished", (_torch.bool, _torch.uint8), dev, score.shape) if finished is not None else 0
-    if not 0 <= end <= _MOST:
-        raise ValueError(f"end is {end}: it must be a column")
-    pm, ldm, rows = _mask(mask, T, V, dev)
-    empty, where = _torch.empty, logits.device
-    got = (empty((B, top), dtype=_torch.float32, device=where), empty((B, top), dtype=_torch.int32, device=where),
-           empty((B, top), dtype=_torch.int32, device=where))
-    size = _lib.sgemm_beam_step_workspace_size(B, W, top)
-    ws = empty((size,), dtype=_torch.uint8, device=where)
-    status = _lib.sgemm_beam_step(B, W, V, _codes[dt], pz, ldz, scale, pm, ldm, rows, ps, pf, end, top, got[0].data_ptr(),
-                                  got[1].data_ptr(), got[2].data_ptr(), ws.data_ptr(), size, _on(dev, stream))
-    if status:
-        _check(status, "sgemm_beam_step")
-    if keep is not None:
-        keep += [*got, ws]
-    return got
+    fn = (_native or _load_native()).beam_step
+    return fn(logits, score, top, scale, mask, finished, end, None) if stream is None else _elsewhere(fn, stream, logits, score, top, scale, mask, finished, end)
 
 
-def _runs(a, b):
-    """(outer, inner, run of a, run of b): rows of a and b, tensors of the same shape behind the
-    first dimension, as `outer` runs of `inner` elements, which are runs apart in each."""
-    dims = []  # (size, stride in a, stride in b), the first ones outermost, merged where both follow on
-    for n, s, t in zip(a.shape[1:], a.stride()[1:], b.stride()[1:]):
-        if n == 1:
-            continue
-        if dims and dims[-1][1] == n * s and dims[-1][2] == n * t:
-            n *= dims.pop()[0]
-        dims.append((n, s, t))
-    if not dims or dims[-1][1:] != (1, 1):
-        dims.append((1, 1, 1))
-    if len(dims) > 2:
-        raise ValueError("rows of states must be one dense run, or runs at one distance from each other")
-    outer, s, t = dims[0] if len(dims) == 2 else (1, 0, 0)
-    return outer, dims[-1][0], s, t
-
-
-@_foreign
-def beam_reorder(state, parent, out=None, stream=None, *, keep=None):
+def beam_reorder(state, parent, out=None, stream=None):
     """Rows of ``state`` ((B W) x ..., of any type) as the beams of a step were chosen: row
     b top + k of the result is row b W + parent[b, k] of the state, for ``parent`` (B x top, int32) as
     ``beam_step`` returns it.  Rows whose parent is no beam are left as they are.
@@ -756,34 +571,5 @@ def beam_reorder(state, parent, out=None, stream=None, *, keep=None):
     ``out`` receives the rows; it may be the state itself (top = W), which is then reordered
     in place, where rows that stay cost nothing.  What belongs to a row may be one dense run or runs at
     one distance, as in ``cache[:, :, :length]``.  Has no gradient, and autograd does not see it."""
-    if _torch is None:
-        _start()
-    dev = state.get_device()
-    if dev < 0 or state.dim() < 1:
-        raise TypeError("state must be a CUDA tensor with a row for each beam")
-    pp = _beams(parent, "parent", (_torch.int32,), dev)
-    B, top = parent.shape
-    T = state.shape[0]
-    if (T % B if B else T):
-        raise ValueError(f"state has {T} rows, which are not {B} groups of as many beams")
-    W = T // B if B else 1
-    if B and not (1 <= W <= 32 and 1 <= top <= 32):
-        raise ValueError(f"{W} beams and {top} parents: they must be 1 .. 32")
-    shape = (B * top, *state.shape[1:])
-    if out is None:
-        out = _torch.empty(shape, dtype=state.dtype, device=state.device)
-        if keep is not None:
-            keep.append(out)
-    elif out.dtype is not state.dtype or out.get_device() != dev:
-        raise TypeError(f"out must be a {state.dtype} tensor on {state.device}")
-    elif out.shape != shape:
-        raise ValueError(f"out is {tuple(out.shape)}, not {shape}")
-    if not B or not out.numel():
-        return out
-    outer, inner, run_in, run_out = _runs(state, out)
-    size = state.element_size()
-    status = _lib.sgemm_beam_reorder(B, W, top, outer, inner * size, state.data_ptr(), state.stride(0) * size, run_in * size, pp,
-                                     out.data_ptr(), out.stride(0) * size, run_out * size, _on(dev, stream))
-    if status:
-        _check(status, "sgemm_beam_reorder")
-    return out
+    fn = (_native or _load_native()).beam_reorder
+    return fn(state, parent, out, None) if stream is None else _elsewhere(fn, stream, state, parent, out)
