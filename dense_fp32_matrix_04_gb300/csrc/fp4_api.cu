@@ -7,7 +7,9 @@
 #include <cstdint>
 
 #include "fp4_mma.cuh"
+#include "fp4_pair.cuh"
 #include "fp4_quantize.cuh"
+#include "fp4_rows.cuh"
 #include "host.h"
 
 namespace {
@@ -73,26 +75,28 @@ int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx,
 
 // ---------------------------------------------------------------- the product
 
-// Tokens a tile, and the blocks that share one: the smallest estimate, in cycles, of
-// rounds over the SMs times the length of one.
+// How a product is shared out: tiles of 16 to 128 tokens on one SM, for which the
+// blocks of a cluster can split K, or of 256 on a pair.  The smallest estimate, in
+// cycles, of rounds over the SMs times the length of one, from steps measured on
+// GB300 (a step is 256 columns).
 struct Fp4Plan {
-    int tok = 256, splits = 1;
+    int tok = 16, splits = 1;  // tok 256: a pair
     Fp4Plan(int M, int N, int K, int sms) {
         static constexpr struct {
             int tok;
-            double step;
-        } kSteps[] = {{16, 420}, {32, 430}, {64, 450}, {128, 500}, {192, 560}, {256, 700}};
+            double step, drain;
+        } kSteps[] = {{16, 350, 300}, {32, 360, 400}, {64, 420, 700}, {128, 480, 1200}, {256, 620, 2400}};
         double best = 1e300;
         const int steps = (K + 255) / 256;
         for (const auto &c : kSteps) {
             if (c.tok < 64 && M > c.tok) continue;  // see Fp4Tile
-            const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + 127) / 128);
-            for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-                if (s > 1 && tiles * s > 2 * sms) break;
-                const int64_t rounds = (tiles * s + sms - 1) / sms;
-                const double drain = c.tok <= 192 ? 600 : 14. * c.tok;
-                double t = (double)rounds * (((steps + s - 1) / s) * c.step + drain) + 3000 + 14. * c.tok;
-                if (s > 1) t += 2000 + 20. * c.tok;
+            const bool pair = c.tok == 256;
+            const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + (pair ? 255 : 127)) / (pair ? 256 : 128));
+            const int slots = pair ? sms / 2 : sms;
+            for (int s = 1; s == 1 || (!pair && s <= 8 && s <= steps && tiles * s <= sms - 8); s *= 2) {
+                const int64_t rounds = (tiles * s + slots - 1) / slots;
+                double t = (double)rounds * (((steps + s - 1) / s) * c.step) + (double)(rounds - 1) * (pair ? 1000 : 200) + c.drain;
+                if (s > 1) t += 1500 + 12. * c.tok;
                 if (t < best) best = t, tok = c.tok, splits = s;
             }
             if (M <= c.tok) break;
@@ -121,6 +125,54 @@ int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, const Device 
                         sgemm_host::test_flags());
 }
 
+template <int BLOCK>
+int launch_pair(const Fp4Args &p, const Fp4Operands &o, const Device &dev, cudaStream_t stream) {
+    using T = Fp4PairTile<256, BLOCK>;
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = fp4_pair_kernel<256, BLOCK>;
+    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, T::THREADS, T::SMEM_BYTES)) return SGEMM_ERR_LAUNCH;
+    const int64_t words = (int64_t)fp4_tiles(p.K, BLOCK) * (kFp4TileBytes / 8);
+    CUtensorMap tw, tx, tws, txs;
+    if (!sgemm_host::encode_i8(&tw, o.B, p.N, code_bytes(p.K), o.ldb, T::ROWS / 2, T::BYTES) ||
+        !sgemm_host::encode_i8(&tx, o.A, p.M, code_bytes(p.K), o.lda, T::TOK / 2, T::BYTES) ||
+        !sgemm_host::encode_words(&tws, p.b_tiles, (p.N + 127) / 128, words, 1, T::WS_BYTES / 8) ||
+        !sgemm_host::encode_words(&txs, p.a_tiles, (p.M + 127) / 128, words, 2, T::WS_BYTES / 8))
+        return SGEMM_ERR_LAUNCH;
+    const int64_t tiles = (int64_t)((p.M + T::TOK - 1) / T::TOK) * ((p.N + T::ROWS - 1) / T::ROWS);
+    return launch<true>(kernel, dim3((unsigned)(2 * std::min<int64_t>(tiles, dev.sms / 2))), dim3(T::THREADS), T::SMEM_BYTES, stream,
+                        2, tw, tx, tws, txs, p, dev.err_word, sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
+}
+
+// Up to four tokens whose codes fit shared memory go to the kernel that reads whole rows.
+bool takes_rows(int M, int K) {
+    return M <= kFp4RowsTokens && fp4_rows_smem(M == 3 ? 4 : M, K) <= kFp4RowsSmem;
+}
+
+template <int MT, int XT, int BLOCK>
+int launch_rows(const Fp4RowsArgs &a, const Device &dev, cudaStream_t stream) {
+    static std::atomic<int> regs[sgemm_host::kMaxDevices];
+    const auto kernel = fp4_rows_kernel<MT, XT, BLOCK>;
+    const int smem = (int)fp4_rows_smem(MT, a.p.K);
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, kFp4RowsThreads, smem);
+    if (!fit) return SGEMM_ERR_LAUNCH;
+    const int groups = (a.p.N + 127) / 128 * 16;
+    return launch(kernel, dim3((unsigned)std::min(groups, dev.sms * fit)), dim3(kFp4RowsThreads), (size_t)smem, stream, 1, a);
+}
+
+// xtype -1: the tokens are codes.
+int rows_product(const Fp4RowsArgs &a, int xtype, int block, const Device &dev, cudaStream_t stream) {
+    return by_block(block, [&](auto b) {
+        constexpr int BLOCK = decltype(b)::value;
+        auto by_tokens = [&](auto xt) {
+            constexpr int XT = decltype(xt)::value;
+            return a.p.M <= 1   ? launch_rows<1, XT, BLOCK>(a, dev, stream)
+                   : a.p.M <= 2 ? launch_rows<2, XT, BLOCK>(a, dev, stream)
+                                : launch_rows<4, XT, BLOCK>(a, dev, stream);
+        };
+        return xtype < 0 ? by_tokens(std::integral_constant<int, -1>{}) : by_dtype(xtype, by_tokens);
+    });
+}
+
 int product(const Fp4Args &p, const Fp4Operands &o, int block, const Device &dev, cudaStream_t stream) {
     const Fp4Plan plan(p.M, p.N, p.K, dev.sms);
     return by_block(block, [&](auto b) {
@@ -130,8 +182,7 @@ int product(const Fp4Args &p, const Fp4Operands &o, int block, const Device &dev
             case 32: return launch_mma<32, BLOCK>(p, o, plan.splits, dev, stream);
             case 64: return launch_mma<64, BLOCK>(p, o, plan.splits, dev, stream);
             case 128: return launch_mma<128, BLOCK>(p, o, plan.splits, dev, stream);
-            case 192: return launch_mma<192, BLOCK>(p, o, plan.splits, dev, stream);
-            default: return launch_mma<256, BLOCK>(p, o, plan.splits, dev, stream);
+            default: return launch_pair<BLOCK>(p, o, dev, stream);
         }
     });
 }
@@ -226,12 +277,13 @@ int sgemm_fp4(int M, int N, int K, int block, const unsigned char *A, int lda, c
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     const Fp4Args p{M, N, K, a_block, b_block, a_scale, b_scale, bias, C, ldc, ctype};
     if (K == 0) return empty_product(p, dev, stream);
+    if (takes_rows(M, K)) return rows_product({p, A, B, lda, ldb, nullptr, 0}, -1, block, dev, stream);
     return product(p, {A, B, lda, ldb}, block, dev, stream);
 }
 
 // The tokens' codes, their block scales, their scales.
 size_t sgemm_linear_fp4_workspace_size(int M, int K, int block) {
-    if (M <= 0 || K <= 0 || M > kMaxSize || K > kMaxSize || !block_ok(block)) return 0;
+    if (M <= 0 || K <= 0 || M > kMaxSize || K > kMaxSize || !block_ok(block) || takes_rows(M, K)) return 0;
     return (size_t)(up256((int64_t)M * code_pitch(K)) + up256(tile_bytes(M, K, block)) + (block == 16 ? up256((int64_t)M * 4) : 0));
 }
 
@@ -246,7 +298,7 @@ int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int
     const size_t need = sgemm_linear_fp4_workspace_size(M, K, block);
     if (!aligned(workspace, 16) || (need && (!workspace || workspace_bytes < need))) return SGEMM_ERR_INVALID_ARG;
     const int64_t nb = tile_bytes(N, K, block);
-    const Range c(C, M, N, ldc, dtype_size(ctype)), ws(workspace, 1, (int64_t)need, (int64_t)need, 1);
+    const Range c(C, M, N, ldc, dtype_size(ctype)), ws(need ? workspace : nullptr, 1, (int64_t)need, (int64_t)need, 1);
     for (const Range &in : {Range(X, M, K, ldx, size), Range(B, N, code_bytes(K), ldb, 1), Range(b_block, 1, nb, nb, 1),
                             Range(b_scale, 1, N, N, 4), Range(bias, 1, N, N, 4)})
         if (c.overlaps(in) || ws.overlaps(in)) return SGEMM_ERR_ALIAS;
@@ -255,6 +307,7 @@ int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     Fp4Args p{M, N, K, nullptr, b_block, nullptr, b_scale, bias, C, ldc, ctype};
     if (K == 0) return empty_product(p, dev, stream);
+    if (takes_rows(M, K)) return rows_product({p, nullptr, B, 0, ldb, X, ldx}, xtype, block, dev, stream);
     uint8_t *codes = static_cast<uint8_t *>(workspace), *tiles = codes + up256((int64_t)M * code_pitch(K));
     float *scale = block == 16 ? reinterpret_cast<float *>(tiles + up256(tile_bytes(M, K, block))) : nullptr;
     const int st = quantize({M, M, K, codes, code_pitch(K), tiles, scale}, xtype, block, X, ldx, dev, stream);

@@ -19,6 +19,7 @@
 #include <cuda.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "fp4_quantize.cuh"
 #include "ptx.cuh"
@@ -76,30 +77,61 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+// Stores COLS columns of an accumulator: column j is token m + j of column `col` of C, whose row of B
+// this lane is.  token_scales: those of the COLS tokens, in shared memory (read four at a time by
+// the whole warp; exchanged between lanes they were a chain of latencies: 4096 x 4096 x 512, of which
+// storing is the most, 31 us against 24).
+template <int COLS, class T>
+__device__ __forceinline__ void fp4_store_as(T *c, int64_t ldc, const float *v, const float *token_scales, float scale, float bias,
+                                             int count) {
+    constexpr int DT = sizeof(T) == 4 ? SGEMM_F32 : std::is_same_v<T, __half> ? SGEMM_F16 : SGEMM_BF16;
+#pragma unroll
+    for (int j = 0; j < COLS; j += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(token_scales + j);
+        const float s[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i, c += ldc)
+            if (j + i < count) *c = Elem<DT>::from_float(fmaf(v[j + i] * s[i], scale, bias));
+    }
+}
+template <int COLS>
+__device__ __forceinline__ void fp4_store(const Fp4Args &p, const float *v, const float *token_scales, float scale, float bias,
+                                          int m, int col) {
+    const int64_t at = (int64_t)m * p.ldc + col;
+    const int count = p.M - m;
+    if (p.ctype == SGEMM_F32) fp4_store_as<COLS>(static_cast<float *>(p.C) + at, p.ldc, v, token_scales, scale, bias, count);
+    else if (p.ctype == SGEMM_BF16)
+        fp4_store_as<COLS>(static_cast<__nv_bfloat16 *>(p.C) + at, p.ldc, v, token_scales, scale, bias, count);
+    else fp4_store_as<COLS>(static_cast<__half *>(p.C) + at, p.ldc, v, token_scales, scale, bias, count);
+}
+
 template <int TOK_, int BLOCK_>
 struct Fp4Tile {
     static constexpr int ROWS = 128, TOK = TOK_, BLOCK = BLOCK_;
     static constexpr int BK = 256, BYTES = BK / 2;  // a k-step's columns, and bytes of codes a row
-    static constexpr int DRAIN = 2, THREADS = 32 * (DRAIN + 4);
-    // 512-byte tiles of scales: along a k-step, and of the 128 rows each that the tokens reach into.
-    // A product's scales start on an even column of tensor memory, 64 rows: narrower tiles serve only
-    // where one holds all tokens.
-    static constexpr int KT = BK / BLOCK / 4, XT = TOK <= 128 ? 1 : 2;
+    // warps: 0 copies, 1 products, then sets of four that drain; a set takes COLS tokens of a tile
+    static constexpr int SETS = TOK > 64 ? 2 : 1, COLS = TOK / SETS, DRAIN = 2, THREADS = 32 * (DRAIN + 4 * SETS);
+    // 512-byte tiles of scales along a k-step; the tokens are in one row of tiles, from a multiple of 64
+    // on: a product's scales start on an even column of tensor memory.  Narrower tiles serve only where
+    // one holds all tokens.
+    static constexpr int KT = BK / BLOCK / 4;
     static constexpr int W_BYTES = ROWS * BYTES, X_BYTES = TOK * BYTES;
-    static constexpr int WS_BYTES = KT * kFp4TileBytes, XS_BYTES = XT * WS_BYTES;
+    static constexpr int WS_BYTES = KT * kFp4TileBytes, XS_BYTES = WS_BYTES;
     static constexpr int STAGE = W_BYTES + X_BYTES + WS_BYTES + XS_BYTES;
-    static constexpr int STAGES_FIT = (227 * 1024 - 1024 - 256) / STAGE, STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-    static constexpr int SMEM_BYTES = STAGES * STAGE + 1024 + 256;
-    // tensor memory: accumulators, then two places for the scales of a k-step
-    static constexpr int ACCS = TOK <= 192 ? 2 : 1, ACC_COLS = TOK < 32 ? 32 : TOK;
-    static constexpr int SCALES = ACCS * ACC_COLS, SCALE_COLS = 4 * KT * (1 + XT), TMEM_COLS = 512;
+    // tensor memory: accumulators, then a place for the scales of each stage
+    static constexpr int ACCS = 2, ACC_COLS = TOK < 32 ? 32 : TOK;
+    static constexpr int SCALES = ACCS * ACC_COLS, SCALE_COLS = 8 * KT, TMEM_COLS = 512;
+    static constexpr int FIT_SMEM = (227 * 1024 - 1024 - 256 - 16 * TOK) / STAGE, FIT_TMEM = (TMEM_COLS - SCALES) / SCALE_COLS;
+    static constexpr int FIT = FIT_SMEM < FIT_TMEM ? FIT_SMEM : FIT_TMEM, STAGES = FIT < 8 ? FIT : 8;
+    // the ring, the tokens' scales of each drain warp, barriers
+    static constexpr int SMEM_BYTES = STAGES * STAGE + 16 * TOK + 1024 + 256;
     // A = B = e2m1 (1 at bits 7 and 10), both K-major, N >> 3 at bit 17, e8m0 scales at bit 23, M >> 4 at
     // bit 24; which pair of bytes of a scale's word is used, at bits 4 (B) and 29 (A)
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(TOK >> 3) << 17) |
                                       ((BLOCK == 32 ? 1u : 0u) << 23) | ((uint32_t)(ROWS >> 4) << 24);
     static constexpr uint32_t SECOND_PAIR = (2u << 4) | (2u << 29);
-    static_assert(TOK == 16 || TOK == 32 || TOK == 64 || (TOK % 64 == 0 && TOK <= 256), "columns of one product");
-    static_assert(STAGES >= 4 && SCALES + 2 * SCALE_COLS <= TMEM_COLS, "a ring, and tensor memory");
+    static_assert(TOK == 16 || TOK == 32 || TOK == 64 || TOK == 128, "columns of one product");
+    static_assert(STAGES >= 4, "a ring that hides the copies");
 };
 
 // Unit u is tile u / splits, part u % splits of K (the rank in the cluster); with
@@ -117,7 +149,8 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
     unsigned char *smem = smem_raw + (base - raw);
     // stages of the tokens, of B (128-byte swizzled boxes start on 1024 bytes), of their scales; the barriers
     const uint32_t w_base = base + T::STAGES * T::X_BYTES, ws_base = w_base + T::STAGES * T::W_BYTES;
-    const uint32_t xs_base = ws_base + T::STAGES * T::WS_BYTES, bars = xs_base + T::STAGES * T::XS_BYTES;
+    const uint32_t xs_base = ws_base + T::STAGES * T::WS_BYTES;
+    const uint32_t scales_base = xs_base + T::STAGES * T::XS_BYTES, bars = scales_base + 16 * TOK;
     // copies done, stage read by the products; accumulator final, accumulator read
     const uint32_t full0 = bars, empty0 = full0 + 8 * T::STAGES;
     const uint32_t acc_full0 = empty0 + 8 * T::STAGES, acc_empty0 = acc_full0 + 8 * T::ACCS;
@@ -128,7 +161,7 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles_n = (p.N + T::ROWS - 1) / T::ROWS, tiles_m = (p.M + TOK - 1) / TOK;
     const int units = tiles_m * tiles_n * splits;
-    const int steps = (p.K + T::BK - 1) / T::BK, k_tiles = fp4_tiles(p.K, BLOCK), m_tiles = (p.M + 127) / 128;
+    const int steps = (p.K + T::BK - 1) / T::BK, k_tiles = fp4_tiles(p.K, BLOCK);
     auto unit = [&](int u, int &m0, int &n0, int &k0, int &n) {
         int tn, tm;
         grouped_tile<8>(u / splits, tiles_n, tiles_m, tn, tm);
@@ -150,7 +183,7 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
         }
         for (int b = 0; b < T::ACCS; ++b) {
             mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, 4);  // one arrival per drain warp
+            mbar_init(acc_empty0 + 8 * b, 4 * T::SETS);  // one arrival per drain warp
         }
         mbar_init(drained, 1);
         *abort_flag = 0;
@@ -169,11 +202,10 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
             prefetch_tensor_map(&tmX);
         }
         // Copies of step k of a unit into a stage: B's part, which announces both, and the tokens'.
-        auto copy_b = [&](uint32_t at, int k, int m0, int n0) {
+        auto copy_b = [&](uint32_t at, int k, int n0) {
             if (elect_one()) {
                 const uint32_t kt = (uint32_t)min(T::KT, k_tiles - k * T::KT) * kFp4TileBytes;
-                const uint32_t xt = (uint32_t)min(T::XT, m_tiles - m0 / 128);
-                mbar_arrive_expect_tx(full0 + 8 * at, T::W_BYTES + T::X_BYTES + kt * (1 + xt));
+                mbar_arrive_expect_tx(full0 + 8 * at, T::W_BYTES + T::X_BYTES + 2 * kt);
                 tma_load_2d(w_base + at * T::W_BYTES, &tmW, k * T::BYTES, n0, full0 + 8 * at);
                 bulk_load(ws_base + at * T::WS_BYTES, p.b_tiles + ((int64_t)(n0 / 128) * k_tiles + k * T::KT) * kFp4TileBytes,
                           kt, full0 + 8 * at);
@@ -183,11 +215,8 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
             if (elect_one()) {
                 const uint32_t kt = (uint32_t)min(T::KT, k_tiles - k * T::KT) * kFp4TileBytes;
                 tma_load_2d(base + at * T::X_BYTES, &tmX, k * T::BYTES, m0, full0 + 8 * at);
-#pragma unroll
-                for (int r = 0; r < T::XT; ++r)
-                    if (m0 / 128 + r < m_tiles)
-                        bulk_load(xs_base + at * T::XS_BYTES + r * T::WS_BYTES,
-                                  p.a_tiles + ((int64_t)(m0 / 128 + r) * k_tiles + k * T::KT) * kFp4TileBytes, kt, full0 + 8 * at);
+                bulk_load(xs_base + at * T::XS_BYTES, p.a_tiles + ((int64_t)(m0 / 128) * k_tiles + k * T::KT) * kFp4TileBytes,
+                          kt, full0 + 8 * at);
             }
         };
         // The tokens' codes may come from the kernel before; B does not: the first unit's first stages
@@ -195,7 +224,7 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
         int ahead = 0, m0, n0, k0, n;
         if (!(debug & 1) && (int)blockIdx.x < units) {
             unit(blockIdx.x, m0, n0, k0, n);
-            for (ahead = min(n, T::STAGES); issued < ahead; ++issued) copy_b(issued, k0 + issued, m0, n0);
+            for (ahead = min(n, T::STAGES); issued < ahead; ++issued) copy_b(issued, k0 + issued, n0);
         }
         griddep_wait();
         for (int k = 0; k < ahead; ++k, s.next()) copy_tokens(k, k0 + k, m0);
@@ -209,7 +238,7 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
                     ok = false;
                     break;
                 }
-                copy_b(s.at, k, m0, n0);
+                copy_b(s.at, k, n0);
                 copy_tokens(s.at, k, m0);
                 __syncwarp();
                 ++issued;
@@ -217,158 +246,129 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        // the whole warp walks the steps, so that addresses stay uniform; one lane issues
-        RingPlace<T::STAGES> s, before;
-        RingPlace<T::ACCS> b;
-        const uint64_t x_desc0 = umma_desc_128b(base), w_desc0 = umma_desc_128b(w_base);
-        const uint64_t xs_desc0 = umma_desc_scales(xs_base), ws_desc0 = umma_desc_scales(ws_base);
-        bool ok = true;
-        int i = 0, step = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-            int m0, n0, k0, n;
-            unit(u, m0, n0, k0, n);
-            // the drain warps are done with this accumulator's previous tile
-            if (i >= T::ACCS) ok = mbar_wait_polite(acc_empty0 + 8 * b.at, b.round ^ 1, wait_limit_ns, 0);
-            const uint32_t acc = tmem + b.at * T::ACC_COLS;
-            for (int k = 0; k < n; ++k, ++step) {
-                ok = ok && mbar_wait_polite(full0 + 8 * s.at, s.round, wait_limit_ns, 0);
-                // the place of this step's scales has been read by the products of the step before the last
-                if (step >= 2) {
-                    ok = ok && mbar_wait_polite(empty0 + 8 * before.at, before.round, wait_limit_ns, 0);
-                    before.next();
+        // one lane walks the steps: what it spends on one bounds the products of few tokens
+        if (elect_one()) {
+            RingPlace<T::STAGES> s;
+            RingPlace<T::ACCS> b;
+            const uint64_t x_desc0 = umma_desc_128b(base), w_desc0 = umma_desc_128b(w_base);
+            const uint64_t xs_desc0 = umma_desc_scales(xs_base), ws_desc0 = umma_desc_scales(ws_base);
+            // The scales' and codes' products of a step of N times 64 columns.  The scales have a place for each
+            // stage: it was read by the time that the stage was refilled.
+            auto issue = [&](uint32_t acc, uint32_t x_first, bool first, auto n_const) {
+                constexpr int N = decltype(n_const)::value;
+                const uint64_t w = w_desc0 + s.at * (T::W_BYTES >> 4), x = x_desc0 + s.at * (T::X_BYTES >> 4);
+                const uint64_t ws = ws_desc0 + s.at * (T::WS_BYTES >> 4), xs = xs_desc0 + s.at * (T::XS_BYTES >> 4);
+                const uint32_t w_scales = tmem + T::SCALES + s.at * T::SCALE_COLS, x_scales = w_scales + 4 * T::KT;
+#pragma unroll
+                for (int t = 0; t * (BLOCK / 16) < N; ++t) {
+                    tmem_copy_scales(w_scales + 4 * t, ws + t * (kFp4TileBytes >> 4));
+                    tmem_copy_scales(x_scales + 4 * t, xs + t * (kFp4TileBytes >> 4));
                 }
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after_sync();
-                if (elect_one()) {
-                    const uint64_t w = w_desc0 + s.at * (T::W_BYTES >> 4), x = x_desc0 + s.at * (T::X_BYTES >> 4);
-                    const uint64_t ws = ws_desc0 + s.at * (T::WS_BYTES >> 4), xs = xs_desc0 + s.at * (T::XS_BYTES >> 4);
-                    const uint32_t w_scales = tmem + T::SCALES + (step & 1) * T::SCALE_COLS, x_scales = w_scales + 4 * T::KT;
-                    // products of 64 columns; the last step may have fewer
-                    const int products = min(T::BK / 64, (p.K - (k0 + k) * T::BK + 63) / 64);
 #pragma unroll
-                    for (int t = 0; t < T::KT; ++t) {
-                        if (t * (BLOCK / 16) >= products) break;
-                        tmem_copy_scales(w_scales + 4 * t, ws + t * (kFp4TileBytes >> 4));
-#pragma unroll
-                        for (int r = 0; r < T::XT; ++r)
-                            tmem_copy_scales(x_scales + 4 * (T::XT * t + r), xs + (r * T::KT + t) * (kFp4TileBytes >> 4));
-                    }
-                    const uint32_t x_first = TOK % 128 ? (uint32_t)(m0 % 128 / 32) : 0u;
-#pragma unroll
-                    for (int kk = 0; kk < T::BK / 64; ++kk) {
-                        if (kk >= products) break;
-                        const int t = kk / (BLOCK / 16);
-                        umma_fp4<BLOCK>(acc, w + 2 * kk, x + 2 * kk, BLOCK == 32 && kk % 2 ? T::IDESC | T::SECOND_PAIR : T::IDESC,
-                                        w_scales + 4 * t, x_scales + 4 * T::XT * t + x_first, kk > 0 || k > 0);
-                    }
-                    umma_commit(empty0 + 8 * s.at);  // the stage may be refilled once these have read it
-                    // the tile is final once its products are done
-                    if (k + 1 == n) umma_commit(acc_full0 + 8 * b.at);
+                for (int kk = 0; kk < N; ++kk) {
+                    const int t = kk / (BLOCK / 16);
+                    umma_fp4<BLOCK>(acc, w + 2 * kk, x + 2 * kk, BLOCK == 32 && kk % 2 ? T::IDESC | T::SECOND_PAIR : T::IDESC,
+                                    w_scales + 4 * t, x_scales + 4 * t + x_first, kk > 0 || !first);
                 }
-                __syncwarp();
-                s.next();
+                umma_commit(empty0 + 8 * s.at);  // the stage may be refilled once these have read it
+            };
+            const int last = (p.K - (steps - 1) * T::BK + 63) / 64;  // products of the last step of K
+            bool ok = true, ready = false;
+            int i = 0;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++i, b.next()) {
+                int m0, n0, k0, n;
+                unit(u, m0, n0, k0, n);
+                // the drain warps are done with this accumulator's previous tile
+                if (i >= T::ACCS) ok = mbar_wait_polite(acc_empty0 + 8 * b.at, b.round ^ 1, wait_limit_ns, 0);
+                const uint32_t acc = tmem + b.at * T::ACC_COLS, x_first = TOK % 128 ? (uint32_t)(m0 % 128 / 32) : 0u;
+                for (int k = 0; ok && k < n; ++k) {
+                    if (!ready && !(ok = mbar_wait_polite(full0 + 8 * s.at, s.round, wait_limit_ns, 0))) break;
+                    tc_fence_after_sync();
+                    RingPlace<T::STAGES> next = s;
+                    next.next();
+                    ready = mbar_try_wait(full0 + 8 * next.at, next.round);  // asked early, looked at next time
+                    if (k0 + k + 1 < steps || last == 4) issue(acc, x_first, k == 0, std::integral_constant<int, 4>{});
+                    else if (last == 3) issue(acc, x_first, k == 0, std::integral_constant<int, 3>{});
+                    else if (last == 2) issue(acc, x_first, k == 0, std::integral_constant<int, 2>{});
+                    else issue(acc, x_first, k == 0, std::integral_constant<int, 1>{});
+                    if (k + 1 == n) umma_commit(acc_full0 + 8 * b.at);  // the tile is final once its products are done
+                    s = next;
+                }
             }
-            if (!__all_sync(0xffffffffu, ok)) {
-                *abort_flag = 1;
-                break;
-            }
-            b.next();
+            if (!ok) *abort_flag = 1;
+            umma_commit(drained);
         }
-        // every product issued above has completed before the block moves on
-        if (elect_one()) umma_commit(drained);
         __syncwarp();
+        // every product issued above has completed before the block moves on
         (void)mbar_wait_polite(drained, 0, wait_limit_ns, 0);
     } else {
         // drain warps: a lane is a row of B (a column of C), a column of the accumulator a token
         griddep_wait();  // the tokens' scales
-        const int q = warp & 3;
+        constexpr int COLS = T::COLS, LOAD = COLS < 32 ? 16 : COLS < 64 ? 32 : 64;
+        const int q = warp & 3, c0 = (warp - T::DRAIN) / 4 * COLS;
+        float *token_scales = reinterpret_cast<float *>(smem + (scales_base - base)) + (warp - T::DRAIN) * COLS;
         RingPlace<T::ACCS> b;
         for (int u = blockIdx.x; u < units; u += gridDim.x, b.next()) {
             int m0, n0, k0, n;
             unit(u, m0, n0, k0, n);
+            m0 += c0;
             const int col = n0 + 32 * q + lane;
             const bool in = col < p.N;
-            // the scales are here before the accumulator is: lane l holds those of tokens l, l + 32, ...
-            float token_scales[(TOK + 31) / 32];
-#pragma unroll
-            for (int i = 0; i < (TOK + 31) / 32; ++i) {
-                const int m = m0 + 32 * i + lane;
-                token_scales[i] = p.a_scale && m < p.M ? p.a_scale[m] : 1.f;
-            }
+            // the scales are here before the accumulator is
+            for (int j = lane; j < COLS; j += 32) token_scales[j] = p.a_scale && m0 + j < p.M ? p.a_scale[m0 + j] : 1.f;
             const float scale = in && p.b_scale ? p.b_scale[col] : 1.f, bias = in && p.bias ? p.bias[col] : 0.f;
             // a finished tile is stored whatever another role decided since
-            if (!mbar_wait_warp(acc_full0 + 8 * b.at, b.round, wait_limit_ns, 200)) {
+            if (!mbar_wait_warp(acc_full0 + 8 * b.at, b.round, wait_limit_ns, 20)) {
                 if (lane == 0) *abort_flag = 1;
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b.at * T::ACC_COLS;
-            constexpr int CHUNK = TOK % 32 ? 16 : 32;
-#pragma unroll 1
-            for (int c0 = 0; c0 < TOK; c0 += CHUNK) {
-                float v[32];
-                if constexpr (CHUNK == 32) tmem_ld32(acc + (uint32_t)c0, v);
-                else tmem_ld16(acc + (uint32_t)c0, v);
-                if (c0 + CHUNK == TOK) {
-                    // the accumulator is read: hand it back to the product thread
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty0 + 8 * b.at);
-                }
-                const int m = m0 + c0, count = min(CHUNK, p.M - m);
-                if (count <= 0) continue;
-                if (splits > 1) {
-                    // the ring's copies have landed and been read: its first bytes hold this block's part
-                    float *part = reinterpret_cast<float *>(smem) + 32 * q + lane;
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b.at * T::ACC_COLS + (uint32_t)c0;
+            float v[LOAD];
+            if constexpr (LOAD == 16) tmem_ld16(acc, v);
+            else if constexpr (LOAD == 32) tmem_ld32(acc, v);
+            else tmem_ld64(acc, v);
+            // the accumulator is read: hand it back to the product thread
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty0 + 8 * b.at);
+            if (splits > 1) {
+                // the ring's copies have landed and been read: its first bytes hold this block's part
+                float *part = reinterpret_cast<float *>(smem) + c0 * T::ROWS + 32 * q + lane;
 #pragma unroll
-                    for (int j = 0; j < CHUNK; ++j) part[(c0 + j) * T::ROWS] = v[j];
-                    continue;
-                }
-                float token_scale = token_scales[0];
-#pragma unroll
-                for (int i = 1; i < (TOK + 31) / 32; ++i)
-                    if (c0 / 32 == i) token_scale = token_scales[i];
-#pragma unroll
-                for (int j = 0; j < CHUNK; ++j) {
-                    const float s = __shfl_sync(0xffffffffu, token_scale, c0 % 32 + j);
-                    v[j] = fmaf(v[j] * s, scale, bias);
-                }
-                if (in) {
-                    const int64_t at = (int64_t)m * p.ldc + col;
-                    if (p.ctype == SGEMM_F32) {
-#pragma unroll
-                        for (int j = 0; j < CHUNK; ++j)
-                            if (j < count) static_cast<float *>(p.C)[at + j * p.ldc] = v[j];
-                    } else if (p.ctype == SGEMM_BF16) {
-#pragma unroll
-                        for (int j = 0; j < CHUNK; ++j)
-                            if (j < count) static_cast<__nv_bfloat16 *>(p.C)[at + j * p.ldc] = __float2bfloat16_rn(v[j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < CHUNK; ++j)
-                            if (j < count) static_cast<__half *>(p.C)[at + j * p.ldc] = __float2half_rn(v[j]);
-                    }
-                }
+                for (int j = 0; j < COLS; ++j) part[j * T::ROWS] = v[j];
+            } else if (in) {
+                fp4_store<COLS>(p, v, token_scales, scale, bias, m0, col);
             }
+            __syncwarp();  // the scales are read before the next tile's take their place
         }
     }
 
     __syncwarp();
     if (splits > 1) {
         cluster_sync();
-        if (warp >= T::DRAIN) {
-            // this block's tokens of the tile: the parts in order of their rank
+        if (warp >= T::DRAIN && warp < T::DRAIN + 4) {
+            // this block's tokens of the tile: the parts in order of their rank, eight tokens' on their way
+            constexpr int U = 8;
             int m0, n0, k0, n;
             unit(blockIdx.x, m0, n0, k0, n);
-            const int row = 32 * (warp & 3) + lane, col = n0 + row;
+            const int row = 32 * (warp & 3) + lane, col = n0 + row, tokens = min(TOK, p.M - m0);
             const float scale = col < p.N && p.b_scale ? p.b_scale[col] : 1.f, bias = col < p.N && p.bias ? p.bias[col] : 0.f;
-            for (int j = blockIdx.x % splits; j < TOK && m0 + j < p.M; j += splits) {
-                float sum = 0.f;
+            for (int j = blockIdx.x % splits; j < tokens; j += U * splits) {
+                float sum[U] = {};
 #pragma unroll 4
-                for (int r = 0; r < splits; ++r)
-                    sum += __uint_as_float(dsmem_ld_u32(dsmem_map(base + 4 * (j * T::ROWS + row), (uint32_t)r)));
-                const float s = p.a_scale ? p.a_scale[m0 + j] : 1.f;
-                if (col < p.N) store_c(p.C, (int64_t)(m0 + j) * p.ldc + col, p.ctype, fmaf(sum * s, scale, bias));
+                for (int r = 0; r < splits; ++r) {
+                    const uint32_t from = dsmem_map(base + 4 * (j * T::ROWS + row), (uint32_t)r);
+#pragma unroll
+                    for (int i = 0; i < U; ++i)
+                        if (j + i * splits < tokens) sum[i] += __uint_as_float(dsmem_ld_u32(from + 4 * T::ROWS * i * splits));
+                }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const int m = m0 + j + i * splits;
+                    if (j + i * splits < tokens && col < p.N)
+                        store_c(p.C, (int64_t)m * p.ldc + col, p.ctype, fmaf(sum[i] * (p.a_scale ? p.a_scale[m] : 1.f), scale, bias));
+                }
             }
         }
         cluster_sync();  // no block leaves while another reads its part

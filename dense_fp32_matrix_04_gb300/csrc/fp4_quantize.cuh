@@ -93,11 +93,10 @@ struct Fp4Rows {
     float *scale;
 };
 
-// The codes and the scale of columns c .. c + 15 of row m, of which a thread has the
-// values and the largest magnitude's bits; all lanes of a warp call it, with columns
-// beside each other, the first lane's a multiple of 512.
+// The codes of 16 columns, from their values and their largest magnitude's bits, and the bits
+// of their block's scale; all lanes of a warp call it, neighbours with columns beside each other.
 template <int BLOCK>
-__device__ __forceinline__ void fp4_put(const Fp4Rows &a, int64_t m, int c, float (&v)[16], uint32_t top, const Fp4Row &r) {
+__device__ __forceinline__ uint32_t fp4_encode(float (&v)[16], uint32_t top, const Fp4Row &r, uint2 &codes) {
     uint32_t s;
     float inv;
     if constexpr (BLOCK == 16) {
@@ -111,8 +110,17 @@ __device__ __forceinline__ void fp4_put(const Fp4Rows &a, int64_t m, int c, floa
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] *= inv;
-    uint2 codes = make_uint2(e2m1x8(v), e2m1x8(v + 8));
+    codes = make_uint2(e2m1x8(v), e2m1x8(v + 8));
     if (inv == 0.f) codes = make_uint2(0, 0);
+    return s;
+}
+
+// The codes and the scale of columns c .. c + 15 of row m are written; as fp4_encode, with the
+// first lane's c a multiple of 512.
+template <int BLOCK>
+__device__ __forceinline__ void fp4_put(const Fp4Rows &a, int64_t m, int c, float (&v)[16], uint32_t top, const Fp4Row &r) {
+    uint2 codes;
+    uint32_t s = fp4_encode<BLOCK>(v, top, r, codes);
     const bool in = m < a.M && c < a.K;
     if (in) {
         uint8_t *to = a.q + m * a.ldq + c / 2;

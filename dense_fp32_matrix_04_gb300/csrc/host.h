@@ -35,6 +35,10 @@ __attribute__((visibility("hidden"))) bool encode_f16(CUtensorMap *map, const vo
 __attribute__((visibility("hidden"))) bool encode_i8(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols,
                                                      int64_t ld, int box_rows, int box_cols);
 
+// The same of 64-bit words in dense rows, not swizzled.
+__attribute__((visibility("hidden"))) bool encode_words(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols,
+                                                        int box_rows, int box_cols);
+
 // Nanoseconds a kernel may wait for its own copies before it gives up.
 __attribute__((visibility("hidden"))) unsigned long long wait_limit_ns();
 

@@ -187,6 +187,10 @@ bool sgemm_host::encode_i8(CUtensorMap *map, const void *ptr, int64_t rows, int6
                        box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+bool sgemm_host::encode_words(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int box_rows, int box_cols) {
+    return encode_rows(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, ptr, rows, cols, cols, box_rows, box_cols, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 namespace {
 
 // The four phase maps of a rows x cols operand (leading dimension ld, rows

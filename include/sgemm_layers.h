@@ -284,8 +284,8 @@ int sgemm_fp4_lay_out_scales(int rows, int K, int block, const unsigned char *s,
 /*
  * C = A B^T + bias for the matrices that codes and scales stand for (A: M x K, B:
  * N x K, both quantised with the same block, as sgemm_quantize_fp4 lays them out):
- * the products of a block and its scales are exact, the sums over K are FP32, in an
- * order fixed by the shape; the rows' scales and the bias are applied in FP32 and the
+ * the products of codes and the blocks' scales are exact, the sums over K are FP32, in
+ * an order fixed by the shape; the rows' scales and the bias are applied in FP32 and the
  * result is rounded once to ctype.
  *   a_scale, b_scale: M and N FP32 values, or NULL (1).  Beside weights that were
  *       quantised elsewhere b_scale can hold whatever scale they have beyond their
@@ -307,7 +307,8 @@ int sgemm_fp4(int M, int N, int K, int block,
  * sgemm_quantize_fp4 of the M x K rows of X (xtype), then sgemm_fp4.
  *   workspace: sgemm_linear_fp4_workspace_size(M, K, block) bytes, 16-byte aligned,
  *       with contents that do not matter; calls that share one must not overlap on
- *       the GPU.
+ *       the GPU.  Up to four rows of up to 22528 columns (two of 45056, one of 90112)
+ *       need none.
  */
 int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int block,
                      const unsigned char *B, int ldb, const unsigned char *b_block, const float *b_scale,
