@@ -29,57 +29,66 @@ struct BeamArgs {
     int32_t *parent, *token;
 };
 
-// score - ln(sum) - the part of it that the rounded reference holds: 64 bits where FP32
-// would round numbers of the size of the score (the sum's fraction has a logarithm below
-// 0.7, which FP32 has to 2^-25).
-__device__ __forceinline__ double beam_base(float score, float2 r, float c) {
-    const float M = SoftmaxState::reference(r.x, c), off = SoftmaxState::usual(M) ? -fmaf(r.x, c, -M) : 0.f;
+// score - ln(sum) - the part of it that the rounded reference holds - scale times the largest:
+// what a candidate's scaled logit is added to.  64 bits where FP32 would round numbers of the size
+// of the score (the sum's fraction has a logarithm below 0.7, which FP32 has to 2^-25).
+__device__ __forceinline__ double beam_base(float score, float2 r, float scale) {
+    const float c = scale * kLog2e, M = SoftmaxState::reference(r.x, c), off = SoftmaxState::usual(M) ? -fmaf(r.x, c, -M) : 0.f;
     const uint32_t bits = __float_as_uint(r.y);
     const int e = (int)(bits >> 23) - 127;  // the sum is at least about 1/2, the largest's own term
     const float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-    return (double)score - (double)logf(f) - ((double)e + (double)off) * 0.6931471805599453;
+    return (double)score - (double)logf(f) - ((double)e + (double)off) * 0.6931471805599453 - (double)r.x * (double)scale;
+}
+
+// A whole number in the order of the values (not NaN): comparisons in 64 bits without the few units
+// that there are for FP64.
+__device__ __forceinline__ int64_t ordered(double v) {
+    const int64_t b = __double_as_longlong(v + 0.0);  // (of the two zeros the positive one)
+    return b >= 0 ? b : b ^ 0x7fffffffffffffffll;
 }
 
 // A block a group, a warp a beam.
 __global__ void __launch_bounds__(1024) beam_join_kernel(const BeamArgs a) {
-    __shared__ double list[32][32];
+    __shared__ int64_t list[32][32];
+    __shared__ double base[32];
     const int beam = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row0 = (int64_t)blockIdx.x * a.W;
     griddep_wait();
-    const int row = blockIdx.x * a.W + beam;
+    // a lane of the first warp a beam: FP64 takes a warp as long for one lane as for all
+    if (beam == 0 && lane < a.W) {
+        const float score = a.score[row0 + lane];
+        const bool goes_on = row_takes_part(score, a.finished ? a.finished + row0 + lane : nullptr);
+        base[lane] = goes_on ? beam_base(score, a.reference[row0 + lane], a.scale) : (double)score;
+    }
+    const int64_t row = row0 + beam;
     const float score = a.score[row];
     const bool ended = a.finished && a.finished[row];
-    // candidates of different beams may lie closer than FP32 tells apart
-    double v = -INFINITY;
     int token = -1;
+    float z = 0.f;
     if (lane < a.top && row_takes_part(score, nullptr)) {
         if (ended) {
-            if (lane == 0) {
-                v = score;
-                token = a.end;
-            }
+            if (lane == 0) token = a.end;
         } else {
-            token = a.id[(int64_t)row * a.top + lane];
-            if (token >= 0) {
-                const float2 r = a.reference[row];
-                const double z = a.value[(int64_t)row * a.top + lane];
-                v = beam_base(score, r, a.scale * kLog2e) + (z - (double)r.x) * (double)a.scale;
-            }
+            token = a.id[row * a.top + lane];
+            z = a.value[row * a.top + lane];
         }
     }
-    list[beam][lane] = v;
+    __syncthreads();
+    // candidates of different beams may lie closer than FP32 tells apart
+    const double v = token < 0 ? -INFINITY : fma((double)z, (double)a.scale, base[beam]);
+    const int64_t key = ordered(v);
+    list[beam][lane] = key;
     __syncthreads();
     if (lane >= a.top) return;
     int place = lane;
     for (int j = 0; j < a.W; ++j) {
         if (j == beam) continue;
         // the candidates of beam j that come first: the larger ones, and of a lower beam the equal ones
+        const int64_t least = j < beam ? key : key + 1;
         int n = 0;
 #pragma unroll
         for (int step = 32; step; step >>= 1)
-            if (n + step <= a.top) {
-                const double o = list[j][n + step - 1];
-                if (j < beam ? o >= v : o > v) n += step;
-            }
+            if (n + step <= a.top && list[j][n + step - 1] >= least) n += step;
         place += n;
     }
     if (place >= a.top) return;

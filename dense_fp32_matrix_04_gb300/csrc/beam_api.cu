@@ -72,7 +72,7 @@ int sgemm_beam_step(int B, int W, int V, int dtype, const void *logits, int ldz,
                     int32_t *parent, int32_t *token, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!groups_ok(B, W, top)) return SGEMM_ERR_INVALID_ARG;
     const int T = B * W;
-    if (!sgemm_host::logprobs_shape_ok(T, V, dtype, logits, ldz, scale, mask, ldm, mask_rows)) return SGEMM_ERR_INVALID_ARG;
+    if (!sgemm_host::logprobs_shape_ok(T, V, dtype, sgemm_host::Rows{logits, ldz}, scale, mask, ldm, mask_rows)) return SGEMM_ERR_INVALID_ARG;
     if (finished && end < 0) return SGEMM_ERR_INVALID_ARG;
     if (T == 0) return SGEMM_OK;
     if (!score || !out_score || !parent || !token || !aligned(score, 4) || !aligned(out_score, 4) || !aligned(parent, 4) ||
@@ -98,7 +98,11 @@ int sgemm_beam_step(int B, int W, int V, int dtype, const void *logits, int ldz,
     float2 *reference = reinterpret_cast<float2 *>(ws + at.reference);
     const LogprobArgs rows{T, V, logits, ldz, scale, mask, mask_rows > 1 ? ldm : 0, nullptr, nullptr, nullptr, nullptr, top,
                            value, id, score, finished, reference};
-    const int st = sgemm_host::logprobs(rows, dtype, dev, stream);
+    const int st = sgemm_host::by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return mask ? sgemm_host::logprobs_by_length<DT, true, true>(rows, dev, stream)
+                    : sgemm_host::logprobs_by_length<DT, false, true>(rows, dev, stream);
+    });
     if (st != SGEMM_OK) return st;
     const BeamArgs a{B, W, top, scale, value, id, reference, score, finished, end, out_score, parent, token};
     return launch<true>(beam_join_kernel, dim3(B), dim3(32 * W), 0, stream, 1, a);

@@ -109,8 +109,16 @@ struct Fp4Operands {
     int64_t lda, ldb;
 };
 
+// launch, beside the kernel before where `early` holds.
+template <class... Params, class... Args>
+int launch_beside(bool early, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,
+                  Args &&...args) {
+    return early ? launch<true>(kernel, grid, block, smem, stream, cluster, std::forward<Args>(args)...)
+                 : launch(kernel, grid, block, smem, stream, cluster, std::forward<Args>(args)...);
+}
+
 template <int TOK, int BLOCK>
-int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, const Device &dev, cudaStream_t stream) {
+int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, bool early, const Device &dev, cudaStream_t stream) {
     using T = Fp4Tile<TOK, BLOCK>;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
     const auto kernel = fp4_mma_kernel<TOK, BLOCK>;
@@ -120,13 +128,13 @@ int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, const Device 
         !sgemm_host::encode_i8(&tx, o.A, p.M, code_bytes(p.K), o.lda, TOK, T::BYTES))
         return SGEMM_ERR_LAUNCH;
     const int64_t units = (int64_t)((p.M + TOK - 1) / TOK) * ((p.N + T::ROWS - 1) / T::ROWS) * splits;
-    return launch<true>(kernel, dim3((unsigned)(splits > 1 ? units : std::min<int64_t>(units, dev.sms))), dim3(T::THREADS),
-                        T::SMEM_BYTES, stream, (unsigned)splits, tw, tx, p, splits, dev.err_word, sgemm_host::wait_limit_ns(),
-                        sgemm_host::test_flags());
+    return launch_beside(early, kernel, dim3((unsigned)(splits > 1 ? units : std::min<int64_t>(units, dev.sms))), dim3(T::THREADS),
+                         T::SMEM_BYTES, stream, (unsigned)splits, tw, tx, p, splits, dev.err_word, sgemm_host::wait_limit_ns(),
+                         sgemm_host::test_flags());
 }
 
 template <int BLOCK>
-int launch_pair(const Fp4Args &p, const Fp4Operands &o, const Device &dev, cudaStream_t stream) {
+int launch_pair(const Fp4Args &p, const Fp4Operands &o, bool early, const Device &dev, cudaStream_t stream) {
     using T = Fp4PairTile<256, BLOCK>;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
     const auto kernel = fp4_pair_kernel<256, BLOCK>;
@@ -139,8 +147,8 @@ int launch_pair(const Fp4Args &p, const Fp4Operands &o, const Device &dev, cudaS
         !sgemm_host::encode_words(&txs, p.a_tiles, (p.M + 127) / 128, words, 2, T::WS_BYTES / 8))
         return SGEMM_ERR_LAUNCH;
     const int64_t tiles = (int64_t)((p.M + T::TOK - 1) / T::TOK) * ((p.N + T::ROWS - 1) / T::ROWS);
-    return launch<true>(kernel, dim3((unsigned)(2 * std::min<int64_t>(tiles, dev.sms / 2))), dim3(T::THREADS), T::SMEM_BYTES, stream,
-                        2, tw, tx, tws, txs, p, dev.err_word, sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
+    return launch_beside(early, kernel, dim3((unsigned)(2 * std::min<int64_t>(tiles, dev.sms / 2))), dim3(T::THREADS), T::SMEM_BYTES,
+                         stream, 2, tw, tx, tws, txs, p, dev.err_word, sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
 }
 
 // Up to four tokens whose codes fit shared memory go to the kernel that reads whole rows.
@@ -173,16 +181,17 @@ int rows_product(const Fp4RowsArgs &a, int xtype, int block, const Device &dev, 
     });
 }
 
-int product(const Fp4Args &p, const Fp4Operands &o, int block, const Device &dev, cudaStream_t stream) {
+// early: the kernel before is this call's own, which does not write B.
+int product(const Fp4Args &p, const Fp4Operands &o, int block, bool early, const Device &dev, cudaStream_t stream) {
     const Fp4Plan plan(p.M, p.N, p.K, dev.sms);
     return by_block(block, [&](auto b) {
         constexpr int BLOCK = decltype(b)::value;
         switch (plan.tok) {
-            case 16: return launch_mma<16, BLOCK>(p, o, plan.splits, dev, stream);
-            case 32: return launch_mma<32, BLOCK>(p, o, plan.splits, dev, stream);
-            case 64: return launch_mma<64, BLOCK>(p, o, plan.splits, dev, stream);
-            case 128: return launch_mma<128, BLOCK>(p, o, plan.splits, dev, stream);
-            default: return launch_pair<BLOCK>(p, o, dev, stream);
+            case 16: return launch_mma<16, BLOCK>(p, o, plan.splits, early, dev, stream);
+            case 32: return launch_mma<32, BLOCK>(p, o, plan.splits, early, dev, stream);
+            case 64: return launch_mma<64, BLOCK>(p, o, plan.splits, early, dev, stream);
+            case 128: return launch_mma<128, BLOCK>(p, o, plan.splits, early, dev, stream);
+            default: return launch_pair<BLOCK>(p, o, early, dev, stream);
         }
     });
 }
@@ -278,7 +287,7 @@ int sgemm_fp4(int M, int N, int K, int block, const unsigned char *A, int lda, c
     const Fp4Args p{M, N, K, a_block, b_block, a_scale, b_scale, bias, C, ldc, ctype};
     if (K == 0) return empty_product(p, dev, stream);
     if (takes_rows(M, K)) return rows_product({p, A, B, lda, ldb, nullptr, 0}, -1, block, dev, stream);
-    return product(p, {A, B, lda, ldb}, block, dev, stream);
+    return product(p, {A, B, lda, ldb}, block, false, dev, stream);
 }
 
 // The tokens' codes, their block scales, their scales.
@@ -314,7 +323,7 @@ int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int
     if (st != SGEMM_OK) return st;
     p.a_tiles = tiles;
     p.a_scale = scale;
-    return product(p, {codes, B, code_pitch(K), ldb}, block, dev, stream);
+    return product(p, {codes, B, code_pitch(K), ldb}, block, true, dev, stream);
 }
 
 }  // extern "C"

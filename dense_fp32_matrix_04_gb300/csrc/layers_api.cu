@@ -23,6 +23,8 @@ using sgemm_host::dtype_ok;
 using sgemm_host::dtype_size;
 using sgemm_host::launch;
 using sgemm_host::kMaxWidth;
+using sgemm_host::logprobs_by_length;
+using sgemm_host::logprobs_shape_ok;
 using sgemm_host::most_grad_runners;
 using sgemm_host::Range;
 using sgemm_host::row_threads;
@@ -106,37 +108,6 @@ bool norm_shape_ok(int T, int D, int dtype, int wdtype, const void *w_pre, const
 
 // ---------------------------------------------------------------- log probabilities
 
-template <int DT, int THREADS, bool TOP, bool MASK>
-int launch_logprobs(const LogprobArgs &a, unsigned parts, const Device &dev, cudaStream_t stream) {
-    static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = logprobs_kernel<DT, THREADS, TOP, MASK>;
-    constexpr int smem = kLogprobRing<DT, THREADS, MASK>;
-    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, THREADS, smem)) return SGEMM_ERR_LAUNCH;
-    const dim3 grid(parts, (unsigned)std::min(a.T, 1024 / THREADS * dev.sms));
-    return launch(kernel, grid, dim3(THREADS), smem, stream, parts, a);
-}
-
-template <int DT, bool MASK>
-int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t stream) {
-    // few rows are shared by clusters of up to 8 blocks, until there are two blocks per SM; many
-    // are walked by the blocks the SMs hold
-    unsigned parts = 1;
-    while (parts < 8 && (int64_t)a.T * parts * 2 <= 2 * dev.sms && a.V / (int)(parts * 2) >= 2048) parts *= 2;
-    // two warps a row where a row is short, or nothing but its sums is wanted: what a row costs a
-    // warp beside its columns weighs less (64000 x 1000 302 -> 81 us, 4096 x 50001 without
-    // alternatives 91 -> 80 us; with five alternatives 104 -> 110 us)
-    if (parts == 1 && !a.top) return launch_logprobs<DT, 64, false, MASK>(a, 1, dev, stream);
-    if (parts == 1 && a.V < 16384) return launch_logprobs<DT, 64, true, MASK>(a, 1, dev, stream);
-    // four warps for longer rows with alternatives, where there are two for each block that the SMs
-    // hold (4096 x 50001 104 -> 89 us; 2000 x 32000 with 20 alternatives 44 -> 49 us), and while
-    // the columns that may be alternatives are few, which grows with top and with what a thread
-    // sees of a row (4096 x 100001 with 5 alternatives 173 -> 171 us, with 20 205 -> 256 us)
-    if (parts == 1 && a.T >= 2 * 8 * dev.sms && (int64_t)a.top * a.V <= 1 << 20)
-        return launch_logprobs<DT, 128, true, MASK>(a, 1, dev, stream);
-    return a.top ? launch_logprobs<DT, 256, true, MASK>(a, parts, dev, stream)
-                 : launch_logprobs<DT, 256, false, MASK>(a, parts, dev, stream);
-}
-
 template <int DT, int VW>
 int launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t stream) {
     constexpr int THREADS = 256, U = VW > 1 ? 4 : 8;
@@ -147,31 +118,7 @@ int launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t stream) {
     return launch(logprobs_grad_kernel<DT, VW, THREADS, U, false>, grid, dim3(THREADS), 0, stream, 1, a);
 }
 
-bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, const int32_t *mask, int ldm,
-                       int mask_rows) {
-    if (T < 0 || V < 0 || T > kMaxRows || V > kMaxRows || !dtype_ok(dtype)) return false;
-    // (a larger scale's product with log2(e) would not be finite)
-    if (!(scale > 0.f && scale <= 0x1p127f) || mask_rows < 0) return false;
-    if (T == 0) return true;
-    if (V > 0 && !z.ok(V, dtype_size(dtype))) return false;
-    if ((mask != nullptr) != (mask_rows > 0)) return false;
-    if (!mask) return true;
-    return aligned(mask, 4) && (mask_rows == 1 || mask_rows == T) && (mask_rows == 1 || ldm >= (V + 31) / 32);
-}
-
 }  // namespace
-
-int sgemm_host::logprobs(const LogprobArgs &a, int dtype, const Device &dev, cudaStream_t stream) {
-    return by_dtype(dtype, [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        return a.mask ? logprobs_by_length<DT, true>(a, dev, stream) : logprobs_by_length<DT, false>(a, dev, stream);
-    });
-}
-
-bool sgemm_host::logprobs_shape_ok(int T, int V, int dtype, const void *z, int ldz, float scale, const int32_t *mask, int ldm,
-                                   int mask_rows) {
-    return ::logprobs_shape_ok(T, V, dtype, Rows{z, ldz}, scale, mask, ldm, mask_rows);
-}
 
 extern "C" {
 
@@ -300,7 +247,10 @@ int sgemm_logprobs(int T, int V, int dtype, const void *logits, int ldz, float s
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     const LogprobArgs a{T, V, logits, ldz, scale, mask, mask_rows > 1 ? ldm : 0, target, logprob, entropy, lse, top,
                         top_logprob, top_id, nullptr, nullptr, nullptr};
-    return sgemm_host::logprobs(a, dtype, dev, stream);
+    return by_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return mask ? logprobs_by_length<DT, true, false>(a, dev, stream) : logprobs_by_length<DT, false, false>(a, dev, stream);
+    });
 }
 
 int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz, float scale, const int32_t *mask,

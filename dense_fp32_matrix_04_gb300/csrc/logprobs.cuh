@@ -56,7 +56,8 @@ struct LogprobArgs {
     float *top_logprob;
     int32_t *top_id;
     // For beams (beam.cuh): rows that take no part are passed over, top_logprob receives the
-    // logits themselves, and `reference` each row's largest logit m and its sum s.  Null otherwise.
+    // logits themselves, and `reference` each row's largest logit m and its sum s; logprob, entropy and
+    // lse are null.
     const float *score;
     const uint8_t *finished;
     float2 *reference;
@@ -116,8 +117,10 @@ __device__ __forceinline__ bool better(float v, int id, float v2, int id2) {
     return v > v2 || (v == v2 && id < id2);
 }
 
-// The running sums of a thread, or of several joined.
-struct SoftmaxState {
+// The running sums of a thread, or of several joined.  ENTROPY: s1 is wanted too (without it a
+// term of -infinity is a plain 0).
+template <bool ENTROPY>
+struct SoftmaxSums {
     float m = -INFINITY, M = -INFINITY, s = 0.f, s1 = 0.f;
     // (a product of its own: fused into a difference it would not be the M that the terms saw)
     __device__ static float reference(float m, float c) { return __fmul_rn(m, c); }
@@ -133,7 +136,7 @@ struct SoftmaxState {
     __device__ void raise(float m2, float c) {
         if (m2 > m) {
             const float M2 = reference(m2, c), d = step(m, M, m2, M2, c), f = exp2_approx(d);
-            s1 = m == -INFINITY ? s1 : f * fmaf(s, fmaxf(d, -1000.f), s1);
+            if (ENTROPY) s1 = m == -INFINITY ? s1 : f * fmaf(s, fmaxf(d, -1000.f), s1);
             s *= f;
             m = m2;
             M = M2;
@@ -151,7 +154,11 @@ struct SoftmaxState {
                 const float2 x = t.both();
                 const F2 e(exp2_approx(x.x), exp2_approx(x.y));
                 sum = sum + e;
-                sum1 = fma(e, t, sum1);
+                if (ENTROPY) sum1 = fma(e, t, sum1);
+            }
+            if (!ENTROPY) {
+                s = sum.sum();
+                return;
             }
             const float s1_new = sum1.sum();
             if (s1_new == s1_new) {
@@ -165,7 +172,7 @@ struct SoftmaxState {
         for (int j = 0; j < N; ++j) {
             const float t = usual(M) ? fmaf(v[j], c, -M) : (v[j] - m) * c, e = exp2_approx(t);
             s += e;
-            s1 = fmaf(e, fmaxf(t, -1000.f), s1);
+            if (ENTROPY) s1 = fmaf(e, fmaxf(t, -1000.f), s1);
         }
     }
     // joins the states of the warp's lanes: the largest maximum first, then plain sums relative to it
@@ -175,15 +182,16 @@ struct SoftmaxState {
         for (int o = 16; o; o >>= 1) m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
         if (m > -INFINITY) {  // otherwise s is 0, or NaN
             const float d = step(m, M, m2, reference(m2, c), c), f = exp2_approx(d);
-            s1 = f * fmaf(s, fmaxf(d, -1000.f), s1);
+            if (ENTROPY) s1 = f * fmaf(s, fmaxf(d, -1000.f), s1);
             s *= f;
         }
         m = m2;
         M = reference(m2, c);
         s = warp_sum(s);
-        s1 = warp_sum(s1);
+        if (ENTROPY) s1 = warp_sum(s1);
     }
 };
+using SoftmaxState = SoftmaxSums<true>;
 
 // Exchanges (v, id) with the lane `stride` away, keeping the better of the two
 // where `keep_better` holds and the other elsewhere.
@@ -233,8 +241,8 @@ struct WarpTop {
     }
 };
 
-// The k-th largest (k = 1 .. 32) of the lanes' values: a bitonic sort over lanes.
-__device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
+// The lanes' values in descending order: a bitonic sort.
+__device__ __forceinline__ float warp_sorted(float x, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
@@ -242,7 +250,19 @@ __device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
             const float o = __shfl_xor_sync(0xffffffffu, x, stride);
             x = ((lane & stride) == 0) == ((lane & size) == 0) ? fmaxf(x, o) : fminf(x, o);
         }
-    return __shfl_sync(0xffffffffu, x, k - 1);
+    return x;
+}
+
+// The k-th largest (k = 1 .. 32) of the lanes' values.
+__device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
+    return __shfl_sync(0xffffffffu, warp_sorted(x, lane), k - 1);
+}
+
+// The same of two values a lane: sorted lists of 32 joined by taking the larger of each one's i-th and
+// the other's i-th from the end, which leaves the 32 largest.
+__device__ __forceinline__ float warp_kth_largest(float x, float y, int k, int lane) {
+    const float a = __shfl_sync(0xffffffffu, warp_sorted(x, lane), lane), b = __shfl_sync(0xffffffffu, warp_sorted(y, lane), 31 - lane);
+    return __shfl_sync(0xffffffffu, warp_sorted(fmaxf(a, b), lane), k - 1);
 }
 
 // Columns that may be among a row's best, in any order, up to CAP of them.
@@ -286,9 +306,12 @@ constexpr int kLogprobRing = kLogprobDepth * kLogprobPieces<DT> * THREADS * (MAS
 // THREADS: 256, or fewer where a row gives a thread so few columns that what a
 // row costs a warp beside them counts.  Registers for 1024 threads an SM (768
 // where it takes more).
-template <int DT, int THREADS, bool TOP, bool MASK>
+// BEAM: for beams (beam.cuh), the sums and the best columns alone; see LogprobArgs.
+template <int DT, int THREADS, bool TOP, bool MASK, bool BEAM>
 __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !TOP ? 768 : 1024) / THREADS)
     logprobs_kernel(const LogprobArgs a) {
+    using State = SoftmaxSums<!BEAM>;
+    if (BEAM) griddep_launch_dependents();  // the kernel that joins the beams, which waits for this one
     using E = Elem<DT>;
     using type = typename E::type;
     constexpr int VEC = E::VEC, WARPS = THREADS / 32, U = kLogprobPieces<DT>,
@@ -300,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
     __shared__ Candidates<TOP ? kTopBuffer : 1> found;
     __shared__ uint8_t again[TOP ? THREADS : 1];
     __shared__ int again_count;
-    __shared__ float group_max[32];
+    __shared__ float group_max[32], fine_max[TOP ? 64 : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = gridDim.x, part = blockIdx.x, log_parts = __ffs(parts) - 1;  // parts: a power of two
     const float c = a.scale * kLog2e;
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         return r;
     };
     auto passed_over = [&](int64_t t) {
-        return a.score && !row_takes_part(a.score[t], a.finished ? a.finished + t : nullptr);
+        return BEAM && !row_takes_part(a.score[t], a.finished ? a.finished + t : nullptr);
     };
     // the chunk that is copied next: of row `ahead_t`, from piece `ahead_p` on
     int64_t ahead_t = blockIdx.y;
@@ -369,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         const int32_t *mask = row.mask;
         const int head = row.head, tail0 = head + row.pieces * VEC;
 
-        SoftmaxState st;
+        State st;
         // adds the n columns v of this thread, -infinity where there is none; top: their largest
         auto add = [&](const float *v, float top, auto n_const) {
             constexpr int n = decltype(n_const)::value;
@@ -436,7 +459,18 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             if (threadIdx.x == 0) found.count = again_count = 0;
             if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
             __syncthreads();
-            const float floor_v = warp_kth_largest(group_max[lane], a.top, lane);
+            float floor_v = warp_kth_largest(group_max[lane], a.top, lane);
+            if (a.top > 16 && WARPS >= 2) {
+                // of as many groups as alternatives the smallest maximum would be the bound: twice as many
+                // are compared, and the bound is about their median
+                __syncthreads();
+                float f = thread_max;
+#pragma unroll
+                for (int o = 64 / WARPS; o < 32; o <<= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o));
+                if (lane < 64 / WARPS) fine_max[warp * (64 / WARPS) + lane] = f;
+                __syncthreads();
+                floor_v = warp_kth_largest(fine_max[lane], fine_max[32 + lane], a.top, lane);
+            }
             if (thread_max >= floor_v && thread_max > -INFINITY) again[atomicAdd(&again_count, 1)] = (uint8_t)threadIdx.x;
             if (outside.v >= floor_v && outside.v > -INFINITY) found.push(outside.v, outside.id);
             __syncthreads();
@@ -498,11 +532,11 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             warp_state[2][warp] = st.s1;
         }
         __syncthreads();
-        SoftmaxState all;
+        State all;
         if (warp == 0) {
             if (lane < WARPS) {
                 all.m = warp_state[0][lane];
-                all.M = SoftmaxState::reference(all.m, c);
+                all.M = State::reference(all.m, c);
                 all.s = warp_state[1][lane];
                 all.s1 = warp_state[2][lane];
             }
@@ -518,11 +552,11 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             cluster_sync();
             if (part == 0) {
                 if (warp == 0) {
-                    all = SoftmaxState{};
+                    all = State{};
                     if (lane < parts) {
                         const uint32_t s = dsmem_map(smem_addr(block_state), (uint32_t)lane);
                         all.m = __uint_as_float(dsmem_ld_u32(s));
-                        all.M = SoftmaxState::reference(all.m, c);
+                        all.M = State::reference(all.m, c);
                         all.s = __uint_as_float(dsmem_ld_u32(s + 4));
                         all.s1 = __uint_as_float(dsmem_ld_u32(s + 8));
                     }
@@ -555,10 +589,10 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
         if (part == 0 && warp == 0) {
             const bool none = all.m == -INFINITY && !(all.s != all.s);
             // ln of the sum relative to exactly m
-            const float off = SoftmaxState::usual(all.M) ? -fmaf(all.m, c, -all.M) : 0.f;
+            const float off = State::usual(all.M) ? -fmaf(all.m, c, -all.M) : 0.f;
             const float log_s = logf(all.s), log_sum = fmaf(kLn2, off, log_s);
             if (lane == 0) {
-                if (a.reference) a.reference[t] = make_float2(all.m, all.s);
+                if (BEAM) a.reference[t] = make_float2(all.m, all.s);
                 if (a.lse) a.lse[t] = none ? -INFINITY : fmaf(all.m, a.scale, log_sum);
                 if (a.entropy) a.entropy[t] = none ? 0.f : log_s - kLn2 * (all.s1 / all.s);
                 if (a.logprob) {
@@ -578,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
                     const Candidate e = block_list[lane];
                     const bool bad = all.s != all.s;
                     const bool has = e.v > -INFINITY && !bad;
-                    a.top_logprob[t * a.top + lane] = a.reference ? e.v : bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_sum) : -INFINITY;
+                    a.top_logprob[t * a.top + lane] = BEAM ? e.v : bad ? NAN : has ? fmaf(e.v - all.m, a.scale, -log_sum) : -INFINITY;
                     a.top_id[t * a.top + lane] = has ? e.id : -1;
                 }
             }
