@@ -41,24 +41,36 @@ int by_block(int block, F &&f) {
 
 // ---------------------------------------------------------------- quantising
 
-template <int DT, int VW, int BLOCK>
-int launch_quantize(const Fp4Rows &a, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
+template <int DT, bool ALIGNED, int BLOCK, int EACH, int DEPTH>
+int launch_quantize_rows(const Fp4Rows &a, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
     using type = typename Elem<DT>::type;
-    const type *from = static_cast<const type *>(x);
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    if (a.K > 16384) {
-        const auto kernel = quantize_fp4_wide_kernel<DT, VW, BLOCK>;
-        const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, 1024, 0);
-        if (!fit) return SGEMM_ERR_LAUNCH;
-        return launch(kernel, dim3((unsigned)std::min(a.rows, dev.sms * fit)), dim3(1024), 0, stream, 1, a, from, ldx);
-    }
-    const auto kernel = quantize_fp4_kernel<DT, VW, BLOCK>;
-    const int threads = (a.K + 511) / 512 * 32;  // 16 columns a thread
+    const auto kernel = quantize_fp4_kernel<DT, ALIGNED, BLOCK, EACH, DEPTH>;
+    const int threads = (a.K + 512 * EACH - 1) / (512 * EACH) * 32;
     const dim3 block(threads, threads == 32 ? 4 : 1);
-    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, (int)(block.x * block.y), 0);
+    const int smem = DEPTH * EACH * Fp4Piece<DT, ALIGNED>::WARP_PIECES * 16 * (int)(block.x * block.y / 32);
+    const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, (int)(block.x * block.y), smem);
     if (!fit) return SGEMM_ERR_LAUNCH;
     const int64_t groups = ((int64_t)a.rows + block.y - 1) / block.y;
-    return launch(kernel, dim3((unsigned)std::min<int64_t>(groups, (int64_t)dev.sms * fit)), block, 0, stream, 1, a, from, ldx);
+    return launch(kernel, dim3((unsigned)std::min<int64_t>(groups, (int64_t)dev.sms * fit)), block, (size_t)smem, stream, 1, a,
+                  static_cast<const type *>(x), ldx);
+}
+
+template <int DT, bool ALIGNED, int BLOCK>
+int launch_quantize(const Fp4Rows &a, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
+    using type = typename Elem<DT>::type;
+    if (a.K > 16384) {
+        static std::atomic<int> regs[sgemm_host::kMaxDevices];
+        const auto kernel = quantize_fp4_wide_kernel<DT, ALIGNED, BLOCK>;
+        const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, 1024, 0);
+        if (!fit) return SGEMM_ERR_LAUNCH;
+        return launch(kernel, dim3((unsigned)std::min(a.rows, dev.sms * fit)), dim3(1024), 0, stream, 1, a,
+                      static_cast<const type *>(x), ldx);
+    }
+    if (a.K <= 4096) return launch_quantize_rows<DT, ALIGNED, BLOCK, 1, 4>(a, x, ldx, dev, stream);
+    // four rows of more than 8192 FP32 columns do not fit shared memory
+    return DT == SGEMM_F32 && a.K > 8192 ? launch_quantize_rows<DT, ALIGNED, BLOCK, 2, DT == SGEMM_F32 ? 2 : 4>(a, x, ldx, dev, stream)
+                                         : launch_quantize_rows<DT, ALIGNED, BLOCK, 2, 4>(a, x, ldx, dev, stream);
 }
 
 int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
@@ -67,8 +79,8 @@ int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx,
         const bool vec = a.K % VEC == 0 && aligned(x, 16) && ldx % VEC == 0;
         return by_block(block, [&](auto b) {
             constexpr int BLOCK = decltype(b)::value;
-            return vec ? launch_quantize<DT, VEC, BLOCK>(a, x, ldx, dev, stream)
-                       : launch_quantize<DT, 1, BLOCK>(a, x, ldx, dev, stream);
+            return vec ? launch_quantize<DT, true, BLOCK>(a, x, ldx, dev, stream)
+                       : launch_quantize<DT, false, BLOCK>(a, x, ldx, dev, stream);
         });
     });
 }
@@ -151,33 +163,27 @@ int launch_pair(const Fp4Args &p, const Fp4Operands &o, bool early, const Device
                          stream, 2, tw, tx, tws, txs, p, dev.err_word, sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
 }
 
-// Up to four tokens whose codes fit shared memory go to the kernel that reads whole rows.
-bool takes_rows(int M, int K) {
-    return M <= kFp4RowsTokens && fp4_rows_smem(M == 3 ? 4 : M, K) <= kFp4RowsSmem;
-}
+// One token whose codes fit shared memory goes to the kernel that reads whole rows (two by
+// 4096 x 4096 took 7.6 us there, on the tensor cores 7.3; one 5.0 and 6.8).
+bool takes_rows(int M, int K) { return M == 1 && fp4_rows_smem(K) <= kFp4RowsSmem; }
 
-template <int MT, int XT, int BLOCK>
+template <int XT, int BLOCK>
 int launch_rows(const Fp4RowsArgs &a, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = fp4_rows_kernel<MT, XT, BLOCK>;
-    const int smem = (int)fp4_rows_smem(MT, a.p.K);
+    const auto kernel = fp4_rows_kernel<XT, BLOCK>;
+    const int smem = (int)fp4_rows_smem(a.p.K);
     const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, kFp4RowsThreads, smem);
     if (!fit) return SGEMM_ERR_LAUNCH;
-    const int groups = (a.p.N + 127) / 128 * 16;
+    const int groups = (a.p.N + 127) / 128 * 8;
     return launch(kernel, dim3((unsigned)std::min(groups, dev.sms * fit)), dim3(kFp4RowsThreads), (size_t)smem, stream, 1, a);
 }
 
-// xtype -1: the tokens are codes.
+// xtype -1: the token is codes.
 int rows_product(const Fp4RowsArgs &a, int xtype, int block, const Device &dev, cudaStream_t stream) {
     return by_block(block, [&](auto b) {
         constexpr int BLOCK = decltype(b)::value;
-        auto by_tokens = [&](auto xt) {
-            constexpr int XT = decltype(xt)::value;
-            return a.p.M <= 1   ? launch_rows<1, XT, BLOCK>(a, dev, stream)
-                   : a.p.M <= 2 ? launch_rows<2, XT, BLOCK>(a, dev, stream)
-                                : launch_rows<4, XT, BLOCK>(a, dev, stream);
-        };
-        return xtype < 0 ? by_tokens(std::integral_constant<int, -1>{}) : by_dtype(xtype, by_tokens);
+        if (xtype < 0) return launch_rows<-1, BLOCK>(a, dev, stream);
+        return by_dtype(xtype, [&](auto xt) { return launch_rows<decltype(xt)::value, BLOCK>(a, dev, stream); });
     });
 }
 
@@ -286,7 +292,7 @@ int sgemm_fp4(int M, int N, int K, int block, const unsigned char *A, int lda, c
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     const Fp4Args p{M, N, K, a_block, b_block, a_scale, b_scale, bias, C, ldc, ctype};
     if (K == 0) return empty_product(p, dev, stream);
-    if (takes_rows(M, K)) return rows_product({p, A, B, lda, ldb, nullptr, 0}, -1, block, dev, stream);
+    if (takes_rows(M, K)) return rows_product({p, A, B, ldb, nullptr}, -1, block, dev, stream);
     return product(p, {A, B, lda, ldb}, block, false, dev, stream);
 }
 
@@ -316,7 +322,7 @@ int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int
     if (sgemm_host::device(dev) != SGEMM_OK) return SGEMM_ERR_DEVICE;
     Fp4Args p{M, N, K, nullptr, b_block, nullptr, b_scale, bias, C, ldc, ctype};
     if (K == 0) return empty_product(p, dev, stream);
-    if (takes_rows(M, K)) return rows_product({p, nullptr, B, 0, ldb, X, ldx}, xtype, block, dev, stream);
+    if (takes_rows(M, K)) return rows_product({p, nullptr, B, ldb, X}, xtype, block, dev, stream);
     uint8_t *codes = static_cast<uint8_t *>(workspace), *tiles = codes + up256((int64_t)M * code_pitch(K));
     float *scale = block == 16 ? reinterpret_cast<float *>(tiles + up256(tile_bytes(M, K, block))) : nullptr;
     const int st = quantize({M, M, K, codes, code_pitch(K), tiles, scale}, xtype, block, X, ldx, dev, stream);

@@ -1,16 +1,17 @@
-// The product of 4-bit operands for up to four tokens: the time is that of reading
-// B, its codes and scales, once.
+// The product of 4-bit operands for one token: the time is that of reading B, its
+// codes and scales, once.
 //
-// A warp takes a row of B at a time, 512 contiguous bytes of codes a load.  Codes
-// become FP16 numbers, two an instruction, and are multiplied with the tokens' codes,
-// which are FP16 in shared memory, in packed FMAs: eight products of at most 36, in
-// quarters, in each half, are exact (288 is 1152 quarters, below the 2048 that FP16
-// counts to).  The blocks' sums are then scaled and added in FP32.
+// A warp takes two rows of B at a time, 512 contiguous bytes of codes of each a load.
+// Codes become FP16 numbers, two an instruction, and are multiplied with the token's
+// codes, which are FP16 in shared memory (read once for both rows: read for each, they
+// took longer than B), in packed FMAs: eight products of at most 36, in quarters, in each
+// half, are exact (288 is 1152 quarters, below the 2048 that FP16 counts to).  The blocks'
+// sums are then scaled and added in FP32.
 //
-// The scales of B lie in tiles of 128 rows by 4 blocks, where 32 bytes hold a word
-// each of the rows 2 i, 2 i + 1 and those 32, 64 and 96 further on: the eight warps of a
-// block take such rows, so that what one reads of them serves all.  Tokens that come
-// unquantised are quantised by every block itself while its first row of B is on its way.
+// The scales of B lie in tiles of 128 rows by 4 blocks, where 32 bytes hold a word each of
+// the rows 2 i, 2 i + 1 and those 32, 64 and 96 further on: four warps of a block take these
+// pairs, so that what one reads of them serves all.  A token that comes unquantised is
+// quantised by every block itself while its first rows of B are on their way.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -23,18 +24,17 @@
 
 namespace sgemm {
 
-constexpr int kFp4RowsTokens = 4;
 constexpr int kFp4RowsThreads = 256;
 constexpr int kFp4RowsPieces = 4;    // loads of 16 bytes a lane has in flight
 constexpr int kFp4RowsChunk = 1024;  // columns of a warp's load
 constexpr int kFp4RowsSmem = 200 * 1024;
 
-// Columns of a token in shared memory: whole loads.
+// Columns of the token in shared memory: whole loads.
 __host__ __device__ constexpr int64_t fp4_rows_columns(int K) { return ((int64_t)K + kFp4RowsChunk - 1) / kFp4RowsChunk * kFp4RowsChunk; }
-// Bytes of MT tokens: FP16 codes, an FP32 scale for every 16 columns (blocks of 32: twice the same).
-__host__ __device__ constexpr int64_t fp4_rows_smem(int MT, int K) { return MT * fp4_rows_columns(K) / 16 * 36; }
+// Its bytes: FP16 codes, an FP32 scale for every 16 columns (blocks of 32: twice the same).
+__host__ __device__ constexpr int64_t fp4_rows_smem(int K) { return fp4_rows_columns(K) / 16 * 36; }
 
-// Place of columns c .. c + 7 (c a multiple of 8) among a token's codes: within a chunk, the four
+// Place of columns c .. c + 7 (c a multiple of 8) among the token's codes: within a chunk, the four
 // pieces of a lane's 32 columns are 32 pieces apart, so that lanes read beside each other.
 __device__ __forceinline__ int fp4_rows_place(int c) {
     return (c & ~(kFp4RowsChunk - 1)) + ((c >> 3 & 3) * 32 + (c >> 5 & 31)) * 8;
@@ -82,161 +82,143 @@ __device__ __forceinline__ uint32_t fp4_load_scales(const uint8_t *tiles, int64_
 struct Fp4RowsArgs {
     Fp4Args p;
     const uint8_t *A, *B;
-    int64_t lda, ldb;
-    const void *X;  // tokens that are not quantised yet
-    int64_t ldx;
+    int64_t ldb;
+    const void *X;  // the token, where it is not quantised yet
 };
 
-// XT: the tokens are codes (-1) or values of that element type.
-template <int MT, int XT, int BLOCK>
-__global__ void __launch_bounds__(kFp4RowsThreads, MT == 1 ? 4 : MT == 2 ? 3 : 2) fp4_rows_kernel(const Fp4RowsArgs a) {
+// XT: the token is codes (-1) or values of that element type.
+template <int XT, int BLOCK>
+__global__ void __launch_bounds__(kFp4RowsThreads, 3) fp4_rows_kernel(const Fp4RowsArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float slots[kFp4RowsThreads / 32], row_scales[MT];
+    __shared__ float slots[kFp4RowsThreads / 32];
     constexpr int WARPS = kFp4RowsThreads / 32;
     static_assert(WARPS == 8);
     const Fp4Args &p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, K = p.K;
-    const int columns = (int)fp4_rows_columns(K), n_tiles = fp4_tiles(K, BLOCK), bytes = (K + 1) / 2;
-    __half *codes = reinterpret_cast<__half *>(smem);                         // MT x columns
-    float *scales = reinterpret_cast<float *>(codes + MT * columns);          // MT x columns / 16
-    const int groups = (p.N + 127) / 128 * 16;
+    const int columns = (int)fp4_rows_columns(K), n_tiles = fp4_tiles(K, BLOCK);
+    __half *codes = reinterpret_cast<__half *>(smem);
+    float *scales = reinterpret_cast<float *>(codes + columns);
+    // a group is 16 rows, pairs 2 i and 2 i + 2 of 128 and the three that share their scales' sectors
+    const int groups = (p.N + 127) / 128 * 8;
     int group = blockIdx.x;
-    auto row_of = [&](int g) { return g / 16 * 128 + g % 16 * 2 + (warp & 1) + (warp >> 1) * 32; };
+    auto row_of = [&](int g) { return g / 8 * 128 + g % 8 * 4 + (warp >> 2) * 2 + (warp & 3) * 32; };
 
-    uint4 w[kFp4RowsPieces];
-    uint32_t ws[kFp4RowsPieces];
+    uint4 w[2][kFp4RowsPieces];
+    uint32_t ws[2][kFp4RowsPieces];
     auto load = [&](int row, int c0) {
 #pragma unroll
-        for (int j = 0; j < kFp4RowsPieces; ++j) {
-            const int c = c0 + kFp4RowsChunk * j + 32 * lane;
-            const bool in = row < p.N && c < K;
-            // (rows are whole 16-byte pieces; what lies behind K meets tokens of 0)
-            w[j] = in ? __ldg(reinterpret_cast<const uint4 *>(a.B + row * a.ldb + c / 2)) : make_uint4(0, 0, 0, 0);
-            ws[j] = in ? fp4_load_scales<BLOCK>(p.b_tiles, row, c / 32, n_tiles) : 0u;
-        }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < kFp4RowsPieces; ++j) {
+                const int c = c0 + kFp4RowsChunk * j + 32 * lane;
+                const bool in = row + r < p.N && c < K;
+                // (rows are whole 16-byte pieces; what lies behind K meets a token of 0)
+                w[r][j] = in ? __ldg(reinterpret_cast<const uint4 *>(a.B + (row + r) * a.ldb + c / 2)) : make_uint4(0, 0, 0, 0);
+                ws[r][j] = in ? fp4_load_scales<BLOCK>(p.b_tiles, row + r, c / 32, n_tiles) : 0u;
+            }
     };
     int row = row_of(group);
     load(row, 0);
 
-    auto put = [&](int m, int c, const __half2 (&h)[4]) {
-        *reinterpret_cast<uint4 *>(codes + m * columns + fp4_rows_place(c)) = *reinterpret_cast<const uint4 *>(h);
+    auto put = [&](int c, const __half2 (&h)[4]) {
+        *reinterpret_cast<uint4 *>(codes + fp4_rows_place(c)) = *reinterpret_cast<const uint4 *>(h);
     };
+    float row_scale = 1.f;
     if constexpr (XT < 0) {
-        for (int m = 0; m < MT; ++m)
-            for (int c = 32 * tid; c < columns; c += 32 * kFp4RowsThreads) {
-                const bool in = m < p.M && c < K;
-                const uint4 q = in ? __ldg(reinterpret_cast<const uint4 *>(a.A + m * a.lda + c / 2)) : make_uint4(0, 0, 0, 0);
-                uint32_t word[4] = {q.x, q.y, q.z, q.w};
-                const float2 s = fp4_scale_values<BLOCK>(in ? fp4_load_scales<BLOCK>(p.a_tiles, m, c / 32, n_tiles) : 0u);
+        const int bytes = (K + 1) / 2;
+        for (int c = 32 * tid; c < columns; c += 32 * kFp4RowsThreads) {
+            const bool in = c < K;
+            const uint4 q = in ? __ldg(reinterpret_cast<const uint4 *>(a.A + c / 2)) : make_uint4(0, 0, 0, 0);
+            const uint32_t word[4] = {q.x, q.y, q.z, q.w};
+            *reinterpret_cast<float2 *>(scales + c / 16) =
+                fp4_scale_values<BLOCK>(in ? fp4_load_scales<BLOCK>(p.a_tiles, 0, c / 32, n_tiles) : 0u);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // bytes behind the row's end may hold anything
-                    const int left = bytes - c / 2 - 4 * i;
-                    word[i] = left >= 4 ? word[i] : left > 0 ? word[i] & ((1u << 8 * left) - 1) : 0u;
-                    __half2 h[4];
-                    e2m1x8_to_f16(word[i], h);
-                    put(m, c + 8 * i, h);
-                }
-                *reinterpret_cast<float2 *>(scales + (m * columns + c) / 16) = s;
+            for (int i = 0; i < 4; ++i) {
+                // bytes behind the row's end may hold anything
+                const int left = bytes - c / 2 - 4 * i;
+                __half2 h[4];
+                e2m1x8_to_f16(left >= 4 ? word[i] : left > 0 ? word[i] & ((1u << 8 * left) - 1) : 0u, h);
+                put(c + 8 * i, h);
             }
-        if (tid < MT) row_scales[tid] = p.a_scale && tid < p.M ? p.a_scale[tid] : 1.f;
-    } else {
-        // the block's warps are shared out to the tokens, which are quantised side by side; a thread takes
-        // 16 columns at a time
-        using E = Elem<XT < 0 ? 0 : XT>;
-        constexpr int SHARE = WARPS / MT, DT = XT < 0 ? 0 : XT;
-        const int m = warp / SHARE, first = (warp % SHARE) * 32 + lane, step = SHARE * 32;
-        const typename E::type *x = static_cast<const typename E::type *>(a.X) + min(m, p.M - 1) * a.ldx;
-        const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
-        auto values = [&](int c, float (&v)[16]) {
-            if (vec && c + 16 <= K) {
-                Fp4Piece<DT, E::VEC> piece;
-                piece.load(x, c, K);
-                return piece.unpack(v);
-            }
-            Fp4Piece<DT, 1> piece;
-            piece.load(x, c, K);
-            return piece.unpack(v);
-        };
-        float v[16];
-        uint32_t top = 0;
-        if constexpr (BLOCK == 16) {
-            for (int i = first; 16 * i < K; i += step) top = max(top, values(16 * i, v));
-            top = warp_max(top);
-            if (lane == 0) slots[warp] = __uint_as_float(top);
-            __syncthreads();
-            for (int i = 0; i < SHARE; ++i) top = max(top, __float_as_uint(slots[m * SHARE + i]));
         }
-        const Fp4Row r(top);
-        for (int i = first; 16 * i < columns; i += step) {
-            const int c = 16 * i;
-            const uint32_t most = values(c, v);
+        if (p.a_scale) row_scale = *p.a_scale;
+    } else {
+        // a thread takes 16 columns at a time
+        constexpr int DT = XT < 0 ? 0 : XT;
+        const typename Elem<DT>::type *x = static_cast<const typename Elem<DT>::type *>(a.X);
+        Fp4Piece<DT, false> piece;
+        F2 v[8];
+        uint32_t top = 0, most = 0;
+        if constexpr (BLOCK == 16) {
+            // (the columns that the loop below begins with come last, and stay)
+            for (int c = 16 * tid + (columns - 1) / (16 * kFp4RowsThreads) * (16 * kFp4RowsThreads); c >= 0; c -= 16 * kFp4RowsThreads) {
+                piece.load(x, c, K);
+                top = piece.unpack(x, c, K, v);
+                most = max(most, top);
+            }
+            most = warp_max(most);
+            if (lane == 0) slots[warp] = __uint_as_float(most);
+            __syncthreads();
+            for (int i = 0; i < WARPS; ++i) most = max(most, __float_as_uint(slots[i]));
+        }
+        const Fp4Row r(most);
+        for (int c = 16 * tid; c < columns; c += 16 * kFp4RowsThreads) {
+            if (BLOCK == 32 || c >= 16 * kFp4RowsThreads) {
+                piece.load(x, c, K);
+                top = piece.unpack(x, c, K, v);
+            }
             uint2 q;
-            const uint32_t s = fp4_encode<BLOCK>(v, most, r, q);
+            const uint32_t s = fp4_encode<BLOCK>(v, top, r, q);
             __half2 h[4];
             e2m1x8_to_f16(q.x, h);
-            put(m, c, h);
+            put(c, h);
             e2m1x8_to_f16(q.y, h);
-            put(m, c + 8, h);
-            float scale;
-            if constexpr (BLOCK == 16) scale = fp4_scale_values<16>(s).x;
-            else scale = e8m0_value(s);
-            scales[m * (columns / 16) + i] = scale;
+            put(c + 8, h);
+            if constexpr (BLOCK == 16) scales[c / 16] = fp4_scale_values<16>(s).x;
+            else scales[c / 16] = e8m0_value(s);
         }
-        if (warp % SHARE == 0 && lane == 0) row_scales[m] = BLOCK == 16 ? r.scale : 1.f;
+        if (BLOCK == 16) row_scale = r.scale();
     }
     __syncthreads();
 
     for (; group < groups; group += gridDim.x) {
-        float acc[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m] = 0.f;
+        float acc[2] = {0.f, 0.f};
         for (int c0 = 0; c0 < columns; c0 += kFp4RowsChunk * kFp4RowsPieces) {
             if (c0 > 0) load(row, c0);
 #pragma unroll
             for (int j = 0; j < kFp4RowsPieces; ++j) {
                 const int c = c0 + kFp4RowsChunk * j;
                 if (c >= columns) break;
-                __half2 b[16];
-                const uint32_t word[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                const float2 sx = *reinterpret_cast<const float2 *>(scales + c / 16 + 2 * lane);
+                __half2 s[2][2] = {};  // of each row, a half of the 32 columns each
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e2m1x8_to_f16(word[i], b + 4 * i);
-                const float2 sb = fp4_scale_values<BLOCK>(ws[j]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(codes + c + 8 * lane + i * 256);
+                    const __half2 *x = reinterpret_cast<const __half2 *>(&q);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const __half *x = codes + m * columns + c + 8 * lane;
-                    const float2 sx = *reinterpret_cast<const float2 *>(scales + (m * columns + c) / 16 + 2 * lane);
-                    float sum[2];
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t word = i == 0 ? w[r][j].x : i == 1 ? w[r][j].y : i == 2 ? w[r][j].z : w[r][j].w;
+                        __half2 b[4];
+                        e2m1x8_to_f16(word, b);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        __half2 s = __float2half2_rn(0.f);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 q = *reinterpret_cast<const uint4 *>(x + (2 * h + i) * 256);
-                            const __half2 *t = reinterpret_cast<const __half2 *>(&q);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s = __hfma2(b[8 * h + 4 * i + e], t[e], s);
-                        }
-                        const float2 f = __half22float2(s);
-                        sum[h] = f.x + f.y;
+                        for (int e = 0; e < 4; ++e) s[r][i / 2] = __hfma2(b[e], x[e], s[r][i / 2]);
                     }
-                    acc[m] = fmaf(sum[0], sb.x * sx.x, acc[m]);
-                    acc[m] = fmaf(sum[1], sb.y * sx.y, acc[m]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 sb = fp4_scale_values<BLOCK>(ws[r][j]), f = __half22float2(s[r][0]), g = __half22float2(s[r][1]);
+                    acc[r] = fmaf(f.x + f.y, sb.x * sx.x, acc[r]);
+                    acc[r] = fmaf(g.x + g.y, sb.y * sx.y, acc[r]);
                 }
             }
         }
-        const int done = row;
+        const int done = row + lane;
         row = row_of(group + gridDim.x);
         if (group + (int)gridDim.x < groups) load(row, 0);
-        float mine = 0.f;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float s = warp_sum(acc[m]);
-            if (lane == m) mine = s;
-        }
-        if (lane < MT && lane < p.M && done < p.N)
-            store_c(p.C, lane * p.ldc + done, p.ctype,
-                    fmaf(mine * row_scales[lane], p.b_scale ? p.b_scale[done] : 1.f, p.bias ? p.bias[done] : 0.f));
+        const float sums[2] = {warp_sum(acc[0]), warp_sum(acc[1])};
+        if (lane < 2 && done < p.N)
+            store_c(p.C, done, p.ctype,
+                    fmaf((lane ? sums[1] : sums[0]) * row_scale, p.b_scale ? p.b_scale[done] : 1.f, p.bias ? p.bias[done] : 0.f));
     }
 }
 

@@ -24,19 +24,6 @@ __device__ __forceinline__ uint2 i8x4_to_f16(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-// 16 bytes from byte `shift` (0 .. 15) of the 32 in a and b: by two words, by
-// one word, by bytes.
-__device__ __forceinline__ uint4 shift_codes(const uint4 &a, const uint4 &b, unsigned shift) {
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
-    const unsigned bits = 8 * (shift & 3);
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
 // Bytes k .. k + 15 of a row of K 8-bit integers, of any alignment; bytes from K
 // on are unspecified, and nothing beyond the 16-byte granule of the row's last
 // byte is read.  ALIGNED: the row starts on 16 bytes; k is a multiple of 16.
@@ -50,7 +37,7 @@ __device__ __forceinline__ uint4 load_codes(const int8_t *row, int k, int K) {
         const uint4 a = k < K ? __ldg(reinterpret_cast<const uint4 *>(lo)) : zero;
         const uint4 b = k < K && lo + 16 < reinterpret_cast<uintptr_t>(row) + K
                             ? __ldg(reinterpret_cast<const uint4 *>(lo + 16)) : zero;
-        return shift_codes(a, b, (unsigned)(reinterpret_cast<uintptr_t>(row) & 15));
+        return shift_bytes(a, b, (unsigned)(reinterpret_cast<uintptr_t>(row) & 15));
     }
 }
 

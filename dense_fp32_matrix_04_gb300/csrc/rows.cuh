@@ -82,6 +82,19 @@ __device__ __forceinline__ uint4 pack16(const float *v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes from byte `shift` (0 .. 15) of the 32 in a and b: by two words, by
+// one word, by bytes.
+__device__ __forceinline__ uint4 shift_bytes(const uint4 &a, const uint4 &b, unsigned shift) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+    const unsigned bits = 8 * (shift & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
 // A thread's part of a row: NV pieces of VW elements, piece v at column
 // (v * threads + thread) * VW.  VW is 16 bytes' worth (rows that are 16-byte
 // aligned and whole pieces long) or 1 (any other row).

@@ -307,8 +307,7 @@ int sgemm_fp4(int M, int N, int K, int block,
  * sgemm_quantize_fp4 of the M x K rows of X (xtype), then sgemm_fp4.
  *   workspace: sgemm_linear_fp4_workspace_size(M, K, block) bytes, 16-byte aligned,
  *       with contents that do not matter; calls that share one must not overlap on
- *       the GPU.  Up to four rows of up to 22528 columns (two of 45056, one of 90112)
- *       need none.
+ *       the GPU.  One row of up to 90112 columns needs none.
  */
 int sgemm_linear_fp4(int M, int N, int K, int xtype, const void *X, int ldx, int block,
                      const unsigned char *B, int ldb, const unsigned char *b_block, const float *b_scale,
