@@ -38,8 +38,9 @@ struct LayerNormGradArgs {
     void *dx;
     int64_t lddx;
     void *dw, *db;
-    float *partial;    // runners x 2 x D: dw, db
-    int runners;
+    float *partial;    // partials x 2 x D: dw, db
+    int runners;       // of the rows: blocks (or clusters), or for narrow rows the four warps of each
+    int partials;      // blocks (or clusters)
     int ranks, width;
 };
 
@@ -156,8 +157,9 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const LayerNormA
 // With h = (x - mean) rstd and u = dn w the gradient of a row is
 //     dx = dr + rstd (u - mean(u) - h mean(u h)),
 // two sums, taken at once, so a row costs one barrier.  dw = sum dn h and db = sum dn
-// over a runner's rows stay in registers; what a runner has of them goes to `partial`,
-// where a second kernel adds the runners in order.
+// over a runner's rows stay in registers; what a block has of them (of narrow rows its four
+// warps, added in shared memory: 16000 x 512 BF16 18.9 us without) goes to `partial`, where a
+// second kernel adds the blocks in order.
 template <int DT, bool ALIGNED, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNormGradArgs a) {
     using L = RowLayout<DT, ALIGNED, NV>;
@@ -165,6 +167,7 @@ __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNor
     constexpr int N = L::N, V = L::VEC, P = V / 2, S = kLayerNormGradStages;  // P pairs a piece
     extern __shared__ uint4 ring[];
     __shared__ float slots[RowReducer::SLOTS];
+    griddep_launch_dependents();  // the kernel that joins the runners' sums, which waits for this one
     RowReducer red{slots, (int)(blockDim.x >> 5), a.ranks};
     const int rank = (int)(blockIdx.x % (unsigned)a.ranks), group_id = (int)(blockIdx.x / (unsigned)a.ranks);
     const int c0 = rank * a.width;  // this block's columns
@@ -172,9 +175,9 @@ __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNor
     const int cols = c0 + l.col;
     const float inv_d = 1.f / (float)a.D;
     const int runner = group_id * blockDim.y + threadIdx.y;
-    if (runner >= a.runners) return;  // only where a warp is a runner: no barrier spans warps
     const RowRuns runs(a.T, a.runners);
-    const int begin = runs.first(runner), end = runs.first(runner + 1);
+    const bool idle = runner >= a.runners;  // only where a warp is a runner
+    const int begin = idle ? 0 : runs.first(runner), end = idle ? 0 : runs.first(runner + 1);
     const int arrays = a.dr ? 3 : 2, pieces = l.pieces(), stride = arrays * pieces;
     uint4 *mine = l.place(ring, S * arrays);
 
@@ -249,17 +252,33 @@ __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNor
             l.store(static_cast<type *>(a.dx) + ((int64_t)t * (int)a.lddx + cols), v * V, d);
         }
     }
+    // (a.D is no more than NV pieces of a warp where a block has several runners)
+    const bool shared = blockDim.y > 1;
+    float *sums = shared ? reinterpret_cast<float *>(ring) + threadIdx.y * 2 * a.D : a.partial + (int64_t)group_id * 2 * a.D;
+    if (shared) {
+        cp_async_wait<0>();
+        __syncthreads();  // nobody's rows are on their way, or read, any more
+    }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        float *p = a.partial + ((int64_t)runner * 2 * a.D + cols);
-        l.put(p, v * V, dw + v * P, false);
-        if (a.db) l.put(p + a.D, v * V, db + v * P, false);
+        l.put(sums + cols, v * V, dw + v * P, false);
+        if (a.db) l.put(sums + a.D + cols, v * V, db + v * P, false);
+    }
+    if (shared) {
+        __syncthreads();
+        const int n = (a.db ? 2 : 1) * a.D;
+        for (int i = threadIdx.y * 32 + threadIdx.x; i < n; i += 32 * blockDim.y) {
+            const float *from = reinterpret_cast<const float *>(ring) + i;
+            float sum = from[0];
+            for (int y = 1; y < (int)blockDim.y; ++y) sum += from[y * 2 * a.D];
+            a.partial[(int64_t)group_id * 2 * a.D + i] = sum;
+        }
     }
     if (a.ranks > 1) cluster_sync();
 }
 
-// Adds the runners' partial sums, blockIdx.y 0 of dw and 1 of db: 32 columns by
-// kLayerNormJoinSlices slices of the runners, each added in order with LOADS loads on
+// Adds the blocks' partial sums, blockIdx.y 0 of dw and 1 of db: 32 columns by
+// kLayerNormJoinSlices slices of the blocks, each added in order with LOADS loads on
 // their way, then the slices in order.
 constexpr int kLayerNormJoinSlices = 16;
 template <int DT>
@@ -270,11 +289,11 @@ __global__ void __launch_bounds__(32 * kLayerNormJoinSlices) layer_norm_grad_joi
     griddep_wait();
     float s = 0.f;
     if (c < a.D)
-        for (int b = threadIdx.y; b < a.runners; b += LOADS * SLICES) {
+        for (int b = threadIdx.y; b < a.partials; b += LOADS * SLICES) {
             float v[LOADS];
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
-                v[i] = b + i * SLICES < a.runners ? __ldcg(a.partial + ((int64_t)(b + i * SLICES) * 2 + k) * a.D + c) : 0.f;
+                v[i] = b + i * SLICES < a.partials ? __ldcg(a.partial + ((int64_t)(b + i * SLICES) * 2 + k) * a.D + c) : 0.f;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) s += v[i];
         }

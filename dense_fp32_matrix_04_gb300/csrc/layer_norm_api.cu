@@ -65,6 +65,7 @@ int launch_norm_grad(LayerNormGradArgs a, const Device &dev, cudaStream_t stream
     a.runners = std::min(sgemm_host::most_grad_runners(a.T, a.D, dev.sms),
                          std::max(1, dev.sms * fit / plan.ranks) * (int)plan.block.y);
     const unsigned groups = (a.runners + plan.block.y - 1) / plan.block.y;
+    a.partials = (int)groups;
     const int st = launch(kernel, dim3(groups * plan.ranks), plan.block, plan.smem, stream, (unsigned)plan.ranks, a);
     if (st != SGEMM_OK) return st;
     return launch<true>(layer_norm_grad_join_kernel<DT>, dim3((a.D + 31) / 32, a.db ? 2 : 1), dim3(32, kLayerNormJoinSlices), 0,
@@ -158,7 +159,7 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
     if (workspace_bytes < need) return SGEMM_ERR_INVALID_ARG;
     if (!clear({outs[0], outs[1], outs[2], Range(workspace, 1, (int64_t)need, (int64_t)need, 1)})) return SGEMM_ERR_ALIAS;
     const LayerNormGradArgs a{T, D, x, dn, dr, ldx, lddn, lddr, w, wdtype == SGEMM_F32, stats, dx, lddx, dw, db,
-                              static_cast<float *>(workspace), 0, 1, D};
+                              static_cast<float *>(workspace), 0, 0, 1, D};
     const bool vec = D % (16 / size) == 0 && X.vec(size) && DN.vec(size) && DR.vec(size) && DX.vec(size) && aligned(w, 16);
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value, PER = DT == SGEMM_F32 ? 8 : 16;

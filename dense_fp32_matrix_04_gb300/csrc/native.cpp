@@ -212,11 +212,13 @@ class Call {
     cudaStream_t stream() const { return stream_; }
     Tensor empty(at::IntArrayRef sizes, ScalarType type) {
         Unlocked other_threads;
-        Tensor t = at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index_)), std::nullopt);
-        if (other_)
-            c10::cuda::CUDACachingAllocator::recordStream(
-                t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream_, static_cast<c10::DeviceIndex>(index_)));
-        return t;
+        return used(at::detail::empty_cuda(sizes, type, device(), std::nullopt));
+    }
+    // Rows of bytes, `pitch` apart.
+    Tensor empty_rows(int64_t rows, int64_t cols, int64_t pitch) {
+        Unlocked other_threads;
+        const int64_t sizes[2] = {rows, cols}, strides[2] = {pitch, 1};
+        return used(at::detail::empty_strided_cuda(sizes, strides, ScalarType::Byte, device()));
     }
     // Calls the library.
     template <class F>
@@ -235,6 +237,14 @@ class Call {
     }
 
    private:
+    c10::Device device() const { return c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index_)); }
+    Tensor used(Tensor t) const {
+        if (other_)
+            c10::cuda::CUDACachingAllocator::recordStream(
+                t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream_, static_cast<c10::DeviceIndex>(index_)));
+        return t;
+    }
+
     int index_;
     std::optional<c10::cuda::CUDAGuard> guard_;
     cudaStream_t stream_;
@@ -415,7 +425,7 @@ PyObject *quantize_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Call call(x, a[2]);
     const int64_t pitch = std::max<int64_t>((X.cols + 31) / 32 * 16, 16);
     const Tiles shape(X.rows, X.cols, block);
-    const Tensor packed = call.empty({X.rows, pitch}, ScalarType::Byte), tiles = call.empty({shape.rows, shape.bytes}, scales_type(block));
+    const Tensor packed = call.empty_rows(X.rows, (X.cols + 1) / 2, pitch), tiles = call.empty({shape.rows, shape.bytes}, scales_type(block));
     Tensor scale;
     if (block == 16) scale = call.empty({X.rows}, ScalarType::Float);
     call.run("sgemm_quantize_fp4", [&] {
@@ -423,7 +433,7 @@ PyObject *quantize_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
                              (int)pitch, static_cast<unsigned char *>(tiles.data_ptr()),
                              block == 16 ? static_cast<float *>(scale.data_ptr()) : nullptr, call.stream());
     });
-    return tuple({packed.narrow(1, 0, (X.cols + 1) / 2), tiles, scale});
+    return tuple({packed, tiles, scale});
     END_HANDLE_TH_ERRORS
 }
 
