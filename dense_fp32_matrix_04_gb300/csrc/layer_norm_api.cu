@@ -45,23 +45,23 @@ int launch_norm(LayerNormArgs a, const Device &dev, cudaStream_t stream) {
 template <int DT, bool ALIGNED>
 int norm_by_width(const LayerNormArgs &a, const Device &dev, cudaStream_t stream) {
     constexpr int VEC = Elem<DT>::VEC;
+    // 16 elements a thread, and two blocks an SM while 320 threads are enough (rows of single elements
+    // too: 3907 x 5119 BF16 54 us, with one block 62, with 640 threads of 8 elements 58)
     if (a.D > 5120) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
-    if constexpr (!ALIGNED)
-        if (a.D <= 2048) return launch_norm<DT, false, 8 / VEC, 256, 3>(a, dev, stream);
-    return launch_norm<DT, ALIGNED, 16 / VEC, 320, ALIGNED ? 2 : 1>(a, dev, stream);
+    return launch_norm<DT, ALIGNED, 16 / VEC, 320, 2>(a, dev, stream);
 }
 
-template <int DT, bool ALIGNED, int PER>
+template <int DT, bool ALIGNED, int PER, int MAXT>
 int launch_norm_grad(LayerNormGradArgs a, const Device &dev, cudaStream_t stream) {
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    constexpr int most = ALIGNED ? 512 : 480;  // single elements take more registers
-    const auto kernel = layer_norm_grad_kernel<DT, ALIGNED, PER / Elem<DT>::VEC, most>;
+    const auto kernel = layer_norm_grad_kernel<DT, ALIGNED, PER / Elem<DT>::VEC, MAXT>;
     constexpr int size = sizeof(typename Elem<DT>::type);
-    const RowPlan plan(a.D, size, kLayerNormGradStages * (a.dr ? 3 : 2), PER, most);
+    const RowPlan plan(a.D, size, kLayerNormGradStages * (a.dr ? 3 : 2), PER, MAXT);
     a.ranks = plan.ranks;
     a.width = plan.width;
-    if (!sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem)) return SGEMM_ERR_LAUNCH;
-    const int fit = std::max(1, std::min(512 / plan.threads(), 226 * 1024 / (int)(plan.smem + 2048)));
+    const int held = sgemm_host::blocks_per_sm(regs, dev, kernel, plan.threads(), (int)plan.smem);
+    if (!held) return SGEMM_ERR_LAUNCH;
+    const int fit = std::max(1, std::min(512 / plan.threads(), held));  // (the workspace has room for no more)
     a.runners = std::min(sgemm_host::most_grad_runners(a.T, a.D, dev.sms),
                          std::max(1, dev.sms * fit / plan.ranks) * (int)plan.block.y);
     const unsigned groups = (a.runners + plan.block.y - 1) / plan.block.y;
@@ -162,8 +162,11 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
                               static_cast<float *>(workspace), 0, 0, 1, D};
     const bool vec = D % (16 / size) == 0 && X.vec(size) && DN.vec(size) && DR.vec(size) && DX.vec(size) && aligned(w, 16);
     return by_dtype(dtype, [&](auto dt) {
+        // 16-bit rows of single elements: 320 threads of 16, which take more registers (6664 x 3001 BF16
+        // 47.6 us, with 8 elements 59.5; 3907 x 5119, where those are a cluster's, 55 and 106)
         constexpr int DT = decltype(dt)::value, PER = DT == SGEMM_F32 ? 8 : 16;
-        return vec ? launch_norm_grad<DT, true, PER>(a, dev, stream) : launch_norm_grad<DT, false, 8>(a, dev, stream);
+        return vec ? launch_norm_grad<DT, true, PER, 512>(a, dev, stream)
+                   : launch_norm_grad<DT, false, PER, DT == SGEMM_F32 ? 480 : 320>(a, dev, stream);
     });
 }
 
