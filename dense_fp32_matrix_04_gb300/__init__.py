@@ -12,9 +12,10 @@ library is missing or fails to load, ``load()`` raises.
   status.
 * ``matmul(A, B, out=None)`` -- convenience wrapper for 2-D float32 CUDA tensors
   with unit column stride (row-major, possibly with a padded row stride).
-* ``block_norm``, ``quantize_i8``, ``matmul_i8``, ``linear_i8``, ``logprobs`` and
-  the two backward passes -- the operators of a language model around its
-  products, on CUDA tensors (``layers``; include/sgemm_layers.h).
+* ``block_norm``, ``layer_norm``, ``quantize_i8``, ``matmul_i8``, ``linear_i8``,
+  ``quantize_fp4``, ``matmul_fp4``, ``linear_fp4``, ``logprobs``, ``beam_step``,
+  ``beam_reorder`` and the three backward passes -- the operators of a language
+  model around its products, on CUDA tensors (``layers``; include/sgemm_layers.h).
 """
 
 from __future__ import annotations

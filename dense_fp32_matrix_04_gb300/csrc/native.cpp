@@ -406,6 +406,10 @@ BlockScales block_scales(PyObject *o, const char *name, int64_t rows, int64_t K,
 // Packed codes of `cols` bytes a row (any number of rows where `rows` is negative).
 Matrix codes(PyObject *o, const char *name, int index, int64_t rows, int64_t cols) {
     Matrix m = matrix(o, name, ScalarType::Byte, index, rows, cols);
+    if (!m.cols) {
+        m.ld = 16;
+        return m;
+    }
     if (m.rows > 1 && m.ld % 16)
         refuse(PyExc_ValueError, "%s has rows %d bytes apart: they must be a multiple of 16, as quantize_fp4 lays them out", name, m.ld);
     if (reinterpret_cast<uintptr_t>(m.p) % 16) refuse(PyExc_ValueError, "%s must start on 16 bytes", name);

@@ -535,7 +535,9 @@ def matmul_fp4(a, a_block, a_scale, w, w_block, w_scale, bias=None, out_dtype=No
     Codes and scales are as ``quantize_fp4`` returns them, of the same block; ``a_scale`` and
     ``w_scale`` may be None (1).  For inference: autograd does not see it."""
     fn = (_native or _load_native()).matmul_fp4
-    return fn(a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out, None) if stream is None else _elsewhere(fn, stream, a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out)
+    if stream is not None:
+        return _elsewhere(fn, stream, a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out)
+    return fn(a, a_block, a_scale, w, w_block, w_scale, bias, out_dtype, out, None)
 
 
 def linear_fp4(x, w, w_block, w_scale=None, bias=None, out_dtype=None, out=None, workspace=None, stream=None):
@@ -545,7 +547,9 @@ def linear_fp4(x, w, w_block, w_scale=None, bias=None, out_dtype=None, out=None,
     ``sgemm_linear_fp4_workspace_size`` gives; allocated if None.  For inference: autograd does
     not see the call."""
     fn = (_native or _load_native()).linear_fp4
-    return fn(x, w, w_block, w_scale, bias, out_dtype, out, workspace, None) if stream is None else _elsewhere(fn, stream, x, w, w_block, w_scale, bias, out_dtype, out, workspace)
+    if stream is not None:
+        return _elsewhere(fn, stream, x, w, w_block, w_scale, bias, out_dtype, out, workspace)
+    return fn(x, w, w_block, w_scale, bias, out_dtype, out, workspace, None)
 
 
 def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=0, stream=None):
@@ -560,7 +564,9 @@ def beam_step(logits, score, top=None, scale=1.0, mask=None, finished=None, end=
     ``top`` continuations the rest have score -infinity, parent -1 and token -1.
     Has no gradient, and autograd does not see it."""
     fn = (_native or _load_native()).beam_step
-    return fn(logits, score, top, scale, mask, finished, end, None) if stream is None else _elsewhere(fn, stream, logits, score, top, scale, mask, finished, end)
+    if stream is not None:
+        return _elsewhere(fn, stream, logits, score, top, scale, mask, finished, end)
+    return fn(logits, score, top, scale, mask, finished, end, None)
 
 
 def beam_reorder(state, parent, out=None, stream=None):

@@ -1,8 +1,9 @@
 /*
  * libsgemm -- the operators of a language model that sit around its matrix
  * products, on one NVIDIA GB300 (sm_103a): the norms, gate and residual sum
- * between two blocks, the product with 8-bit weights, and the log
- * probabilities that the last product's logits are turned into.
+ * between two blocks, the products with 8-bit and 4-bit weights, and the log
+ * probabilities, or the steps of beam search, that the last product's logits
+ * are turned into.
  *
  * Conventions are those of sgemm.h: row-major DEVICE matrices owned by the
  * caller, a leading dimension (elements between rows) for each, every call
@@ -13,8 +14,9 @@
  * element type allows is accepted.  The calls launch kernels only, so after
  * one call on a device they can be captured into a CUDA graph.  Results are
  * the same bits on every run.  (A backward pass over no rows, T == 0, clears the
- * gradients of the weights and the gate by cudaMemsetAsync and cudaMemset2DAsync
- * instead of a kernel.)
+ * gradients of the weights, the bias and the gate by cudaMemsetAsync and
+ * cudaMemset2DAsync instead of a kernel; rows of no columns quantised to 4 bits
+ * have their scales cleared so.)
  */
 #ifndef SGEMM_LAYERS_H
 #define SGEMM_LAYERS_H

@@ -194,3 +194,227 @@ def test_product(sg, M, N, K, block):
     check(got, a, w, K, block, use_bias, out)
     # the layer quantises the same codes itself
     assert bool((sg.linear_fp4(x, *w, bias=use_bias, out_dtype=td(out)) == got).all())
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(1, 4200, 5000), (1, 300, 90112), (2, 128, 90113), (20, 512, 8192), (14, 260, 20000), (50, 1000, 3000),
+                                   (100, 128, 16384), (64, 4096, 2112), (600, 520, 4096), (1100, 4200, 1000), (700, 9000, 2113),
+                                   (2000, 2300, 4160), (257, 20000, 64), (4100, 4000, 40)])
+def test_product_of_every_plan(sg, M, N, K, block):
+    """One token; few tiles that clusters share; tiles of 64 and 128 tokens; pairs of SMs; K that ends
+    inside a step, with one to four products of it."""
+    x, w, bias = operands(sg, M, N, K, M + K, block, "bf16")
+    a = sg.quantize_fp4(x, block)
+    out = "bf16" if (M + N) % 3 else "f32"
+    got = sg.matmul_fp4(*a, *w, bias, out_dtype=td(out))
+    check(got, a, w, K, block, bias, out)
+    assert bool((sg.linear_fp4(x, *w, bias=bias, out_dtype=td(out)) == got).all())
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+
+
+@pytest.mark.parametrize("M,N", [(3, 5000), (30, 700), (130, 256), (300, 4096), (1500, 4608)])
+def test_many_steps_wrap_the_rings(sg, M, N):
+    K = 12000
+    x, w, _ = operands(sg, M, N, K, 5, 16)
+    a = sg.quantize_fp4(x)
+    got = sg.matmul_fp4(*a, *w)
+    rows = [0, M // 2, M - 1]
+    few = (a[0][rows], a[1], a[2][rows])
+    A = values_of(a[0], a[1], K, 16)[rows]
+    B = values_of(w[0], w[1], K, 16)
+    s = np.outer(few[2].double().cpu().numpy(), w[2].double().cpu().numpy())
+    err = np.abs(got[rows].double().cpu().numpy() - A @ B.T * s)
+    assert (err <= (2 * K * U * (np.abs(A) @ np.abs(B).T) + 4 * U * np.abs(A @ B.T)) * s).all()
+    assert bool((sg.matmul_fp4(*a, *w) == got).all())
+
+
+@pytest.mark.parametrize("M", [1, 7, 60, 200, 1300])
+@pytest.mark.parametrize("block", [16, 32])
+def test_strides_and_what_lies_around(sg, M, block):
+    """Rows of codes further apart than they are long, with anything between them and behind; scales
+    of rows behind the matrix that are not numbers; an output inside a wider one."""
+    import torch
+    N, K = 4300, 1130
+    x, w, bias = operands(sg, M, N, K, 3, block)
+    a = sg.quantize_fp4(x, block)
+    want = sg.matmul_fp4(*a, *w, bias)
+
+    def apart(q, rows):
+        big = torch.full((rows + 3, q.shape[1] // 16 * 16 + 80), 0x5D, dtype=torch.uint8, device="cuda")
+        big[:rows, :q.shape[1]] = q
+        return big[:rows, :q.shape[1]]
+
+    def dirty(s, rows):
+        t = s.view(torch.uint8).clone()
+        r, j = torch.arange(128, device="cuda")[:, None], torch.arange(t.shape[1] // 128, device="cuda")[None]
+        if rows % 128:
+            at = (j // 4 * 512 + r % 32 * 16 + r // 32 * 4 + j % 4)[rows % 128:].reshape(-1)
+            t[-1, at] = 0x7F if block == 16 else 0xFF
+        return t.view(s.dtype)
+    out = torch.full((M + 2, N + 7), 5.0, device="cuda")
+    got = sg.matmul_fp4(apart(a[0], M), dirty(a[1], M), a[2], apart(w[0], N), dirty(w[1], N), w[2], bias, out=out[1:M + 1, 3:N + 3])
+    assert torch.equal(got, want)
+    out[1:M + 1, 3:N + 3] = 5.0
+    assert bool((out == 5.0).all()), "wrote outside C"
+
+
+@pytest.mark.parametrize("dtype,offset,pad", [("f32", 1, 0), ("f32", 3, 2), ("bf16", 1, 0), ("bf16", 5, 3), ("f16", 7, 1), ("bf16", 8, 8)])
+@pytest.mark.parametrize("M,K", [(1, 1111), (1, 5000), (9, 2047), (140, 600), (2, 16400)])
+def test_rows_of_any_alignment(sg, M, K, dtype, offset, pad):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(offset)
+    buf = torch.full((M * (K + pad) + offset + 9,), float("nan"), dtype=td(dtype), device="cuda")
+    x = buf[offset:offset + M * (K + pad)].view(M, K + pad)[:, :K]
+    x.copy_(torch.randn(M, K, generator=g, device="cuda"))
+    w = sg.quantize_fp4(torch.randn(300, K, generator=g, device="cuda"))
+    for block in (16, 32):
+        for p, q in zip(sg.quantize_fp4(x, block), sg.quantize_fp4(x.contiguous().clone(), block)):
+            assert p is None and q is None or torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+    assert torch.equal(sg.linear_fp4(x, *w), sg.linear_fp4(x.contiguous().clone(), *w))
+
+
+@pytest.mark.parametrize("M", [1, 5, 70, 1200])
+@pytest.mark.parametrize("block", [16, 32])
+def test_a_row_that_is_not_finite_stays_alone(sg, M, block):
+    import torch
+    x, w, bias = operands(sg, M, 4200, 300, 9, block)
+    want = sg.linear_fp4(x, *w, bias=bias)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        y = x.clone()
+        y[M // 2, 17] = value
+        got = sg.linear_fp4(y, *w, bias=bias)
+        assert bool(torch.isnan(got[M // 2]).all())
+        rest = [i for i in range(M) if i != M // 2]
+        assert torch.equal(got[rest], want[rest])
+
+
+def test_empty_sums_and_empty_matrices(sg):
+    import torch
+    bias = torch.randn(5, device="cuda")
+    for block in (16, 32):
+        a, w = (sg.quantize_fp4(torch.empty(n, 0, device="cuda"), block) for n in (3, 5))
+        assert a[0].shape == (3, 0) and a[1].shape == (1, 0)
+        if block == 16:
+            assert bool((a[2] == 0).all())
+        for scale in (a[2], None if a[2] is None else torch.full((3,), float("nan"), device="cuda")):
+            assert bool((sg.matmul_fp4(a[0], a[1], scale, *w, bias=bias) == bias).all())
+        assert bool((sg.linear_fp4(torch.empty(3, 0, device="cuda"), *w, out_dtype=torch.bfloat16) == 0).all())
+        none, w = sg.quantize_fp4(torch.empty(0, 64, device="cuda"), block), sg.quantize_fp4(torch.randn(5, 64, device="cuda"), block)
+        assert sg.matmul_fp4(*none, *w).shape == (0, 5) and sg.matmul_fp4(*w, *none).shape == (5, 0)
+        assert sg.linear_fp4(torch.empty(0, 64, device="cuda"), *w).shape == (0, 5)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("rows,K", [(1, 1), (5, 100), (130, 64), (300, 1111)])
+def test_scales_laid_out(sg, rows, K, block):
+    import torch
+    q, s, _ = sg.quantize_fp4(torch.randn(rows, K, device="cuda"), block)
+    n = -(-K // block)
+    plain = torch.zeros(rows, n + 3, dtype=torch.uint8, device="cuda")[:, :n]
+    plain.copy_(torch.from_numpy(bits_of(s, rows, n).astype(np.uint8)))
+    got = sg.lay_out_fp4_scales(plain.view(s.dtype))
+    assert got.dtype is s.dtype and torch.equal(got.view(torch.uint8), s.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 2048), (20, 4096, 2048), (200, 6000, 1024), (1300, 8000, 1024)])
+def test_weights_and_tokens_that_are_written_just_before(sg, M, N, K):
+    """A product whose weights the call before quantised, with other bytes in their place until then."""
+    import torch
+    x = torch.randn(M, K, device="cuda")
+    sets = [torch.randn(N, K, device="cuda") for _ in range(2)]
+    done = [sg.quantize_fp4(w) for w in sets]
+    torch.cuda.synchronize()
+    want = [sg.linear_fp4(x, *w) for w in done]
+    a = sg.quantize_fp4(x)
+    lib = sg.load()
+    q, s, r = (t.clone() for t in done[0])
+    stream = torch.cuda.current_stream().cuda_stream
+    for turn in range(10):
+        w = sets[turn % 2]
+        status = lib.sgemm_quantize_fp4(N, K, 0, w.data_ptr(), K, 16, q.data_ptr(), K // 2, s.data_ptr(), r.data_ptr(), stream)
+        assert status == 0
+        got = sg.matmul_fp4(*a, q, s, r)
+        assert torch.equal(got, want[turn % 2]), f"call {turn}"
+        status = lib.sgemm_quantize_fp4(N, K, 0, sets[1 - turn % 2].data_ptr(), K, 16, q.data_ptr(), K // 2, s.data_ptr(), r.data_ptr(),
+                                        stream)
+        assert status == 0 and torch.equal(sg.linear_fp4(x, q, s, r), want[1 - turn % 2])
+
+
+@pytest.mark.parametrize("M", [1, 20, 300, 1300])
+def test_another_stream_a_graph_and_the_same_bits(sg, M):
+    import torch
+    x = torch.randn(M, 1024, device="cuda").to(torch.bfloat16)
+    w = sg.quantize_fp4(torch.randn(4100, 1024, device="cuda"))
+    want = sg.linear_fp4(x, *w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = sg.linear_fp4(x, *w, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    with torch.cuda.stream(side):
+        got = sg.linear_fp4(x, *w)
+    side.synchronize()
+    assert torch.equal(got, want)
+    # two graphs of the same call, replayed one after the other
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(sg.linear_fp4(x, *w))
+    x.neg_()
+    for graph in graphs:
+        graph.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, -want)
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 512, 8192), (40, 4096, 512), (300, 520, 4096), (1300, 8000, 1024)])
+def test_a_wait_that_runs_out_is_reported(sg, M, N, K):
+    import torch
+    x, w, _ = operands(sg, M, N, K, 12, 16)
+    a = sg.quantize_fp4(x)
+    want = sg.matmul_fp4(*a, *w)
+    sg.sgemm_test_switches(1, 50_000_000)     # no copies: every wait runs out after 50 ms
+    try:
+        sg.matmul_fp4(*a, *w)
+        assert sg.sgemm_device_status() == sg.SGEMM_ERR_TIMEOUT
+    finally:
+        sg.sgemm_test_switches(0)
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+    assert torch.equal(sg.matmul_fp4(*a, *w), want)
+
+
+def test_refusals(sg):
+    import torch
+    x = torch.randn(4, 64, device="cuda")
+    a, w = sg.quantize_fp4(x), sg.quantize_fp4(torch.randn(6, 64, device="cuda"))
+    b32 = sg.quantize_fp4(x, 32)
+    tight = torch.zeros(4, 20, dtype=torch.uint8, device="cuda")
+    for call, error, match in [
+            (lambda: sg.quantize_fp4(x, 64), ValueError, "block"), (lambda: sg.quantize_fp4(x.int()), TypeError, "float32"),
+            (lambda: sg.quantize_fp4(x.T), ValueError, "stride"), (lambda: sg.quantize_fp4(x[0]), TypeError, "2-D"),
+            (lambda: sg.matmul_fp4(a[0].int(), *a[1:], *w), TypeError, "uint8"),
+            (lambda: sg.matmul_fp4(*b32, *w), ValueError, "blocks of 32"),
+            (lambda: sg.matmul_fp4(a[0], a[1].view(torch.uint8), a[2], *w), TypeError, "float8"),
+            (lambda: sg.matmul_fp4(*a, w[0], w[1][:, :-1], w[2]), ValueError, "tiles"),
+            (lambda: sg.matmul_fp4(*a, w[0], w[1], w[2][:5]), ValueError, "elements"),
+            (lambda: sg.matmul_fp4(*a, w[0], w[1], w[2].double()), TypeError, "w_scale"),
+            (lambda: sg.matmul_fp4(*a, w[0][:, :16], w[1], w[2]), ValueError, "w is"),
+            (lambda: sg.linear_fp4(torch.randn(4, 40, device="cuda"), tight, w[1], None), ValueError, "multiple of 16"),
+            (lambda: sg.linear_fp4(x, w[0][:, 1:], w[1], w[2]), ValueError, "w is"),
+            (lambda: sg.matmul_fp4(*a, *w, out=torch.empty(4, 5, device="cuda")), ValueError, "out is"),
+            (lambda: sg.matmul_fp4(*a, *w, out_dtype=torch.int32), TypeError, "out_dtype"),
+            (lambda: sg.matmul_fp4(*a, *w, bias=torch.zeros(6, 1, device="cuda")), TypeError, "bias"),
+            (lambda: sg.linear_fp4(x, *w, workspace=torch.empty(16, device="cuda")), sg.SgemmError, "linear_fp4"),
+            (lambda: sg.linear_fp4(x, *w, workspace=torch.empty(1 << 16)), TypeError, "workspace"),
+            (lambda: sg.linear_fp4(x, *w, workspace=torch.empty(2, 1 << 16, device="cuda").T), ValueError, "workspace"),
+            (lambda: sg.linear_fp4(x, *w, out=x[:, :6]), sg.SgemmError, "linear_fp4"),
+            (lambda: sg.lay_out_fp4_scales(x), TypeError, "float8"),
+            (lambda: sg.linear_fp4(x, *w, None, None, None, None, None, 3), TypeError, "positional")]:
+        with pytest.raises(error, match=match):
+            call()
+    # a view that starts inside 16 bytes
+    off = torch.zeros(200, dtype=torch.uint8, device="cuda")[4:36].view(1, 32)
+    with pytest.raises(ValueError, match="16 bytes"):
+        sg.matmul_fp4(off, a[1], None, *w)
