@@ -89,15 +89,18 @@ int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx,
 
 // How a product is shared out: tiles of 16 to 128 tokens on one SM, for which the
 // blocks of a cluster can split K, or of 256 on a pair.  The smallest estimate, in
-// cycles, of rounds over the SMs times the length of one, from steps measured on
-// GB300 (a step is 256 columns).
+// cycles, of rounds over the SMs times the length of one, from times on GB300 (a step
+// is 256 columns).  A split costs a cluster's launch, two of its barriers and the
+// join: worth it for long rows only (16 x 4096 x 16384 18.9 us whole, 12.0 in four
+// parts; x 4096 8.9 and 8.6, in eight parts 14.6).  Pairs take a cluster's launch too:
+// 600 x 4096 x 4096 14.8 us on single SMs and 14.7, 2048 x 8192 x 4096 39.2 and 33.2.
 struct Fp4Plan {
     int tok = 16, splits = 1;  // tok 256: a pair
     Fp4Plan(int M, int N, int K, int sms) {
         static constexpr struct {
             int tok;
-            double step, drain;
-        } kSteps[] = {{16, 350, 300}, {32, 360, 400}, {64, 420, 700}, {128, 480, 1200}, {256, 620, 2400}};
+            double step, round;
+        } kSteps[] = {{16, 395, 600}, {32, 395, 600}, {64, 400, 800}, {128, 450, 1200}, {256, 610, 2200}};
         double best = 1e300;
         const int steps = (K + 255) / 256;
         for (const auto &c : kSteps) {
@@ -105,10 +108,12 @@ struct Fp4Plan {
             const bool pair = c.tok == 256;
             const int64_t tiles = (int64_t)((M + c.tok - 1) / c.tok) * ((N + (pair ? 255 : 127)) / (pair ? 256 : 128));
             const int slots = pair ? sms / 2 : sms;
-            for (int s = 1; s == 1 || (!pair && s <= 8 && s <= steps && tiles * s <= sms - 8); s *= 2) {
+            // (clusters of four leave some SMs without a block)
+            for (int s = 1; s == 1 || (!pair && s <= 4 && s <= steps && tiles * s <= sms - 8); s *= 2) {
                 const int64_t rounds = (tiles * s + slots - 1) / slots;
-                double t = (double)rounds * (((steps + s - 1) / s) * c.step) + (double)(rounds - 1) * (pair ? 1000 : 200) + c.drain;
-                if (s > 1) t += 1500 + 12. * c.tok;
+                double t = (double)rounds * (((steps + s - 1) / s) * c.step + c.round);
+                if (s > 1) t += 1300 + 112. * c.tok;
+                if (pair) t += 5000;
                 if (t < best) best = t, tok = c.tok, splits = s;
             }
             if (M <= c.tok) break;

@@ -347,27 +347,40 @@ __global__ void __launch_bounds__(Fp4Tile<TOK, BLOCK>::THREADS, 1)
     __syncwarp();
     if (splits > 1) {
         cluster_sync();
-        if (warp >= T::DRAIN && warp < T::DRAIN + 4) {
-            // this block's tokens of the tile: the parts in order of their rank, eight tokens' on their way
-            constexpr int U = 8;
+        if (warp >= T::DRAIN) {
+            // this block's tokens of the tile, a warp each and a lane four of its rows: the parts in order of
+            // their rank, four tokens' on their way
+            constexpr int U = 4, WARPS = 4 * T::SETS;
             int m0, n0, k0, n;
             unit(blockIdx.x, m0, n0, k0, n);
-            const int row = 32 * (warp & 3) + lane, col = n0 + row, tokens = min(TOK, p.M - m0);
-            const float scale = col < p.N && p.b_scale ? p.b_scale[col] : 1.f, bias = col < p.N && p.bias ? p.bias[col] : 0.f;
-            for (int j = blockIdx.x % splits; j < tokens; j += U * splits) {
-                float sum[U] = {};
+            const int tokens = min(TOK, p.M - m0), col = n0 + 4 * lane, step = splits * WARPS;
+            float scale[4], bias[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                scale[i] = col + i < p.N && p.b_scale ? p.b_scale[col + i] : 1.f;
+                bias[i] = col + i < p.N && p.bias ? p.bias[col + i] : 0.f;
+            }
+            for (int j = blockIdx.x % splits + (warp - T::DRAIN) * splits; j < tokens; j += U * step) {
+                float4 sum[U] = {};
 #pragma unroll 4
                 for (int r = 0; r < splits; ++r) {
-                    const uint32_t from = dsmem_map(base + 4 * (j * T::ROWS + row), (uint32_t)r);
+                    const uint32_t from = dsmem_map(base + 4 * (j * T::ROWS + 4 * lane), (uint32_t)r);
 #pragma unroll
-                    for (int i = 0; i < U; ++i)
-                        if (j + i * splits < tokens) sum[i] += __uint_as_float(dsmem_ld_u32(from + 4 * T::ROWS * i * splits));
+                    for (int i = 0; i < U; ++i) {
+                        if (j + i * step >= tokens) break;
+                        const ulonglong2 v = dsmem_ld_v2u64(from + 4 * T::ROWS * i * step);
+                        const float2 lo = f32x2_unpack(v.x), hi = f32x2_unpack(v.y);
+                        sum[i].x += lo.x, sum[i].y += lo.y, sum[i].z += hi.x, sum[i].w += hi.y;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    const int m = m0 + j + i * splits;
-                    if (j + i * splits < tokens && col < p.N)
-                        store_c(p.C, (int64_t)m * p.ldc + col, p.ctype, fmaf(sum[i] * (p.a_scale ? p.a_scale[m] : 1.f), scale, bias));
+                    if (j + i * step >= tokens) break;
+                    const int64_t m = m0 + j + i * step;
+                    const float s = p.a_scale ? p.a_scale[m] : 1.f, v[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < p.N) store_c(p.C, m * p.ldc + col + e, p.ctype, fmaf(v[e] * s, scale[e], bias[e]));
                 }
             }
         }
