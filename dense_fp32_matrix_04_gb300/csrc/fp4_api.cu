@@ -23,7 +23,8 @@ using sgemm_host::dtype_size;
 using sgemm_host::launch;
 using sgemm_host::Range;
 
-constexpr int kMaxSize = 1 << 30;  // of rows and columns: row numbers and a round of them fit 32 bits
+constexpr int kMaxRows = 1 << 30;     // row numbers and a round of them fit 32 bits
+constexpr int kMaxColumns = 1 << 24;  // a tile's products over more would come near the limit of a wait
 
 bool block_ok(int block) { return block == 16 || block == 32; }
 int64_t code_bytes(int K) { return ((int64_t)K + 1) / 2; }
@@ -219,7 +220,7 @@ bool codes_ok(const unsigned char *q, int ld, const unsigned char *tiles, const 
 }
 
 bool shapes_ok(int M, int N, int K, int block, int ldb, int ldc, int ctype) {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize) return false;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxColumns) return false;
     return block_ok(block) && dtype_ok(ctype) && ldb >= std::max<int64_t>(code_bytes(K), 1) && ldc >= std::max(N, 1);
 }
 
@@ -232,13 +233,13 @@ bool output_ok(const void *C, int ctype, const float *bias) {
 extern "C" {
 
 size_t sgemm_fp4_scales_size(int rows, int K, int block) {
-    if (rows < 0 || K < 0 || rows > kMaxSize || K > kMaxSize || !block_ok(block)) return 0;
+    if (rows < 0 || K < 0 || rows > kMaxRows || K > kMaxColumns || !block_ok(block)) return 0;
     return (size_t)tile_bytes(rows, K, block);
 }
 
 int sgemm_quantize_fp4(int M, int K, int dtype, const void *x, int ldx, int block, unsigned char *q, int ldq,
                        unsigned char *block_scale, float *scale, cudaStream_t stream) {
-    if (M < 0 || K < 0 || M > kMaxSize || K > kMaxSize || !dtype_ok(dtype) || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
+    if (M < 0 || K < 0 || M > kMaxRows || K > kMaxColumns || !dtype_ok(dtype) || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
     if (ldx < std::max(K, 1) || ldq < std::max<int64_t>(code_bytes(K), 1)) return SGEMM_ERR_INVALID_ARG;
     if ((block == 16) != (scale != nullptr) && M > 0) return SGEMM_ERR_INVALID_ARG;
     if (M == 0) return SGEMM_OK;
@@ -267,7 +268,7 @@ int sgemm_quantize_fp4(int M, int K, int dtype, const void *x, int ldx, int bloc
 
 int sgemm_fp4_lay_out_scales(int rows, int K, int block, const unsigned char *s, int lds, unsigned char *tiles,
                              cudaStream_t stream) {
-    if (rows < 0 || K < 0 || rows > kMaxSize || K > kMaxSize || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
+    if (rows < 0 || K < 0 || rows > kMaxRows || K > kMaxColumns || !block_ok(block)) return SGEMM_ERR_INVALID_ARG;
     if (rows == 0 || K == 0) return SGEMM_OK;
     const int blocks = fp4_blocks(K, block);
     if (!s || lds < blocks || !tiles || !aligned(tiles, 16)) return SGEMM_ERR_INVALID_ARG;
@@ -303,7 +304,7 @@ int sgemm_fp4(int M, int N, int K, int block, const unsigned char *A, int lda, c
 
 // The tokens' codes, their block scales, their scales.
 size_t sgemm_linear_fp4_workspace_size(int M, int K, int block) {
-    if (M <= 0 || K <= 0 || M > kMaxSize || K > kMaxSize || !block_ok(block) || takes_rows(M, K)) return 0;
+    if (M <= 0 || K <= 0 || M > kMaxRows || K > kMaxColumns || !block_ok(block) || takes_rows(M, K)) return 0;
     return (size_t)(up256((int64_t)M * code_pitch(K)) + up256(tile_bytes(M, K, block)) + (block == 16 ? up256((int64_t)M * 4) : 0));
 }
 

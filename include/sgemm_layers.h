@@ -267,7 +267,7 @@ int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz
  *       (r / 128, j / 4); tiles of the same rows follow each other.  Scales of
  *       blocks and rows behind the matrix are 0.
  *   scale: M FP32 values (block 16).
- * M, K <= 2^30.  Serves for activations and for weights stored N x K.
+ * M <= 2^30, K <= 2^24.  Serves for activations and for weights stored N x K.
  */
 int sgemm_quantize_fp4(int M, int K, int dtype, const void *x, int ldx, int block,
                        unsigned char *q, int ldq, unsigned char *block_scale, float *scale,
@@ -292,7 +292,7 @@ int sgemm_fp4_lay_out_scales(int rows, int K, int block, const unsigned char *s,
  *   a_scale, b_scale: M and N FP32 values, or NULL (1).  Beside weights that were
  *       quantised elsewhere b_scale can hold whatever scale they have beyond their
  *       blocks', repeated for each row.
- *   bias: N FP32 values or NULL.  M, N, K <= 2^30.
+ *   bias: N FP32 values or NULL.  M, N <= 2^30, K <= 2^24.
  *   Scales of rows behind the matrix do not matter; those of blocks behind K must be
  *   finite.
  * K == 0: every sum is empty (C = bias, or 0, whatever the scales).

@@ -197,7 +197,8 @@ def test_product(sg, M, N, K, block):
 
 
 @pytest.mark.parametrize("block", [16, 32])
-@pytest.mark.parametrize("M,N,K", [(1, 4200, 5000), (1, 300, 90112), (2, 128, 90113), (20, 512, 8192), (14, 260, 20000), (50, 1000, 3000),
+@pytest.mark.parametrize("M,N,K", [(1, 4200, 5000), (1, 300, 90112), (1, 128, 90120), (2, 128, 90113),
+                                   (20, 512, 8192), (14, 260, 20000), (50, 1000, 3000),
                                    (100, 128, 16384), (64, 4096, 2112), (600, 520, 4096), (1100, 4200, 1000), (700, 9000, 2113),
                                    (2000, 2300, 4160), (257, 20000, 64), (4100, 4000, 40)])
 def test_product_of_every_plan(sg, M, N, K, block):

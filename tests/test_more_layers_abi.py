@@ -52,7 +52,7 @@ def test_layer_norm_backward_refuses(lib, change, want):
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(M=-1), BAD), (dict(K=-1), BAD), (dict(M=2 ** 30 + 1), BAD), (dict(K=2 ** 30 + 1), BAD), (dict(dtype=3), BAD), (dict(block=8), BAD),
+    (dict(M=-1), BAD), (dict(K=-1), BAD), (dict(M=2 ** 30 + 1), BAD), (dict(K=2 ** 24 + 1, ldx=2 ** 24 + 1, ldq=2 ** 24), BAD), (dict(dtype=3), BAD), (dict(block=8), BAD),
     (dict(x=0), BAD), (dict(x=P[0] + 2), BAD), (dict(ldx=99), BAD), (dict(q=0), BAD), (dict(q=P[1] + 8), BAD), (dict(ldq=48), BAD),
     (dict(ldq=56), BAD), (dict(tiles=0), BAD), (dict(tiles=P[2] + 8), BAD), (dict(scale=0), BAD), (dict(scale=P[3] + 2), BAD),
     (dict(block=32), BAD),                        # blocks of 32 have no row scale
@@ -98,7 +98,8 @@ def fp4_args(**change):
 
 
 @pytest.mark.parametrize("change,want", [
-    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=-1), BAD), (dict(N=2 ** 30 + 1, ldc=2 ** 30 + 1), BAD), (dict(block=4), BAD),
+    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=-1), BAD), (dict(N=2 ** 30 + 1, ldc=2 ** 30 + 1), BAD), (dict(K=2 ** 24 + 1, lda=2 ** 24, ldb=2 ** 24), BAD),
+    (dict(block=4), BAD),
     (dict(lda=48), BAD), (dict(ldb=48), BAD), (dict(lda=56), BAD), (dict(ldb=72), BAD), (dict(ldc=7), BAD), (dict(A=0), BAD), (dict(B=0), BAD),
     (dict(C=0), BAD), (dict(a_block=0), BAD), (dict(b_block=0), BAD), (dict(A=P[0] + 8), BAD), (dict(b_block=P[4] + 4), BAD),
     (dict(a_scale=P[2] + 2), BAD), (dict(bias=P[6] + 1), BAD), (dict(C=P[7] + 2), BAD), (dict(ctype=5), BAD),
