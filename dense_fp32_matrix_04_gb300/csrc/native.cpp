@@ -22,6 +22,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <array>
 #include <cstdarg>
 #include <limits>
 #include <optional>
@@ -214,6 +215,35 @@ class Call {
         Unlocked other_threads;
         return used(at::detail::empty_cuda(sizes, type, device(), std::nullopt));
     }
+    // Several tensors, dense and of types of their own.  Small ones share an allocation: each costs
+    // the host about a microsecond, a third of it the memory's.  (Only small ones, because one that
+    // lives on keeps the memory of all.)
+    struct Wanted {
+        c10::DimVector sizes;
+        ScalarType type;
+    };
+    template <size_t N>
+    std::array<Tensor, N> empty(const std::array<Wanted, N> &wanted) {
+        std::array<Tensor, N> made;
+        int64_t at[N], bytes = 0;
+        for (size_t i = 0; i < N; ++i) {
+            at[i] = bytes;
+            bytes += (c10::multiply_integers(wanted[i].sizes) * (int64_t)c10::elementSize(wanted[i].type) + 255) / 256 * 256;
+        }
+        if (bytes > kShared) {
+            for (size_t i = 0; i < N; ++i) made[i] = empty(wanted[i].sizes, wanted[i].type);
+            return made;
+        }
+        const Tensor whole = empty({bytes}, ScalarType::Byte);
+        for (size_t i = 0; i < N; ++i) {
+            made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
+                                                               c10::scalarTypeToTypeMeta(wanted[i].type));
+            c10::TensorImpl *impl = made[i].unsafeGetTensorImpl();
+            impl->set_sizes_contiguous(wanted[i].sizes);
+            impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(wanted[i].type));
+        }
+        return made;
+    }
     // Rows of bytes, `pitch` apart.
     Tensor empty_rows(int64_t rows, int64_t cols, int64_t pitch) {
         Unlocked other_threads;
@@ -237,6 +267,8 @@ class Call {
     }
 
    private:
+    static constexpr int64_t kShared = 1 << 17;
+
     c10::Device device() const { return c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index_)); }
     Tensor used(Tensor t) const {
         if (other_)
@@ -320,12 +352,15 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (add) A = matrix(a[3], "add", dt, dev, T, D);
     if (out) R = matrix(a[5], "out", dt, dev, T, D);
     Call call(x, a[6]);
-    Tensor r;
+    Tensor r, normed, stats;
     if (add && !out) {
-        r = call.empty({T, D}, dt);
-        R = Matrix{r.data_ptr(), X.cols ? (int)X.cols : 1, T, D};
+        const auto made = call.empty<3>({{{{T, D}, dt}, {{T, D}, dt}, {{2, T}, ScalarType::Float}}});
+        r = made[0], normed = made[1], stats = made[2];
+        R = Matrix{r.data_ptr(), D ? (int)D : 1, T, D};
+    } else {
+        const auto made = call.empty<2>({{{{T, D}, dt}, {{2, T}, ScalarType::Float}}});
+        normed = made[0], stats = made[1];
     }
-    const Tensor normed = call.empty({T, D}, dt), stats = call.empty({2, T}, ScalarType::Float);
     call.run("sgemm_layer_norm", [&] {
         return sgemm_layer_norm((int)T, (int)D, code, X.p, X.ld, add ? A.p : nullptr, A.ld, w, b, code_of(wt), eps, add ? R.p : nullptr,
                            R.ld, normed.data_ptr(), D ? (int)D : 1, static_cast<float *>(stats.data_ptr()), call.stream());
@@ -359,9 +394,14 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         refuse(PyExc_ValueError, "stats must be the (2, T) float32 tensor that layer_norm returned");
     const bool bias = truth(a[5]);
     Call call(x, a[6]);
-    const Tensor dx = call.empty({T, D}, dt), dw = call.empty({D}, wt);
-    Tensor db;
-    if (bias) db = call.empty({D}, wt);
+    Tensor dx, dw, db;
+    if (bias) {
+        const auto made = call.empty<3>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt}}});
+        dx = made[0], dw = made[1], db = made[2];
+    } else {
+        const auto made = call.empty<2>({{{{T, D}, dt}, {{D}, wt}}});
+        dx = made[0], dw = made[1];
+    }
     const size_t need = sgemm_layer_norm_backward_workspace_size((int)T, (int)D);
     const Tensor ws = call.empty({(int64_t)need}, ScalarType::Byte);
     call.run("sgemm_layer_norm_backward", [&] {
@@ -450,8 +490,8 @@ PyObject *lay_out_fp4_scales(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!block || !s.is_cuda() || s.dim() != 2)
         refuse(PyExc_TypeError, "s must be a 2-D CUDA tensor of float8_e4m3fn (blocks of 16) or float8_e8m0fnu (of 32)");
     const Matrix S = rows_of(s, "s");
-    if (S.cols > (1 << 30) / block)
-        refuse(PyExc_ValueError, "s has %lld blocks of %d: more than 2^30 columns", (long long)S.cols, block);
+    if (S.cols > (1 << 24) / block)
+        refuse(PyExc_ValueError, "s has %lld blocks of %d: more than 2^24 columns", (long long)S.cols, block);
     const int64_t K = S.cols * block;
     Call call(s, a[1]);
     const Tiles shape(S.rows, K, block);
@@ -570,8 +610,8 @@ PyObject *beam_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!V) mask = Matrix{};  // no words, and no pointer to them
     }
     Call call(z, a[7]);
-    const Tensor best = call.empty({B, top}, ScalarType::Float), parent = call.empty({B, top}, ScalarType::Int),
-                 token = call.empty({B, top}, ScalarType::Int);
+    const auto made = call.empty<3>({{{{B, top}, ScalarType::Float}, {{B, top}, ScalarType::Int}, {{B, top}, ScalarType::Int}}});
+    const Tensor &best = made[0], &parent = made[1], &token = made[2];
     const size_t size = sgemm_beam_step_workspace_size((int)B, (int)W, (int)top);
     const Tensor ws = call.empty({(int64_t)size}, ScalarType::Byte);
     call.run("sgemm_beam_step", [&] {

@@ -158,3 +158,25 @@ def test_layer_norm_refusals(sg):
         sg.layer_norm(far, w)
     with pytest.raises(ValueError, match="2\\^31"):
         sg.quantize_fp4(far)
+
+
+@pytest.mark.parametrize("T", [1, 3, 400])
+def test_small_results_that_share_memory_are_tensors_of_their_own(sg, T):
+    """What one result is used for does not reach the others, on whichever stream."""
+    import torch
+    x, w = torch.randn(T, 96, device="cuda"), torch.ones(96, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        made = list(sg.layer_norm(x, w, w, x, stream=stream)) + list(sg.layer_norm_backward(x, w, torch.ones(2, T, device="cuda"), x, stream=stream))
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in made]
+        for i, t in enumerate(made):
+            assert t.is_contiguous() and not t.requires_grad and t.data_ptr() % 16 == 0
+            t.zero_()
+            for u, k in zip(made[i + 1:], kept[i + 1:]):
+                assert torch.equal(u, k)
+        first = made[0]
+        del made
+        others = [torch.full((T, 96), 7.0, device="cuda") for _ in range(8)]
+        assert bool((first == 0).all()) and all(bool((o == 7).all()) for o in others)
+    leaf = x.clone().requires_grad_()
+    assert not any(t.requires_grad for t in sg.layer_norm(leaf.detach(), w, add=x))
