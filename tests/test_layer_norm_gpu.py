@@ -239,3 +239,48 @@ def test_same_bits_on_every_run(sg):
         again = sg.layer_norm(s["x"], s["w"], s["b"], s["add"])
         assert all(torch.equal(a, b) for a, b in zip(first, again))
         assert all(torch.equal(a, b) for a, b in zip(grads, sg.layer_norm_backward(first[0], s["w"], first[2], s["dn"], s["dr"])))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [1, 3, 9, 255, 257, 513, 1111, 5121, 9001])
+def test_rows_anywhere_have_the_same_bits_and_leave_what_is_between_them(sg, D, dtype):
+    """Every array starts and steps on its own alignment, and the outputs' rows lie in guards.
+    (Widths of no whole 16 bytes, whose rows are all read alike.)"""
+    import torch
+    from dense_fp32_matrix_04_gb300 import layers
+    T = 5
+    dt, code = td(dtype), {"f32": 0, "bf16": 1, "f16": 2}[dtype]
+    s = inputs(T, D, dtype, True, True, seed=D)
+    r, n, stats = sg.layer_norm(s["x"], s["w"], bias=s["b"], add=s["add"])
+    dx, dw, db = sg.layer_norm_backward(r, s["w"], stats, s["dn"], s["dr"])
+    stream = torch.cuda.current_stream().cuda_stream
+    size = sg.layers._lib.sgemm_layer_norm_backward_workspace_size(T, D)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def room(values, start, pad):
+        buf = torch.full((start + T * (D + pad) + 8,), -77.0, dtype=dt, device="cuda")
+        v = buf[start:start + T * (D + pad)].view(T, D + pad)[:, :D]
+        if values is not None:
+            v.copy_(values)
+        return buf, v
+
+    def untouched(buf, v):
+        v.fill_(-77.0)
+        return bool((buf == -77.0).all())
+
+    for k in range(8):
+        start, pad = [k, (3 * k + 1) % 8, (5 * k + 2) % 8, 7 - k], [k % 3, (k + 1) % 4, 8 * k % 5, k]
+        X, A, R, N = (room(v, start[i], pad[i]) for i, v in enumerate((s["x"], s["add"], None, None)))
+        S = torch.zeros(2, T, device="cuda")
+        assert layers._lib.sgemm_layer_norm(
+            T, D, code, X[1].data_ptr(), D + pad[0], A[1].data_ptr(), D + pad[1], s["w"].data_ptr(), s["b"].data_ptr(), 0, 1e-5,
+            R[1].data_ptr(), D + pad[2], N[1].data_ptr(), D + pad[3], S.data_ptr(), stream) == 0
+        assert torch.equal(R[1], r) and torch.equal(N[1], n) and torch.equal(S, stats)
+        DN, DR, DX = room(s["dn"], start[1], pad[1]), room(s["dr"], start[3], pad[3]), room(None, start[2], pad[2])
+        DW, DB = torch.empty_like(dw), torch.empty_like(db)
+        assert layers._lib.sgemm_layer_norm_backward(
+            T, D, code, R[1].data_ptr(), D + pad[2], s["w"].data_ptr(), 0, S.data_ptr(), DN[1].data_ptr(), D + pad[1],
+            DR[1].data_ptr(), D + pad[3], DX[1].data_ptr(), D + pad[2], DW.data_ptr(), DB.data_ptr(), ws.data_ptr(), size,
+            stream) == 0
+        assert torch.equal(DX[1], dx) and torch.equal(DW, dw) and torch.equal(DB, db)
+        assert all(untouched(*made) for made in (R, N, DX))
