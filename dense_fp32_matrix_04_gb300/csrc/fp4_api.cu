@@ -42,14 +42,14 @@ int by_block(int block, F &&f) {
 
 // ---------------------------------------------------------------- quantising
 
-template <int DT, bool ALIGNED, int BLOCK, int EACH, int DEPTH>
+template <int DT, bool ALIGNED, int BLOCK, int EACH>
 int launch_quantize_rows(const Fp4Rows &a, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {
     using type = typename Elem<DT>::type;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = quantize_fp4_kernel<DT, ALIGNED, BLOCK, EACH, DEPTH>;
+    const auto kernel = quantize_fp4_kernel<DT, ALIGNED, BLOCK, EACH>;
     const int threads = (a.K + 512 * EACH - 1) / (512 * EACH) * 32;
     const dim3 block(threads, threads == 32 ? 4 : 1);
-    const int smem = DEPTH * EACH * Fp4Piece<DT, ALIGNED>::WARP_PIECES * 16 * (int)(block.x * block.y / 32);
+    const int smem = kFp4RowSlots * EACH * Fp4Piece<DT, ALIGNED>::WARP_PIECES * 16 * (int)(block.x * block.y / 32);
     const int fit = sgemm_host::blocks_per_sm(regs, dev, kernel, (int)(block.x * block.y), smem);
     if (!fit) return SGEMM_ERR_LAUNCH;
     const int64_t groups = ((int64_t)a.rows + block.y - 1) / block.y;
@@ -68,10 +68,8 @@ int launch_quantize(const Fp4Rows &a, const void *x, int64_t ldx, const Device &
         return launch(kernel, dim3((unsigned)std::min(a.rows, dev.sms * fit)), dim3(1024), 0, stream, 1, a,
                       static_cast<const type *>(x), ldx);
     }
-    if (a.K <= 4096) return launch_quantize_rows<DT, ALIGNED, BLOCK, 1, 4>(a, x, ldx, dev, stream);
-    // four rows of more than 8192 FP32 columns do not fit shared memory
-    return DT == SGEMM_F32 && a.K > 8192 ? launch_quantize_rows<DT, ALIGNED, BLOCK, 2, DT == SGEMM_F32 ? 2 : 4>(a, x, ldx, dev, stream)
-                                         : launch_quantize_rows<DT, ALIGNED, BLOCK, 2, 4>(a, x, ldx, dev, stream);
+    return a.K <= 4096 ? launch_quantize_rows<DT, ALIGNED, BLOCK, 1>(a, x, ldx, dev, stream)
+                       : launch_quantize_rows<DT, ALIGNED, BLOCK, 2>(a, x, ldx, dev, stream);
 }
 
 int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx, const Device &dev, cudaStream_t stream) {

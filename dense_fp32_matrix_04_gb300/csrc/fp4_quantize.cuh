@@ -231,13 +231,15 @@ struct Fp4Piece {
 };
 
 // A row to the threads of blockDim.x, EACH times 16 columns a thread; blocks walk several rows: the next
-// DEPTH - 1 are on their way into each warp's own places in shared memory while one is worked
-// on (one row ahead in registers: 8192 x 8192 BF16 39.5 us).
-template <int DT, bool ALIGNED, int BLOCK, int EACH, int DEPTH>
+// is on its way into each warp's own places in shared memory while one is worked on (into registers:
+// 8192 x 8192 BF16 39.5 us, so 32.9; with three rows on their way fewer blocks fit, 35.4 and FP32 76.9
+// instead of 51.5).
+constexpr int kFp4RowSlots = 2;
+template <int DT, bool ALIGNED, int BLOCK, int EACH>
 __global__ void __launch_bounds__(EACH == 1 ? 256 : 512)
     quantize_fp4_kernel(const Fp4Rows a, const typename Elem<DT>::type *__restrict__ x, int64_t ldx) {
     using Piece16 = Fp4Piece<DT, ALIGNED>;
-    constexpr int SLOT = Piece16::WARP_PIECES;
+    constexpr int SLOT = Piece16::WARP_PIECES, DEPTH = kFp4RowSlots;
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ float slots[RowReducer::SLOTS];
     griddep_launch_dependents();
