@@ -89,17 +89,19 @@ int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx,
 // How a product is shared out: tiles of 16 to 128 tokens on one SM, for which the
 // blocks of a cluster can split K, or of 256 on a pair.  The smallest estimate, in
 // cycles, of rounds over the SMs times the length of one, from times on GB300 (a step
-// is 256 columns).  A split costs a cluster's launch, two of its barriers and the
-// join: worth it for long rows only (16 x 4096 x 16384 18.9 us whole, 12.0 in four
-// parts; x 4096 8.9 and 8.6, in eight parts 14.6).  Pairs take a cluster's launch too:
-// 600 x 4096 x 4096 14.8 us on single SMs and 14.7, 2048 x 8192 x 4096 39.2 and 33.2.
+// is 256 columns; a round is no shorter than what it stores takes).  A split costs a
+// cluster's launch, two of its barriers and the join: worth it for long rows only
+// (16 x 4096 x 16384 18.9 us whole, 12.0 in four parts; x 4096 8.9 and 8.6, in eight
+// parts 14.6).  Pairs take a cluster's launch too: on single SMs and on pairs
+// 600 x 4096 x 4096 takes 14.6 and 12.9 us, 2432 x 4096 x 1024 13.8 and 14.9,
+// 8192 x 8192 x 1024 57.7 and 44.6.
 struct Fp4Plan {
     int tok = 16, splits = 1;  // tok 256: a pair
     Fp4Plan(int M, int N, int K, int sms) {
         static constexpr struct {
             int tok;
-            double step, round;
-        } kSteps[] = {{16, 395, 600}, {32, 395, 600}, {64, 400, 800}, {128, 450, 1200}, {256, 610, 2200}};
+            double step, round, least;
+        } kSteps[] = {{16, 395, 600, 0}, {32, 395, 600, 0}, {64, 400, 800, 2400}, {128, 450, 1200, 3100}, {256, 610, 1300, 5000}};
         double best = 1e300;
         const int steps = (K + 255) / 256;
         for (const auto &c : kSteps) {
@@ -110,9 +112,9 @@ struct Fp4Plan {
             // (clusters of four leave some SMs without a block)
             for (int s = 1; s == 1 || (!pair && s <= 4 && s <= steps && tiles * s <= sms - 8); s *= 2) {
                 const int64_t rounds = (tiles * s + slots - 1) / slots;
-                double t = (double)rounds * (((steps + s - 1) / s) * c.step + c.round);
+                double t = (double)rounds * std::max(((steps + s - 1) / s) * c.step + c.round, c.least);
                 if (s > 1) t += 1300 + 112. * c.tok;
-                if (pair) t += 5000;
+                if (pair) t += 3500;
                 if (t < best) best = t, tok = c.tok, splits = s;
             }
             if (M <= c.tok) break;
