@@ -11,6 +11,13 @@
 // block drains the accumulator of its own 128 rows: sixteen warps take 64 columns of 32 rows
 // each into registers, so that the next tile's products, which need the same columns of
 // tensor memory, wait for little more than that.
+//
+// 8192 x 8192 x 8192 takes 164 us with blocks of 16 and 151 with blocks of 32, 6.7 and 7.3
+// PFLOP/s: 14 rounds of 76 tiles where 13.5 would do, of 32 steps of some 610 cycles (the
+// products of one take 512) and some 1000 to hand the accumulator over, at the 1.73 GHz that
+// the power cap leaves.  Short K is bound by what a round stores: 4864 x 4096 x 512 with
+// BF16 results 15.4 us, 5000 cycles a round; FP32 results leave at 23 bytes a cycle and SM,
+// as fast as a fill writes them.
 #pragma once
 
 #include <cuda.h>

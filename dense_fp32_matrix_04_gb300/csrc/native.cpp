@@ -2,7 +2,8 @@
 // checked, outputs and workspaces allocated and the library called without a Python
 // statement in between.  A call through ctypes costs the host some 16 us with three
 // outputs (1.5 us of them an argument list of 17, 1.5 - 3 an allocation, 0.5 - 0.7 a
-// tensor that is checked), a multiple of what the GPU needs for a few rows.
+// tensor that is checked), a multiple of what the GPU needs for a few rows; here a
+// layer norm of a few rows costs it 4.2 us, a linear layer 3.5 to 5.6, a beam step 6.1.
 //
 // Every function takes its arguments by place, as layers.py passes them on, the last
 // being the raw handle of the stream (None: torch's current one).  On another stream
@@ -215,40 +216,47 @@ class Call {
         Unlocked other_threads;
         return used(at::detail::empty_cuda(sizes, type, device(), std::nullopt));
     }
-    // Several tensors, dense and of types of their own.  Small ones share an allocation: each costs
-    // the host about a microsecond, a third of it the memory's.  (Only small ones, because one that
-    // lives on keeps the memory of all.)
+    // Several tensors of types of their own, results and workspaces.  Small ones share an allocation:
+    // each costs the host about a microsecond, a third of it the memory's.  (Only small ones, because
+    // one that lives on keeps the memory of all.)
     struct Wanted {
         c10::DimVector sizes;
         ScalarType type;
+        int64_t pitch = 0;  // elements from a row to the next; 0: dense
+        bool wanted = true;
     };
     template <size_t N>
-    std::array<Tensor, N> empty(const std::array<Wanted, N> &wanted) {
+    std::array<Tensor, N> empty(const std::array<Wanted, N> &all) {
         std::array<Tensor, N> made;
         int64_t at[N], bytes = 0;
         for (size_t i = 0; i < N; ++i) {
+            const Wanted &w = all[i];
             at[i] = bytes;
-            bytes += (c10::multiply_integers(wanted[i].sizes) * (int64_t)c10::elementSize(wanted[i].type) + 255) / 256 * 256;
+            const int64_t n = !w.wanted ? 0 : w.pitch ? w.sizes[0] * w.pitch : c10::multiply_integers(w.sizes);
+            bytes += (n * (int64_t)c10::elementSize(w.type) + 255) / 256 * 256;
         }
-        if (bytes > kShared) {
-            for (size_t i = 0; i < N; ++i) made[i] = empty(wanted[i].sizes, wanted[i].type);
-            return made;
-        }
-        const Tensor whole = empty({bytes}, ScalarType::Byte);
+        Tensor whole;
+        if (bytes <= kShared) whole = empty({bytes}, ScalarType::Byte);
         for (size_t i = 0; i < N; ++i) {
-            made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(),
-                                                               c10::scalarTypeToTypeMeta(wanted[i].type));
+            const Wanted &w = all[i];
+            if (!w.wanted) continue;
+            const int64_t strides[2] = {w.pitch, 1};
+            if (!whole.defined()) {
+                if (w.pitch) {
+                    Unlocked other_threads;
+                    made[i] = used(at::detail::empty_strided_cuda(w.sizes, strides, w.type, device()));
+                } else {
+                    made[i] = empty(w.sizes, w.type);
+                }
+                continue;
+            }
+            made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(w.type));
             c10::TensorImpl *impl = made[i].unsafeGetTensorImpl();
-            impl->set_sizes_contiguous(wanted[i].sizes);
-            impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(wanted[i].type));
+            if (w.pitch) impl->set_sizes_and_strides(w.sizes, strides);
+            else impl->set_sizes_contiguous(w.sizes);
+            impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(w.type));
         }
         return made;
-    }
-    // Rows of bytes, `pitch` apart.
-    Tensor empty_rows(int64_t rows, int64_t cols, int64_t pitch) {
-        Unlocked other_threads;
-        const int64_t sizes[2] = {rows, cols}, strides[2] = {pitch, 1};
-        return used(at::detail::empty_strided_cuda(sizes, strides, ScalarType::Byte, device()));
     }
     // Calls the library.
     template <class F>
@@ -303,15 +311,17 @@ void count_arguments(Py_ssize_t n, Py_ssize_t want) {
     if (n != want) refuse(PyExc_TypeError, "%zd arguments, not %zd", n, want);
 }
 
-// An output that is given, or a new one of type `code` of shape M x N.
+// An output that is given, or a new one of type `code` of shape M x N; with `bytes` also a
+// workspace of that size.
 struct Output {
     Tensor made;
+    Tensor space;
     Matrix m;
     int code;
     PyObject *given_object = nullptr;
     PyObject *result() const { return given_object ? Py_NewRef(given_object) : THPVariable_Wrap(made); }
 };
-Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType otherwise, int64_t M, int64_t N) {
+Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType otherwise, int64_t M, int64_t N, size_t bytes = 0) {
     Output o;
     ScalarType type = otherwise;
     if (given(out)) {
@@ -320,6 +330,7 @@ Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType
         if (o.code < 0) refuse(PyExc_TypeError, "out must be float32, bfloat16 or float16");
         o.m = matrix(out, "out", type, call.index(), M, N);
         o.given_object = out;
+        if (bytes) o.space = call.empty({(int64_t)bytes}, ScalarType::Byte);
         return o;
     }
     if (given(out_dtype)) {
@@ -328,7 +339,8 @@ Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType
     }
     o.code = code_of(type);
     if (o.code < 0) refuse(PyExc_TypeError, "out_dtype must be float32, bfloat16 or float16");
-    o.made = call.empty({M, N}, type);
+    const auto made = call.empty<2>({{{{M, N}, type}, {{(int64_t)bytes}, ScalarType::Byte, 0, bytes > 0}}});
+    o.made = made[0], o.space = made[1];
     o.m = Matrix{o.made.data_ptr(), (int)std::max<int64_t>(N, 1), M, N};
     return o;
 }
@@ -394,16 +406,9 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         refuse(PyExc_ValueError, "stats must be the (2, T) float32 tensor that layer_norm returned");
     const bool bias = truth(a[5]);
     Call call(x, a[6]);
-    Tensor dx, dw, db;
-    if (bias) {
-        const auto made = call.empty<3>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt}}});
-        dx = made[0], dw = made[1], db = made[2];
-    } else {
-        const auto made = call.empty<2>({{{{T, D}, dt}, {{D}, wt}}});
-        dx = made[0], dw = made[1];
-    }
     const size_t need = sgemm_layer_norm_backward_workspace_size((int)T, (int)D);
-    const Tensor ws = call.empty({(int64_t)need}, ScalarType::Byte);
+    const auto made = call.empty<4>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt, 0, bias}, {{(int64_t)need}, ScalarType::Byte}}});
+    const Tensor &dx = made[0], &dw = made[1], &db = made[2], &ws = made[3];
     call.run("sgemm_layer_norm_backward", [&] {
         return sgemm_layer_norm_backward((int)T, (int)D, code, X.p, X.ld, w, code_of(wt), static_cast<const float *>(stats.data_ptr()),
                                     DN.p, DN.ld, given(a[4]) ? DR.p : nullptr, DR.ld, dx.data_ptr(), D ? (int)D : 1,
@@ -469,9 +474,10 @@ PyObject *quantize_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Call call(x, a[2]);
     const int64_t pitch = std::max<int64_t>((X.cols + 31) / 32 * 16, 16);
     const Tiles shape(X.rows, X.cols, block);
-    const Tensor packed = call.empty_rows(X.rows, (X.cols + 1) / 2, pitch), tiles = call.empty({shape.rows, shape.bytes}, scales_type(block));
-    Tensor scale;
-    if (block == 16) scale = call.empty({X.rows}, ScalarType::Float);
+    const auto made = call.empty<3>({{{{X.rows, (X.cols + 1) / 2}, ScalarType::Byte, pitch},
+                                      {{shape.rows, shape.bytes}, scales_type(block)},
+                                      {{X.rows}, ScalarType::Float, 0, block == 16}}});
+    const Tensor &packed = made[0], &tiles = made[1], &scale = made[2];
     call.run("sgemm_quantize_fp4", [&] {
         return sgemm_quantize_fp4((int)X.rows, (int)X.cols, code, X.p, X.ld, block, static_cast<unsigned char *>(packed.data_ptr()),
                              (int)pitch, static_cast<unsigned char *>(tiles.data_ptr()),
@@ -552,12 +558,9 @@ PyObject *linear_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         size = t.nbytes();
     }
     Call call(x, a[8]);
-    const Output out = product_output(call, a[6], a[5], x.scalar_type(), M, N);
-    Tensor made;
-    if (!given(a[7]) && (size = sgemm_linear_fp4_workspace_size((int)M, (int)K, ws.block))) {
-        made = call.empty({(int64_t)size}, ScalarType::Byte);
-        space = made.data_ptr();
-    }
+    const size_t need = given(a[7]) ? 0 : sgemm_linear_fp4_workspace_size((int)M, (int)K, ws.block);
+    const Output out = product_output(call, a[6], a[5], x.scalar_type(), M, N, need);
+    if (need) space = out.space.data_ptr(), size = need;
     call.run("sgemm_linear_fp4", [&] {
         return sgemm_linear_fp4((int)M, (int)N, (int)K, code, X.p, X.ld, ws.block, static_cast<const unsigned char *>(W.p), W.ld, ws.p,
                            w_scale, bias, out.m.p, out.m.ld, out.code, space, size, call.stream());
@@ -610,10 +613,12 @@ PyObject *beam_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!V) mask = Matrix{};  // no words, and no pointer to them
     }
     Call call(z, a[7]);
-    const auto made = call.empty<3>({{{{B, top}, ScalarType::Float}, {{B, top}, ScalarType::Int}, {{B, top}, ScalarType::Int}}});
-    const Tensor &best = made[0], &parent = made[1], &token = made[2];
     const size_t size = sgemm_beam_step_workspace_size((int)B, (int)W, (int)top);
-    const Tensor ws = call.empty({(int64_t)size}, ScalarType::Byte);
+    const auto made = call.empty<4>({{{{B, top}, ScalarType::Float},
+                                      {{B, top}, ScalarType::Int},
+                                      {{B, top}, ScalarType::Int},
+                                      {{(int64_t)size}, ScalarType::Byte}}});
+    const Tensor &best = made[0], &parent = made[1], &token = made[2], &ws = made[3];
     call.run("sgemm_beam_step", [&] {
         return sgemm_beam_step((int)B, (int)W, (int)V, code, Z.p, Z.ld, scale, static_cast<const int32_t *>(mask.p), mask.ld,
                           (int)mask.rows, static_cast<const float *>(score.data_ptr()), finished, end, (int)top,
