@@ -7,8 +7,10 @@
 // are each warp's own, about its own mean, joined with one barrier.
 //
 // Memory bounds both: 8192 x 5120 BF16 with a sum and a bias takes 61.4 us, 5.5 TB/s, the
-// gradient of 8192 x 4096 with one from r 42.4 us, 6.3 TB/s and 3 us of joining the blocks'
-// sums.  Rows that are not whole 16 bytes are read and written as single elements and
+// gradient of 8192 x 4096 with one from r 51.3 us, 5.2 TB/s (without 40.5), some 4 of them
+// joining the blocks' sums.  (Clusters of two or four blocks that add theirs first: the same, and 40 %
+// slower, as fours leave SMs without a block.  L2 fetches of 128 and 256 bytes: the same.)
+// Rows that are not whole 16 bytes are read and written as single elements and
 // take 1.0 (FP32 forward) to 2 times as long: 4000 x 5119 BF16 50 us, x 5120 29.  (Whole
 // pieces of them, shifted in registers and handed on to the neighbouring lane, took three
 // times the instructions: forward 7 % slower, the gradient 10 % faster; not kept.)

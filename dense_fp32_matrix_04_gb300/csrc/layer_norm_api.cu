@@ -170,6 +170,17 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
         // one piece a lane where a warp's are enough (64000 x 128 BF16 21.9 us, with two 28.2)
         if (D <= 32 * ONE)
             return vec ? launch_norm_grad<DT, true, ONE, 128>(a, dev, stream) : launch_norm_grad<DT, false, ONE, 128>(a, dev, stream);
+        // FP32 rows that 16 elements a thread keep within fewer blocks, and the widest (4096 x 5120 56 us, with 8
+        // 98; 4000 x 5119 72 and 134; 501 x 22223 95 and 154; but 2000 x 7167, two blocks either way, 88 and 81)
+        if constexpr (DT == SGEMM_F32) {
+            auto blocks = [&](int most) {
+                int ranks = 1;
+                while (ranks < 8 && ranks * most < D) ranks *= 2;
+                return ranks;
+            };
+            if (vec ? blocks(16 * 512) < blocks(8 * 512) : blocks(16 * 320) < blocks(8 * 480) || D > 4 * 8 * 480)
+                return vec ? launch_norm_grad<DT, true, 16, 512>(a, dev, stream) : launch_norm_grad<DT, false, 16, 320>(a, dev, stream);
+        }
         return vec ? launch_norm_grad<DT, true, PER, 512>(a, dev, stream)
                    : launch_norm_grad<DT, false, PER, DT == SGEMM_F32 ? 480 : 320>(a, dev, stream);
     });

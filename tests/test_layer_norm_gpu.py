@@ -284,3 +284,13 @@ def test_rows_anywhere_have_the_same_bits_and_leave_what_is_between_them(sg, D, 
             stream) == 0
         assert torch.equal(DX[1], dx) and torch.equal(DW, dw) and torch.equal(DB, db)
         assert all(untouched(*made) for made in (R, N, DX))
+
+
+@pytest.mark.parametrize("T,D", [(7, 3841), (310, 4501), (5, 5119), (3, 7777), (2, 16001), (310, 5120)])
+@pytest.mark.parametrize("dr", [False, True])
+def test_backward_of_wide_fp32_rows(sg, T, D, dr):
+    s = inputs(T, D, "f32", False, True, seed=T + D)
+    if not dr:
+        s["dr"] = None
+    stats = sg.layer_norm(s["x"], s["w"])[2]
+    check_backward(s, stats, sg.layer_norm_backward(s["x"], s["w"], stats, s["dn"], s["dr"]), "f32")
