@@ -167,7 +167,7 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
         // 16-bit rows of single elements: 320 threads of 16, which take more registers (6664 x 3001 BF16
         // 47.6 us, with 8 elements 59.5; 3907 x 5119, where those are a cluster's, 55 and 106)
         constexpr int DT = decltype(dt)::value, PER = DT == SGEMM_F32 ? 8 : 16, ONE = Elem<DT>::VEC;
-        // one piece a lane where a warp's are enough (64000 x 128 BF16 21.9 us, with two 28.2)
+        // one piece a lane where a warp's are enough (64000 x 128 BF16 20.8 us, with two 27)
         if (D <= 32 * ONE)
             return vec ? launch_norm_grad<DT, true, ONE, 128>(a, dev, stream) : launch_norm_grad<DT, false, ONE, 128>(a, dev, stream);
         // FP32 rows that 16 elements a thread keep within fewer blocks, and the widest (4096 x 5120 56 us, with 8
