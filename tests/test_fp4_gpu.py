@@ -419,3 +419,41 @@ def test_refusals(sg):
     off = torch.zeros(200, dtype=torch.uint8, device="cuda")[4:36].view(1, 32)
     with pytest.raises(ValueError, match="16 bytes"):
         sg.matmul_fp4(off, a[1], None, *w)
+
+
+# ---------------------------------------------------------------- pairs of SMs
+#
+# Which sizes go to pairs is a matter of measured times; these do (rounds of tiles that fill them).
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(4300, 4100, 40), (9000, 4100, 64), (6000, 4999, 130), (1300, 8000, 1400), (1300, 8001, 1450),
+                                   (1300, 8000, 1500), (1700, 4301, 1130)])
+def test_product_on_pairs(sg, M, N, K, block):
+    test_product_of_every_plan(sg, M, N, K, block)
+
+
+@pytest.mark.parametrize("M", [1700, 2900])
+@pytest.mark.parametrize("block", [16, 32])
+def test_strides_and_what_lies_around_on_pairs(sg, M, block):
+    test_strides_and_what_lies_around(sg, M, block)
+
+
+def test_weights_and_tokens_that_are_written_just_before_pairs(sg):
+    test_weights_and_tokens_that_are_written_just_before(sg, 1300, 8000, 2048)
+
+
+@pytest.mark.parametrize("M", [3000, 4100])
+def test_another_stream_a_graph_and_the_same_bits_on_pairs(sg, M):
+    test_another_stream_a_graph_and_the_same_bits(sg, M)
+
+
+@pytest.mark.parametrize("M,N,K", [(1300, 8000, 1500), (4300, 4100, 512), (10, 6400, 4096)])
+def test_a_wait_that_runs_out_on_pairs_and_halves(sg, M, N, K):
+    test_a_wait_that_runs_out_is_reported(sg, M, N, K)
+
+
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("M,N,K", [(10, 6400, 4096), (3, 5001, 3300)])
+def test_product_of_halves(sg, M, N, K, block):
+    """Clusters of two."""
+    test_product_of_every_plan(sg, M, N, K, block)
