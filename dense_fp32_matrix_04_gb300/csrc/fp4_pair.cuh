@@ -16,7 +16,7 @@
 // PFLOP/s: 14 rounds of 76 tiles where 13.5 would do, of 32 steps of some 610 cycles (the
 // products of one take 512) and some 1000 to hand the accumulator over, at the 1.73 GHz that
 // the power cap leaves.  Short K is bound by what a round stores: 4864 x 4096 x 512 with
-// BF16 results 15.4 us, 5000 cycles a round; FP32 results leave at 23 bytes a cycle and SM,
+// BF16 results 14.1 us, some 4500 cycles a round; FP32 results leave at 23 bytes a cycle and SM,
 // as fast as a fill writes them.
 #pragma once
 
@@ -89,6 +89,67 @@ __device__ __forceinline__ void umma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, 
 }
 __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// ---------------------------------------------------------------- results
+
+// fp4_store of 16-bit numbers whose rows start on 4 bytes, by whole warps: two lanes, which have
+// two columns of two tokens, exchange one each, so that a lane stores both columns of a token.
+// left: the columns from this lane pair's first to C's end.  4864 x 4096 x 512 BF16 15.4 us, so 14.1;
+// the four and eight warps that drain on single SMs lose by it what it saves (3001 x 5000 x 512 15.7 us, 17.1).
+template <int COLS, class T>
+__device__ __forceinline__ void fp4_store_pairs(T *c, int64_t ldc, const float *v, const float *token_scales, float scale, float bias,
+                                                int count, int left) {
+    const bool odd = threadIdx.x & 1;
+    const uint32_t take = odd ? 0x3276u : 0x5410u;  // the upper halves, the neighbour's first; the lower, the own first
+    // exchanged first, sixteen tokens' at a time, and then stored: one by one each would wait for the other
+#pragma unroll
+    for (int g = 0; g < COLS; g += 16) {
+        uint32_t both[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(token_scales + g + 2 * i);
+            const float s[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int j = g + 2 * (i + h);
+                const float x = fmaf(v[j] * s[2 * h], scale, bias), y = fmaf(v[j + 1] * s[2 * h + 1], scale, bias);
+                if constexpr (std::is_same_v<T, __half>) {
+                    const __half2 w = __floats2half2_rn(x, y);
+                    both[i + h] = *reinterpret_cast<const uint32_t *>(&w);
+                } else {
+                    const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+                    both[i + h] = *reinterpret_cast<const uint32_t *>(&w);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) both[i] = __byte_perm(both[i], __shfl_xor_sync(0xffffffffu, both[i], 1), take);
+        if (left > 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (g + 2 * i + odd < count) *reinterpret_cast<uint32_t *>(c + (int64_t)(2 * i) * ldc) = both[i];
+        } else if (left > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (g + 2 * i + odd < count) *reinterpret_cast<uint16_t *>(c + (int64_t)(2 * i) * ldc) = (uint16_t)both[i];
+        }
+        __syncwarp();
+        c += 16 * ldc;
+    }
+}
+template <int COLS>
+__device__ __forceinline__ void fp4_store_warp(const Fp4Args &p, const float *v, const float *token_scales, float scale, float bias,
+                                               int m, int col) {
+    if (p.ctype != SGEMM_F32 && p.ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(p.C) & 3) == 0) {
+        const int odd = threadIdx.x & 1, count = p.M - m, left = p.N - (col - odd);
+        const int64_t at = (int64_t)(m + odd) * p.ldc + (col - odd);
+        if (p.ctype == SGEMM_BF16)
+            fp4_store_pairs<COLS>(static_cast<__nv_bfloat16 *>(p.C) + at, p.ldc, v, token_scales, scale, bias, count, left);
+        else fp4_store_pairs<COLS>(static_cast<__half *>(p.C) + at, p.ldc, v, token_scales, scale, bias, count, left);
+    } else if (col < p.N) {
+        fp4_store<COLS>(p, v, token_scales, scale, bias, m, col);
+    }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -309,7 +370,7 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(dsmem_map(acc_empty0 + 8 * b.at, 0));
-            if (in) fp4_store<T::COLS>(p, v, token_scales, scale, bias, m0, col);
+            fp4_store_warp<T::COLS>(p, v, token_scales, scale, bias, m0, col);
             __syncwarp();  // the scales are read before the next tile's take their place
         }
     }

@@ -457,3 +457,21 @@ def test_a_wait_that_runs_out_on_pairs_and_halves(sg, M, N, K):
 def test_product_of_halves(sg, M, N, K, block):
     """Clusters of two."""
     test_product_of_every_plan(sg, M, N, K, block)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+@pytest.mark.parametrize("N", [8000, 8001, 7937])
+def test_16_bit_results_on_pairs_anywhere(sg, N, out):
+    """Rows that start on four bytes are stored two columns at a time, others one by one; the same bits."""
+    import torch
+    M, K = 1301, 1450
+    x, w, bias = operands(sg, M, N, K, N, 16)
+    a = sg.quantize_fp4(x)
+    want = sg.matmul_fp4(*a, *w, bias).to(td(out))   # FP32 results, rounded once
+    for start, pitch in ((0, N + N % 2), (1, N + N % 2), (2, N + 9 - N % 2), (0, N + 6 + N % 2)):
+        room = torch.full((M + 2, pitch + 16), 7.0, dtype=td(out), device="cuda").view(-1)
+        to = room[pitch + start:pitch + start + M * pitch].view(M, pitch)[:, :N]
+        got = sg.matmul_fp4(*a, *w, bias, out=to)
+        assert torch.equal(got, want)
+        to.fill_(7.0)
+        assert bool((room == 7.0).all()), "wrote outside C"
