@@ -34,7 +34,7 @@ constexpr int kFp4RowsSmem = 200 * 1024;
 
 // Columns of the token in shared memory: whole loads.
 __host__ __device__ constexpr int64_t fp4_rows_columns(int K) { return ((int64_t)K + kFp4RowsChunk - 1) / kFp4RowsChunk * kFp4RowsChunk; }
-// Its bytes: FP16 codes, an FP32 scale for every 16 columns (blocks of 32: twice the same).
+// Its bytes: FP16 codes, an FP32 scale for every 16 columns (blocks of 32: two factors of one).
 __host__ __device__ constexpr int64_t fp4_rows_smem(int K) { return fp4_rows_columns(K) / 16 * 36; }
 
 // Place of columns c .. c + 7 (c a multiple of 8) among the token's codes: within a chunk, the four
@@ -58,19 +58,21 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, __half2 *h) {
     for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const __half2 *>(&r[i]);
 }
 
-// The value of an e8m0 scale.
-__device__ __forceinline__ float e8m0_value(uint32_t s) {
-    return __uint_as_float(s == 0 ? 0x400000u : s == 255 ? 0x7fc00000u : s << 23);
+// The power of two of an e8m0 scale as two factors of about its root: the product of two scales may
+// leave FP32 where what they scale does not, that of two factors never does.
+__device__ __forceinline__ float2 e8m0_factors(uint32_t s) {
+    const int e = (int)s - 127, half = e >> 1;
+    return make_float2(__uint_as_float((uint32_t)(127 + half) << 23),
+                       __uint_as_float(s == 255 ? 0x7fc00000u : (uint32_t)(127 + e - half) << 23));
 }
-// Two block scales of 16 columns each from the 16 bits of two e4m3 scales, or the 8 bits of one e8m0.
+// What 32 columns are scaled by: two e4m3 scales of 16 columns each, or the factors of one e8m0.
 template <int BLOCK>
 __device__ __forceinline__ float2 fp4_scale_values(uint32_t s) {
     if constexpr (BLOCK == 16) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3);
         return __half22float2(__half2(h));
     } else {
-        const float v = e8m0_value(s & 255u);
-        return make_float2(v, v);
+        return e8m0_factors(s & 255u);
     }
 }
 // The bits of those scales for row r and columns 32 c .. 32 c + 31.
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kFp4RowsThreads, 3) fp4_rows_kernel(const Fp4R
             put(c, h);
             e2m1x8_to_f16(q.y, h);
             put(c + 8, h);
-            if constexpr (BLOCK == 16) scales[c / 16] = fp4_scale_values<16>(s).x;
-            else scales[c / 16] = e8m0_value(s);
+            const float2 f = fp4_scale_values<BLOCK>(s);
+            scales[c / 16] = BLOCK == 32 && (c & 16) ? f.y : f.x;
         }
         if (BLOCK == 16) row_scale = r.scale();
     }
@@ -210,8 +212,13 @@ __global__ void __launch_bounds__(kFp4RowsThreads, 3) fp4_rows_kernel(const Fp4R
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float2 sb = fp4_scale_values<BLOCK>(ws[r][j]), f = __half22float2(s[r][0]), g = __half22float2(s[r][1]);
-                    acc[r] = fmaf(f.x + f.y, sb.x * sx.x, acc[r]);
-                    acc[r] = fmaf(g.x + g.y, sb.y * sx.y, acc[r]);
+                    if constexpr (BLOCK == 16) {
+                        acc[r] = fmaf(f.x + f.y, sb.x * sx.x, acc[r]);
+                        acc[r] = fmaf(g.x + g.y, sb.y * sx.y, acc[r]);
+                    } else {
+                        // (exact up to the last addition, and infinite only where the product is)
+                        acc[r] = fmaf((f.x + f.y + g.x + g.y) * (sb.x * sx.x), sb.y * sx.y, acc[r]);
+                    }
                 }
             }
         }
