@@ -78,7 +78,10 @@ int code_of(ScalarType t) {
 
 const Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) refuse(PyExc_TypeError, "%s must be a CUDA tensor, not %s", name, Py_TYPE(o)->tp_name);
-    return THPVariable_Unpack(o);
+    const Tensor &t = THPVariable_Unpack(o);
+    // views whose numbers are not those in memory
+    if (t.is_conj() || t.is_neg()) refuse(PyExc_ValueError, "%s is a conjugate or negated view: resolve_conj() and resolve_neg() make it plain", name);
+    return t;
 }
 
 bool given(PyObject *o) { return o != Py_None; }
