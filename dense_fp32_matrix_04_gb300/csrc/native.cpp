@@ -3,7 +3,7 @@
 // statement in between.  A call through ctypes costs the host some 16 us with three
 // outputs (1.5 us of them an argument list of 17, 1.5 - 3 an allocation, 0.5 - 0.7 a
 // tensor that is checked), a multiple of what the GPU needs for a few rows; here a
-// layer norm of a few rows costs it 4.2 us, a linear layer 3.5 to 5.6, a beam step 6.1.
+// layer norm of a few rows costs it 4.6 us, a linear layer 3.3 to 5.7, a beam step 6.9.
 //
 // Every function takes its arguments by place, as layers.py passes them on, the last
 // being the raw handle of the stream (None: torch's current one).  On another stream
@@ -13,7 +13,6 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -215,51 +214,37 @@ class Call {
     }
     int index() const { return index_; }
     cudaStream_t stream() const { return stream_; }
-    Tensor empty(at::IntArrayRef sizes, ScalarType type) {
+    // Memory of the call's own: a workspace, given back to torch when the call returns.
+    c10::DataPtr memory(int64_t bytes) {
         Unlocked other_threads;
-        return used(at::detail::empty_cuda(sizes, type, device(), std::nullopt));
+        return allocate(bytes);
     }
-    // Several tensors of types of their own, results and workspaces.  Small ones share an allocation:
-    // each costs the host about a microsecond, a third of it the memory's.  (Only small ones, because
-    // one that lives on keeps the memory of all.)
+    // A tensor of its own, with a storage of its own: what a call returns may be saved, resized or
+    // given back one by one.
     struct Wanted {
         c10::DimVector sizes;
         ScalarType type;
         int64_t pitch = 0;  // elements from a row to the next; 0: dense
         bool wanted = true;
+        int64_t bytes() const {
+            return (pitch ? sizes[0] * pitch : c10::multiply_integers(sizes)) * (int64_t)c10::elementSize(type);
+        }
     };
     template <size_t N>
     std::array<Tensor, N> empty(const std::array<Wanted, N> &all) {
+        std::array<c10::DataPtr, N> at;
+        {
+            Unlocked other_threads;
+            for (size_t i = 0; i < N; ++i)
+                if (all[i].wanted) at[i] = allocate(all[i].bytes());
+        }
         std::array<Tensor, N> made;
-        int64_t at[N], bytes = 0;
-        for (size_t i = 0; i < N; ++i) {
-            const Wanted &w = all[i];
-            at[i] = bytes;
-            const int64_t n = !w.wanted ? 0 : w.pitch ? w.sizes[0] * w.pitch : c10::multiply_integers(w.sizes);
-            bytes += (n * (int64_t)c10::elementSize(w.type) + 255) / 256 * 256;
-        }
-        Tensor whole;
-        if (bytes <= kShared) whole = empty({bytes}, ScalarType::Byte);
-        for (size_t i = 0; i < N; ++i) {
-            const Wanted &w = all[i];
-            if (!w.wanted) continue;
-            const int64_t strides[2] = {w.pitch, 1};
-            if (!whole.defined()) {
-                if (w.pitch) {
-                    Unlocked other_threads;
-                    made[i] = used(at::detail::empty_strided_cuda(w.sizes, strides, w.type, device()));
-                } else {
-                    made[i] = empty(w.sizes, w.type);
-                }
-                continue;
-            }
-            made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(w.type));
-            c10::TensorImpl *impl = made[i].unsafeGetTensorImpl();
-            if (w.pitch) impl->set_sizes_and_strides(w.sizes, strides);
-            else impl->set_sizes_contiguous(w.sizes);
-            impl->set_storage_offset(at[i] / (int64_t)c10::elementSize(w.type));
-        }
+        for (size_t i = 0; i < N; ++i)
+            if (all[i].wanted) made[i] = tensor_of(all[i], std::move(at[i]));
         return made;
+    }
+    Tensor empty(at::IntArrayRef sizes, ScalarType type) {
+        return empty<1>({{{c10::DimVector(sizes.begin(), sizes.end()), type}}})[0];
     }
     // Calls the library.
     template <class F>
@@ -278,13 +263,22 @@ class Call {
     }
 
    private:
-    static constexpr int64_t kShared = 1 << 17;
-
-    c10::Device device() const { return c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index_)); }
-    Tensor used(Tensor t) const {
+    c10::DataPtr allocate(int64_t bytes) const {
+        c10::DataPtr p = c10::cuda::CUDACachingAllocator::get()->allocate((size_t)bytes);
         if (other_)
             c10::cuda::CUDACachingAllocator::recordStream(
-                t.storage().data_ptr(), c10::cuda::getStreamFromExternal(stream_, static_cast<c10::DeviceIndex>(index_)));
+                p, c10::cuda::getStreamFromExternal(stream_, static_cast<c10::DeviceIndex>(index_)));
+        return p;
+    }
+    // (at::empty's own steps, which are a third of what at::empty costs)
+    static Tensor tensor_of(const Wanted &w, c10::DataPtr p) {
+        auto storage = c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), (size_t)w.bytes(), std::move(p),
+                                                             c10::cuda::CUDACachingAllocator::get(), /*resizable=*/true);
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(std::move(storage)), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                            c10::scalarTypeToTypeMeta(w.type));
+        const int64_t strides[2] = {w.pitch, 1};
+        if (w.pitch) t.unsafeGetTensorImpl()->set_sizes_and_strides(w.sizes, strides);
+        else t.unsafeGetTensorImpl()->set_sizes_contiguous(w.sizes);
         return t;
     }
 
@@ -318,7 +312,7 @@ void count_arguments(Py_ssize_t n, Py_ssize_t want) {
 // workspace of that size.
 struct Output {
     Tensor made;
-    Tensor space;
+    c10::DataPtr space;
     Matrix m;
     int code;
     PyObject *given_object = nullptr;
@@ -327,13 +321,13 @@ struct Output {
 Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType otherwise, int64_t M, int64_t N, size_t bytes = 0) {
     Output o;
     ScalarType type = otherwise;
+    if (bytes) o.space = call.memory((int64_t)bytes);
     if (given(out)) {
         type = tensor(out, "out").scalar_type();
         o.code = code_of(type);
         if (o.code < 0) refuse(PyExc_TypeError, "out must be float32, bfloat16 or float16");
         o.m = matrix(out, "out", type, call.index(), M, N);
         o.given_object = out;
-        if (bytes) o.space = call.empty({(int64_t)bytes}, ScalarType::Byte);
         return o;
     }
     if (given(out_dtype)) {
@@ -342,8 +336,7 @@ Output product_output(Call &call, PyObject *out, PyObject *out_dtype, ScalarType
     }
     o.code = code_of(type);
     if (o.code < 0) refuse(PyExc_TypeError, "out_dtype must be float32, bfloat16 or float16");
-    const auto made = call.empty<2>({{{{M, N}, type}, {{(int64_t)bytes}, ScalarType::Byte, 0, bytes > 0}}});
-    o.made = made[0], o.space = made[1];
+    o.made = call.empty<1>({{{{M, N}, type}}})[0];
     o.m = Matrix{o.made.data_ptr(), (int)std::max<int64_t>(N, 1), M, N};
     return o;
 }
@@ -410,12 +403,13 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const bool bias = truth(a[5]);
     Call call(x, a[6]);
     const size_t need = sgemm_layer_norm_backward_workspace_size((int)T, (int)D);
-    const auto made = call.empty<4>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt, 0, bias}, {{(int64_t)need}, ScalarType::Byte}}});
-    const Tensor &dx = made[0], &dw = made[1], &db = made[2], &ws = made[3];
+    const c10::DataPtr ws = call.memory((int64_t)need);
+    const auto made = call.empty<3>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt, 0, bias}}});
+    const Tensor &dx = made[0], &dw = made[1], &db = made[2];
     call.run("sgemm_layer_norm_backward", [&] {
         return sgemm_layer_norm_backward((int)T, (int)D, code, X.p, X.ld, w, code_of(wt), static_cast<const float *>(stats.data_ptr()),
                                     DN.p, DN.ld, given(a[4]) ? DR.p : nullptr, DR.ld, dx.data_ptr(), D ? (int)D : 1,
-                                    dw.data_ptr(), bias ? db.data_ptr() : nullptr, ws.data_ptr(), need, call.stream());
+                                    dw.data_ptr(), bias ? db.data_ptr() : nullptr, ws.get(), need, call.stream());
     });
     return tuple({dx, dw, db});
     END_HANDLE_TH_ERRORS
@@ -563,7 +557,7 @@ PyObject *linear_fp4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     Call call(x, a[8]);
     const size_t need = given(a[7]) ? 0 : sgemm_linear_fp4_workspace_size((int)M, (int)K, ws.block);
     const Output out = product_output(call, a[6], a[5], x.scalar_type(), M, N, need);
-    if (need) space = out.space.data_ptr(), size = need;
+    if (need) space = out.space.get(), size = need;
     call.run("sgemm_linear_fp4", [&] {
         return sgemm_linear_fp4((int)M, (int)N, (int)K, code, X.p, X.ld, ws.block, static_cast<const unsigned char *>(W.p), W.ld, ws.p,
                            w_scale, bias, out.m.p, out.m.ld, out.code, space, size, call.stream());
@@ -617,16 +611,14 @@ PyObject *beam_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     Call call(z, a[7]);
     const size_t size = sgemm_beam_step_workspace_size((int)B, (int)W, (int)top);
-    const auto made = call.empty<4>({{{{B, top}, ScalarType::Float},
-                                      {{B, top}, ScalarType::Int},
-                                      {{B, top}, ScalarType::Int},
-                                      {{(int64_t)size}, ScalarType::Byte}}});
-    const Tensor &best = made[0], &parent = made[1], &token = made[2], &ws = made[3];
+    const c10::DataPtr ws = call.memory((int64_t)size);
+    const auto made = call.empty<3>({{{{B, top}, ScalarType::Float}, {{B, top}, ScalarType::Int}, {{B, top}, ScalarType::Int}}});
+    const Tensor &best = made[0], &parent = made[1], &token = made[2];
     call.run("sgemm_beam_step", [&] {
         return sgemm_beam_step((int)B, (int)W, (int)V, code, Z.p, Z.ld, scale, static_cast<const int32_t *>(mask.p), mask.ld,
                           (int)mask.rows, static_cast<const float *>(score.data_ptr()), finished, end, (int)top,
                           static_cast<float *>(best.data_ptr()), static_cast<int32_t *>(parent.data_ptr()),
-                          static_cast<int32_t *>(token.data_ptr()), ws.data_ptr(), size, call.stream());
+                          static_cast<int32_t *>(token.data_ptr()), ws.get(), size, call.stream());
     });
     return tuple({best, parent, token});
     END_HANDLE_TH_ERRORS

@@ -456,8 +456,7 @@ def logprobs_backward(logits, target, lse, entropy, g_logprob, g_entropy=None, s
 # ---------------------------------------------------------------- through the native binding
 #
 # The operators below check and allocate in C++ (csrc/native.cpp): a call with three outputs
-# costs the host a quarter to a half of what the ones above do.  Small results of a call (128 KB
-# in all) are tensors of their own in one storage.
+# costs the host a quarter to a half of what the ones above do.
 
 _native = None
 
