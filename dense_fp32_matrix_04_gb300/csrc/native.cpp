@@ -453,7 +453,8 @@ Matrix codes(PyObject *o, const char *name, int index, int64_t rows, int64_t col
         return m;
     }
     if (m.rows > 1 && m.ld % 16)
-        refuse(PyExc_ValueError, "%s has rows %d bytes apart: they must be a multiple of 16, as quantize_fp4 lays them out", name, m.ld);
+        refuse(PyExc_ValueError, "%s has rows %d bytes apart: they must be a multiple of 16, as quantize_fp4 lays them out. Dense rows, as "
+               "copies between devices have them, become such by torch.nn.functional.pad(q, (0, -q.shape[1] %% 16))[:, :q.shape[1]]", name, m.ld);
     if (reinterpret_cast<uintptr_t>(m.p) % 16) refuse(PyExc_ValueError, "%s must start on 16 bytes", name);
     if (m.rows <= 1) m.ld = (int)std::max<int64_t>((m.cols + 15) / 16 * 16, 16);
     return m;

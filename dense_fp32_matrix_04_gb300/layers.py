@@ -517,7 +517,14 @@ def quantize_fp4(x, block=16, stream=None):
     ``q`` (M x ceil(K / 2), uint8) holds two codes a byte, the even column in the low half, on
     rows a multiple of 16 bytes apart; ``block_scale`` is in tiles of 128 rows by 4 blocks (one row of
     tiles a row of the tensor), with the format's type.  Has no gradient, and autograd does not
-    see it."""
+    see it.
+
+    ``torch.save`` keeps the distance of q's rows.  ``clone``, ``contiguous`` and ``to`` another device do
+    not, where K is not a multiple of 32: rows that lie beside each other are refused by the products, and
+
+        q = torch.nn.functional.pad(q, (0, -q.shape[1] % 16))[:, :q.shape[1]]
+
+    puts them apart again."""
     fn = (_native or _load_native()).quantize_fp4
     return fn(x, block, None) if stream is None else _elsewhere(fn, stream, x, block)
 
