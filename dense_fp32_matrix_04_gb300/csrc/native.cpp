@@ -383,10 +383,10 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// x, w, stats, dn, dr, bias, stream
+// x, w, stats, dn, dr, bias, out, stream
 PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    count_arguments(n, 7);
+    count_arguments(n, 8);
     const Tensor &x = tensor(a[0], "x");
     const int code = first_code(x, "x"), dev = x.get_device();
     const Matrix X = rows_of(x, "x");
@@ -400,17 +400,21 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (stats.scalar_type() != ScalarType::Float || stats.dim() != 2 || stats.size(0) != 2 || stats.size(1) != T ||
         !stats.is_contiguous() || stats.get_device() != dev)
         refuse(PyExc_ValueError, "stats must be the (2, T) float32 tensor that layer_norm returned");
-    const bool bias = truth(a[5]);
-    Call call(x, a[6]);
+    const bool bias = truth(a[5]), out = given(a[6]);
+    Matrix DX;
+    if (out) DX = matrix(a[6], "out", dt, dev, T, D);
+    Call call(x, a[7]);
     const size_t need = sgemm_layer_norm_backward_workspace_size((int)T, (int)D);
     const c10::DataPtr ws = call.memory((int64_t)need);
-    const auto made = call.empty<3>({{{{T, D}, dt}, {{D}, wt}, {{D}, wt, 0, bias}}});
-    const Tensor &dx = made[0], &dw = made[1], &db = made[2];
+    const auto made = call.empty<3>({{{{T, D}, dt, 0, !out}, {{D}, wt}, {{D}, wt, 0, bias}}});
+    const Tensor &dx = out ? tensor(a[6], "out") : made[0], &dw = made[1], &db = made[2];
+    if (!out) DX = Matrix{dx.data_ptr(), D ? (int)D : 1, T, D};
     call.run("sgemm_layer_norm_backward", [&] {
         return sgemm_layer_norm_backward((int)T, (int)D, code, X.p, X.ld, w, code_of(wt), static_cast<const float *>(stats.data_ptr()),
-                                    DN.p, DN.ld, given(a[4]) ? DR.p : nullptr, DR.ld, dx.data_ptr(), D ? (int)D : 1,
+                                    DN.p, DN.ld, given(a[4]) ? DR.p : nullptr, DR.ld, DX.p, DX.ld,
                                     dw.data_ptr(), bias ? db.data_ptr() : nullptr, ws.get(), need, call.stream());
     });
+    // (a tensor that is given comes back as the object that it is: THPVariable_Wrap finds it)
     return tuple({dx, dw, db});
     END_HANDLE_TH_ERRORS
 }

@@ -501,12 +501,14 @@ def layer_norm(x, w, bias=None, add=None, eps=1e-5, out=None, stream=None):
     return fn(x, w, bias, add, eps, out, None) if stream is None else _elsewhere(fn, stream, x, w, bias, add, eps, out)
 
 
-def layer_norm_backward(x, w, stats, dn, dr=None, bias=True, stream=None):
+def layer_norm_backward(x, w, stats, dn, dr=None, bias=True, stream=None, *, out=None):
     """Gradients ``(dx, dw, db)`` of ``layer_norm`` from those of its n and r (``dr`` None: zero);
     ``x`` is the r that it returned, and ``dx`` the gradient of x and of ``add``.  ``bias`` False: db
-    is not computed, and None."""
+    is not computed, and None.  ``out`` receives dx; it may be dn, dr or x."""
     fn = (_native or _load_native()).layer_norm_backward
-    return fn(x, w, stats, dn, dr, bias, None) if stream is None else _elsewhere(fn, stream, x, w, stats, dn, dr, bias)
+    if stream is not None:
+        return _elsewhere(fn, stream, x, w, stats, dn, dr, bias, out)
+    return fn(x, w, stats, dn, dr, bias, out, None)
 
 
 def quantize_fp4(x, block=16, stream=None):
