@@ -170,15 +170,15 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
         // one piece a lane where a warp's are enough (64000 x 128 BF16 20.8 us, with two 27)
         if (D <= 32 * ONE)
             return vec ? launch_norm_grad<DT, true, ONE, 128>(a, dev, stream) : launch_norm_grad<DT, false, ONE, 128>(a, dev, stream);
-        // FP32 rows that 16 elements a thread keep within fewer blocks, and the widest (4096 x 5120 56 us, with 8
-        // 98; 4000 x 5119 72 and 134; 501 x 22223 95 and 154; but 2000 x 7167, two blocks either way, 88 and 81)
+        // FP32 rows that 8 elements a thread would share out over a cluster: 16 elements, which keep them within
+        // fewer blocks (2000 x 5120 with dr 32 us, with 8 53), or where three inputs of a row fill the ring sooner
+        // within as many (x 8192 64.6 and 65.0, x 12800 192 and 201).  Rows of single elements: where there are
+        // fewer blocks (x 8191 91 and 136; but x 16383 323 and 284), or where 192 threads leave room for a second
+        // block an SM (x 6001 57 and 76, x 11001 165 and 266; with 224 threads x 7167 87 and 81).
         if constexpr (DT == SGEMM_F32) {
-            auto blocks = [&](int most) {
-                int ranks = 1;
-                while (ranks < 8 && ranks * most < D) ranks *= 2;
-                return ranks;
-            };
-            if (vec ? blocks(16 * 512) < blocks(8 * 512) : blocks(16 * 320) < blocks(8 * 480) || D > 4 * 8 * 480)
+            const int slots = kLayerNormGradStages * (dr ? 3 : 2);
+            const RowPlan wide(D, size, slots, 16, 320), narrow(D, size, slots, 8, 480);
+            if (vec ? D > 8 * 512 : narrow.ranks > 1 && (wide.ranks < narrow.ranks || wide.threads() <= 192))
                 return vec ? launch_norm_grad<DT, true, 16, 512>(a, dev, stream) : launch_norm_grad<DT, false, 16, 320>(a, dev, stream);
         }
         return vec ? launch_norm_grad<DT, true, PER, 512>(a, dev, stream)
