@@ -74,6 +74,13 @@ int launch_norm_grad(LayerNormGradArgs a, const Device &dev, cudaStream_t stream
                         stream, 1, a);
 }
 
+// The most partial sums that the gradient writes, whatever the type and the alignment: one a block, of
+// which rows that every type gives to a warp have four runners each, and elsewhere one a runner.
+int64_t most_grad_partials(int T, int D, int sms) {
+    const int runners = sgemm_host::most_grad_runners(T, D, sms);
+    return D <= 256 ? (runners + 3) / 4 : runners;
+}
+
 // Checks that the forward and the backward pass share.
 bool norm_shape_ok(int T, int D, int dtype, int wdtype, const void *w) {
     if (T < 0 || D < 0 || T > kMaxRows || D > sgemm_host::kMaxWidth || !dtype_ok(dtype)) return false;
@@ -116,7 +123,7 @@ int sgemm_layer_norm(int T, int D, int dtype, const void *x, int ldx, const void
 size_t sgemm_layer_norm_backward_workspace_size(int T, int D) {
     Device dev;
     if (T <= 0 || D <= 0 || T > kMaxRows || D > sgemm_host::kMaxWidth || sgemm_host::device(dev) != SGEMM_OK) return 0;
-    return (size_t)sgemm_host::most_grad_runners(T, D, dev.sms) * 2 * (size_t)D * sizeof(float);
+    return (size_t)most_grad_partials(T, D, dev.sms) * 2 * (size_t)D * sizeof(float);
 }
 
 int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, const void *w, int wdtype, const float *stats,

@@ -137,8 +137,8 @@ int sgemm_layer_norm_backward(int T, int D, int dtype,
                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Workspace bytes of sgemm_layer_norm_backward on the current device (0 if the device
- * cannot be queried or T or D is 0): 8 D for each block, or for narrow rows each warp, that
- * sums over rows, of which an SM holds 1 to 16. */
+ * cannot be queried or T or D is 0): 8 D for each block that sums over rows, of which an SM
+ * holds 1 to 16, for the type and alignment that has the most. */
 size_t sgemm_layer_norm_backward_workspace_size(int T, int D);
 
 /*
