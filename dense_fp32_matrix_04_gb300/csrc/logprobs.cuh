@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
     using type = typename E::type;
     constexpr int VEC = E::VEC, WARPS = THREADS / 32, U = kLogprobPieces<DT>,
                   DEPTH = kLogprobDepth;
+    static_assert(WARPS >= 2, "64 groups of threads");
     extern __shared__ uint4 ring[];
     __shared__ float warp_state[3][WARPS];
     __shared__ float block_state[3];
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
     __shared__ Candidates<TOP ? kTopBuffer : 1> found;
     __shared__ uint8_t again[TOP ? THREADS : 1];
     __shared__ int again_count;
-    __shared__ float group_max[32], fine_max[TOP ? 64 : 1];
+    __shared__ float group_max[TOP ? 64 : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = gridDim.x, part = blockIdx.x, log_parts = __ffs(parts) - 1;  // parts: a power of two
     const float c = a.scale * kLog2e;
@@ -452,25 +453,23 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             // At least `top` columns reach the top-th largest of the maxima of the block's 32 groups
             // of threads, so only threads whose own maximum does have columns to look at again: a
             // handful, unless many logits are equal.  Their pieces, one a lane, come from L2.
-            float g = thread_max;
+            // (More than 16 of 32 groups would have about the smallest maximum as the bound: then there are
+            // 64, and the bound is about their median.)
+            const bool fine = a.top > 16;
+            auto group = [&](auto groups_const) {
+                constexpr int EACH = decltype(groups_const)::value / WARPS;  // groups a warp
+                float g = thread_max;
 #pragma unroll
-            for (int o = 32 / WARPS; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-            if (lane < 32 / WARPS) group_max[warp * (32 / WARPS) + lane] = g;
+                for (int o = EACH; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+                if (lane < EACH) group_max[warp * EACH + lane] = g;
+            };
+            if (fine) group(std::integral_constant<int, 64>{});
+            else group(std::integral_constant<int, 32>{});
             if (threadIdx.x == 0) found.count = again_count = 0;
             if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
             __syncthreads();
-            float floor_v = warp_kth_largest(group_max[lane], a.top, lane);
-            if (a.top > 16 && WARPS >= 2) {
-                // of as many groups as alternatives the smallest maximum would be the bound: twice as many
-                // are compared, and the bound is about their median
-                __syncthreads();
-                float f = thread_max;
-#pragma unroll
-                for (int o = 64 / WARPS; o < 32; o <<= 1) f = fmaxf(f, __shfl_xor_sync(0xffffffffu, f, o));
-                if (lane < 64 / WARPS) fine_max[warp * (64 / WARPS) + lane] = f;
-                __syncthreads();
-                floor_v = warp_kth_largest(fine_max[lane], fine_max[32 + lane], a.top, lane);
-            }
+            const float floor_v = fine ? warp_kth_largest(group_max[lane], group_max[32 + lane], a.top, lane)
+                                       : warp_kth_largest(group_max[lane], a.top, lane);
             if (thread_max >= floor_v && thread_max > -INFINITY) again[atomicAdd(&again_count, 1)] = (uint8_t)threadIdx.x;
             if (outside.v >= floor_v && outside.v > -INFINITY) found.push(outside.v, outside.id);
             __syncthreads();
