@@ -36,7 +36,11 @@ int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t str
     // two warps a row where a row is short, or nothing but its sums is wanted: what a row costs a
     // warp beside its columns weighs less (64000 x 1000 302 -> 81 us, 4096 x 50001 without
     // alternatives 91 -> 80 us; with five alternatives 104 -> 110 us)
-    if (parts == 1 && !a.top) return launch_logprobs<DT, 64, false, MASK, BEAM>(a, 1, dev, stream);
+    if constexpr (!BEAM) {  // (a step of beams has alternatives)
+        if (!a.top)
+            return parts == 1 ? launch_logprobs<DT, 64, false, MASK, false>(a, 1, dev, stream)
+                              : launch_logprobs<DT, 256, false, MASK, false>(a, parts, dev, stream);
+    }
     if (parts == 1 && a.V < 16384) return launch_logprobs<DT, 64, true, MASK, BEAM>(a, 1, dev, stream);
     // four warps for longer rows with alternatives, where there are two for each block that the SMs
     // hold (4096 x 50001 104 -> 89 us; 2000 x 32000 with 20 alternatives 44 -> 49 us), and while
@@ -44,8 +48,7 @@ int logprobs_by_length(const LogprobArgs &a, const Device &dev, cudaStream_t str
     // sees of a row (4096 x 100001 with 5 alternatives 173 -> 171 us, with 20 205 -> 256 us)
     if (parts == 1 && a.T >= 2 * 8 * dev.sms && (int64_t)a.top * a.V <= 1 << 20)
         return launch_logprobs<DT, 128, true, MASK, BEAM>(a, 1, dev, stream);
-    return a.top ? launch_logprobs<DT, 256, true, MASK, BEAM>(a, parts, dev, stream)
-                 : launch_logprobs<DT, 256, false, MASK, BEAM>(a, parts, dev, stream);
+    return launch_logprobs<DT, 256, true, MASK, BEAM>(a, parts, dev, stream);
 }
 
 inline bool logprobs_shape_ok(int T, int V, int dtype, const Rows &z, float scale, const int32_t *mask, int ldm,
