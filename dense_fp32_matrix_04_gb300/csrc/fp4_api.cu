@@ -153,9 +153,9 @@ int launch_mma(const Fp4Args &p, const Fp4Operands &o, int splits, bool early, c
 
 template <int BLOCK>
 int launch_pair(const Fp4Args &p, const Fp4Operands &o, bool early, const Device &dev, cudaStream_t stream) {
-    using T = Fp4PairTile<256, BLOCK>;
+    using T = Fp4PairTile<BLOCK>;
     static std::atomic<int> regs[sgemm_host::kMaxDevices];
-    const auto kernel = fp4_pair_kernel<256, BLOCK>;
+    const auto kernel = fp4_pair_kernel<BLOCK>;
     if (!sgemm_host::blocks_per_sm(regs, dev, kernel, T::THREADS, T::SMEM_BYTES)) return SGEMM_ERR_LAUNCH;
     const int64_t words = (int64_t)fp4_tiles(p.K, BLOCK) * (kFp4TileBytes / 8);
     CUtensorMap tw, tx, tws, txs;

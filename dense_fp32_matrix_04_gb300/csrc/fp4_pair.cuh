@@ -154,9 +154,9 @@ __device__ __forceinline__ void fp4_store_warp(const Fp4Args &p, const float *v,
 
 // ---------------------------------------------------------------- the kernel
 
-template <int TOK_, int BLOCK_>
+template <int BLOCK_>
 struct Fp4PairTile {
-    static constexpr int ROWS = 256, TOK = TOK_, BLOCK = BLOCK_;  // of the pair
+    static constexpr int ROWS = 256, TOK = 256, BLOCK = BLOCK_;  // of the pair: two rows of tiles of scales, 64 columns a load
     static constexpr int BK = 256, BYTES = BK / 2;
     static constexpr int DRAIN = 4, DRAIN_WARPS = 16, COLS = TOK / 4, THREADS = 32 * (DRAIN + DRAIN_WARPS);
     static constexpr int KT = BK / BLOCK / 4;
@@ -168,23 +168,22 @@ struct Fp4PairTile {
     static constexpr int SCALE_BYTES = 4 * DRAIN_WARPS * COLS;
     static constexpr int STAGES = (227 * 1024 - 1024 - 256 - SCALE_BYTES) / STAGE;
     static constexpr int SMEM_BYTES = STAGES * STAGE + SCALE_BYTES + 1024 + 256;
-    static constexpr int ACCS = TOK <= 192 ? 2 : 1;
-    static constexpr int SCALES = ACCS * TOK, SCALE_COLS = 4 * KT * 3, TMEM_COLS = 512;
+    // tensor memory: the accumulator, then a place for the scales of each stage
+    static constexpr int SCALES = TOK, SCALE_COLS = 4 * KT * 3, TMEM_COLS = 512;
     static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(TOK >> 3) << 17) |
                                       ((BLOCK == 32 ? 1u : 0u) << 23) | ((uint32_t)(ROWS >> 4) << 24);
     static constexpr uint32_t SECOND_PAIR = (2u << 4) | (2u << 29);
-    static_assert(TOK == 256, "two rows of tiles of scales; 64 columns a load");
     static_assert(STAGES >= 4 && STAGES <= 8 && SCALES + STAGES * SCALE_COLS <= TMEM_COLS, "a ring, and tensor memory");
 };
 
 // Pair b (blocks 2 b and 2 b + 1, a cluster) takes tiles b, b + pairs, ...  tmWS, tmXS: the
 // scales' tiles, a row of tiles a row, in elements of 8 bytes.
-template <int TOK, int BLOCK>
-__global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
+template <int BLOCK>
+__global__ void __launch_bounds__(Fp4PairTile<BLOCK>::THREADS, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmWS, const __grid_constant__ CUtensorMap tmXS, const Fp4Args p,
                     int *__restrict__ err_word, unsigned long long wait_limit_ns, int debug) {
-    using T = Fp4PairTile<TOK, BLOCK>;
+    using T = Fp4PairTile<BLOCK>;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -195,20 +194,19 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
     // copies of both blocks done (of the first block), stage read by the products; accumulator final,
     // accumulator read by both (of the first block)
     const uint32_t full0 = bars, empty0 = full0 + 8 * T::STAGES;
-    const uint32_t acc_full0 = empty0 + 8 * T::STAGES, acc_empty0 = acc_full0 + 8 * T::ACCS;
-    const uint32_t drained = acc_empty0 + 8 * T::ACCS;
+    const uint32_t acc_full = empty0 + 8 * T::STAGES, acc_empty = acc_full + 8, drained = acc_empty + 8;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + (drained + 8 - base));
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + (drained + 12 - base));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
-    const int tiles_n = (p.N + T::ROWS - 1) / T::ROWS, tiles_m = (p.M + TOK - 1) / TOK, tiles = tiles_m * tiles_n;
+    const int tiles_n = (p.N + T::ROWS - 1) / T::ROWS, tiles_m = (p.M + T::TOK - 1) / T::TOK, tiles = tiles_m * tiles_n;
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int steps = (p.K + T::BK - 1) / T::BK;
     auto tile = [&](int u, int &m0, int &n0) {
         int tn, tm;
         grouped_tile<8>(u, tiles_n, tiles_m, tn, tm);
-        m0 = tm * TOK;
+        m0 = tm * T::TOK;
         n0 = tn * T::ROWS;
     };
 
@@ -218,10 +216,8 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        for (int b = 0; b < T::ACCS; ++b) {
-            mbar_init(acc_full0 + 8 * b, 1);
-            mbar_init(acc_empty0 + 8 * b, 2 * T::DRAIN_WARPS);
-        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * T::DRAIN_WARPS);
         mbar_init(drained, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -251,7 +247,7 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
         };
         auto copy_tokens = [&](uint32_t at, int k, int m0) {
             if (elect_one()) {
-                tma_load_2d_pair(base + at * T::X_BYTES, &tmX, k * T::BYTES, m0 + (int)rank * (TOK / 2), first_full0 + 8 * at);
+                tma_load_2d_pair(base + at * T::X_BYTES, &tmX, k * T::BYTES, m0 + (int)rank * (T::TOK / 2), first_full0 + 8 * at);
                 tma_load_2d_pair(xs_base + at * T::XS_BYTES, &tmXS, k * (T::WS_BYTES / 8), m0 / 128, first_full0 + 8 * at);
             }
         };
@@ -287,12 +283,11 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
         // for each, a step took 760 cycles of issue alone.)
         if (elect_one()) {
             RingPlace<T::STAGES> s;
-            RingPlace<T::ACCS> b;
             const uint64_t x_desc0 = umma_desc_128b(base), w_desc0 = umma_desc_128b(w_base);
             const uint64_t xs_desc0 = umma_desc_scales(xs_base), ws_desc0 = umma_desc_scales(ws_base);
             // The scales' and codes' products of a step of N times 64 columns.  The scales have a place for each
             // stage: it was read by the time that the stage was refilled.
-            auto issue = [&](uint32_t acc, bool first, auto n_const) {
+            auto issue = [&](bool first, auto n_const) {
                 constexpr int N = decltype(n_const)::value;
                 const uint64_t w = w_desc0 + s.at * (T::W_BYTES >> 4), x = x_desc0 + s.at * (T::X_BYTES >> 4);
                 const uint64_t ws = ws_desc0 + s.at * (T::WS_BYTES >> 4), xs = xs_desc0 + s.at * (T::XS_BYTES >> 4);
@@ -307,30 +302,27 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < N; ++kk) {
                     const int t = kk / (BLOCK / 16);
-                    umma_fp4_pair<BLOCK>(acc, w + 2 * kk, x + 2 * kk, BLOCK == 32 && kk % 2 ? T::IDESC | T::SECOND_PAIR : T::IDESC,
+                    umma_fp4_pair<BLOCK>(tmem, w + 2 * kk, x + 2 * kk, BLOCK == 32 && kk % 2 ? T::IDESC | T::SECOND_PAIR : T::IDESC,
                                          w_scales + 4 * t, x_scales + 8 * t, kk > 0 || !first);
                 }
                 umma_commit_pair(empty0 + 8 * s.at);
             };
             const int last = (p.K - (steps - 1) * T::BK + 63) / 64;  // products of the last step
             bool ok = true, ready = false;
-            int i = 0;
-            for (int u = pair; ok && u < tiles; u += pairs, ++i, b.next()) {
-                int m0, n0;
-                tile(u, m0, n0);
-                if (i >= T::ACCS) ok = mbar_wait_polite(acc_empty0 + 8 * b.at, b.round ^ 1, wait_limit_ns, 0);
-                const uint32_t acc = tmem + b.at * TOK;
+            uint32_t turn = 0;  // of the accumulator: the parity of the tiles before
+            for (int u = pair; ok && u < tiles; u += pairs, turn ^= 1) {
+                if (u != pair) ok = mbar_wait_polite(acc_empty, turn ^ 1, wait_limit_ns, 0);
                 for (int k = 0; ok && k < steps; ++k) {
                     if (!ready && !(ok = mbar_wait_polite(full0 + 8 * s.at, s.round, wait_limit_ns, 0))) break;
                     tc_fence_after_sync();
                     RingPlace<T::STAGES> next = s;
                     next.next();
                     ready = mbar_try_wait(full0 + 8 * next.at, next.round);  // asked early, looked at next time
-                    if (k + 1 < steps || last == 4) issue(acc, k == 0, std::integral_constant<int, 4>{});
-                    else if (last == 3) issue(acc, k == 0, std::integral_constant<int, 3>{});
-                    else if (last == 2) issue(acc, k == 0, std::integral_constant<int, 2>{});
-                    else issue(acc, k == 0, std::integral_constant<int, 1>{});
-                    if (k + 1 == steps) umma_commit_pair(acc_full0 + 8 * b.at);
+                    if (k + 1 < steps || last == 4) issue(k == 0, std::integral_constant<int, 4>{});
+                    else if (last == 3) issue(k == 0, std::integral_constant<int, 3>{});
+                    else if (last == 2) issue(k == 0, std::integral_constant<int, 2>{});
+                    else issue(k == 0, std::integral_constant<int, 1>{});
+                    if (k + 1 == steps) umma_commit_pair(acc_full);
                     s = next;
                 }
             }
@@ -348,8 +340,8 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
         griddep_wait();  // the tokens' scales
         const int q = warp & 3, c0 = (warp - T::DRAIN) / 4 * T::COLS;
         float *token_scales = reinterpret_cast<float *>(smem + (scales_base - base)) + (warp - T::DRAIN) * T::COLS;
-        RingPlace<T::ACCS> b;
-        for (int u = pair; u < tiles; u += pairs, b.next()) {
+        uint32_t turn = 0;
+        for (int u = pair; u < tiles; u += pairs, turn ^= 1) {
             int m0, n0;
             tile(u, m0, n0);
             m0 += c0;
@@ -359,17 +351,17 @@ __global__ void __launch_bounds__(Fp4PairTile<TOK, BLOCK>::THREADS, 1)
 #pragma unroll
             for (int j = lane; j < T::COLS; j += 32) token_scales[j] = p.a_scale && m0 + j < p.M ? p.a_scale[m0 + j] : 1.f;
             const float scale = in && p.b_scale ? p.b_scale[col] : 1.f, bias = in && p.bias ? p.bias[col] : 0.f;
-            if (!mbar_wait_warp(acc_full0 + 8 * b.at, b.round, wait_limit_ns, 20)) {
+            if (!mbar_wait_warp(acc_full, turn, wait_limit_ns, 20)) {
                 if (lane == 0) *abort_flag = 1;
                 break;
             }
             tc_fence_after_sync();
             float v[T::COLS];
-            tmem_ld64(tmem + ((uint32_t)(32 * q) << 16) + b.at * TOK + (uint32_t)c0, v);
+            tmem_ld64(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)c0, v);
             // the accumulator is read: hand it back to the product warp
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(dsmem_map(acc_empty0 + 8 * b.at, 0));
+            if (lane == 0) mbar_arrive_cluster(dsmem_map(acc_empty, 0));
             fp4_store_warp<T::COLS>(p, v, token_scales, scale, bias, m0, col);
             __syncwarp();  // the scales are read before the next tile's take their place
         }
