@@ -373,6 +373,16 @@ def sgemm_f32_3xtf32_plan_model(M: int, N: int, K: int, sms: int):
     return int(w.value), int(s.value)
 
 
+def sgemm_fp4_plan_model(M: int, N: int, K: int, sms: int):
+    """Test-only: (tokens of a tile, parts of its K) of an M x N x K product of 4-bit
+    operands on a GPU with ``sms`` SMs, computed without a device; see
+    include/sgemm_layers_testing.h."""
+    t, s = ctypes.c_int(0), ctypes.c_int(0)
+    _check(load().sgemm_fp4_plan_model(int(M), int(N), int(K), int(sms), ctypes.byref(t), ctypes.byref(s)),
+           "sgemm_fp4_plan_model")
+    return int(t.value), int(s.value)
+
+
 def sgemm_f32_streamk_plan_model(M: int, N: int, K: int, sms: int, blocks_per_sm: int = 2):
     """Test-only: (stream-K blocks, workspace bytes) of sgemm_f32_streamk for
     an M x N x K product of aligned operands on a GPU with ``sms`` SMs and

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "../../include/sgemm_layers_testing.h"
 #include "fp4_mma.cuh"
 #include "fp4_pair.cuh"
 #include "fp4_quantize.cuh"
@@ -231,6 +232,16 @@ bool output_ok(const void *C, int ctype, const float *bias) {
 }  // namespace
 
 extern "C" {
+
+int sgemm_fp4_plan_model(int M, int N, int K, int sms, int *tokens, int *parts) {
+    if (!tokens || !parts || M < 1 || N < 1 || K < 1 || M > kMaxRows || N > kMaxRows || K > kMaxColumns || sms < 2)
+        return SGEMM_ERR_INVALID_ARG;
+    const Fp4Plan plan(M, N, K, sms);
+    const bool rows = takes_rows(M, K);
+    *tokens = rows ? 1 : plan.tok;
+    *parts = rows ? 1 : plan.splits;
+    return SGEMM_OK;
+}
 
 size_t sgemm_fp4_scales_size(int rows, int K, int block) {
     if (rows < 0 || K < 0 || rows > kMaxRows || K > kMaxColumns || !block_ok(block)) return 0;

@@ -38,6 +38,7 @@ SIGNATURES = {
     "sgemm_fp4_scales_size": (_S, [_I, _I, _I]),
     "sgemm_fp4_lay_out_scales": (_I, [_I, _I, _I, _P, _I, _P, _P]),
     "sgemm_fp4": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _P]),
+    "sgemm_fp4_plan_model": (_I, [_I, _I, _I, _I, _P, _P]),
     "sgemm_linear_fp4": (_I, [_I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
     "sgemm_linear_fp4_workspace_size": (_S, [_I, _I, _I]),
     "sgemm_logprobs": (_I, [_I, _I, _I, _P, _I, _F, _P, _I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
