@@ -35,15 +35,17 @@ struct BeamArgs {
     int32_t *parent, *token;
 };
 
-// score - ln(sum) - the part of it that the rounded reference holds - scale times the largest:
-// what a candidate's scaled logit is added to.  64 bits where FP32 would round numbers of the size
-// of the score (the sum's fraction has a logarithm below 0.7, which FP32 has to 2^-25).
+// score - ln of the sum relative to the largest's own term: what a candidate's scaled distance from the
+// largest is added to.  Of one column, or where no other counts, the quotient is 1 and the score stays as it
+// is, so that equal beams which have one way to go on stay equal.  64 bits where FP32 would round numbers
+// of the size of the score (the fraction has a logarithm below 0.7, which FP32 has to 2^-25).
 __device__ __forceinline__ double beam_base(float score, float2 r, float scale) {
-    const float c = scale * kLog2e, M = SoftmaxState::reference(r.x, c), off = SoftmaxState::usual(M) ? -fmaf(r.x, c, -M) : 0.f;
-    const uint32_t bits = __float_as_uint(r.y);
-    const int e = (int)(bits >> 23) - 127;  // the sum is at least about 1/2, the largest's own term
+    const float c = scale * kLog2e, M = SoftmaxState::reference(r.x, c);
+    const float own = SoftmaxState::usual(M) ? exp2_approx(fmaf(r.x, c, -M)) : 1.f;  // as the pass computes it
+    const uint32_t bits = __float_as_uint(__fdiv_rn(r.y, own));
+    const int e = (int)(bits >> 23) - 127;
     const float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-    return (double)score - (double)logf(f) - ((double)e + (double)off) * 0.6931471805599453 - (double)r.x * (double)scale;
+    return (double)score - fma((double)e, 0.6931471805599453, (double)logf(f));
 }
 
 // A whole number in the order of the values (not NaN): comparisons in 64 bits without the few units
@@ -56,7 +58,7 @@ __device__ __forceinline__ int64_t ordered(double v) {
 // A block a group, a warp a beam.
 __global__ void __launch_bounds__(1024) beam_join_kernel(const BeamArgs a) {
     __shared__ int64_t list[32][32];
-    __shared__ double base[32];
+    __shared__ double base[32], largest[32];
     const int beam = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row0 = (int64_t)blockIdx.x * a.W;
     griddep_wait();
@@ -64,7 +66,9 @@ __global__ void __launch_bounds__(1024) beam_join_kernel(const BeamArgs a) {
     if (beam == 0 && lane < a.W) {
         const float score = a.score[row0 + lane];
         const bool goes_on = row_takes_part(score, a.finished ? a.finished + row0 + lane : nullptr);
-        base[lane] = goes_on ? beam_base(score, a.reference[row0 + lane], a.scale) : (double)score;
+        const float2 r = goes_on ? a.reference[row0 + lane] : make_float2(0.f, 1.f);
+        base[lane] = goes_on ? beam_base(score, r, a.scale) : (double)score;
+        largest[lane] = (double)r.x;
     }
     const int64_t row = row0 + beam;
     const float score = a.score[row];
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(1024) beam_join_kernel(const BeamArgs a) {
     }
     __syncthreads();
     // candidates of different beams may lie closer than FP32 tells apart
-    const double v = token < 0 ? -INFINITY : fma((double)z, (double)a.scale, base[beam]);
+    const double v = token < 0 ? -INFINITY : fma((double)z - largest[beam], (double)a.scale, base[beam]);
     const int64_t key = ordered(v);
     list[beam][lane] = key;
     __syncthreads();

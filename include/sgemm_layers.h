@@ -326,7 +326,9 @@ size_t sgemm_linear_fp4_workspace_size(int M, int K, int block);
  *                                                               mask allows)
  * the `top` best are written, best first: their scores, their beams (0 .. W - 1) and their
  * columns.  Equal scores go by the lower beam, then the lower column.  The scores are
- * compared in 64 bits (from FP32 sums) and rounded once when they are written.
+ * compared in 64 bits (those of one beam by their logits) and rounded once when they are
+ * written; they come from FP32 sums, whose order, and so their last bit, depends on where in
+ * 16 bytes a row starts.  The only continuation of a beam has the beam's score, exactly.
  *   logits, scale, mask: as in sgemm_logprobs.  score: B x W, dense.
  *   finished: B x W bytes or NULL.  A beam whose byte is not 0 has one continuation, the
  *       column `end` (>= 0) with the score it has; its logits are not read.
