@@ -241,14 +241,15 @@ struct WarpTop {
     }
 };
 
-// The lanes' values in descending order: a bitonic sort.
+// The lanes' values in order, the largest first (or last): a bitonic sort.
+template <bool LAST = false>
 __device__ __forceinline__ float warp_sorted(float x, int lane) {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1)
 #pragma unroll
         for (int stride = size >> 1; stride; stride >>= 1) {
             const float o = __shfl_xor_sync(0xffffffffu, x, stride);
-            x = ((lane & stride) == 0) == ((lane & size) == 0) ? fmaxf(x, o) : fminf(x, o);
+            x = (((lane & stride) == 0) == ((lane & size) == 0)) != LAST ? fmaxf(x, o) : fminf(x, o);
         }
     return x;
 }
@@ -258,11 +259,16 @@ __device__ __forceinline__ float warp_kth_largest(float x, int k, int lane) {
     return __shfl_sync(0xffffffffu, warp_sorted(x, lane), k - 1);
 }
 
-// The same of two values a lane: sorted lists of 32 joined by taking the larger of each one's i-th and
-// the other's i-th from the end, which leaves the 32 largest.
+// The same of two values a lane: the larger of one list's i-th and the other's i-th from the end are the 32
+// largest, a bitonic sequence, which a merge sorts.
 __device__ __forceinline__ float warp_kth_largest(float x, float y, int k, int lane) {
-    const float a = __shfl_sync(0xffffffffu, warp_sorted(x, lane), lane), b = __shfl_sync(0xffffffffu, warp_sorted(y, lane), 31 - lane);
-    return __shfl_sync(0xffffffffu, warp_sorted(fmaxf(a, b), lane), k - 1);
+    float v = fmaxf(warp_sorted(x, lane), warp_sorted<true>(y, lane));
+#pragma unroll
+    for (int stride = 16; stride; stride >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, stride);
+        v = (lane & stride) == 0 ? fmaxf(v, o) : fminf(v, o);
+    }
+    return __shfl_sync(0xffffffffu, v, k - 1);
 }
 
 // Columns that may be among a row's best, in any order, up to CAP of them.
@@ -454,22 +460,26 @@ __global__ void __launch_bounds__(THREADS, (TOP && MASK || DT == SGEMM_F32 && !T
             // of threads, so only threads whose own maximum does have columns to look at again: a
             // handful, unless many logits are equal.  Their pieces, one a lane, come from L2.
             // (More than 16 of 32 groups would have about the smallest maximum as the bound: then there are
-            // 64, and the bound is about their median.)
-            const bool fine = a.top > 16;
+            // 64, and the bound is about their median: 64000 x 1000 with 20 190 -> 189 us, with 32 651 -> 220.
+            // One branch holds all that differs: with two around the barrier, five took 152 us instead of 149.)
+            if (threadIdx.x == 0) found.count = again_count = 0;
+            if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
             auto group = [&](auto groups_const) {
                 constexpr int EACH = decltype(groups_const)::value / WARPS;  // groups a warp
                 float g = thread_max;
 #pragma unroll
                 for (int o = EACH; o < 32; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
                 if (lane < EACH) group_max[warp * EACH + lane] = g;
+                __syncthreads();
             };
-            if (fine) group(std::integral_constant<int, 64>{});
-            else group(std::integral_constant<int, 32>{});
-            if (threadIdx.x == 0) found.count = again_count = 0;
-            if (warp == 0) block_list[lane] = {-INFINITY, INT_MAX};
-            __syncthreads();
-            const float floor_v = fine ? warp_kth_largest(group_max[lane], group_max[32 + lane], a.top, lane)
-                                       : warp_kth_largest(group_max[lane], a.top, lane);
+            float floor_v;
+            if (a.top > 16) {
+                group(std::integral_constant<int, 64>{});
+                floor_v = warp_kth_largest(group_max[lane], group_max[32 + lane], a.top, lane);
+            } else {
+                group(std::integral_constant<int, 32>{});
+                floor_v = warp_kth_largest(group_max[lane], a.top, lane);
+            }
             if (thread_max >= floor_v && thread_max > -INFINITY) again[atomicAdd(&again_count, 1)] = (uint8_t)threadIdx.x;
             if (outside.v >= floor_v && outside.v > -INFINITY) found.push(outside.v, outside.id);
             __syncthreads();
