@@ -6,11 +6,12 @@
 // a candidate's place in the joined list is its place in its own plus, for each other
 // list, the number of candidates there that are better, found by halving.
 //
-// 48 groups of 8 beams over 50001 BF16 logits with 16 continuations take 18.1 us: the pass
-// over the logits is 15 of them, 13 instructions a logit beside an occupancy of half the
-// SM and three rows an SM where 2.5 would do; 1 group of 4 over 131072, 10.3 us, launches
-// and a dozen barriers.  States are copied at the rate of memory: 8 groups of 8 beams,
-// 16 x 4001 x 128 BF16 each, 288 us, 6.0 TB/s of the parents read and the rows written.
+// 48 groups of 8 beams over 50001 BF16 logits with 16 continuations take 19.5 us: most of them the pass
+// over the logits, 13 instructions a logit beside an occupancy of half the
+// SM and three rows an SM where 2.5 would do; 1 group of 4 over 131072 FP32 with a mask 11.6 us,
+// launches and a dozen barriers, on 32 of the SMs.  States are copied at the rate of memory: 8 groups of 8 beams,
+// 16 x 4001 x 128 BF16 each, 290 us, 6.0 TB/s of the parents read and the rows written; in place,
+// where rows that stay are not written, 265.  (Inputs in turn over more than L2 holds.)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -92,10 +92,10 @@ int quantize(const Fp4Rows &a, int dtype, int block, const void *x, int64_t ldx,
 // cycles, of rounds over the SMs times the length of one, from times on GB300 (a step
 // is 256 columns; a round is no shorter than what it stores takes).  A split costs a
 // cluster's launch, two of its barriers and the join: worth it for long rows only
-// (16 x 4096 x 16384 18.9 us whole, 12.0 in four parts; x 4096 8.9 and 8.6, in eight
-// parts 14.6).  Pairs take a cluster's launch too: on single SMs and on pairs
-// 600 x 4096 x 4096 takes 14.6 and 12.9 us, 2432 x 4096 x 1024 13.8 and 14.9,
-// 8192 x 8192 x 1024 57.7 and 44.6.
+// (weights in turn: 16 x 4096 x 16384 18.4 us whole, 12.2 in four parts; x 4096 7.8 and 7.5;
+// 64 x 4096 x 4096 8.2 and 9.4).  Pairs take a cluster's launch too: on single SMs and on pairs
+// 600 x 4096 x 4096 takes 13.4 and 11.8 us, 512 tokens 9.1 and 11.7, 2432 x 4096 x 1024 11.7
+// and 13.2, 8192 x 8192 x 1024 55 and 42.
 struct Fp4Plan {
     int tok = 16, splits = 1;  // tok 256: a pair
     Fp4Plan(int M, int N, int K, int sms) {
@@ -170,8 +170,8 @@ int launch_pair(const Fp4Args &p, const Fp4Operands &o, bool early, const Device
                          stream, 2, tw, tx, tws, txs, p, dev.err_word, sgemm_host::wait_limit_ns(), sgemm_host::test_flags());
 }
 
-// One token whose codes fit shared memory goes to the kernel that reads whole rows (two by
-// 4096 x 4096 took 7.6 us there, on the tensor cores 7.3; one 5.0 and 6.8).
+// One token whose codes fit shared memory goes to the kernel that reads whole rows (by 4096 x 4096,
+// weights in turn, 5.7 us there, on the tensor cores 7.5).
 bool takes_rows(int M, int K) { return M == 1 && fp4_rows_smem(K) <= kFp4RowsSmem; }
 
 template <int XT, int BLOCK>

@@ -15,11 +15,11 @@
 // memory, in a fixed order.  Every wait is bounded; a block that gives up records an
 // error code and frees its tensor memory.
 //
-// Few tokens wait for B: 24 x 16384 x 4096 takes 7.3 us, of which its 36 MB need 5.3 and
-// launch, first copies and last stores the rest.  64 to 512 tokens by 4096 x 4096 take 7.7 to
-// 8.6 us whatever their number: a step of 64 or 128 tokens lasts 400 to 450 cycles, those
-// of issuing twelve instructions and their way through the pipe, where the products alone
-// need 64 to 256.
+// Few tokens wait for one block's chain of steps: one of up to 128 tokens lasts 395 to 450
+// cycles, those of issuing twelve instructions and their way through the pipe, where the
+// products alone need 64 to 256.  24 x 4096 x 4096 takes 7.8 us with weights in turn, from HBM
+// (7.5 with the same ones in L2), 24 x 16384 x 4096, whose 36 MB need 5.3, 10.6 (7.7); 64 to
+// 512 tokens by 4096 x 4096 take 8.4 to 9.2 whatever their number.
 #pragma once
 
 #include <cuda.h>

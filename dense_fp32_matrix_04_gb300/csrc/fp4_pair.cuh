@@ -14,9 +14,10 @@
 //
 // 8192 x 8192 x 8192 takes 164 us with blocks of 16 and 151 with blocks of 32, 6.7 and 7.3
 // PFLOP/s: 14 rounds of 76 tiles where 13.5 would do, of 32 steps of some 610 cycles (the
-// products of one take 512) and some 1000 to hand the accumulator over, at the 1.73 GHz that
+// products of one take 512 in instructions of 64 columns; PTX has one of 96 for this chip, at up
+// to 1.5 times the rate, which is not used) and some 1000 to hand the accumulator over, at the 1.73 GHz that
 // the power cap leaves.  Short K is bound by what a round stores: 4864 x 4096 x 512 with
-// BF16 results 14.1 us, some 4500 cycles a round; FP32 results leave at 23 bytes a cycle and SM,
+// BF16 results 14.0 us, some 4500 cycles a round; FP32 results leave at 23 bytes a cycle and SM,
 // as fast as a fill writes them.
 #pragma once
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t d
 
 // fp4_store of 16-bit numbers whose rows start on 4 bytes, by whole warps: two lanes, which have
 // two columns of two tokens, exchange one each, so that a lane stores both columns of a token.
-// left: the columns from this lane pair's first to C's end.  4864 x 4096 x 512 BF16 15.4 us, so 14.1;
+// left: the columns from this lane pair's first to C's end.  4864 x 4096 x 512 BF16 15.4 us, so 13.8 (weights in L2);
 // the four and eight warps that drain on single SMs lose by it what it saves (3001 x 5000 x 512 15.7 us, 17.1).
 template <int COLS, class T>
 __device__ __forceinline__ void fp4_store_pairs(T *c, int64_t ldc, const float *v, const float *token_scales, float scale, float bias,

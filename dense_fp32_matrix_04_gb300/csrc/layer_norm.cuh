@@ -6,12 +6,16 @@
 // A row is read once into registers and walked as in block_norm.cuh; its two moments
 // are each warp's own, about its own mean, joined with one barrier.
 //
-// Memory bounds both: 8192 x 5120 BF16 with a sum and a bias takes 61.4 us, 5.5 TB/s, the
-// gradient of 8192 x 4096 with one from r 47.7 us, 5.6 TB/s (without 38.9), 2 of them
-// joining the blocks' sums.  (Clusters of two or four blocks that add theirs first: the same, and 40 %
+// Memory bounds both: 8192 x 5120 BF16 with a sum and a bias takes 61.5 us, 5.5 TB/s, the
+// gradient of 8192 x 4096 with one from r 48.3 us, 5.6 TB/s (without 39.1), 2 of them
+// joining the blocks' sums.  (Inputs in turn over more than L2 holds, here and below unless said
+// otherwise.)  (Clusters of two or four blocks that add theirs first: the same, and 40 %
 // slower, as fours leave SMs without a block.  L2 fetches of 128 and 256 bytes: the same.)
+// Rows of a cluster of blocks, beyond 8192 columns (FP32 with a sum: 7168), are bound by its barriers,
+// two a row one after the other with nothing else on the SM: 501 x 22224 BF16 76 us forward and 65
+// backward, 2000 x 8192 FP32 87, where memory needs 13 and 39.
 // Rows that are not whole 16 bytes are read and written as single elements and
-// take 1.0 (FP32 forward) to 2 times as long: 4000 x 5119 BF16 50 us, x 5120 29.  (Whole
+// take 1.0 (FP32 forward) to 2 times as long: 4000 x 5119 BF16 50 us, x 5120 30.  (Whole
 // pieces of them, shifted in registers and handed on to the neighbouring lane, took three
 // times the instructions: forward 7 % slower, the gradient 10 % faster; not kept.)
 #pragma once
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(MAXT, MINB) layer_norm_kernel(const LayerNormA
 //     dx = dr + rstd (u - mean(u) - h mean(u h)),
 // two sums, taken at once, so a row costs one barrier.  dw = sum dn h and db = sum dn
 // over a runner's rows stay in registers; what a block has of them (of narrow rows its four
-// warps, added in shared memory: 16000 x 512 BF16 18.9 us without) goes to `partial`, where a
+// warps, added in shared memory: 16000 x 512 BF16 in L2 12.4 us, 18.9 without) goes to `partial`, where a
 // second kernel adds the blocks in order.
 template <int DT, bool ALIGNED, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNormGradArgs a) {
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(MAXT, 1) layer_norm_grad_kernel(const LayerNor
 // Adds the blocks' partial sums, blockIdx.y 0 of dw and 1 of db: 32 columns by
 // kLayerNormJoinSlices slices of the blocks, each added in order with LOADS loads on
 // their way, then the slices in order.  (With an address computed in 64 bits for each load the
-// kernel took 600 instructions a warp, and the gradient of 300 x 4096 12.4 us instead of 8.6.)
+// kernel took 600 instructions a warp, and the gradient of 300 x 4096, in L2, 12.4 us instead of 8.6.)
 constexpr int kLayerNormJoinSlices = 16;
 template <int DT>
 __global__ void __launch_bounds__(32 * kLayerNormJoinSlices) layer_norm_grad_join_kernel(const LayerNormGradArgs a) {

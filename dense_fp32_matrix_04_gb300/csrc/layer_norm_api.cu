@@ -47,7 +47,7 @@ int norm_by_width(const LayerNormArgs &a, const Device &dev, cudaStream_t stream
     constexpr int VEC = Elem<DT>::VEC;
     // 16 elements a thread, and two blocks an SM while 320 threads are enough (rows of single elements
     // too: 3907 x 5119 BF16 54 us, with one block 62, with 640 threads of 8 elements 58)
-    // one piece a lane where a warp's are enough (64000 x 128 BF16 18.3 us, with two 24.2)
+    // one piece a lane where a warp's are enough (64000 x 128 BF16 with a sum 19.1 us, with two 25.3)
     if (a.D <= 32 * VEC) return launch_norm<DT, ALIGNED, 1, 128, 6>(a, dev, stream);
     if (a.D > 5120) return launch_norm<DT, ALIGNED, 16 / VEC, 512, 1>(a, dev, stream);
     return launch_norm<DT, ALIGNED, 16 / VEC, 320, 2>(a, dev, stream);
@@ -174,7 +174,7 @@ int sgemm_layer_norm_backward(int T, int D, int dtype, const void *x, int ldx, c
         // 16-bit rows of single elements: 320 threads of 16, which take more registers (6664 x 3001 BF16
         // 47.6 us, with 8 elements 59.5; 3907 x 5119, where those are a cluster's, 55 and 106)
         constexpr int DT = decltype(dt)::value, PER = DT == SGEMM_F32 ? 8 : 16, ONE = Elem<DT>::VEC;
-        // one piece a lane where a warp's are enough (64000 x 128 BF16 20.8 us, with two 27)
+        // one piece a lane where a warp's are enough (64000 x 128 BF16 with dr 22.1 us, with two 28.3)
         if (D <= 32 * ONE)
             return vec ? launch_norm_grad<DT, true, ONE, 128>(a, dev, stream) : launch_norm_grad<DT, false, ONE, 128>(a, dev, stream);
         // FP32 rows that 8 elements a thread would share out over a cluster: 16 elements, which keep them within

@@ -18,7 +18,7 @@
 // have such a column, a handful, have theirs looked at again, and the few columns
 // that reach it are ranked against each other.  That is a dozen barriers and a
 // second look at a part of the row, which grows with top and V: 4096 x 50001 takes
-// 80 us without alternatives and 89 with five, 4096 x 100001 205 with twenty.
+// 80 us without alternatives and 89 with five, 4096 x 100001 197 with twenty.
 //
 // Of 16-bit logits the pass is bound by the issue of instructions (about 12 an
 // element, one of them the exponential, which alone would take 44 us at 4096 x
@@ -26,7 +26,7 @@
 // -infinity, whose term 0 times -infinity is NaN, so a chunk with one is added a
 // second time, column by column: 4096 x 50001 takes 181 us with a mask, FP32 4096
 // x 32000 115 against 92.  Three rows of 131072 with 20 alternatives, shared by 24
-// blocks, take 13 us: a latency to read, one to join a cluster, and the row's end.
+// blocks, take 10 us: a latency to read, one to join a cluster, and the row's end.
 // The gradient reads and writes once: 4096 x 32000 FP32 151 us, 511 x 128001 BF16
 // 50 us (5.2 TB/s).
 #pragma once

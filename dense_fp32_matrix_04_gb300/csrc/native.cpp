@@ -85,7 +85,7 @@ const Tensor &tensor(PyObject *o, const char *name) {
 
 bool given(PyObject *o) { return o != Py_None; }
 
-// A number that fits the library's 32 bits; others become the nearest that does, which it refuses.
+// A number that fits the library's 32 bits.
 int whole(PyObject *o, const char *name) {
     int over = 0;
     const long long v = PyLong_AsLongLongAndOverflow(o, &over);

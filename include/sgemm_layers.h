@@ -102,8 +102,9 @@ size_t sgemm_block_norm_backward_workspace_size(int T, int D);
  *     n = (r - mean) rstd w + b,   mean = mean(r), rstd = rsqrt(mean((r - mean)^2) + eps)
  * The sum is rounded to dtype, once, and what is normalised is the r that is written,
  * so the backward pass needs r alone; everything else is FP32, and n is rounded once.
- * The squares are summed about means of parts of the row, so a mean that is large beside
- * the deviation costs nothing more than what rounded inputs hold.
+ * The squares are summed about means of parts of the row, so no difference of large numbers
+ * is taken for the deviation; the mean is an FP32 sum, off by up to about 50 2^-24 of the row's
+ * mean magnitude, which shifts the whole row.
  *   dtype: the type of x, add, r and n.  r is needed exactly when add is given; it may be
  *       x or add (same pointer and leading dimension).
  *   w, b: D weights each, of type wdtype (FP32, or the same as dtype); b may be NULL (0).
@@ -251,7 +252,9 @@ int sgemm_logprobs_backward(int T, int V, int dtype, const void *logits, int ldz
  *   block 32: each block has a power of two, s = the smallest with
  *       max|x| / s <= 6, as its exponent + 127 in 8 bits (e8m0); the codes are
  *       e2m1(x / s), a column stands for code * s, and there is no row scale
- *       (scale is NULL).
+ *       (scale is NULL).  (The microscaling formats' own rule, the exponent of the largest
+ *       less 2, would let magnitudes above 6 s saturate; the products take scales of
+ *       either rule.)
  * All by FP32 operations each rounded once (1 / 6 is the FP32 number next to it), to
  * nearest with ties to even, so codes and scales are defined to the bit.  Blocks whose
  * scale comes out as 0 have codes 0.  A row (block 16), or a block (block 32), that
